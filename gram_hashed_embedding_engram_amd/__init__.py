@@ -16,11 +16,14 @@ LIB_PATH = os.path.join(HERE, "libengram.so")
 OK = 0
 E_ARG, E_RANGE, E_UNSUPPORTED, E_STATE, E_HIP, E_DEVICE = -1, -2, -3, -4, -5, -6
 DEVERR_TOKEN, DEVERR_ROW, DEVERR_POSITION = 1, 2, 4
+DEVERR_PAGE, DEVERR_SEQUENCE = 8, 16
 FMT_Q2K, FMT_E4M3 = 0, 1
 Q2K_ROW_BYTES = 84
 STREAM_ROW_BYTES = 12288      # engram_stream_read's row (ENGRAM_STREAM_ROW_BYTES)
 STREAM_SINK_WORDS = 8192      # its sink (ENGRAM_STREAM_SINK_WORDS)
 STATIC_SCRATCH_BYTES = 32 << 20   # engram_layer_static's scratch (ENGRAM_STATIC_SCRATCH_BYTES)
+PAGE_TOKENS = 64              # positions a cache page holds (ENGRAM_PAGE_TOKENS)
+NORM_GROUP = 32               # values a scale of 8- and 4-bit rows covers (ENGRAM_NORM_GROUP)
 STAGES = ("hash", "gather", "project", "gate")
 
 # Every symbol include/engram.h declares.
@@ -35,6 +38,8 @@ EXPORTS = (
     "engram_ctx_set_timing",
     "engram_ctx_timing", "engram_ctx_destroy", "engram_map_host", "engram_stream_read",
     "engram_ctx_set_graph_mode", "engram_ctx_set_position", "engram_layer_static",
+    "engram_add_norm", "engram_project_w4", "engram_cache_append", "engram_cache_attend_bytes",
+    "engram_cache_attend",
 )
 
 
@@ -64,6 +69,18 @@ class ConfigC(ctypes.Structure):
                 ("eps", ctypes.c_float), ("batch", ctypes.c_int32),
                 ("max_tokens", ctypes.c_int64), ("max_seq", ctypes.c_int64),
                 ("hash", HashTablesC)]
+
+
+class CacheC(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p),
+                ("d_k_scales", ctypes.c_void_p), ("d_v_scales", ctypes.c_void_p)]
+
+
+class SequencesC(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("d_pages", ctypes.c_void_p), ("d_start", ctypes.c_void_p),
+                ("d_cu", ctypes.c_void_p), ("d_err", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,6 +127,13 @@ def lib():
             "engram_ctx_set_position": (i32, [p, i64, p]),
             "engram_layer_static": (i32, [p, i32, p, p, p, i32, i64, ctypes.c_float, p, i64,
                                           i64, p, i64, p, p, p]),
+            "engram_add_norm": (i32, [p, p, i32, p, ctypes.c_float, p, p, p, i64, i64, p]),
+            "engram_project_w4": (i32, [p, p, p, p, p, i64, i64, i64, p]),
+            "engram_cache_append": (i32, [p, p, p, i64, i64, p, i64, i64, p, i64, i64, p, i32, p,
+                                          i32, i32, i64, p]),
+            "engram_cache_attend_bytes": (ctypes.c_size_t, [p, p, i32, i64]),
+            "engram_cache_attend": (i32, [p, p, p, i64, i64, p, i32, i64, ctypes.c_float, i64, p,
+                                          ctypes.c_size_t, p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -325,6 +349,171 @@ def layer_static(tables: HashTables, hash_index, table: Table, d_wkv, d_qk, eps,
                                      int(dim), float(eps), _ptr(d_ids), T, int(start_pos),
                                      _ptr(d_history), int(d_history.numel()), _ptr(d_h),
                                      _ptr(d_err), _stream(stream)))
+
+
+def _typed(t, name, dtypes, shape=None):
+    """Refuse a tensor of another type, shape or, for the kernels that take
+    rows back to back, a strided view."""
+    if str(t.dtype)[6:] not in dtypes:
+        raise EngramError(E_ARG, f"{name}: {t.dtype}, one of {', '.join(dtypes)} is needed")
+    if not t.is_contiguous():
+        raise EngramError(E_ARG, f"{name}: a contiguous tensor is needed")
+    if shape is not None and tuple(t.shape) != shape:
+        raise EngramError(E_ARG, f"{name}: shape {tuple(t.shape)}, {shape} is needed")
+
+
+_BF16 = ("bfloat16", "int16")                       # bf16 values or their bits
+_E4M3 = ("uint8", "float8_e4m3fn")
+_E8M0 = ("uint8", "float8_e8m0fnu")
+
+
+def add_norm(d_x, d_res, d_w, eps, d_codes, d_scales, d_sum=None, stream=None):
+    """Residual addition, root-mean-square norm and 8-bit output
+    (engram_add_norm): d_sum = d_res + d_x, d_codes / d_scales = the normed
+    sum in e4m3 with a scale per 32 values.  d_res [..., dim] f32 or bf16,
+    d_x bf16 of the same shape or None, d_sum None = in place on d_res."""
+    if d_sum is None:
+        d_sum = d_res
+    shape = tuple(d_res.shape)
+    dim = shape[-1]
+    _typed(d_res, "res", ("float32",) + _BF16)
+    rows = d_res.numel() // dim if dim else 0
+    if d_sum is not d_res:
+        _typed(d_sum, "sum", (str(d_res.dtype)[6:],), shape)
+    if d_x is not None:
+        _typed(d_x, "x", _BF16, shape)
+    _typed(d_w, "w", _BF16, (dim,))
+    _typed(d_codes, "codes", _E4M3, shape)
+    _typed(d_scales, "scales", _E8M0, shape[:-1] + (dim // NORM_GROUP,))
+    _check(lib().engram_add_norm(None if d_x is None else d_x.data_ptr(), d_res.data_ptr(),
+                                 d_res.element_size() == 2, d_w.data_ptr(), eps,
+                                 d_sum.data_ptr(), d_codes.data_ptr(), d_scales.data_ptr(), rows,
+                                 dim, _stream(stream)))
+
+
+class W4:
+    """A weight matrix in 4 bits: d_w [N, K/2] e2m1 codes (the even value in
+    the low nibble), d_scales [N, K/32] exponents + 127."""
+
+    def __init__(self, d_w, d_scales):
+        N, half = d_w.shape
+        _typed(d_w, "w", ("uint8",))
+        _typed(d_scales, "w scales", _E8M0, (N, 2 * half // NORM_GROUP))
+        self.w, self.scales = d_w, d_scales
+        self.N, self.K = N, 2 * half
+
+
+def project_w4(d_x, weights: W4, d_y, d_xs=None, stream=None):
+    """y = x w^T through 4-bit weights (engram_project_w4): d_x [T, K] bf16,
+    or e4m3 codes with d_xs [T, K/32]; d_y [T, N] bf16."""
+    T = d_x.shape[0]
+    if d_xs is None:
+        _typed(d_x, "x", _BF16, (T, weights.K))
+    else:
+        _typed(d_x, "x", _E4M3, (T, weights.K))
+        _typed(d_xs, "x scales", _E8M0, (T, weights.K // NORM_GROUP))
+    _typed(d_y, "y", _BF16, (T, weights.N))
+    _check(lib().engram_project_w4(d_x.data_ptr(), None if d_xs is None else d_xs.data_ptr(),
+                                   weights.w.data_ptr(), weights.scales.data_ptr(),
+                                   d_y.data_ptr(), T, weights.K, weights.N, _stream(stream)))
+
+
+class Cache:
+    """A paged 8-bit cache of keys and values (engram_cache): codes
+    [n_pages, kv_heads, 64, head_dim], scales [n_pages, kv_heads] f32."""
+
+    def __init__(self, d_k, d_v, d_k_scales, d_v_scales):
+        n_pages, kv_heads, page, head_dim = d_k.shape
+        _typed(d_k, "k", _E4M3, (n_pages, kv_heads, PAGE_TOKENS, head_dim))
+        _typed(d_v, "v", _E4M3, tuple(d_k.shape))
+        _typed(d_k_scales, "k scales", ("float32",), (n_pages, kv_heads))
+        _typed(d_v_scales, "v scales", ("float32",), (n_pages, kv_heads))
+        self.keep = (d_k, d_v, d_k_scales, d_v_scales)
+        self.kv_heads, self.head_dim, self.n_pages = kv_heads, head_dim, n_pages
+        self.c = CacheC(kv_heads, head_dim, n_pages, d_k.data_ptr(), d_v.data_ptr(),
+                        d_k_scales.data_ptr(), d_v_scales.data_ptr())
+
+
+class Sequences:
+    """The sequences of a step (engram_seqs): d_pages [B, max_pages] int32,
+    d_start [B] int32, d_cu [B+1] int32 token bounds (None: every sequence
+    brings as many tokens), d_err an int32 error word or None."""
+
+    def __init__(self, d_pages, d_start, d_cu=None, d_err=None):
+        B, width = d_pages.shape
+        _typed(d_pages, "pages", ("int32",))
+        _typed(d_start, "start", ("int32",), (B,))
+        if d_cu is not None:
+            _typed(d_cu, "cu", ("int32",), (B + 1,))
+        if d_err is not None:
+            _typed(d_err, "err", ("int32",))
+            _need(d_err, "err", 4)
+        self.keep = (d_pages, d_start, d_cu, d_err)
+        self.B = B
+        self.c = SequencesC(B, width, d_pages.data_ptr(), d_start.data_ptr(), _ptr(d_cu),
+                            _ptr(d_err))
+
+
+def _heads(t, name, T, heads, head_dim):
+    """(address, token stride, head stride) of bf16 heads [T, heads, head_dim]
+    that may be a view of a wider row; a head's values lie side by side."""
+    if str(t.dtype)[6:] not in _BF16:
+        raise EngramError(E_ARG, f"{name}: {t.dtype}, bfloat16 is needed")
+    if tuple(t.shape) != (T, heads, head_dim):
+        raise EngramError(E_ARG, f"{name}: shape {tuple(t.shape)}, {(T, heads, head_dim)} is needed")
+    token, head, one = t.stride()
+    if one != 1:
+        raise EngramError(E_ARG, f"{name}: a head's values must lie side by side")
+    return t.data_ptr(), token, head
+
+
+def cache_append(cache: Cache, seqs: Sequences, d_k, d_v, d_freq, d_q=None, d_q_out=None,
+                 halves=True, stream=None):
+    """Rotates the step's queries and keys and appends its keys and values to
+    the cache (engram_cache_append).  d_k, d_v [T, kv_heads, head_dim] and d_q
+    [T, q_heads, head_dim] bf16, as views of one projection's output if need
+    be; d_freq [rot/2] f32 or None (no rotation); d_q_out as d_q, contiguous."""
+    T = d_k.shape[0]
+    kp, kt, kh = _heads(d_k, "k", T, cache.kv_heads, cache.head_dim)
+    vp, vt, vh = _heads(d_v, "v", T, cache.kv_heads, cache.head_dim)
+    qp = qt = qh = q_heads = qo = 0
+    if d_q is not None:
+        q_heads = d_q.shape[1]
+        qp, qt, qh = _heads(d_q, "q", T, q_heads, cache.head_dim)
+        if d_q_out is None:
+            raise EngramError(E_ARG, "q_out: queries are given and no place for them")
+        _typed(d_q_out, "q_out", _BF16, (T, q_heads, cache.head_dim))
+        qo = d_q_out.data_ptr()
+    rot = fp = 0
+    if d_freq is not None:
+        _typed(d_freq, "freq", ("float32",))
+        rot, fp = 2 * d_freq.numel(), d_freq.data_ptr()
+    _check(lib().engram_cache_append(ctypes.byref(cache.c), ctypes.byref(seqs.c), kp, kt, kh, vp,
+                                     vt, vh, qp, qt, qh, qo, q_heads, fp, rot,
+                                     1 if halves else 0, T, _stream(stream)))
+
+
+def cache_attend_bytes(cache: Cache, seqs: Sequences, q_heads, T):
+    """Workspace bytes a cache_attend of T tokens needs (may be 0)."""
+    return lib().engram_cache_attend_bytes(ctypes.byref(cache.c), ctypes.byref(seqs.c),
+                                           int(q_heads), int(T))
+
+
+def cache_attend(cache: Cache, seqs: Sequences, d_q, d_out, scale, window=0, d_ws=None,
+                 stream=None):
+    """Attention of the step's queries over the cache (engram_cache_attend):
+    d_q [T, q_heads, head_dim] bf16 (a view if need be), d_out contiguous of
+    that shape, d_ws a uint8 tensor of cache_attend_bytes bytes or None."""
+    T, q_heads, _ = d_q.shape
+    qp, qt, qh = _heads(d_q, "q", T, q_heads, cache.head_dim)
+    _typed(d_out, "out", _BF16, (T, q_heads, cache.head_dim))
+    ws, nws = 0, 0
+    if d_ws is not None:
+        _typed(d_ws, "ws", ("uint8",))
+        ws, nws = d_ws.data_ptr(), d_ws.numel()
+    _check(lib().engram_cache_attend(ctypes.byref(cache.c), ctypes.byref(seqs.c), qp, qt, qh,
+                                     d_out.data_ptr(), q_heads, T, scale, window, ws, nws,
+                                     _stream(stream)))
 
 
 class Context:

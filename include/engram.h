@@ -54,6 +54,8 @@ extern "C" {
 #define ENGRAM_DEVERR_TOKEN 1      /* token id < 0 or >= vocab                     */
 #define ENGRAM_DEVERR_ROW 2        /* row id < 0 or >= the table's row count       */
 #define ENGRAM_DEVERR_POSITION 4   /* graph mode: a step past max_seq              */
+#define ENGRAM_DEVERR_PAGE 8       /* page id < 0 or >= the cache's page count     */
+#define ENGRAM_DEVERR_SEQUENCE 16  /* a sequence's start or token bounds           */
 
 /* limits of the hash geometry (the hash constants travel as kernel arguments) */
 #define ENGRAM_MAX_LAYERS 4
@@ -413,6 +415,131 @@ int32_t engram_ctx_set_graph_mode(engram_ctx *ctx, int32_t enable, void *stream)
  * The workspace stays the caller's; work already enqueued on it is not
  * waited for, so destroy a context only after its stream has finished. */
 void engram_ctx_destroy(engram_ctx *ctx);
+
+/* ------------------------------------- the attention sub-layer beside the engram
+ *
+ * What a served token goes through next to the engram on the highway: the
+ * residual's addition with a norm and an 8-bit output (engram_add_norm), a
+ * projection through 4-bit weights (engram_project_w4), the position rotation
+ * with the append to a paged 8-bit cache (engram_cache_append), and attention
+ * over that cache (engram_cache_attend).  None of them allocates, keeps state
+ * between calls or uses atomics on results: equal inputs give equal bits.
+ *
+ * 8-bit values are e4m3fn codes under power-of-two scales: the scale of a
+ * group is the least 2^k, k >= -126, with amax <= 448 * 2^k over the group's
+ * finite values, so no value saturates; rounding is to nearest, ties to even;
+ * a value that is not finite becomes a NaN code. */
+
+/* sum = x + res (rounded once to res' type), y = sum * w / sqrt(mean(sum^2) +
+ * eps) in f32 over each row, and y's codes under one scale per 32 values.
+ *   d_x     [rows][dim] bf16, NULL = nothing is added;
+ *   d_res   [rows][dim] f32 (the highway), or bf16 with res_bf16 != 0;
+ *   d_w     [dim] bf16;  eps >= 0;
+ *   d_sum   [rows][dim] of res' type; may be d_res itself (in place);
+ *   d_codes [rows][dim] e4m3;  d_scales [rows][dim/32], exponent + 127.
+ * dim a multiple of 32 up to 65536, rows below 2^31; d_x, d_res, d_w and
+ * d_sum 16-byte, d_codes 8-byte aligned.  A NaN makes its row NaN codes; an
+ * infinity (or squares that sum past f32's range) makes the norm infinite,
+ * so its row zeros and itself NaN.  rows = 0 is a no-op. */
+#define ENGRAM_NORM_GROUP 32
+int32_t engram_add_norm(const uint16_t *d_x, const void *d_res, int32_t res_bf16,
+                        const uint16_t *d_w, float eps, void *d_sum, uint8_t *d_codes,
+                        uint8_t *d_scales, int64_t rows, int64_t dim, void *stream);
+
+/* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ), f32 sums, w in 4 bits:
+ *   d_w        [N][K/2]: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *              negatives), the even k in the low nibble;
+ *   d_w_scales [N][K/32]: exponents + 127 of a power of two per 32 values
+ *              (255 is NaN);
+ *   d_x        [T][K] e4m3 codes with d_x_scales [T][K/32] of the same kind
+ *              (engram_add_norm's outputs), or bf16 with d_x_scales = NULL;
+ *   d_y        [T][N] bf16.
+ * K a positive multiple of 128 up to 2^20, N a positive multiple of 16 up to
+ * 2^24, T up to 2^22; made for few tokens (the weights are read once per 64 tokens).
+ * d_x and d_w 16-byte, scales 4-byte, d_y 8-byte aligned.  T = 0 is a no-op. */
+int32_t engram_project_w4(const void *d_x, const uint8_t *d_x_scales, const uint8_t *d_w,
+                          const uint8_t *d_w_scales, uint16_t *d_y, int64_t T, int64_t K,
+                          int64_t N, void *stream);
+
+/* A paged cache of keys and values: page p holds ENGRAM_PAGE_TOKENS positions
+ * of one sequence, [n_pages][kv_heads][ENGRAM_PAGE_TOKENS][head_dim] e4m3
+ * codes for each of keys and values, and one f32 scale per page and head,
+ * [n_pages][kv_heads] (engram_cache_append writes powers of two).
+ * head_dim 64, 128 or 256; kv_heads 1..1024; codes 16-byte aligned. */
+#define ENGRAM_PAGE_TOKENS 64
+typedef struct engram_cache {
+    int32_t kv_heads;
+    int32_t head_dim;
+    int64_t n_pages;
+    uint8_t *d_k;
+    uint8_t *d_v;
+    float *d_k_scales;
+    float *d_v_scales;
+} engram_cache;
+
+/* The sequences of one step.  Sequence b holds positions 0 .. d_start[b]-1 in
+ * the cache already and brings tokens d_cu[b] .. d_cu[b+1]-1 of the call's T,
+ * at positions d_start[b] onwards; position p is slot p%64 of page
+ * d_pages[b][p/64].  d_cu [batch+1], non-decreasing within 0..T; NULL gives
+ * every sequence T/batch tokens.  A sequence may bring no token.
+ *   batch 1..65536;  d_pages [batch][max_pages] int32, max_pages below 2^25;
+ *   d_err   nullable.  A sequence with a negative start, token bounds outside
+ *           0..T or in falling order, or positions past its max_pages pages
+ *           sets ENGRAM_DEVERR_SEQUENCE: nothing of it is appended, and its
+ *           attention rows are zeros.  A page id outside the cache sets
+ *           ENGRAM_DEVERR_PAGE: its positions are not written and are masked
+ *           for attention.
+ * Pages that a call appends to belong to one sequence each. */
+typedef struct engram_seqs {
+    int32_t batch;
+    int32_t max_pages;
+    const int32_t *d_pages;
+    const int32_t *d_start;
+    const int32_t *d_cu;
+    int32_t *d_err;
+} engram_seqs;
+
+/* Rotates the step's queries and keys by their positions and appends the
+ * step's keys and values to the cache.
+ *   d_q, d_k, d_v  bf16, head h of token t at + t*token_stride + h*head_stride
+ *                  (in values, multiples of 8; 16-byte aligned), so the heads
+ *                  can sit side by side in one projection's output.  d_q NULL
+ *                  (with q_heads 0): no queries;
+ *   d_freq         [rot/2] f32: pair i of the first `rot` values of a head
+ *                  turns by angle position * freq[i] (formed in 64 bits):
+ *                  (a, b) -> (a cos - b sin, a sin + b cos); pairs are
+ *                  (i, i + rot/2) with halves != 0, else (2i, 2i + 1).
+ *                  rot a multiple of 16 up to head_dim, 0 = no rotation;
+ *   d_q_out        [T][q_heads][head_dim] bf16, the turned queries.
+ * Keys are turned and quantised from f32 (not rounded to bf16 between).  The
+ * scale of a page and head covers the new tokens and, where the page already
+ * holds older positions, is at least its old one; where it rises, the older
+ * codes are rounded again under it.  Slots past the last token keep their
+ * bytes.  T up to 2^22; T = 0 is a no-op. */
+int32_t engram_cache_append(const engram_cache *cache, const engram_seqs *seqs,
+                            const uint16_t *d_k, int64_t k_token_stride, int64_t k_head_stride,
+                            const uint16_t *d_v, int64_t v_token_stride, int64_t v_head_stride,
+                            const uint16_t *d_q, int64_t q_token_stride, int64_t q_head_stride,
+                            uint16_t *d_q_out, int32_t q_heads, const float *d_freq, int32_t rot,
+                            int32_t halves, int64_t T, void *stream);
+
+/* Attention of the step's queries over the cache (append first): query head h
+ * of a token at position p reads key head h / (q_heads/kv_heads) at positions
+ * j <= p, and j > p - window where window > 0:
+ *   out = softmax_j(scale * q . k_j) v_j, in f32, rounded once to bf16.
+ * Queries with no position left to read give zeros.  Tokens of no sequence
+ * are left as they are.
+ *   d_q as for engram_cache_append; d_out [T][q_heads][head_dim] bf16,
+ *   8-byte aligned; q_heads a multiple of kv_heads; scale finite;
+ *   d_ws (256-byte aligned, caller-owned) of engram_cache_attend_bytes bytes:
+ *   the partial results of calls whose keys are split over workgroups; may be
+ *   NULL where that is 0.  Calls that share it must not overlap. */
+size_t engram_cache_attend_bytes(const engram_cache *cache, const engram_seqs *seqs,
+                                 int32_t q_heads, int64_t T);
+int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
+                            const uint16_t *d_q, int64_t q_token_stride, int64_t q_head_stride,
+                            uint16_t *d_out, int32_t q_heads, int64_t T, float scale,
+                            int64_t window, void *d_ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------ measurement */
 

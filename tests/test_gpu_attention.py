@@ -1,0 +1,536 @@
+"""The attention sub-layer's operators on the GPU against their 64-bit forms
+(tests/_attention_ref.py).  Tolerances count roundings: half a step of the
+result's type (bf16 2^-8, e4m3 2^-4 relative), f32 sums of n terms n * 2^-24 of
+the sum of their magnitudes."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import _attention_ref as R  # noqa: E402
+from _gpu_util import log  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module")
+def E():
+    import gram_hashed_embedding_engram_amd as E
+    E.lib()
+    return E
+
+
+def seeded(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def within(got, want, tol, what):
+    got, want = got.to(F64), want.to(F64)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN in other places"
+    off = torch.where(torch.isnan(want), torch.zeros_like(want), (got - want).abs() - tol)
+    worst = float(off.max()) if off.numel() else 0.0
+    assert worst <= 0, f"{what}: {worst:.3e} past the tolerance at {int(off.argmax())}"
+
+
+# ------------------------------------------------------------------- norm
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("rows,dim", [(1, 32), (3, 64), (1, 4096), (5, 96), (64, 1056), (7, 7200),
+                                      (300, 512), (2, 65536), (2, 16416), (9, 10240)])
+def test_add_norm(E, rows, dim, add, bf16):
+    log(f"add_norm {rows} x {dim} add {add} bf16 {bf16}")
+    g = seeded(rows * 7 + dim)
+    t = torch.bfloat16 if bf16 else torch.float32
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    res = (rn(rows, dim) * torch.exp2(rn(rows, 1) * 4)).to(t)
+    x = (rn(rows, dim) * 0.3).bfloat16() if add else None
+    w = (1 + 0.3 * rn(dim)).bfloat16()
+    if rows > 2:
+        res[1] = 0                                     # scales at their floor
+        if x is not None:
+            x[1] = 0
+        res[2, dim // 2] = math.inf if rows % 2 else math.nan
+        w[:32] = 0                                     # a group of zeros
+    codes = torch.zeros(rows, dim, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(rows, dim // 32, dtype=torch.uint8, device="cuda")
+    total = torch.empty_like(res) if rows % 2 else None
+    keep = res.clone()
+    E.add_norm(x, res, w, 1e-6, codes, scales, d_sum=total)
+    torch.cuda.synchronize()
+    s = res if total is None else total
+    if total is not None:
+        assert torch.equal(res.nan_to_num(), keep.nan_to_num())
+    want_s = (keep.float() + (x.float() if add else 0)).to(t)      # one rounding: the same bits
+    assert torch.equal(s.nan_to_num(), want_s.nan_to_num())
+    r = want_s.to(F64)
+    y = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-6) * w.to(F64)
+    # sum of squares: a thread's chain and a tree of ten; then root, quotient, products
+    rel = (dim / 256 + 32) * 2.0 ** -24
+    got_s = torch.exp2(scales.to(F64) - 127)
+    # NaN (a NaN in the row, or an infinity over the infinite norm) is outside a scale
+    amax = y.nan_to_num().abs().view(rows, -1, 32).amax(2)
+    ok = (got_s == R.scale_of(amax)) | R.near_border(amax, 2 * rel)
+    assert bool(ok.all())
+    wide = got_s.repeat_interleave(32, 1)
+    tol = y.abs() * (2.0 ** -4 * (1 + 2 * rel) + rel) + 2.0 ** -10 * wide
+    within(R.e4m3(codes) * wide, y, tol, "codes")
+
+
+# --------------------------------------------------------------------- w4
+def w4_case(seed, T, K, N, fp8, lo=110, hi=130):
+    g = seeded(seed)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(lo, hi, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(T, K, generator=g, device="cuda")
+    if fp8:
+        codes = (x * 100).to(torch.float8_e4m3fn).view(torch.uint8)
+        xs = torch.randint(lo, hi, (T, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+        return w, ws, codes, xs, R.grouped(R.e4m3(codes), xs)
+    return w, ws, x.bfloat16(), None, x.bfloat16().to(F64)
+
+
+def check_w4(E, w, ws, x, xs, x64):
+    T, K, N = x.shape[0], x.shape[1], w.shape[0]
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    E.project_w4(x, E.W4(w, ws), y, xs)
+    torch.cuda.synchronize()
+    w64 = R.grouped(R.e2m1(w), ws)
+    want = x64 @ w64.t()
+    tol = 2.0 ** -8 * want.abs() + K * 2.0 ** -24 * (x64.abs() @ w64.abs().t()) + 1e-38
+    within(y, want, tol, "y")
+    return y
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("T,K,N", [(1, 128, 16), (1, 4096, 6144), (2, 512, 48), (5, 640, 1040),
+                                   (16, 2048, 256), (17, 896, 272), (33, 1152, 4112), (48, 384, 16),
+                                   (64, 6144, 512), (65, 256, 64), (130, 768, 80), (200, 1024, 1296),
+                                   (1, 16384, 32)])
+def test_project_w4(E, T, K, N, fp8):
+    log(f"project_w4 T {T} K {K} N {N} fp8 {fp8}")
+    check_w4(E, *w4_case(T + K + N, T, K, N, fp8))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_project_w4_single_products(E, fp8):
+    """One non-zero value a token: every code, every scale byte at both ends of
+    its range, each k in its own place."""
+    K, N, T = 256, 16, 64
+    g = seeded(3)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(64, 191, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    for first in range(0, K, T):
+        x = torch.zeros(T, K, device="cuda")
+        x[torch.arange(T), first + torch.arange(T)] = 1.0
+        if fp8:
+            codes = x.to(torch.float8_e4m3fn).view(torch.uint8)
+            xs = torch.full((T, K // 32), 127, device="cuda", dtype=torch.uint8)
+            y = check_w4(E, w, ws, codes, xs, x.to(F64))
+        else:
+            y = check_w4(E, w, ws, x.bfloat16(), None, x.to(F64))
+        want = R.grouped(R.e2m1(w), ws)[:, first:first + T].t()
+        assert torch.equal(y.to(F64), want)           # a power of two times a code: exact
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_project_w4_nan(E, fp8):
+    """A NaN scale or value reaches its own outputs and no others."""
+    w, ws, x, xs, x64 = w4_case(11, 20, 512, 64, fp8)
+    ws[5, 3] = 255
+    if fp8:
+        xs[7, 2] = 255
+        x[9, 100] = 0x7F
+        x64 = R.grouped(R.e4m3(x), xs)
+    else:
+        x[7, 64] = math.nan
+        x[9, 100] = math.nan
+        x64 = x.to(F64)
+    y = torch.zeros(20, 64, dtype=torch.bfloat16, device="cuda")
+    E.project_w4(x, E.W4(w, ws), y, xs)
+    bad = torch.zeros(20, 64, dtype=torch.bool, device="cuda")
+    bad[:, 5] = True
+    bad[7] = bad[9] = True
+    assert torch.equal(torch.isnan(y), bad)
+
+
+# ----------------------------------------------------------------- append
+STEPS = [  # new tokens, older positions, kv heads, queries a key head, head_dim
+    ([1], [0], 1, 1, 64), ([1], [63], 2, 4, 128), ([1], [64], 2, 3, 64), ([1, 1, 1], [5, 127, 300], 4, 8, 256),
+    ([3, 0, 70], [62, 10, 0], 2, 4, 128), ([130, 1, 64, 0], [1, 200, 64, 7], 1, 6, 64),
+    ([257], [40], 2, 1, 256), ([2] * 70, [3 * i for i in range(70)], 1, 2, 64),
+    ([0, 5], [0, 60], 3, 1, 128)]
+
+
+def check_append(E, st, freq, halves, cu=True, with_q=True):
+    q, k, v = st.heads()
+    out = torch.full((st.T, st.q, st.d), 9.0, dtype=torch.bfloat16, device="cuda") if with_q else None
+    old_c = [c.clone() for c in st.codes]
+    old_s = [s.clone() for s in st.scales]
+    cache, seqs = st.objects(E, cu=cu)
+    E.cache_append(cache, seqs, k, v, freq, q if with_q else None, out, halves=halves)
+    torch.cuda.synchronize()
+    assert int(st.err) == 0
+    f = freq if freq is not None else torch.zeros(0, device="cuda")
+    pos = torch.cat([torch.arange(o, o + n, device="cuda") for n, o in zip(st.new, st.old)])
+    # an angle is formed in 64 bits, its cosine and sine are f32 of 2^-22, two products and a sum
+    if with_q:
+        want, size = R.rotate(q, pos, f, halves)
+        within(out, want, 2.0 ** -8 * want.abs() + 2.0 ** -21 * size, "q")
+    kr, ksize = R.rotate(k, pos, f, halves)
+    touched = torch.zeros(st.n_pages, dtype=torch.bool, device="cuda")
+    for which, (vals, size) in enumerate(((kr, ksize), (v.to(F64), None))):
+        c, s = st.codes[which], st.scales[which]
+        rel = 2.0 ** -20 if which == 0 and f.numel() else 0.0
+        first = 0
+        for b, (n, o) in enumerate(zip(st.new, st.old)):
+            for blk in range(o // 64, (o + n + 63) // 64 if n else 0):
+                pg = int(st.pages[b, blk])
+                touched[pg] = True
+                lo, hi = max(o, blk * 64), min(o + n, blk * 64 + 64)
+                x = vals[first + lo - o:first + hi - o].transpose(0, 1)
+                a = lo - blk * 64
+                amax = x.abs().amax((1, 2))
+                need = R.scale_of(amax)
+                had = old_s[which][pg].to(F64) if a else torch.zeros_like(need)
+                now = s[pg].to(F64)
+                ok = now == torch.maximum(need, had)
+                if rel:
+                    ok |= R.near_border(amax, rel) & (now >= had)
+                assert bool(ok.all()), f"scales of page {pg}"
+                got = R.e4m3(c[pg, :, a:a + hi - lo]) * now[:, None, None]
+                if which:                       # values: the exact nearest code
+                    exact = (x / now[:, None, None]).float().to(torch.float8_e4m3fn).view(torch.uint8)
+                    assert torch.equal(c[pg, :, a:a + hi - lo], exact)
+                tol = 2.0 ** -4 * x.abs() + 2.0 ** -10 * now[:, None, None]
+                if rel:
+                    tol = tol + 2.0 ** -20 * size[first + lo - o:first + hi - o].transpose(0, 1)
+                within(got, x, tol, f"codes of page {pg}")
+                if a:                           # older codes: rounded once more where the scale rose
+                    ratio = (had / now).float()
+                    exact = (R.e4m3(old_c[which][pg, :, :a]).float() * ratio[:, None, None]) \
+                        .to(torch.float8_e4m3fn).view(torch.uint8)
+                    assert torch.equal(c[pg, :, :a], exact)
+                if a + hi - lo < 64:
+                    assert torch.equal(c[pg, :, a + hi - lo:], old_c[which][pg, :, a + hi - lo:])
+            first += n
+        assert torch.equal(c[~touched], old_c[which][~touched])
+        assert torch.equal(s[~touched].nan_to_num(), old_s[which][~touched].nan_to_num())
+
+
+@pytest.mark.parametrize("halves", [True, False])
+@pytest.mark.parametrize("part", [0, 1, 2])
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_append(E, case, part, halves):
+    new, old, kv, g, d = STEPS[case]
+    log(f"append {new[:6]} after {old[:6]} kv {kv} g {g} d {d} part {part} halves {halves}")
+    st = R.Step(case * 10 + part, new, old, kv, g, d, qstride=8 * (case % 3))
+    if case % 2:
+        st.qkv *= 30                                   # scales rise
+    freq = None if part == 0 else R.freq_of(d // part)
+    check_append(E, st, freq, halves, with_q=case != 2)
+
+
+def test_append_uniform(E):
+    """No token bounds: each sequence brings as many."""
+    for n in (1, 5, 64):
+        st = R.Step(n, [n] * 3, [7, 64, 130], 2, 4, 128)
+        check_append(E, st, R.freq_of(128), True, cu=False)
+
+
+def test_append_far_positions(E):
+    """Angles of far positions: the position times the frequency in 64 bits."""
+    st = R.Step(5, [3, 2], [1000001, 131070], 1, 2, 64)
+    check_append(E, st, R.freq_of(64), True)
+
+
+def test_append_repeats(E):
+    """The same step again finds its own scales: the same bytes."""
+    st = R.Step(6, [3, 70], [62, 1], 2, 4, 128)
+    check_append(E, st, R.freq_of(128), True)
+    c = [x.clone() for x in st.codes + st.scales]
+    q, k, v = st.heads()
+    cache, seqs = st.objects(E)
+    E.cache_append(cache, seqs, k, v, R.freq_of(128), halves=True)
+    for x, y in zip(c, st.codes + st.scales):
+        assert torch.equal(x.nan_to_num(), y.nan_to_num())
+
+
+def test_append_not_finite(E):
+    """A NaN or an infinity becomes a NaN code; the scale covers the rest."""
+    st = R.Step(7, [4], [62], 1, 1, 64)
+    q, k, v = st.heads()
+    v[1, 0, 5] = math.inf
+    v[2, 0, 6] = math.nan
+    v[3] = 0
+    old = [s.clone() for s in st.scales]
+    cache, seqs = st.objects(E)
+    E.cache_append(cache, seqs, k, v, None)
+    p0, p1 = int(st.pages[0, 0]), int(st.pages[0, 1])
+    got = R.e4m3(st.codes[1])
+    assert bool(torch.isnan(got[p0, 0, 63, 5])) and bool(torch.isnan(got[p1, 0, 0, 6]))
+    nan = torch.isnan(got[p1, 0, :2])
+    assert int(nan.sum()) == 1
+    need = torch.maximum(R.scale_of(v[0].abs().amax().to(F64)),
+                         R.scale_of(v[1, 0][torch.isfinite(v[1, 0])].abs().amax().to(F64)))
+    assert float(st.scales[1][p0, 0]) == max(float(need), float(old[1][p0, 0]))
+    # a page of zeros takes the lowest scale
+    st = R.Step(8, [2], [0], 1, 1, 64)
+    st.qkv.zero_()
+    cache, seqs = st.objects(E)
+    q, k, v = st.heads()
+    E.cache_append(cache, seqs, k, v, R.freq_of(64))
+    assert float(st.scales[0][int(st.pages[0, 0]), 0]) == 2.0 ** -126
+
+
+def bad_steps():
+    """(what, its error bit, whether tokens of sequence 0 stay out)."""
+    return [("start", 16), ("width", 16), ("cu_falls", 16), ("cu_past", 16), ("page_high", 8),
+            ("page_low", 8)]
+
+
+def spoil(st, what):
+    if what == "start":
+        st.start[0] = -1
+    elif what == "width":
+        st.start[0] = st.width * 64 - st.new[0] + 1
+    elif what == "cu_falls":
+        st.cu[1] = -2
+    elif what == "cu_past":
+        st.cu[-1] = st.T + 5
+    elif what == "page_high":
+        st.pages[0, st.old[0] // 64] = st.n_pages
+    else:
+        st.pages[0, st.old[0] // 64] = -7
+
+
+@pytest.mark.parametrize("what,bit", bad_steps())
+def test_append_bad_sequences(E, what, bit):
+    """Bad bounds and pages set their bit and write nothing of theirs; the
+    other sequences are appended as ever."""
+    good, st = (R.Step(9, [3, 2, 4], [30, 62, 0], 2, 2, 64) for _ in range(2))
+    spoil(st, what)
+    before = [x.clone() for x in st.codes + st.scales]
+    for s in (good, st):
+        q, k, v = s.heads()
+        cache, seqs = s.objects(E)
+        E.cache_append(cache, seqs, k, v, R.freq_of(64))
+    torch.cuda.synchronize()
+    assert int(st.err) == bit and int(good.err) == 0
+    whole = {0: [what not in ("start", "width", "cu_falls", "page_high", "page_low")],
+             1: [what != "cu_falls"], 2: [what != "cu_past"]}
+    for b in range(3):
+        for blk in range((st.old[b] + st.new[b] + 63) // 64):
+            pg = int(good.pages[b, blk])
+            for x, y, z in zip(st.codes + st.scales, good.codes + good.scales, before):
+                want = y if whole[b][0] else z
+                assert torch.equal(x[pg].nan_to_num(), want[pg].nan_to_num()), (b, blk)
+
+
+# ----------------------------------------------------------------- attend
+def check_attend(E, st, window=0, scale=None, cu=True, q=None, bits=0):
+    scale = scale or 1 / math.sqrt(st.d)
+    q = st.heads()[0] if q is None else q
+    out = torch.full((st.T, st.q, st.d), 9.0, dtype=torch.bfloat16, device="cuda")
+    cache, seqs = st.objects(E, cu=cu)
+    ws = torch.full((E.cache_attend_bytes(cache, seqs, st.q, st.T),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    E.cache_attend(cache, seqs, q, out, scale, window, ws)
+    torch.cuda.synchronize()
+    assert int(st.err) == bits
+    want, tol = R.attend(st, q, scale, window)
+    within(out, want, tol, "out")
+    again = torch.empty_like(out)
+    E.cache_attend(cache, seqs, q, again, scale, window, ws)
+    assert torch.equal(out, again)                      # no order of arrival in the results
+    return out
+
+
+@pytest.mark.parametrize("window", [0, 1, 7, 64, 100])
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_attend(E, case, window):
+    new, old, kv, g, d = STEPS[case]
+    log(f"attend {new[:6]} after {old[:6]} kv {kv} g {g} d {d} window {window}")
+    st = R.Step(100 + case, new, old, kv, g, d, qstride=8 * (case % 3))
+    st.fill_new()
+    check_attend(E, st, window)
+
+
+@pytest.mark.parametrize("new,old,kv,g,d,window", [
+    ([1], [5000], 2, 4, 128, 0), ([1], [131071], 1, 3, 64, 0), ([1], [40000], 2, 8, 256, 0),
+    ([1] * 9, [4096 + 511 * i for i in range(9)], 4, 4, 128, 0), ([4], [9000], 1, 4, 128, 0),
+    ([4, 1], [9000, 3], 2, 8, 64, 500), ([1], [20000], 1, 32, 128, 0), ([1, 1], [30000, 5], 1, 1, 256, 1000),
+    ([3], [6000], 2, 5, 64, 0), ([17], [3000], 1, 20, 128, 0)])
+def test_attend_long(E, new, old, kv, g, d, window):
+    log(f"attend long {new} after {old} kv {kv} g {g} d {d} window {window}")
+    st = R.Step(sum(old), new, old, kv, g, d)
+    st.fill_new()
+    check_attend(E, st, window)
+
+
+@pytest.mark.parametrize("new,old,kv,g,d,window", [
+    ([300], [100], 2, 4, 128, 0), ([513, 60, 0, 129], [0, 700, 5, 63], 1, 4, 64, 0),
+    ([200, 33], [77, 1000], 2, 3, 256, 0), ([400], [900], 1, 8, 128, 150), ([350, 90], [64, 300], 2, 1, 128, 0),
+    ([150], [0], 8, 8, 64, 40), ([100], [1030], 1, 20, 128, 0), ([130], [70], 1, 6, 256, 1),
+    ([1100], [33], 2, 4, 128, 0), ([90] * 5, [11 * i for i in range(5)], 2, 4, 128, 0)])
+def test_attend_prompt(E, new, old, kv, g, d, window):
+    log(f"attend prompt {new} after {old} kv {kv} g {g} d {d} window {window}")
+    st = R.Step(sum(old) + 1, new, old, kv, g, d)
+    st.fill_new()
+    check_attend(E, st, window)
+
+
+def test_attend_uniform(E):
+    for n in (1, 3, 100):
+        st = R.Step(n, [n] * 3, [7, 640, 130], 2, 4, 128)
+        st.fill_new()
+        check_attend(E, st, cu=False)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 90])
+def test_attend_peaked(E, d, n):
+    """Queries of very different sizes within a head and large logits (one key
+    takes nearly all), and all-zero queries (an even mean)."""
+    st = R.Step(n + d, [n, n], [700, 64], 2, 4, d)
+    st.fill_new()
+    q = st.heads()[0].contiguous()
+    q *= torch.exp2(torch.randint(-6, 5, q.shape, generator=st.gen, device="cuda")).bfloat16()
+    q[:, 1] = 0
+    q[:, 2, 3] = 100
+    check_attend(E, st, q=q)
+    check_attend(E, st, q=q * 2.0 ** -100)
+    check_attend(E, st, q=q, scale=2.0)
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_attend_not_finite(E, n):
+    """NaN and infinite queries reach their own rows; NaN keys and values the
+    queries that see them, and no others."""
+    st = R.Step(n, [n, n], [100, 64], 2, 2, 128)
+    st.fill_new()
+    clean = check_attend(E, st)
+    q = st.heads()[0].contiguous()
+    q[0, 0, 3] = math.nan
+    q[-1, 3, 5] = math.inf
+    out = torch.empty_like(clean)
+    cache, seqs = st.objects(E)
+    ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, st.T), dtype=torch.uint8, device="cuda")
+    E.cache_attend(cache, seqs, q, out, 0.1, 0, ws)
+    E.cache_attend(cache, seqs, st.heads()[0].contiguous(), clean, 0.1, 0, ws)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, 0] = bad[-1, 3] = True
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.equal(out[~bad], clean[~bad])
+    # position 100 + n//2 of sequence 0: seen by its token and the later ones
+    at = 100 + n // 2
+    pg = int(st.pages[0, at // 64])
+    for which in (0, 1):
+        keep = st.codes[which][pg, 1, at % 64, 9].clone()
+        st.codes[which][pg, 1, at % 64, 9] = 0xFF
+        E.cache_attend(cache, seqs, st.heads()[0].contiguous(), out, 0.1, 0, ws)
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        if which:
+            bad[n // 2:n, 2:4, 9] = True
+        else:
+            bad[n // 2:n, 2:4] = True
+        assert torch.equal(torch.isnan(out), bad)
+        assert torch.equal(out[~bad], clean[~bad])
+        # a window that ends before it: nobody but the nearest tokens see it
+        E.cache_attend(cache, seqs, st.heads()[0].contiguous(), out, 0.1, 5, ws)
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        if which:
+            bad[n // 2:min(n, n // 2 + 5), 2:4, 9] = True
+        else:
+            bad[n // 2:min(n, n // 2 + 5), 2:4] = True
+        assert torch.equal(torch.isnan(out), bad)
+        st.codes[which][pg, 1, at % 64, 9] = keep
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_attend_bad_sequences(E, n):
+    """Sequences with bad bounds give zeros, positions of bad pages are masked
+    (a row without any is zeros), tokens of no sequence are left alone."""
+    make = lambda: R.Step(n + 20, [n, n, n], [100, 64, 0], 2, 2, 128)  # noqa: E731
+    st = make()
+    st.fill_new()
+    st.pages[0, 0] = -1                                  # 64 positions of sequence 0
+    check_attend(E, st, bits=8)
+    st.pages[2] = st.n_pages                             # all of sequence 2
+    st.err.zero_()
+    out = check_attend(E, st, bits=8)
+    assert not out[2 * n:].any()
+    for what in ("start", "width", "cu_past", "cu_falls"):
+        st = make()
+        st.fill_new()
+        good = check_attend(E, st)
+        spoil(st, what)
+        out = torch.full_like(good, 9.0)
+        cache, seqs = st.objects(E)
+        ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, st.T), dtype=torch.uint8, device="cuda")
+        E.cache_attend(cache, seqs, st.heads()[0], out, 1 / math.sqrt(128), 0, ws)
+        torch.cuda.synchronize()
+        assert int(st.err) == 16
+        if what in ("start", "width"):
+            assert not out[:n].any() and torch.equal(out[n:], good[n:])
+        elif what == "cu_past":
+            assert torch.equal(out[:2 * n], good[:2 * n]) and bool((out[2 * n:] == 9).all())
+        else:
+            assert torch.equal(out[2 * n:], good[2 * n:]) and bool((out[:2 * n] == 9).all())
+
+
+# ------------------------------------------------------- streams and graphs
+def test_stream_and_graph(E):
+    """The four operators on a stream of their own, and captured into a graph
+    that is replayed with eager work between: the same bits each time."""
+    st = R.Step(50, [1, 1, 1], [100, 1000, 3000], 2, 4, 128)
+    T, dim = st.T, 512
+    g = seeded(51)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    res, x, w = rn(T, dim), rn(T, dim).bfloat16(), (1 + 0.1 * rn(dim)).bfloat16()
+    N = (st.q + 2 * st.kv) * st.d
+    wt = E.W4(torch.randint(0, 256, (N, dim // 2), generator=g, device="cuda", dtype=torch.uint8),
+              torch.randint(119, 123, (N, dim // 32), generator=g, device="cuda", dtype=torch.uint8))
+    total, codes = torch.empty_like(res), torch.empty(T, dim, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(T, dim // 32, dtype=torch.uint8, device="cuda")
+    qkv = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    heads = qkv.view(T, st.q + 2 * st.kv, st.d)
+    qo, out = (torch.empty(T, st.q, st.d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache, seqs = st.objects(E)
+    ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, T), dtype=torch.uint8, device="cuda")
+    freq = R.freq_of(128)
+
+    def step(stream=None):
+        E.add_norm(x, res, w, 1e-6, codes, scales, d_sum=total, stream=stream)
+        E.project_w4(codes, wt, qkv, scales, stream=stream)
+        E.cache_append(cache, seqs, heads[:, st.q:st.q + st.kv], heads[:, st.q + st.kv:], freq,
+                       heads[:, :st.q], qo, stream=stream)
+        E.cache_attend(cache, seqs, qo, out, 1 / math.sqrt(128), 0, ws, stream=stream)
+
+    step()
+    torch.cuda.synchronize()
+    want = out.clone()
+    assert bool(torch.isfinite(want).all())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    step(stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        out.zero_()
+        qkv.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {i}"
+        x.copy_(rn(T, dim).bfloat16())               # another step between, eager
+        step()
+        want = out.clone()
