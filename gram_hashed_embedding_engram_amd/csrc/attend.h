@@ -1,0 +1,116 @@
+// Pieces that the attention kernels share: matrix-core types, the split of a
+// query into two 8-bit parts, the masks' bounds, partial results.
+#pragma once
+
+#include "attention.h"
+
+namespace engram {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// E8M0 scale of a query's second part, which is held 2^4 times larger: the
+// residual of e4m3's four bits is at most 2^-4 of the value.
+constexpr int kOne = 127, kLoScale = 127 - 4;
+
+__device__ __forceinline__ uint32_t cvt_bf16x2(float a, float b)
+{
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, b2));
+}
+
+// max / sum over lanes l and l ^ 32 (both get it)
+__device__ __forceinline__ float max_x32(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_x32(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// max / sum over lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float max_x16(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return max_x32(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float add_x16(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return add_x32(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// Thirty-two bf16 query values as two e4m3 parts, q = 2^k (hi + lo / 16):
+// bf16 has eight significant bits and each part four, so the sum is exact
+// down to 2^-15 of the row's largest value and off by at most 2^-19 of it
+// below.  The matrix instructions then take keys as the codes they are.
+__device__ __forceinline__ void split_query(const u32x4 (&x)[4], float inv, i32x8 &hi, i32x8 &lo)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t a = i & 1 ? x[i / 2].z : x[i / 2].x, b = i & 1 ? x[i / 2].w : x[i / 2].y;
+        const float v0 = bf16_lo(a) * inv, v1 = bf16_hi(a) * inv, v2 = bf16_lo(b) * inv,
+                    v3 = bf16_hi(b) * inv;
+        const uint32_t h = e4m3x4(v0, v1, v2, v3);
+        hi[i] = (int)h;
+        lo[i] = (int)e4m3x4((v0 - e4m3_at<0>(h)) * 16.0f, (v1 - e4m3_at<1>(h)) * 16.0f,
+                            (v2 - e4m3_at<2>(h)) * 16.0f, (v3 - e4m3_at<3>(h)) * 16.0f);
+    }
+}
+
+__device__ __forceinline__ float amax_bf16(const u32x4 (&x)[4])
+{
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            a = fmaxf(a, fmaxf(fabsf(bf16_lo(x[i][j])), fabsf(bf16_hi(x[i][j]))));
+    return a;
+}
+
+// Each byte of x that is a NaN code -> 0xFF in the result.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x)
+{
+    const uint32_t top = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return (top >> 7) * 0xFFu;
+}
+
+// What the attention kernels get beside the cache and the sequences.
+struct AttendArgs {
+    engram_cache c;
+    Seqs s;
+    Heads q;
+    uint16_t *out;
+    int32_t heads, g;         // query heads, query heads a key head
+    float scale;              // of the logits, times log2(e)
+    int32_t window;           // 0 = none (a window past every position counts as none)
+    int32_t split_pages;      // pages a split of a row tile's keys covers
+    int32_t splits;           // splits the grid and the workspace provide for
+    float *part;              // partial results, see below
+};
+
+// Partial results of (unit u, split s): kRows rows of m, of l, then of D
+// output sums, at part + (u * splits + s) * part_floats(D).
+constexpr int kRows = 16;
+constexpr int64_t part_floats(int d) { return kRows * (int64_t)(d + 2); }
+
+// A row tile: 16 rows of one sequence and key head.  Row r is query head
+// h*g + r % g of the sequence's token r / g.
+struct RowTile {
+    int32_t b, h, row0, rows;     // rows of the sequence: n * g
+    Seq q;
+};
+
+}  // namespace engram

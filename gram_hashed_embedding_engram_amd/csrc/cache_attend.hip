@@ -1,96 +1,576 @@
 // Attention of a step's queries over the paged 8-bit cache:
 //   out = softmax_j(scale * q . k_j) v_j over j <= p (and j > p - window).
-#include "attention.h"
+//
+// One pass over the keys with a running maximum m and sum l of the softmax
+// (in base 2): a page's logits s give p = 2^(s - m), and what was summed under
+// an older m is multiplied by 2^(m_old - m).
+#include <type_traits>
+
+#include "attend.h"
 
 namespace engram {
 namespace {
 
-// One wavefront per (token, query head).  Keys are taken 64 at a time, a lane
-// each; the running maximum m and sum l of the softmax are per wavefront, and
-// lane i holds the output's values i, i + 64, ...
-template <int D>
-__global__ __launch_bounds__(64) void attend_kernel(engram_cache c, Seqs s, Heads q,
-                                                    uint16_t *out, int heads, float scale,
-                                                    int64_t window)
+constexpr int kWaves = 4;
+
+// The unit a workgroup works on; units are row tiles x key heads, heads
+// fastest.
+__device__ __forceinline__ bool find_tile(const AttendArgs &a, int64_t unit, RowTile &t)
 {
-    __shared__ float qs[D], ps[64];
-    int b, piece;
-    const auto pieces = [&](int i) {
-        const Seq e = seq_at(s, i);
-        if (e.bad)
-            raise(s.err, ENGRAM_DEVERR_SEQUENCE);
-        return e.n;
-    };
-    if (!find_piece(blockIdx.x, s.B, pieces, b, piece))
+    const int kv = a.c.kv_heads;
+    t.h = (int)(unit % kv);
+    const int64_t i = unit / kv;
+    int piece;
+    if (!a.s.cu) {
+        const int tiles = (int)(((int64_t)a.s.each * a.g + kRows - 1) / kRows);
+        t.b = (int)(i / tiles);
+        piece = (int)(i - (int64_t)t.b * tiles);
+    } else if (!find_piece(i, a.s.B,
+                           [&](int b) { return (int)(((int64_t)seq_at(a.s, b).n * a.g + kRows - 1) / kRows); },
+                           t.b, piece)) {
+        return false;
+    }
+    t.q = seq_at(a.s, t.b);
+    t.row0 = piece * kRows;
+    t.rows = t.q.n * a.g;
+    return true;
+}
+
+// First and past-last page that a tile's rows see, and its splits.
+struct Span {
+    int first, last, splits;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs &a, const RowTile &t)
+{
+    Span p;
+    const int pos0 = t.q.start + t.row0 / a.g;
+    const int pos1 = t.q.start + min(t.row0 + kRows - 1, t.rows - 1) / a.g;
+    p.first = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kPage : 0;
+    p.last = t.q.bad ? p.first : pos1 / kPage + 1;
+    p.splits = (p.last - p.first + a.split_pages - 1) / a.split_pages;
+    return p;
+}
+
+__device__ __forceinline__ uint16_t *out_row(const AttendArgs &a, const RowTile &t, int row, int D)
+{
+    return a.out + ((int64_t)(t.q.t0 + row / a.g) * a.heads + t.h * a.g + row % a.g) * D;
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint32_t widen2(uint32_t x)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, HALF));
+}
+
+// O^T += V^T P^T over a page's 64 tokens: vf[j][e] holds, of token
+// 16j + 4(l / 16) + e, the D/16 codes from value (l % 16) * D/16 on, pb[j] the
+// probabilities of those four tokens as bf16.  Output tile u takes value
+// (l % 16) * D/16 + u of every lane: get(u) is what it starts from, put(u, sum)
+// receives it.  Codes of four tokens are paired by byte permutes and widened
+// to bf16, whose eight bits hold a code exactly.
+template <int D, class G, class P>
+__device__ __forceinline__ void values_product(const uint32_t (&vf)[4][4][D / 64],
+                                               const uint32_t (&pb)[4][2], G get, P put)
+{
+    u32x4 pv[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+        pv[h] = u32x4{pb[2 * h][0], pb[2 * h][1], pb[2 * h + 1][0], pb[2 * h + 1][1]};
+#pragma unroll
+    for (int u = 0; u < D / 64; u++) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            acc[i] = get(4 * u + i);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            uint32_t ab[2][2], cd[2][2];          // byte pairs of tokens 0,1 and 2,3
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const uint32_t(&x)[4][D / 64] = vf[2 * h + j];
+                ab[j][0] = __builtin_amdgcn_perm(x[1][u], x[0][u], 0x05010400u);
+                ab[j][1] = __builtin_amdgcn_perm(x[1][u], x[0][u], 0x07030602u);
+                cd[j][0] = __builtin_amdgcn_perm(x[3][u], x[2][u], 0x05010400u);
+                cd[j][1] = __builtin_amdgcn_perm(x[3][u], x[2][u], 0x07030602u);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int b = i / 2;
+                const u32x4 vv = i & 1 ? u32x4{widen2<true>(ab[0][b]), widen2<true>(cd[0][b]),
+                                               widen2<true>(ab[1][b]), widen2<true>(cd[1][b])}
+                                       : u32x4{widen2<false>(ab[0][b]), widen2<false>(cd[0][b]),
+                                               widen2<false>(ab[1][b]), widen2<false>(cd[1][b])};
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, vv), __builtin_bit_cast(bf16x8, pv[h]), acc[i], 0, 0,
+                    0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            put(4 * u + i, acc[i]);
+    }
+}
+
+// A tile of 16 rows against a split of its keys.
+//
+// The four wavefronts take pages in turn and keep m, l and the output sums of
+// their own; the sums meet in LDS at the end.  S^T = K Q^T puts a query in each
+// lane column (lane l holds query l % 16 and tokens 16t + 4(l / 16) + e of a
+// page), so m, l and the rescaling are per lane, and the probabilities are
+// already laid out as the second operand of O^T = V^T P^T, whose contraction
+// takes the tokens in that same order.  Keys go from memory into matrix
+// instructions as the codes they are (the query is split into two e4m3 parts);
+// values are paired by token with byte permutes and widened to bf16.  Nothing
+// of the cache passes through LDS.
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_kernel(AttendArgs a)
+{
+    constexpr int KS = D == 64 ? 1 : D / 128;     // 128-value steps of the logits
+    constexpr int VW = D / 64;                    // dwords of a token's values a lane holds
+    __shared__ float red_o[kWaves][kRows][D + 4];
+    __shared__ float red_m[kWaves][kRows], red_l[kWaves][kRows];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, q4 = lane >> 4;
+    const int split = blockIdx.x % a.splits;
+    const int64_t unit = blockIdx.x / a.splits;
+    RowTile t;
+    if (blockIdx.x < (unsigned)a.splits && tid < 64 && split == 0)
+        for (int b = lane; b < a.s.B; b += 64)
+            if (seq_at(a.s, b).bad)
+                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
+    if (!find_tile(a, unit, t))
         return;
-    const Seq e = seq_at(s, b);
-    const int lane = threadIdx.x, h = blockIdx.y, kh = h / (heads / c.kv_heads);
-    const int64_t t = e.t0 + piece;
-    for (int i = lane; i < D; i += 64)
-        qs[i] = bf16_lo(q.p[t * q.token + h * q.head + i]) * scale;
-    __syncthreads();
-    float m = -INFINITY, sum = 0.0f, o[D / 64] = {};
-    const int pos = e.start + piece;
-    const int64_t lo = window > 0 ? (pos - window + 1 > 0 ? pos - window + 1 : 0) : 0;
-    if (!e.bad) {
-        for (int blk = (int)(lo / kPage); blk <= pos / kPage; blk++) {
-            const int32_t page = s.pages[(int64_t)b * s.max_pages + blk];
-            if (page < 0 || page >= c.n_pages) {
-                raise(s.err, ENGRAM_DEVERR_PAGE);
-                continue;
+    const Span sp = span_of(a, t);
+    if (split >= max(sp.splits, 1))
+        return;
+    const int first = sp.first + split * a.split_pages;
+    const int last = min(first + a.split_pages, sp.last);
+
+    // ---- the queries
+    const int row = t.row0 + r16;
+    const bool valid = row < t.rows;
+    const int tok = valid ? row / a.g : 0;
+    const int pos = t.q.start + tok;
+    const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int pos_lo = t.q.start + t.row0 / a.g;          // the tile's first and last position
+    const int pos_hi = t.q.start + min(t.row0 + kRows - 1, t.rows - 1) / a.g;
+    const int see_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0;     // seen by any row
+    const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0;     // seen by every row
+    i32x8 qh[KS], ql[KS];
+    float qs = 0.0f;
+    {
+        const uint16_t *qp = a.q.p + (int64_t)(t.q.t0 + tok) * a.q.token +
+                             (int64_t)(t.h * a.g + (valid ? row % a.g : 0)) * a.q.head;
+        u32x4 x[KS][4];
+        float amax = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+            const int at = D == 64 ? 16 * q4 : 128 * s + 32 * q4;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                x[s][i] = *(const u32x4 *)(qp + at + 8 * (D == 64 ? i & 1 : i));
+                if (!valid)
+                    x[s][i] = u32x4{0u, 0u, 0u, 0u};
             }
-            const int64_t at = (int64_t)page * c.kv_heads + kh;
-            const uint8_t *kc = c.d_k + at * kPage * D, *vc = c.d_v + at * kPage * D;
-            const float ks = c.d_k_scales[at], vs = c.d_v_scales[at];
-            const int j = blk * kPage + lane;
-            float a = -INFINITY;
-            if (j <= pos && j >= lo) {
-                a = 0.0f;
-                for (int i = 0; i < D; i++)
-                    a += qs[i] * e4m3_to_f32(kc[lane * D + i]);
-                a *= ks;
+            amax = fmaxf(amax, amax_bf16(x[s]));
+        }
+        const int k = e4m3_scale_exp(max_x16(amax));
+        qs = exp2_int(k) * a.scale;
+#pragma unroll
+        for (int s = 0; s < KS; s++)
+            split_query(x[s], exp2_int(-k), qh[s], ql[s]);
+    }
+    // head_dim 64: one instruction takes both parts.  A lane's first 16 codes
+    // are the contraction's indices 16(l / 16) on, under the scales of lanes
+    // 0-31, its last 16 those from 64 on, under the scales of lanes 32-63.
+    const int sel_scale = D == 64 && q4 >= 2 ? kLoScale : kOne;
+    if (D == 64)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            qh[0][4 + i] = ql[0][i];
+
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; i++)
+        o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int32_t *table = a.s.pages + (int64_t)t.b * a.s.max_pages;
+    int ids = 0;
+    // page `w + 4i` of the split; -1 past its end or outside the cache
+    const auto page_id = [&](int i) {
+        if ((i & 63) == 0) {
+            const int at = first + w + kWaves * (i + lane);
+            ids = at < last ? table[at] : -1;
+            if (at < last && (ids < 0 || ids >= a.c.n_pages)) {
+                raise(a.s.err, ENGRAM_DEVERR_PAGE);
+                ids = -1;
             }
-            float top = a;
-            for (int x = 1; x < 64; x <<= 1)
-                top = fmaxf(top, __shfl_xor(top, x));
-            top = fmaxf(top, m);
-            const float base = top == -INFINITY ? 0.0f : top;
-            const float p = expf(a - base), keep = expf(m - base);
+        }
+        return __builtin_amdgcn_readlane(ids, i & 63);
+    };
+    i32x8 kf[4][KS];
+    uint32_t vf[4][4][VW];
+    float ks = 0.0f, vs = 0.0f, vs_next = 0.0f;
+    // a lane's place in a page: 32 bits on top of the page's uniform address
+    const uint32_t k_off = r16 * D + (D == 64 ? 16 : 32) * q4;
+    const uint32_t v_off = 4 * q4 * D + r16 * (4 * VW);
+    const auto load_k = [&](int64_t at) {
+        const uint8_t *kp = a.c.d_k + at * (kPage * D);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                const uint8_t *p = kp + 16 * i * D + 128 * s;
+                const u32x4 u = *(const u32x4 *)(p + k_off);
+                const u32x4 v = D == 64 ? u : *(const u32x4 *)(p + 16 + k_off);
+                kf[i][s] = i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w,
+                                 (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+            }
+        ks = a.c.d_k_scales[at];
+        vs_next = a.c.d_v_scales[at];
+    };
+    const auto load_v = [&](int64_t at) {
+        const uint8_t *vp = a.c.d_v + at * (kPage * D);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const uint8_t *p = vp + (16 * i + e) * D + v_off;
+                if (VW == 1) {
+                    vf[i][e][0] = *(const uint32_t *)p;
+                } else if (VW == 2) {
+                    const u32x2 u = *(const u32x2 *)p;
+                    vf[i][e][0] = u.x;
+                    vf[i][e][1] = u.y;
+                } else {
+                    const u32x4 u = *(const u32x4 *)p;
+                    vf[i][e][0] = u.x;
+                    vf[i][e][1] = u.y;
+                    vf[i][e][2 % VW] = u.z;
+                    vf[i][e][3 % VW] = u.w;
+                }
+            }
+    };
+
+    const int mine = last - first - w > 0 ? (last - first - w + kWaves - 1) / kWaves : 0;
+    int next = mine > 0 ? page_id(0) : -1;
+    if (next >= 0) {
+        const int64_t at = (int64_t)next * a.c.kv_heads + t.h;
+        load_k(at);
+        load_v(at);
+    }
+    for (int i = 0; i < mine; i++) {
+        const int page = next;
+        next = i + 1 < mine ? page_id(i + 1) : -1;
+        const int64_t at_next = (int64_t)next * a.c.kv_heads + t.h;
+        if (page < 0) {
+            if (next >= 0) {
+                load_k(at_next);
+                load_v(at_next);
+            }
+            continue;
+        }
+        const int base = (first + w + kWaves * i) * kPage;
+        // pages that some row does not see whole take the masks, and no loads
+        // ahead (which would not fit the registers beside the masks)
+        const auto step = [&](auto edge_c) {
+        constexpr bool edge = decltype(edge_c)::value;
+        // ---- logits
+        f32x4 s[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < KS; u++) {
+                s[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf[j][u], qh[u], s[j], 0, 0, 0,
+                                                                        kOne, 0, sel_scale);
+                if (D != 64)
+                    s[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        kf[j][u], ql[u], s[j], 0, 0, 0, kOne, 0, kLoScale);
+            }
+        }
+        const float f = qs * ks;
+        vs = vs_next;
+        if (!edge && next >= 0)
+            load_k(at_next);                     // in flight during the rest
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                s[j][e] *= f;
+                if (edge) {
+                    const int p = base + 16 * j + 4 * q4 + e;
+                    s[j][e] = p <= pos && p >= lo ? s[j][e] : -INFINITY;
+                }
+                top = fmaxf(top, s[j][e]);
+            }
+        top = fmaxf(max_x16(top), m);
+        const float zero = top == -INFINITY ? 0.0f : top;
+        if (__any(top != m)) {
+            const float keep = __builtin_amdgcn_exp2f(m - zero);
             m = top;
-            sum = sum * keep + wave_sum(p);
-            __syncthreads();
-            ps[lane] = p;
-            __syncthreads();
-            for (int u = 0; u < D / 64; u++) {
-                float acc = 0.0f;
-                for (int i = 0; i < kPage; i++)
-                    if (blk * kPage + i <= pos && blk * kPage + i >= lo)
-                        acc += ps[i] * e4m3_to_f32(vc[i * D + 64 * u + lane]);
-                o[u] = o[u] * keep + acc * vs;
+            l *= keep;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                o[j] *= keep;
+        }
+        uint32_t pb[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                p[e] = __builtin_amdgcn_exp2f(s[j][e] - zero);
+                l += p[e];
+                const bool masked = edge && s[j][e] == -INFINITY;
+                p[e] = masked ? 0.0f : p[e] * vs;
+            }
+            pb[j][0] = cvt_bf16x2(p[0], p[1]);
+            pb[j][1] = cvt_bf16x2(p[2], p[3]);
+        }
+        // ---- values: what no row sees is zeroed (0 * NaN is NaN); a NaN that
+        // only some rows see is zeroed here and given to them below
+        bool poison = false;
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int p = base + 16 * j + 4 * q4 + e;
+                    const bool seen = p <= pos_hi && p >= see_lo;
+#pragma unroll
+                    for (int u = 0; u < VW; u++)
+                        vf[j][e][u] = seen ? vf[j][e][u] : 0u;
+                }
+            if (pos_lo != pos_hi) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+#pragma unroll
+                        for (int u = 0; u < VW; u++) {
+                            const uint32_t nan = nan_bytes(vf[j][e][u]);
+                            any |= nan;
+                            vf[j][e][u] &= ~nan;
+                        }
+                poison = __any(any != 0);
+            }
+        }
+        values_product<D>(vf, pb, [&](int u) { return o[u]; },
+                          [&](int u, const f32x4 &sum) { o[u] = sum; });
+        if (poison) {
+            // how many NaN codes each row sees, by the same product
+            load_v((int64_t)page * a.c.kv_heads + t.h);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int at = base + 16 * j + 4 * q4 + e;
+                    p[e] = at <= pos && at >= lo ? 1.0f : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < VW; u++)      // 0x38 is 1.0
+                        vf[j][e][u] = nan_bytes(vf[j][e][u]) & 0x38383838u;
+                }
+                pb[j][0] = cvt_bf16x2(p[0], p[1]);
+                pb[j][1] = cvt_bf16x2(p[2], p[3]);
+            }
+            values_product<D>(vf, pb, [&](int) { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; },
+                              [&](int u, const f32x4 &n) {
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    o[u][e] = n[e] > 0.0f ? __uint_as_float(0x7FC00000u) : o[u][e];
+            });
+        }
+        if (next >= 0) {
+            if (edge)
+                load_k(at_next);
+            load_v(at_next);
+        }
+        };
+        if (base + kPage - 1 > pos_lo || base < all_lo)
+            step(std::true_type{});
+        else
+            step(std::false_type{});
+    }
+
+    // ---- the wavefronts' sums
+    l = add_x16(l);
+    if (q4 == 0) {
+        red_m[w][r16] = m;
+        red_l[w][r16] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+#pragma unroll
+        for (int u = 0; u < D / 16; u += 4)
+            *(f32x4 *)&red_o[w][r16][(4 * q4 + e) * (D / 16) + u] =
+                f32x4{o[u][e], o[u + 1][e], o[u + 2][e], o[u + 3][e]};
+    __syncthreads();
+    const bool whole = sp.splits <= 1;
+    float *part = a.part + (unit * a.splits + split) * part_floats(D);
+    constexpr int QUADS = D / 4;
+    for (int i = tid; i < kRows * QUADS; i += 64 * kWaves) {
+        const int r = i / QUADS, d = 4 * (i % QUADS);
+        if (t.row0 + r >= t.rows)
+            continue;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kWaves; u++)
+            mm = fmaxf(mm, red_m[u][r]);
+        const float zero = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f;
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < kWaves; u++) {
+            const float k = __builtin_amdgcn_exp2f(red_m[u][r] - zero);
+            ll += k * red_l[u][r];
+            acc += k * *(const f32x4 *)&red_o[u][r][d];
+        }
+        if (whole) {
+            const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+            u32x2 y;
+            y.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
+            y.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
+            *(u32x2 *)(out_row(a, t, t.row0 + r, D) + d) = y;
+        } else {
+            *(f32x4 *)(part + 2 * kRows + r * D + d) = acc;
+            if (d == 0) {
+                part[r] = mm;
+                part[kRows + r] = ll;
             }
         }
     }
-    for (int u = 0; u < D / 64; u++)
-        out[(t * heads + h) * D + 64 * u + lane] = f32_to_bf16(sum != 0.0f ? o[u] / sum : 0.0f);
+}
+
+// Joins the splits of a row: one workgroup per (unit, row), a thread group per
+// every (256 / (D/4))th split.
+template <int D>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
+{
+    constexpr int QUADS = D / 4, GROUPS = 256 / QUADS;
+    __shared__ f32x4 acc_s[GROUPS][QUADS];
+    __shared__ float l_s[GROUPS], m_s[4];
+    const int tid = threadIdx.x;
+    const int64_t unit = blockIdx.x / kRows;
+    const int r = blockIdx.x % kRows;
+    RowTile t;
+    if (!find_tile(a, unit, t) || t.row0 + r >= t.rows)
+        return;
+    const int splits = span_of(a, t).splits;
+    if (splits <= 1)
+        return;
+    const float *part = a.part + unit * a.splits * part_floats(D);
+    float m = -INFINITY;
+    for (int s = tid; s < splits; s += 256)
+        m = fmaxf(m, part[s * part_floats(D) + r]);
+    m = max_x16(m);
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1)
+        m = fmaxf(m, __shfl_xor(m, x));
+    if ((tid & 63) == 0)
+        m_s[tid >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+    const float zero = m == -INFINITY ? 0.0f : m;
+    const int g = tid / QUADS, d = tid % QUADS;
+    float l = 0.0f;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = g; s < splits; s += GROUPS) {
+        const float *p = part + s * part_floats(D);
+        const float k = __builtin_amdgcn_exp2f(p[r] - zero);
+        l += k * p[kRows + r];
+        acc += k * *(const f32x4 *)(p + 2 * kRows + r * D + 4 * d);
+    }
+    acc_s[g][d] = acc;
+    if (d == 0)
+        l_s[g] = l;
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int u = 1; u < GROUPS; u++) {
+            acc += acc_s[u][d];
+            l += l_s[u];
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        u32x2 y;
+        y.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
+        y.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
+        *(u32x2 *)(out_row(a, t, t.row0 + r, D) + 4 * d) = y;
+    }
+}
+
+// How a call is laid out, from what the host knows: the token count, the
+// sequences and the pages their tables provide for.
+struct Plan {
+    int64_t units;
+    int32_t split_pages, splits;
+};
+Plan plan_of(const engram_cache &c, const Seqs &s, int32_t q_heads, int64_t window)
+{
+    Plan p;
+    const int64_t g = q_heads / c.kv_heads;
+    p.units = (s.cu ? ((int64_t)s.T * g / kRows + s.B)
+                    : (((int64_t)s.each * g + kRows - 1) / kRows) * s.B) * c.kv_heads;
+    // about eight workgroups a CU, a page a wavefront at least
+    const int64_t target = 8 * (int64_t)device_cus();
+    const auto round_up = [](int64_t v) { return (v + kWaves - 1) / kWaves * kWaves; };
+    int64_t pages = s.max_pages;
+    int64_t per = round_up((pages * p.units + target - 1) / target);
+    p.splits = (int32_t)((pages + per - 1) / per);
+    const int64_t seen = (window + kRows) / kPage + 2;
+    if (window > 0 && seen < pages) {
+        // fewer pages: shorter splits, but not more of them (the workspace
+        // is sized without a window)
+        pages = seen;
+        per = (pages * p.units + target - 1) / target;
+        per = round_up(per > (pages + p.splits - 1) / p.splits ? per
+                                                               : (pages + p.splits - 1) / p.splits);
+        p.splits = (int32_t)((pages + per - 1) / per);
+    }
+    p.split_pages = (int32_t)per;
+    return p;
 }
 
 }  // namespace
 
-size_t attend_bytes(const engram_cache &c, const Seqs &s, int32_t q_heads) { return 0; }
+size_t attend_bytes(const engram_cache &c, const Seqs &s, int32_t q_heads)
+{
+    const Plan p = plan_of(c, s, q_heads, 0);
+    return p.splits > 1 ? sizeof(float) * (size_t)(p.units * p.splits * part_floats(c.head_dim)) : 0;
+}
+
+template <int D>
+static void launch_rows(const AttendArgs &a, int64_t units, const Launch &l)
+{
+    dispatch(attend_rows_kernel<D>, dim3((unsigned)(units * a.splits)), dim3(64 * kWaves), l, true,
+             a.splits == 1, a);
+    if (a.splits > 1)
+        dispatch(attend_join_kernel<D>, dim3((unsigned)(units * kRows)), dim3(256), l, false, true,
+                 a);
+}
 
 int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint16_t *out,
                       int32_t q_heads, float scale, int64_t window, void *ws, const Launch &l)
 {
-    const dim3 grid((unsigned)s.T, q_heads), block(64);
+    const Plan p = plan_of(c, s, q_heads, window);
+    if (p.units * p.splits >= ((int64_t)1 << 20) * 4 || p.units >= ((int64_t)1 << 20))
+        return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
+                    (long long)p.units);
+    const int32_t w = window < ((int64_t)1 << 31) ? (int32_t)window : 0;
+    const AttendArgs a{c, s, q, out, q_heads, q_heads / c.kv_heads, scale * kLog2e, w,
+                       p.split_pages, p.splits, (float *)ws};
     if (c.head_dim == 64)
-        dispatch(attend_kernel<64>, grid, block, l, true, true, c, s, q, out, (int)q_heads, scale,
-                 window);
+        launch_rows<64>(a, p.units, l);
     else if (c.head_dim == 128)
-        dispatch(attend_kernel<128>, grid, block, l, true, true, c, s, q, out, (int)q_heads,
-                 scale, window);
+        launch_rows<128>(a, p.units, l);
     else
-        dispatch(attend_kernel<256>, grid, block, l, true, true, c, s, q, out, (int)q_heads,
-                 scale, window);
+        launch_rows<256>(a, p.units, l);
     return launch_status("engram cache_attend kernel");
 }
 
