@@ -80,6 +80,12 @@ __device__ __forceinline__ float amax_bf16(const u32x4 (&x)[4])
     return a;
 }
 
+template <bool HALF>
+__device__ __forceinline__ uint32_t widen2(uint32_t x)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, HALF));
+}
+
 // Each byte of x that is a NaN code -> 0xFF in the result.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x)
 {
@@ -112,5 +118,9 @@ struct RowTile {
     int32_t b, h, row0, rows;     // rows of the sequence: n * g
     Seq q;
 };
+
+// Row tiles of the many-row kernel (attend_prompt.hip) in a call, times heads.
+int64_t prompt_tiles(const engram_cache &c, const Seqs &s, int32_t g);
+int32_t launch_attend_prompt(const AttendArgs &a, const Launch &l);
 
 }  // namespace engram

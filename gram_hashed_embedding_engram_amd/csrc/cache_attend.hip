@@ -56,12 +56,6 @@ __device__ __forceinline__ uint16_t *out_row(const AttendArgs &a, const RowTile 
     return a.out + ((int64_t)(t.q.t0 + row / a.g) * a.heads + t.h * a.g + row % a.g) * D;
 }
 
-template <bool HALF>
-__device__ __forceinline__ uint32_t widen2(uint32_t x)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, HALF));
-}
-
 // O^T += V^T P^T over a page's 64 tokens: vf[j][e] holds, of token
 // 16j + 4(l / 16) + e, the D/16 codes from value (l % 16) * D/16 on, pb[j] the
 // probabilities of those four tokens as bf16.  Output tile u takes value
@@ -537,10 +531,19 @@ Plan plan_of(const engram_cache &c, const Seqs &s, int32_t q_heads, int64_t wind
     return p;
 }
 
+// Which kernel a call takes: tiles of 128 rows where the call has enough of
+// them to fill the chip, else tiles of 16 whose keys are split.
+bool many_rows(const engram_cache &c, const Seqs &s, int32_t g)
+{
+    return (int64_t)s.T * g >= 64 * (int64_t)s.B && prompt_tiles(c, s, g) >= device_cus() / 8;
+}
+
 }  // namespace
 
 size_t attend_bytes(const engram_cache &c, const Seqs &s, int32_t q_heads)
 {
+    if (many_rows(c, s, q_heads / c.kv_heads))
+        return 0;
     const Plan p = plan_of(c, s, q_heads, 0);
     return p.splits > 1 ? sizeof(float) * (size_t)(p.units * p.splits * part_floats(c.head_dim)) : 0;
 }
@@ -558,12 +561,21 @@ static void launch_rows(const AttendArgs &a, int64_t units, const Launch &l)
 int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint16_t *out,
                       int32_t q_heads, float scale, int64_t window, void *ws, const Launch &l)
 {
+    const int32_t g = q_heads / c.kv_heads;
+    const int32_t w = window < ((int64_t)1 << 31) ? (int32_t)window : 0;
+    const int64_t tiles = prompt_tiles(c, s, g);
+    if (many_rows(c, s, g)) {
+        if (tiles >= ((int64_t)1 << 23))
+            return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
+                        (long long)tiles);
+        return launch_attend_prompt(
+            AttendArgs{c, s, q, out, q_heads, g, scale * kLog2e, w, 0, 0, nullptr}, l);
+    }
     const Plan p = plan_of(c, s, q_heads, window);
     if (p.units * p.splits >= ((int64_t)1 << 20) * 4 || p.units >= ((int64_t)1 << 20))
         return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
                     (long long)p.units);
-    const int32_t w = window < ((int64_t)1 << 31) ? (int32_t)window : 0;
-    const AttendArgs a{c, s, q, out, q_heads, q_heads / c.kv_heads, scale * kLog2e, w,
+    const AttendArgs a{c, s, q, out, q_heads, g, scale * kLog2e, w,
                        p.split_pages, p.splits, (float *)ws};
     if (c.head_dim == 64)
         launch_rows<64>(a, p.units, l);
