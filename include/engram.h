@@ -450,7 +450,8 @@ int32_t engram_add_norm(const uint16_t *d_x, const void *d_res, int32_t res_bf16
  *   d_w        [N][K/2]: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  *              negatives), the even k in the low nibble;
  *   d_w_scales [N][K/32]: exponents + 127 of a power of two per 32 values
- *              (255 is NaN);
+ *              (255 is NaN; with bf16 x a weight past f32's range, which takes
+ *              a byte above 252, is infinite);
  *   d_x        [T][K] e4m3 codes with d_x_scales [T][K/32] of the same kind
  *              (engram_add_norm's outputs), or bf16 with d_x_scales = NULL;
  *   d_y        [T][N] bf16.
