@@ -1,100 +1,284 @@
 // The position rotation of a step's queries and keys, and the append of its
 // keys and values to the paged 8-bit cache.
+//
+// One launch with two kinds of workgroup: a page of one sequence (all its key
+// heads in turn, keys and values, so that an angle is formed once a token and
+// pair), or a run of tokens' queries.  Bound by memory: a key or value is read
+// once as bf16 and written once as a code, and stays in registers between the
+// page's maximum and the codes.
 #include "attention.h"
 
 namespace engram {
 namespace {
 
-// x[i] of a head after the rotation by position pos.
-__device__ __forceinline__ float turned(const uint16_t *x, int i, const Rotation &r, int pos)
+constexpr int kThreads = 256;
+
+// cos and sin of a 64-bit angle, rounded to f32.  The angle less the nearest
+// multiple n of pi/2 (pi/2 as the sum of two doubles, so the remainder keeps
+// an absolute error below 2^-60 n), then the Taylor series to x^13 and x^14
+// on [-pi/4, pi/4] (next term below 2^-44), swapped and signed by n mod 4.
+struct Turn {
+    float c, s;
+};
+__device__ __forceinline__ Turn turn_of(int pos, float freq)
 {
-    const float v = bf16_lo(x[i]);
-    if (i >= r.rot)
-        return v;
-    const int half = r.rot / 2;
-    const int pair = r.halves ? (i < half ? i : i - half) : i / 2;
-    const bool first = r.halves ? i < half : !(i & 1);
-    const double a = (double)pos * (double)r.freq[pair];
-    const float c = (float)cos(a), s = (float)sin(a);
-    const float u = bf16_lo(x[r.halves ? (first ? i + half : i - half) : i ^ 1]);
-    return first ? v * c - u * s : u * s + v * c;
+    const double a = (double)pos * (double)freq;
+    const double n = rint(a * 0.63661977236758134308);
+    const double x = fma(-n, 6.123233995736766036e-17, fma(-n, 1.57079632679489661923, a));
+    const double z = x * x;
+    double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
+    s = fma(s, z, -1.0 / 39916800.0);
+    c = fma(c, z, 1.0 / 479001600.0);
+    s = fma(s, z, 1.0 / 362880.0);
+    c = fma(c, z, -1.0 / 3628800.0);
+    s = fma(s, z, -1.0 / 5040.0);
+    c = fma(c, z, 1.0 / 40320.0);
+    s = fma(s, z, 1.0 / 120.0);
+    c = fma(c, z, -1.0 / 720.0);
+    s = fma(s, z, -1.0 / 6.0);
+    c = fma(c, z, 1.0 / 24.0);
+    s = fma(s * z, x, x);
+    c = fma(c, z, -0.5);
+    c = fma(c, z, 1.0);
+    const int q = (int)((int64_t)n & 3);
+    const float fs = (float)(q & 1 ? c : s), fc = (float)(q & 1 ? s : c);
+    return Turn{q == 1 || q == 2 ? -fc : fc, q & 2 ? -fs : fs};
 }
 
-// One workgroup per (page of a sequence, head, keys or values).
-__global__ __launch_bounds__(256) void append_pages_kernel(engram_cache c, Seqs s, Heads k,
-                                                           Heads v, Rotation r)
+// A thread's eight values of a head: values i0 .. i0+3 and i1 .. i1+3.
+//   pairs (i, i + rot/2), inside the turned part: i1 = i0 + rot/2, so the
+//   thread holds both ends of four pairs;
+//   otherwise i1 = i0 + 4 and pairs are neighbours.
+struct Place {
+    int i0, i1, pair;           // pair < 0: not turned
+};
+template <int D>
+__device__ __forceinline__ Place place_of(int e, const Rotation &r)
 {
-    int b, piece;
-    const auto pieces = [&](int i) {
-        const Seq q = seq_at(s, i);
-        if (q.bad)
-            raise(s.err, ENGRAM_DEVERR_SEQUENCE);
-        return q.bad || q.n == 0 ? 0 : (q.start + q.n - 1) / kPage - q.start / kPage + 1;
-    };
-    if (!find_piece(blockIdx.x, s.B, pieces, b, piece))
-        return;
-    const Seq q = seq_at(s, b);
-    const int blk = q.start / kPage + piece;
-    const int32_t page = s.pages[(int64_t)b * s.max_pages + blk];
-    if (page < 0 || page >= c.n_pages) {
-        raise(s.err, ENGRAM_DEVERR_PAGE);
-        return;
+    Place p;
+    if (r.halves && 8 * e < r.rot) {
+        p.i0 = 4 * e;
+        p.i1 = 4 * e + r.rot / 2;
+        p.pair = 4 * e;
+    } else {
+        p.i0 = 8 * e;
+        p.i1 = 8 * e + 4;
+        p.pair = 8 * e < r.rot ? 4 * e : -1;
     }
-    const int h = blockIdx.y, d = c.head_dim;
-    const bool is_v = blockIdx.z;
-    const Heads &src = is_v ? v : k;
-    Rotation rot = r;
-    if (is_v)
-        rot.rot = 0;
-    const int64_t at = (int64_t)page * c.kv_heads + h;
-    uint8_t *codes = (is_v ? c.d_v : c.d_k) + at * kPage * d;
-    float *scale = (is_v ? c.d_v_scales : c.d_k_scales) + at;
-    const int older = max(q.start - blk * kPage, 0);
-    const int last = min(q.start + q.n - blk * kPage, kPage);
-    __shared__ float part[4];
-    const auto value = [&](int i) {
-        const int pos = blk * kPage + older + i / d;
-        return turned(src.p + (q.t0 + (pos - q.start)) * src.token + h * src.head, i % d, rot, pos);
-    };
-    float amax = 0.0f;
-    for (int i = threadIdx.x; i < (last - older) * d; i += 256)
-        amax = fmaxf(amax, finite_abs(value(i)));
-    for (int m = 1; m < 64; m <<= 1)
-        amax = fmaxf(amax, __shfl_xor(amax, m));
-    if ((threadIdx.x & 63) == 0)
-        part[threadIdx.x >> 6] = amax;
-    const float had = older > 0 ? *scale : 0.0f;
-    __syncthreads();
-    amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    const float now = fmaxf(had, exp2_int(e4m3_scale_exp(amax)));
-    if (now != had) {
-        const float ratio = had / now;
-        for (int i = threadIdx.x; i < older * d; i += 256)
-            codes[i] = (uint8_t)e4m3x4(e4m3_to_f32(codes[i]) * ratio, 0.0f, 0.0f, 0.0f);
-    }
-    for (int i = threadIdx.x; i < (last - older) * d; i += 256)
-        codes[older * d + i] = (uint8_t)e4m3x4(value(i) / now, 0.0f, 0.0f, 0.0f);
-    __syncthreads();
-    if (threadIdx.x == 0)
-        *scale = now;
+    return p;
 }
 
-// One workgroup per token's queries.
-__global__ __launch_bounds__(256) void turn_queries_kernel(Seqs s, Heads q, Rotation r,
-                                                           uint16_t *out, int heads, int d)
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ void load8(const uint16_t *p, const Place &at, float (&v)[8])
 {
-    int b, piece;
-    const auto pieces = [&](int i) {
-        const Seq e = seq_at(s, i);
-        return e.bad ? 0 : e.n;
-    };
-    if (!find_piece(blockIdx.x, s.B, pieces, b, piece))
+    const u32x2 a = *(const u32x2 *)(p + at.i0), b = *(const u32x2 *)(p + at.i1);
+    v[0] = bf16_lo(a.x);
+    v[1] = bf16_hi(a.x);
+    v[2] = bf16_lo(a.y);
+    v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(b.x);
+    v[5] = bf16_hi(b.x);
+    v[6] = bf16_lo(b.y);
+    v[7] = bf16_hi(b.y);
+}
+
+__device__ __forceinline__ void turn8(float (&v)[8], const Place &at, bool halves, const Turn (&t)[4])
+{
+    if (at.pair < 0)
         return;
-    const Seq e = seq_at(s, b);
-    const int64_t t = e.t0 + piece;
-    for (int i = threadIdx.x; i < heads * d; i += 256)
-        out[t * heads * d + i] =
-            f32_to_bf16(turned(q.p + t * q.token + i / d * q.head, i % d, r, e.start + piece));
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float &a = v[halves ? i : 2 * i], &b = v[halves ? 4 + i : 2 * i + 1];
+        const float x = a, y = b;
+        a = x * t[i].c - y * t[i].s;
+        b = x * t[i].s + y * t[i].c;
+    }
+}
+
+struct AppendArgs {
+    engram_cache c;
+    Seqs s;
+    Heads k, v, q;
+    uint16_t *q_out;
+    Rotation r;
+    int32_t q_heads, pieces;    // grid: `pieces` x kv_heads page workgroups, then queries
+    int32_t q_blocks;
+};
+
+// One page of one sequence and key head: keys, then values.
+template <int D, bool HALVES>
+__device__ __forceinline__ void append_page(const AppendArgs &a, const Seq &q, int blk,
+                                            int32_t page, int h)
+{
+    constexpr int E = D / 8;                    // threads a token
+    constexpr int TOK = kThreads / E;           // tokens at a time
+    constexpr int N = kPage / TOK;
+    __shared__ float part[2][kThreads / 64];
+    const int tid = threadIdx.x, e = tid % E, g = tid / E;
+    const int page0 = blk * kPage;
+    const int older = max(q.start - page0, 0);
+    const int last = min(q.start + q.n - page0, kPage);
+    const int64_t at = (int64_t)page * a.c.kv_heads + h;
+#pragma unroll
+    for (int z = 0; z < 2; z++) {
+        const Heads &src = z ? a.v : a.k;
+        uint8_t *codes = (z ? a.c.d_v : a.c.d_k) + at * kPage * D;
+        float *scale = (z ? a.c.d_v_scales : a.c.d_k_scales) + at;
+        Rotation r = a.r;
+        r.halves = HALVES;
+        if (z)
+            r.rot = 0;
+        const Place pl = place_of<D>(e, r);
+        float v[N][8];
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int slot = g + TOK * i;
+            if (slot >= older && slot < last) {
+                const int pos = page0 + slot;
+                load8(src.p + (q.t0 + (int64_t)(pos - q.start)) * src.token + h * src.head, pl, v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int slot = g + TOK * i;
+            if (slot >= older && slot < last) {
+                if (!z && pl.pair >= 0) {
+                    Turn t[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        t[j] = turn_of(page0 + slot, r.freq[pl.pair + j]);
+                    turn8(v[i], pl, HALVES, t);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    amax = fmaxf(amax, finite_abs(v[i][j]));
+            }
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1)
+            amax = fmaxf(amax, __shfl_xor(amax, m));
+        if ((tid & 63) == 0)
+            part[z][tid >> 6] = amax;
+        const float had = older > 0 ? *scale : 0.0f;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 64; i++)
+            amax = fmaxf(amax, part[z][i]);
+        const float need = exp2_int(e4m3_scale_exp(amax));
+        const float now = fmaxf(had, need);
+        if (now != had) {                       // (never where the page is new)
+            const float ratio = had / now;
+            for (int i = tid; i < older * (D / 4); i += kThreads) {
+                uint32_t *p = (uint32_t *)codes + i;
+                const uint32_t x = *p;
+                *p = e4m3x4(e4m3_at<0>(x) * ratio, e4m3_at<1>(x) * ratio, e4m3_at<2>(x) * ratio,
+                            e4m3_at<3>(x) * ratio);
+            }
+        }
+        const float inv = 1.0f / now;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int slot = g + TOK * i;
+            if (slot >= older && slot < last) {
+                uint8_t *p = codes + slot * D;
+                *(uint32_t *)(p + pl.i0) = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+                *(uint32_t *)(p + pl.i1) = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+            }
+        }
+        if (tid == 0)                           // all have read it before the barrier
+            *scale = now;
+    }
+}
+
+template <int D, bool HALVES>
+__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
+{
+    const int tid = threadIdx.x;
+    const int pages = a.pieces * a.c.kv_heads;
+    if (blockIdx.x == 0)
+        for (int i = tid; i < a.s.B; i += kThreads)
+            if (seq_at(a.s, i).bad)
+                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
+    if ((int)blockIdx.x < pages) {
+        const int h = blockIdx.x % a.c.kv_heads;
+        int i = blockIdx.x / a.c.kv_heads, b, piece;
+        const auto touched = [&](int x) {
+            const Seq q = seq_at(a.s, x);
+            return q.bad || q.n == 0 ? 0 : (q.start + q.n - 1) / kPage - q.start / kPage + 1;
+        };
+        if (!a.s.cu) {                          // every sequence has room for as many pages
+            const int each = a.pieces / a.s.B;
+            b = i / each;
+            piece = i % each;
+            if (piece >= touched(b))
+                return;
+        } else if (!find_piece(i, a.s.B, touched, b, piece)) {
+            return;
+        }
+        const Seq q = seq_at(a.s, b);
+        const int blk = q.start / kPage + piece;
+        const int32_t page = a.s.pages[(int64_t)b * a.s.max_pages + blk];
+        if (page < 0 || page >= a.c.n_pages) {
+            if (h == 0 && tid == 0)
+                raise(a.s.err, ENGRAM_DEVERR_PAGE);
+            return;
+        }
+        append_page<D, HALVES>(a, q, blk, page, h);
+        return;
+    }
+    // queries: a thread takes eight values of a token's head, heads in turn
+    constexpr int E = D / 8, ROWS = kThreads / E;
+    const int e = tid % E, g = tid / E;
+    const int t = blockIdx.x - pages;
+    int b, piece;
+    if (!a.s.cu) {
+        b = t / a.s.each;
+        piece = t % a.s.each;
+    } else if (!find_piece(t, a.s.B,
+                           [&](int x) {
+                               const Seq q = seq_at(a.s, x);
+                               return q.bad ? 0 : q.n;
+                           },
+                           b, piece)) {
+        return;
+    }
+    const Seq q = seq_at(a.s, b);
+    if (q.bad)
+        return;
+    const int64_t tok = q.t0 + piece;
+    Rotation r = a.r;
+    r.halves = HALVES;
+    const Place pl = place_of<D>(e, r);
+    Turn turn[4];
+    if (pl.pair >= 0)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            turn[j] = turn_of(q.start + piece, r.freq[pl.pair + j]);
+    for (int h = g; h < a.q_heads; h += ROWS) {
+        float v[8];
+        load8(a.q.p + tok * a.q.token + h * a.q.head, pl, v);
+        turn8(v, pl, HALVES, turn);
+        uint16_t *o = a.q_out + (tok * a.q_heads + h) * D;
+        u32x2 lo, hi;
+        lo.x = pack_bf16x2(v[0], v[1]);
+        lo.y = pack_bf16x2(v[2], v[3]);
+        hi.x = pack_bf16x2(v[4], v[5]);
+        hi.y = pack_bf16x2(v[6], v[7]);
+        *(u32x2 *)(o + pl.i0) = lo;
+        *(u32x2 *)(o + pl.i1) = hi;
+    }
+}
+
+template <int D>
+void launch_dim(const AppendArgs &a, const Launch &l)
+{
+    const dim3 grid((unsigned)((int64_t)a.pieces * a.c.kv_heads + a.q_blocks)), block(kThreads);
+    if (a.r.halves)
+        dispatch(append_kernel<D, true>, grid, block, l, true, true, a);
+    else
+        dispatch(append_kernel<D, false>, grid, block, l, true, true, a);
 }
 
 }  // namespace
@@ -103,13 +287,19 @@ int32_t launch_append(const engram_cache &c, const Seqs &s, const Heads &k, cons
                       const Heads &q, uint16_t *q_out, int32_t q_heads, const Rotation &r,
                       const Launch &l)
 {
-    // pages: at most one partly filled at each end of a sequence
-    const int64_t pieces = s.T / kPage + 2 * (int64_t)s.B;
-    dispatch(append_pages_kernel, dim3((unsigned)pieces, c.kv_heads, 2), dim3(256), l, true,
-             q_heads == 0, c, s, k, v, r);
-    if (q_heads)
-        dispatch(turn_queries_kernel, dim3((unsigned)s.T), dim3(256), l, false, true, s, q, r,
-                 q_out, (int)q_heads, (int)c.head_dim);
+    // pages a call can touch: n tokens meet (n + 62) / 64 + 1 at most
+    const int64_t pieces = s.cu ? s.T / kPage + 2 * (int64_t)s.B
+                                : (int64_t)s.B * ((s.each + kPage - 2) / kPage + 1);
+    if (pieces * c.kv_heads + s.T >= ((int64_t)1 << 24))
+        return fail(ENGRAM_E_RANGE, "engram cache_append: %lld pages of %d heads in one call",
+                    (long long)pieces, c.kv_heads);
+    const AppendArgs a{c, s, k, v, q, q_out, r, q_heads, (int32_t)pieces, q_heads ? s.T : 0};
+    if (c.head_dim == 64)
+        launch_dim<64>(a, l);
+    else if (c.head_dim == 128)
+        launch_dim<128>(a, l);
+    else
+        launch_dim<256>(a, l);
     return launch_status("engram cache_append kernel");
 }
 
