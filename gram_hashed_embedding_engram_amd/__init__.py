@@ -188,10 +188,20 @@ def _need(t, name, nbytes, dense=True):
                                  f"{max(room, 0)} from this address")
 
 
+_current = None
+
+
 def _stream(stream):
+    global _current
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current is None:
+            import torch
+            first = torch.cuda.current_stream().cuda_stream      # initialises the device
+            # the same address without a Stream object a call (0.2 us, not 3)
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current = lambda: raw(device())  # noqa: E731
+            return first
+        return _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -354,17 +364,38 @@ def layer_static(tables: HashTables, hash_index, table: Table, d_wkv, d_qk, eps,
 def _typed(t, name, dtypes, shape=None):
     """Refuse a tensor of another type, shape or, for the kernels that take
     rows back to back, a strided view."""
-    if str(t.dtype)[6:] not in dtypes:
-        raise EngramError(E_ARG, f"{name}: {t.dtype}, one of {', '.join(dtypes)} is needed")
+    if t.dtype not in dtypes:
+        kinds = ", ".join(sorted(str(d)[6:] for d in dtypes))
+        raise EngramError(E_ARG, f"{name}: {t.dtype}, one of {kinds} is needed")
+    if shape is not None and t.shape != shape:
+        raise EngramError(E_ARG, f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise EngramError(E_ARG, f"{name}: a contiguous tensor is needed")
-    if shape is not None and tuple(t.shape) != shape:
-        raise EngramError(E_ARG, f"{name}: shape {tuple(t.shape)}, {shape} is needed")
 
 
-_BF16 = ("bfloat16", "int16")                       # bf16 values or their bits
-_E4M3 = ("uint8", "float8_e4m3fn")
-_E8M0 = ("uint8", "float8_e8m0fnu")
+class _Types:
+    """Element types the attention sub-layer's tensors may have (torch is
+    imported by the first call that needs it)."""
+
+    def __init__(self):
+        import torch as t
+        self.f32 = frozenset((t.float32,))
+        self.i32 = frozenset((t.int32,))
+        self.u8 = frozenset((t.uint8,))
+        self.bf16 = frozenset((t.bfloat16, t.int16))       # bf16 values or their bits
+        self.res = self.f32 | self.bf16
+        self.e4m3 = frozenset((t.uint8, t.float8_e4m3fn))
+        self.e8m0 = frozenset((t.uint8, t.float8_e8m0fnu))
+
+
+_types = None
+
+
+def _kinds():
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
 
 
 def add_norm(d_x, d_res, d_w, eps, d_codes, d_scales, d_sum=None, stream=None):
@@ -372,23 +403,26 @@ def add_norm(d_x, d_res, d_w, eps, d_codes, d_scales, d_sum=None, stream=None):
     (engram_add_norm): d_sum = d_res + d_x, d_codes / d_scales = the normed
     sum in e4m3 with a scale per 32 values.  d_res [..., dim] f32 or bf16,
     d_x bf16 of the same shape or None, d_sum None = in place on d_res."""
-    if d_sum is None:
-        d_sum = d_res
-    shape = tuple(d_res.shape)
+    k = _types or _kinds()
+    shape = d_res.shape
     dim = shape[-1]
-    _typed(d_res, "res", ("float32",) + _BF16)
-    rows = d_res.numel() // dim if dim else 0
-    if d_sum is not d_res:
-        _typed(d_sum, "sum", (str(d_res.dtype)[6:],), shape)
+    _typed(d_res, "res", k.res)
+    res = total = d_res.data_ptr()
+    if d_sum is not None and d_sum is not d_res:
+        _typed(d_sum, "sum", (d_res.dtype,), shape)
+        total = d_sum.data_ptr()
+    x = None
     if d_x is not None:
-        _typed(d_x, "x", _BF16, shape)
-    _typed(d_w, "w", _BF16, (dim,))
-    _typed(d_codes, "codes", _E4M3, shape)
-    _typed(d_scales, "scales", _E8M0, shape[:-1] + (dim // NORM_GROUP,))
-    _check(lib().engram_add_norm(None if d_x is None else d_x.data_ptr(), d_res.data_ptr(),
-                                 d_res.element_size() == 2, d_w.data_ptr(), eps,
-                                 d_sum.data_ptr(), d_codes.data_ptr(), d_scales.data_ptr(), rows,
-                                 dim, _stream(stream)))
+        _typed(d_x, "x", k.bf16, shape)
+        x = d_x.data_ptr()
+    _typed(d_w, "w", k.bf16, (dim,))
+    _typed(d_codes, "codes", k.e4m3, shape)
+    _typed(d_scales, "scales", k.e8m0, shape[:-1] + (dim // NORM_GROUP,))
+    rc = (_lib or lib()).engram_add_norm(
+        x, res, d_res.element_size() == 2, d_w.data_ptr(), eps, total, d_codes.data_ptr(),
+        d_scales.data_ptr(), d_res.numel() // dim if dim else 0, dim, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 class W4:
@@ -397,25 +431,32 @@ class W4:
 
     def __init__(self, d_w, d_scales):
         N, half = d_w.shape
-        _typed(d_w, "w", ("uint8",))
-        _typed(d_scales, "w scales", _E8M0, (N, 2 * half // NORM_GROUP))
+        k = _kinds()
+        _typed(d_w, "w", k.u8)
+        _typed(d_scales, "w scales", k.e8m0, (N, 2 * half // NORM_GROUP))
         self.w, self.scales = d_w, d_scales
-        self.N, self.K = N, 2 * half
+        self.N, self.K, self.groups = N, 2 * half, 2 * half // NORM_GROUP
+        self.at = (d_w.data_ptr(), d_scales.data_ptr())
 
 
 def project_w4(d_x, weights: W4, d_y, d_xs=None, stream=None):
     """y = x w^T through 4-bit weights (engram_project_w4): d_x [T, K] bf16,
     or e4m3 codes with d_xs [T, K/32]; d_y [T, N] bf16."""
-    T = d_x.shape[0]
+    k = _types or _kinds()
+    T, K, N = d_x.shape[0], weights.K, weights.N
+    xs = None
     if d_xs is None:
-        _typed(d_x, "x", _BF16, (T, weights.K))
+        _typed(d_x, "x", k.bf16, (T, K))
     else:
-        _typed(d_x, "x", _E4M3, (T, weights.K))
-        _typed(d_xs, "x scales", _E8M0, (T, weights.K // NORM_GROUP))
-    _typed(d_y, "y", _BF16, (T, weights.N))
-    _check(lib().engram_project_w4(d_x.data_ptr(), None if d_xs is None else d_xs.data_ptr(),
-                                   weights.w.data_ptr(), weights.scales.data_ptr(),
-                                   d_y.data_ptr(), T, weights.K, weights.N, _stream(stream)))
+        _typed(d_x, "x", k.e4m3, (T, K))
+        _typed(d_xs, "x scales", k.e8m0, (T, weights.groups))
+        xs = d_xs.data_ptr()
+    _typed(d_y, "y", k.bf16, (T, N))
+    w, ws = weights.at
+    rc = (_lib or lib()).engram_project_w4(d_x.data_ptr(), xs, w, ws, d_y.data_ptr(), T, K, N,
+                                           _stream(stream))
+    if rc:
+        _check(rc)
 
 
 class Cache:
@@ -424,14 +465,16 @@ class Cache:
 
     def __init__(self, d_k, d_v, d_k_scales, d_v_scales):
         n_pages, kv_heads, page, head_dim = d_k.shape
-        _typed(d_k, "k", _E4M3, (n_pages, kv_heads, PAGE_TOKENS, head_dim))
-        _typed(d_v, "v", _E4M3, tuple(d_k.shape))
-        _typed(d_k_scales, "k scales", ("float32",), (n_pages, kv_heads))
-        _typed(d_v_scales, "v scales", ("float32",), (n_pages, kv_heads))
+        k = _kinds()
+        _typed(d_k, "k", k.e4m3, (n_pages, kv_heads, PAGE_TOKENS, head_dim))
+        _typed(d_v, "v", k.e4m3, d_k.shape)
+        _typed(d_k_scales, "k scales", k.f32, (n_pages, kv_heads))
+        _typed(d_v_scales, "v scales", k.f32, (n_pages, kv_heads))
         self.keep = (d_k, d_v, d_k_scales, d_v_scales)
         self.kv_heads, self.head_dim, self.n_pages = kv_heads, head_dim, n_pages
         self.c = CacheC(kv_heads, head_dim, n_pages, d_k.data_ptr(), d_v.data_ptr(),
                         d_k_scales.data_ptr(), d_v_scales.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
 
 class Sequences:
@@ -441,25 +484,27 @@ class Sequences:
 
     def __init__(self, d_pages, d_start, d_cu=None, d_err=None):
         B, width = d_pages.shape
-        _typed(d_pages, "pages", ("int32",))
-        _typed(d_start, "start", ("int32",), (B,))
+        i32 = _kinds().i32
+        _typed(d_pages, "pages", i32)
+        _typed(d_start, "start", i32, (B,))
         if d_cu is not None:
-            _typed(d_cu, "cu", ("int32",), (B + 1,))
+            _typed(d_cu, "cu", i32, (B + 1,))
         if d_err is not None:
-            _typed(d_err, "err", ("int32",))
+            _typed(d_err, "err", i32)
             _need(d_err, "err", 4)
         self.keep = (d_pages, d_start, d_cu, d_err)
         self.B = B
         self.c = SequencesC(B, width, d_pages.data_ptr(), d_start.data_ptr(), _ptr(d_cu),
                             _ptr(d_err))
+        self.ref = ctypes.byref(self.c)
 
 
 def _heads(t, name, T, heads, head_dim):
     """(address, token stride, head stride) of bf16 heads [T, heads, head_dim]
     that may be a view of a wider row; a head's values lie side by side."""
-    if str(t.dtype)[6:] not in _BF16:
+    if t.dtype not in _types.bf16:
         raise EngramError(E_ARG, f"{name}: {t.dtype}, bfloat16 is needed")
-    if tuple(t.shape) != (T, heads, head_dim):
+    if t.shape != (T, heads, head_dim):
         raise EngramError(E_ARG, f"{name}: shape {tuple(t.shape)}, {(T, heads, head_dim)} is needed")
     token, head, one = t.stride()
     if one != 1:
@@ -473,30 +518,30 @@ def cache_append(cache: Cache, seqs: Sequences, d_k, d_v, d_freq, d_q=None, d_q_
     the cache (engram_cache_append).  d_k, d_v [T, kv_heads, head_dim] and d_q
     [T, q_heads, head_dim] bf16, as views of one projection's output if need
     be; d_freq [rot/2] f32 or None (no rotation); d_q_out as d_q, contiguous."""
-    T = d_k.shape[0]
-    kp, kt, kh = _heads(d_k, "k", T, cache.kv_heads, cache.head_dim)
-    vp, vt, vh = _heads(d_v, "v", T, cache.kv_heads, cache.head_dim)
+    T, kv, d = d_k.shape[0], cache.kv_heads, cache.head_dim
+    kp, kt, kh = _heads(d_k, "k", T, kv, d)
+    vp, vt, vh = _heads(d_v, "v", T, kv, d)
     qp = qt = qh = q_heads = qo = 0
     if d_q is not None:
         q_heads = d_q.shape[1]
-        qp, qt, qh = _heads(d_q, "q", T, q_heads, cache.head_dim)
+        qp, qt, qh = _heads(d_q, "q", T, q_heads, d)
         if d_q_out is None:
             raise EngramError(E_ARG, "q_out: queries are given and no place for them")
-        _typed(d_q_out, "q_out", _BF16, (T, q_heads, cache.head_dim))
+        _typed(d_q_out, "q_out", _types.bf16, (T, q_heads, d))
         qo = d_q_out.data_ptr()
     rot = fp = 0
     if d_freq is not None:
-        _typed(d_freq, "freq", ("float32",))
+        _typed(d_freq, "freq", _types.f32)
         rot, fp = 2 * d_freq.numel(), d_freq.data_ptr()
-    _check(lib().engram_cache_append(ctypes.byref(cache.c), ctypes.byref(seqs.c), kp, kt, kh, vp,
-                                     vt, vh, qp, qt, qh, qo, q_heads, fp, rot,
-                                     1 if halves else 0, T, _stream(stream)))
+    rc = (_lib or lib()).engram_cache_append(cache.ref, seqs.ref, kp, kt, kh, vp, vt, vh, qp, qt, qh, qo,
+                                  q_heads, fp, rot, halves, T, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def cache_attend_bytes(cache: Cache, seqs: Sequences, q_heads, T):
     """Workspace bytes a cache_attend of T tokens needs (may be 0)."""
-    return lib().engram_cache_attend_bytes(ctypes.byref(cache.c), ctypes.byref(seqs.c),
-                                           int(q_heads), int(T))
+    return lib().engram_cache_attend_bytes(cache.ref, seqs.ref, int(q_heads), int(T))
 
 
 def cache_attend(cache: Cache, seqs: Sequences, d_q, d_out, scale, window=0, d_ws=None,
@@ -504,16 +549,17 @@ def cache_attend(cache: Cache, seqs: Sequences, d_q, d_out, scale, window=0, d_w
     """Attention of the step's queries over the cache (engram_cache_attend):
     d_q [T, q_heads, head_dim] bf16 (a view if need be), d_out contiguous of
     that shape, d_ws a uint8 tensor of cache_attend_bytes bytes or None."""
-    T, q_heads, _ = d_q.shape
+    T, q_heads, _ = shape = d_q.shape
     qp, qt, qh = _heads(d_q, "q", T, q_heads, cache.head_dim)
-    _typed(d_out, "out", _BF16, (T, q_heads, cache.head_dim))
+    _typed(d_out, "out", _types.bf16, shape)
     ws, nws = 0, 0
     if d_ws is not None:
-        _typed(d_ws, "ws", ("uint8",))
+        _typed(d_ws, "ws", _types.u8)
         ws, nws = d_ws.data_ptr(), d_ws.numel()
-    _check(lib().engram_cache_attend(ctypes.byref(cache.c), ctypes.byref(seqs.c), qp, qt, qh,
-                                     d_out.data_ptr(), q_heads, T, scale, window, ws, nws,
-                                     _stream(stream)))
+    rc = (_lib or lib()).engram_cache_attend(cache.ref, seqs.ref, qp, qt, qh, d_out.data_ptr(), q_heads, T,
+                                  scale, window, ws, nws, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 class Context:
