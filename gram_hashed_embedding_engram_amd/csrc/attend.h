@@ -102,13 +102,13 @@ struct AttendArgs {
     int32_t heads, g;         // query heads, query heads a key head
     float scale;              // of the logits, times log2(e)
     int32_t window;           // 0 = none (a window past every position counts as none)
-    int32_t split_pages;      // pages a split of a row tile's keys covers
-    int32_t splits;           // splits the grid and the workspace provide for
-    float *part;              // partial results, see below
+    int32_t window_pages;     // pages a tile's windows meet at most, 0 = no bound
+    int32_t parts, least;     // workgroups that share the pages; pages each takes at least
+    int32_t join_rows;        // rows of a unit that the join provides for
+    float *part;              // partial results: two places a workgroup
 };
 
-// Partial results of (unit u, split s): kRows rows of m, of l, then of D
-// output sums, at part + (u * splits + s) * part_floats(D).
+// A partial result: kRows rows of m, of l, then of D output sums.
 constexpr int kRows = 16;
 constexpr int64_t part_floats(int d) { return kRows * (int64_t)(d + 2); }
 

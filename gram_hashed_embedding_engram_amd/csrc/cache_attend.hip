@@ -11,49 +11,110 @@
 namespace engram {
 namespace {
 
-constexpr int kWaves = 4;
+// ---- how the keys are divided
+//
+// A unit is a row tile and a key head.  Every unit of a sequence counts the
+// same number of pages, and all units' pages lie in one row, sequence by
+// sequence; workgroup i takes pages i*share .. (i+1)*share-1 of it, whatever
+// the sequences' lengths are, so that all end together.  A unit that lies in
+// one workgroup is written out there; parts of a unit go to the workgroup's
+// two places in the workspace (0 for its first part, 1 for a last one that is
+// not its first) and are joined by a second kernel.
 
-// The unit a workgroup works on; units are row tiles x key heads, heads
-// fastest.
-__device__ __forceinline__ bool find_tile(const AttendArgs &a, int64_t unit, RowTile &t)
+// Pages that each unit of sequence b counts: 0 where it brings no token.
+__device__ __forceinline__ int unit_pages(const AttendArgs &a, const Seq &q)
 {
-    const int kv = a.c.kv_heads;
-    t.h = (int)(unit % kv);
-    const int64_t i = unit / kv;
-    int piece;
-    if (!a.s.cu) {
-        const int tiles = (int)(((int64_t)a.s.each * a.g + kRows - 1) / kRows);
-        t.b = (int)(i / tiles);
-        piece = (int)(i - (int64_t)t.b * tiles);
-    } else if (!find_piece(i, a.s.B,
-                           [&](int b) { return (int)(((int64_t)seq_at(a.s, b).n * a.g + kRows - 1) / kRows); },
-                           t.b, piece)) {
-        return false;
-    }
-    t.q = seq_at(a.s, t.b);
-    t.row0 = piece * kRows;
-    t.rows = t.q.n * a.g;
-    return true;
+    if (q.n == 0)
+        return 0;
+    if (q.bad)
+        return 1;
+    const int all = (q.start + q.n - 1) / kPage + 1;
+    const int reach = a.window_pages;
+    return reach > 0 && reach < all ? reach : all;
+}
+__device__ __forceinline__ int unit_tiles(const AttendArgs &a, const Seq &q)
+{
+    return (int)(((int64_t)q.n * a.g + kRows - 1) / kRows);
 }
 
-// First and past-last page that a tile's rows see, and its splits.
-struct Span {
-    int first, last, splits;
+// A place in the row of pages.
+struct Place {
+    int b, unit;              // the sequence, its unit (tile * kv_heads + head)
+    int64_t first;            // where the sequence's pages begin
+    int64_t total;            // pages of all sequences
 };
-__device__ __forceinline__ Span span_of(const AttendArgs &a, const RowTile &t)
+// The place of page `at` (BY_UNIT false) or of unit number `at` (true); b = -1
+// past the end.  Called by whole wavefronts.
+template <bool BY_UNIT>
+__device__ __forceinline__ Place find_place(const AttendArgs &a, int64_t at)
 {
-    Span p;
-    const int pos0 = t.q.start + t.row0 / a.g;
-    const int pos1 = t.q.start + min(t.row0 + kRows - 1, t.rows - 1) / a.g;
-    p.first = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kPage : 0;
-    p.last = t.q.bad ? p.first : pos1 / kPage + 1;
-    p.splits = (p.last - p.first + a.split_pages - 1) / a.split_pages;
+    const int lane = threadIdx.x & 63;
+    Place p{-1, 0, 0, 0};
+    int64_t units_before = 0;
+    for (int base = 0; base < a.s.B; base += 64) {
+        int64_t units = 0, pages = 0;
+        int each = 0;
+        if (base + lane < a.s.B) {
+            const Seq q = seq_at(a.s, base + lane);
+            each = unit_pages(a, q);
+            units = (int64_t)unit_tiles(a, q) * a.c.kv_heads;
+            pages = units * each;
+        }
+        int64_t sum_p = pages, sum_u = units;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t up = __shfl_up(sum_p, d), uu = __shfl_up(sum_u, d);
+            sum_p += lane >= d ? up : 0;
+            sum_u += lane >= d ? uu : 0;
+        }
+        const int64_t key = BY_UNIT ? units_before + sum_u : p.total + sum_p;
+        const uint64_t over = __ballot(key > at);
+        if (over && p.b < 0) {
+            const int l = __builtin_ctzll(over);
+            p.b = base + l;
+            p.first = p.total + __shfl(sum_p - pages, l);
+            const int n = __builtin_amdgcn_readlane(each, l);
+            p.unit = BY_UNIT ? (int)(at - (units_before + __shfl(sum_u - units, l)))
+                             : (int)((at - p.first) / (n > 0 ? n : 1));
+        }
+        p.total += __shfl(sum_p, 63);
+        units_before += __shfl(sum_u, 63);
+    }
     return p;
+}
+
+// Pages a workgroup takes.
+__device__ __forceinline__ int64_t share_of(const AttendArgs &a, int64_t total)
+{
+    const int64_t per = (total + a.parts - 1) / a.parts;
+    return per > a.least ? per : a.least;
+}
+
+__device__ __forceinline__ RowTile tile_at(const AttendArgs &a, int b, int unit, const Seq &q)
+{
+    RowTile t;
+    t.b = b;
+    t.h = unit % a.c.kv_heads;
+    t.row0 = unit / a.c.kv_heads * kRows;
+    t.q = q;
+    t.rows = q.n * a.g;
+    return t;
 }
 
 __device__ __forceinline__ uint16_t *out_row(const AttendArgs &a, const RowTile &t, int row, int D)
 {
     return a.out + ((int64_t)(t.q.t0 + row / a.g) * a.heads + t.h * a.g + row % a.g) * D;
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const AttendArgs &a, const RowTile &t, int row, int d,
+                                          f32x4 acc, float l)
+{
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    u32x2 y;
+    y.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
+    y.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
+    *(u32x2 *)(out_row(a, t, row, D) + d) = y;
 }
 
 // O^T += V^T P^T over a page's 64 tokens: vf[j][e] holds, of token
@@ -105,9 +166,9 @@ __device__ __forceinline__ void values_product(const uint32_t (&vf)[4][4][D / 64
     }
 }
 
-// A tile of 16 rows against a split of its keys.
+// Pages p0 .. p0+np-1 of a unit, by W wavefronts.
 //
-// The four wavefronts take pages in turn and keep m, l and the output sums of
+// The wavefronts take pages in turn and keep m, l and the output sums of
 // their own; the sums meet in LDS at the end.  S^T = K Q^T puts a query in each
 // lane column (lane l holds query l % 16 and tokens 16t + 4(l / 16) + e of a
 // page), so m, l and the rescaling are per lane, and the probabilities are
@@ -116,41 +177,26 @@ __device__ __forceinline__ void values_product(const uint32_t (&vf)[4][4][D / 64
 // instructions as the codes they are (the query is split into two e4m3 parts);
 // values are paired by token with byte permutes and widened to bf16.  Nothing
 // of the cache passes through LDS.
-template <int D>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_kernel(AttendArgs a)
+template <int D, int W>
+struct Reduce {
+    float o[W][kRows][D + 4];
+    float m[W][kRows], l[W][kRows];
+};
+
+template <int D, int W>
+__device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &t, int p0, int np,
+                                            float *part, Reduce<D, W> &red)
 {
     constexpr int KS = D == 64 ? 1 : D / 128;     // 128-value steps of the logits
     constexpr int VW = D / 64;                    // dwords of a token's values a lane holds
-    __shared__ float red_o[kWaves][kRows][D + 4];
-    __shared__ float red_m[kWaves][kRows], red_l[kWaves][kRows];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q4 = lane >> 4;
-    const int split = blockIdx.x % a.splits;
-    const int64_t unit = blockIdx.x / a.splits;
-    RowTile t;
-    if (blockIdx.x < (unsigned)a.splits && tid < 64 && split == 0)
-        for (int b = lane; b < a.s.B; b += 64)
-            if (seq_at(a.s, b).bad)
-                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
-    if (!find_tile(a, unit, t))
-        return;
-    const Span sp = span_of(a, t);
-    if (split >= max(sp.splits, 1))
-        return;
-    const int first = sp.first + split * a.split_pages;
-    const int last = min(first + a.split_pages, sp.last);
 
     // ---- the queries
     const int row = t.row0 + r16;
     const bool valid = row < t.rows;
     const int tok = valid ? row / a.g : 0;
-    const int pos = t.q.start + tok;
-    const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    const int pos_lo = t.q.start + t.row0 / a.g;          // the tile's first and last position
-    const int pos_hi = t.q.start + min(t.row0 + kRows - 1, t.rows - 1) / a.g;
-    const int see_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0;     // seen by any row
-    const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0;     // seen by every row
     i32x8 qh[KS], ql[KS];
     float qs = 0.0f;
     {
@@ -184,6 +230,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_ker
         for (int i = 0; i < 4; i++)
             qh[0][4 + i] = ql[0][i];
 
+    // ---- what the rows see
+    const int pos = t.q.start + tok;
+    const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int pos_lo = t.q.start + t.row0 / a.g;          // the tile's first and last position
+    const int pos_hi = t.q.start + min(t.row0 + kRows - 1, t.rows - 1) / a.g;
+    const int see_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0;     // seen by any row
+    const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0;     // seen by every row
+    const int first = see_lo / kPage + p0;
+    const int last = t.q.bad ? first : min(first + np, pos_hi / kPage + 1);
+
     float m = -INFINITY, l = 0.0f;
     f32x4 o[D / 16];
 #pragma unroll
@@ -192,10 +248,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_ker
 
     const int32_t *table = a.s.pages + (int64_t)t.b * a.s.max_pages;
     int ids = 0;
-    // page `w + 4i` of the split; -1 past its end or outside the cache
+    // the wavefront's i-th page; -1 past the last or outside the cache
     const auto page_id = [&](int i) {
         if ((i & 63) == 0) {
-            const int at = first + w + kWaves * (i + lane);
+            const int at = first + w + W * (i + lane);
             ids = at < last ? table[at] : -1;
             if (at < last && (ids < 0 || ids >= a.c.n_pages)) {
                 raise(a.s.err, ENGRAM_DEVERR_PAGE);
@@ -248,7 +304,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_ker
             }
     };
 
-    const int mine = last - first - w > 0 ? (last - first - w + kWaves - 1) / kWaves : 0;
+    const int mine = last - first - w > 0 ? (last - first - w + W - 1) / W : 0;
     int next = mine > 0 ? page_id(0) : -1;
     if (next >= 0) {
         const int64_t at = (int64_t)next * a.c.kv_heads + t.h;
@@ -266,7 +322,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_ker
             }
             continue;
         }
-        const int base = (first + w + kWaves * i) * kPage;
+        const int base = (first + w + W * i) * kPage;
         // pages that some row does not see whole take the masks, and no loads
         // ahead (which would not fit the registers beside the masks)
         const auto step = [&](auto edge_c) {
@@ -395,42 +451,35 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_ker
     // ---- the wavefronts' sums
     l = add_x16(l);
     if (q4 == 0) {
-        red_m[w][r16] = m;
-        red_l[w][r16] = l;
+        red.m[w][r16] = m;
+        red.l[w][r16] = l;
     }
 #pragma unroll
     for (int e = 0; e < 4; e++)
 #pragma unroll
         for (int u = 0; u < D / 16; u += 4)
-            *(f32x4 *)&red_o[w][r16][(4 * q4 + e) * (D / 16) + u] =
+            *(f32x4 *)&red.o[w][r16][(4 * q4 + e) * (D / 16) + u] =
                 f32x4{o[u][e], o[u + 1][e], o[u + 2][e], o[u + 3][e]};
     __syncthreads();
-    const bool whole = sp.splits <= 1;
-    float *part = a.part + (unit * a.splits + split) * part_floats(D);
     constexpr int QUADS = D / 4;
-    for (int i = tid; i < kRows * QUADS; i += 64 * kWaves) {
+    const int rows = min(kRows, t.rows - t.row0);
+    for (int i = tid; i < rows * QUADS; i += 64 * W) {
         const int r = i / QUADS, d = 4 * (i % QUADS);
-        if (t.row0 + r >= t.rows)
-            continue;
         float mm = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kWaves; u++)
-            mm = fmaxf(mm, red_m[u][r]);
+        for (int u = 0; u < W; u++)
+            mm = fmaxf(mm, red.m[u][r]);
         const float zero = mm == -INFINITY ? 0.0f : mm;
         float ll = 0.0f;
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int u = 0; u < kWaves; u++) {
-            const float k = __builtin_amdgcn_exp2f(red_m[u][r] - zero);
-            ll += k * red_l[u][r];
-            acc += k * *(const f32x4 *)&red_o[u][r][d];
+        for (int u = 0; u < W; u++) {
+            const float k = __builtin_amdgcn_exp2f(red.m[u][r] - zero);
+            ll += k * red.l[u][r];
+            acc += k * *(const f32x4 *)&red.o[u][r][d];
         }
-        if (whole) {
-            const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
-            u32x2 y;
-            y.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
-            y.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
-            *(u32x2 *)(out_row(a, t, t.row0 + r, D) + d) = y;
+        if (!part) {
+            store_row<D>(a, t, t.row0 + r, d, acc, ll);
         } else {
             *(f32x4 *)(part + 2 * kRows + r * D + d) = acc;
             if (d == 0) {
@@ -441,27 +490,106 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attend_rows_ker
     }
 }
 
-// Joins the splits of a row: one workgroup per (unit, row), a thread group per
-// every (256 / (D/4))th split.
-template <int D>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
+__device__ __forceinline__ void raise_bad(const AttendArgs &a)
 {
-    constexpr int QUADS = D / 4, GROUPS = 256 / QUADS;
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < a.s.B; b += blockDim.x)
+            if (seq_at(a.s, b).bad)
+                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
+}
+
+// Short tables: a workgroup a unit, nothing to join.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : W / 4) void attend_unit_kernel(AttendArgs a)
+{
+    __shared__ Reduce<D, W> red;
+    int b, unit;
+    if (!a.s.cu) {
+        const int units = (int)(((int64_t)a.s.each * a.g + kRows - 1) / kRows) * a.c.kv_heads;
+        b = blockIdx.x / units;
+        unit = blockIdx.x % units;
+    } else {
+        const Place p = find_place<true>(a, blockIdx.x);
+        if (p.b < 0) {
+            raise_bad(a);
+            return;
+        }
+        b = p.b;
+        unit = p.unit;
+    }
+    raise_bad(a);
+    const RowTile t = tile_at(a, b, unit, seq_at(a.s, b));
+    attend_unit<D, W>(a, t, 0, 1 << 26, nullptr, red);
+}
+
+// Long tables: a workgroup a share of the row of pages.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(AttendArgs a)
+{
+    __shared__ Reduce<D, W> red;
+    raise_bad(a);
+    const Place all = find_place<false>(a, 0);
+    const int64_t share = share_of(a, all.total);
+    int64_t at = blockIdx.x * share;
+    const int64_t end = min(at + share, all.total);
+    if (at >= end)
+        return;
+    const Place p = find_place<false>(a, at);
+    int b = p.b, unit = p.unit;
+    Seq q = seq_at(a.s, b);
+    int each = unit_pages(a, q);
+    int p0 = (int)(at - p.first - (int64_t)unit * each);
+    for (bool lead = true;; lead = false) {
+        const int np = (int)min((int64_t)(each - p0), end - at);
+        const RowTile t = tile_at(a, b, unit, q);
+        float *part = np == each ? nullptr
+                                 : a.part + (2 * (int64_t)blockIdx.x + (lead ? 0 : 1)) * part_floats(D);
+        attend_unit<D, W>(a, t, p0, np, part, red);
+        at += np;
+        if (at >= end)
+            return;
+        p0 = 0;
+        if (++unit == unit_tiles(a, q) * a.c.kv_heads) {
+            unit = 0;
+            do {
+                q = seq_at(a.s, ++b);           // (at < end: there is one)
+                each = unit_pages(a, q);
+            } while (each == 0);
+        }
+        __syncthreads();                        // the sums in LDS have been read
+    }
+}
+
+// Joins the parts of a unit's rows: a workgroup per unit and row, a thread
+// group of D/4 for every (512 / (D/4))th part.
+template <int D>
+__global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
+{
+    constexpr int QUADS = D / 4, GROUPS = 512 / QUADS;
     __shared__ f32x4 acc_s[GROUPS][QUADS];
-    __shared__ float l_s[GROUPS], m_s[4];
+    __shared__ float l_s[GROUPS], m_s[8];
     const int tid = threadIdx.x;
-    const int64_t unit = blockIdx.x / kRows;
-    const int r = blockIdx.x % kRows;
-    RowTile t;
-    if (!find_tile(a, unit, t) || t.row0 + r >= t.rows)
+    const int r = blockIdx.x % a.join_rows;
+    const Place p = find_place<true>(a, blockIdx.x / a.join_rows);
+    if (p.b < 0)
         return;
-    const int splits = span_of(a, t).splits;
-    if (splits <= 1)
+    const Seq q = seq_at(a.s, p.b);
+    const RowTile t = tile_at(a, p.b, p.unit, q);
+    if (t.row0 + r >= t.rows)
         return;
-    const float *part = a.part + unit * a.splits * part_floats(D);
+    const int each = unit_pages(a, q);
+    const int64_t begin = p.first + (int64_t)p.unit * each, share = share_of(a, p.total);
+    const int64_t i0 = begin / share;
+    const int n = (int)((begin + each - 1) / share - i0) + 1;
+    if (n == 1)
+        return;
+    // part i of the unit
+    const auto place = [&](int i) {
+        return a.part + (2 * (i0 + i) + ((i0 + i) * share >= begin ? 0 : 1)) * part_floats(D);
+    };
     float m = -INFINITY;
-    for (int s = tid; s < splits; s += 256)
-        m = fmaxf(m, part[s * part_floats(D) + r]);
+    for (int i = tid; i < n; i += 512)
+        m = fmaxf(m, place(i)[r]);
     m = max_x16(m);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1)
@@ -469,93 +597,79 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
     if ((tid & 63) == 0)
         m_s[tid >> 6] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        m = fmaxf(m, m_s[i]);
     const float zero = m == -INFINITY ? 0.0f : m;
     const int g = tid / QUADS, d = tid % QUADS;
     float l = 0.0f;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int s = g; s < splits; s += GROUPS) {
-        const float *p = part + s * part_floats(D);
-        const float k = __builtin_amdgcn_exp2f(p[r] - zero);
-        l += k * p[kRows + r];
-        acc += k * *(const f32x4 *)(p + 2 * kRows + r * D + 4 * d);
+    for (int i = g; i < n; i += GROUPS) {
+        const float *x = place(i);
+        const float k = __builtin_amdgcn_exp2f(x[r] - zero);
+        l += k * x[kRows + r];
+        acc += k * *(const f32x4 *)(x + 2 * kRows + r * D + 4 * d);
     }
     acc_s[g][d] = acc;
     if (d == 0)
         l_s[g] = l;
     __syncthreads();
     if (g == 0) {
-#pragma unroll
-        for (int u = 1; u < GROUPS; u++) {
+        const int groups = min(n, GROUPS);
+        for (int u = 1; u < groups; u++) {
             acc += acc_s[u][d];
             l += l_s[u];
         }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        u32x2 y;
-        y.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
-        y.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
-        *(u32x2 *)(out_row(a, t, t.row0 + r, D) + 4 * d) = y;
+        store_row<D>(a, t, t.row0 + r, 4 * d, acc, l);
     }
-}
-
-// How a call is laid out, from what the host knows: the token count, the
-// sequences and the pages their tables provide for.
-struct Plan {
-    int64_t units;
-    int32_t split_pages, splits;
-};
-Plan plan_of(const engram_cache &c, const Seqs &s, int32_t q_heads, int64_t window)
-{
-    Plan p;
-    const int64_t g = q_heads / c.kv_heads;
-    p.units = (s.cu ? ((int64_t)s.T * g / kRows + s.B)
-                    : (((int64_t)s.each * g + kRows - 1) / kRows) * s.B) * c.kv_heads;
-    // about eight workgroups a CU, a page a wavefront at least
-    const int64_t target = 8 * (int64_t)device_cus();
-    const auto round_up = [](int64_t v) { return (v + kWaves - 1) / kWaves * kWaves; };
-    int64_t pages = s.max_pages;
-    int64_t per = round_up((pages * p.units + target - 1) / target);
-    p.splits = (int32_t)((pages + per - 1) / per);
-    const int64_t seen = (window + kRows) / kPage + 2;
-    if (window > 0 && seen < pages) {
-        // fewer pages: shorter splits, but not more of them (the workspace
-        // is sized without a window)
-        pages = seen;
-        per = (pages * p.units + target - 1) / target;
-        per = round_up(per > (pages + p.splits - 1) / p.splits ? per
-                                                               : (pages + p.splits - 1) / p.splits);
-        p.splits = (int32_t)((pages + per - 1) / per);
-    }
-    p.split_pages = (int32_t)per;
-    return p;
 }
 
 // Which kernel a call takes: tiles of 128 rows where the call has enough of
-// them to fill the chip, else tiles of 16 whose keys are split.
+// them to fill the chip, else tiles of 16 whose keys are shared out.
 bool many_rows(const engram_cache &c, const Seqs &s, int32_t g)
 {
     return (int64_t)s.T * g >= 64 * (int64_t)s.B && prompt_tiles(c, s, g) >= device_cus() / 8;
+}
+
+// Units of 16 rows that a call has at most.
+int64_t row_units(const engram_cache &c, const Seqs &s, int32_t g)
+{
+    return (s.cu ? (int64_t)s.T * g / kRows + s.B
+                 : (((int64_t)s.each * g + kRows - 1) / kRows) * s.B) * c.kv_heads;
+}
+
+// Tables of so few pages are read by one workgroup a unit.
+constexpr int kShortPages = 16;
+constexpr int kLeastShare = 8;
+
+// Workgroups that share the pages out: two a CU, one with 256-wide heads
+// (whose wavefronts need a SIMD's registers alone).
+int32_t parts_of(const engram_cache &c)
+{
+    return device_cus() * (c.head_dim == 256 ? 1 : 2);
 }
 
 }  // namespace
 
 size_t attend_bytes(const engram_cache &c, const Seqs &s, int32_t q_heads)
 {
-    if (many_rows(c, s, q_heads / c.kv_heads))
+    if (many_rows(c, s, q_heads / c.kv_heads) || s.max_pages <= kShortPages)
         return 0;
-    const Plan p = plan_of(c, s, q_heads, 0);
-    return p.splits > 1 ? sizeof(float) * (size_t)(p.units * p.splits * part_floats(c.head_dim)) : 0;
+    return sizeof(float) * 2 * (size_t)parts_of(c) * (size_t)part_floats(c.head_dim);
 }
 
 template <int D>
 static void launch_rows(const AttendArgs &a, int64_t units, const Launch &l)
 {
-    dispatch(attend_rows_kernel<D>, dim3((unsigned)(units * a.splits)), dim3(64 * kWaves), l, true,
-             a.splits == 1, a);
-    if (a.splits > 1)
-        dispatch(attend_join_kernel<D>, dim3((unsigned)(units * kRows)), dim3(256), l, false, true,
-                 a);
+    if (a.s.max_pages <= kShortPages) {
+        constexpr int W = D == 256 ? 4 : 8;
+        dispatch(attend_unit_kernel<D, W>, dim3((unsigned)units), dim3(64 * W), l, true, true, a);
+        return;
+    }
+    dispatch(attend_share_kernel<D, 4>, dim3((unsigned)a.parts), dim3(256), l, true, false, a);
+    dispatch(attend_join_kernel<D>, dim3((unsigned)(units * a.join_rows)), dim3(512), l, false,
+             true, a);
 }
 
 int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint16_t *out,
@@ -563,26 +677,25 @@ int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint
 {
     const int32_t g = q_heads / c.kv_heads;
     const int32_t w = window < ((int64_t)1 << 31) ? (int32_t)window : 0;
-    const int64_t tiles = prompt_tiles(c, s, g);
-    if (many_rows(c, s, g)) {
-        if (tiles >= ((int64_t)1 << 23))
-            return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
-                        (long long)tiles);
-        return launch_attend_prompt(
-            AttendArgs{c, s, q, out, q_heads, g, scale * kLog2e, w, 0, 0, nullptr}, l);
-    }
-    const Plan p = plan_of(c, s, q_heads, window);
-    if (p.units * p.splits >= ((int64_t)1 << 20) * 4 || p.units >= ((int64_t)1 << 20))
+    AttendArgs a{c, s, q, out, q_heads, g, scale * kLog2e, w, 0, 0, 0, 0, (float *)ws};
+    const bool many = many_rows(c, s, g);
+    const int64_t units = many ? prompt_tiles(c, s, g) : row_units(c, s, g);
+    a.join_rows = !s.cu && (int64_t)s.each * g < kRows ? s.each * g : kRows;
+    if (units * (many ? 1 : a.join_rows) >= ((int64_t)1 << 23))
         return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
-                    (long long)p.units);
-    const AttendArgs a{c, s, q, out, q_heads, g, scale * kLog2e, w,
-                       p.split_pages, p.splits, (float *)ws};
+                    (long long)units);
+    if (many)
+        return launch_attend_prompt(a, l);
+    a.parts = parts_of(c);
+    a.least = kLeastShare;
+    // pages that 16 rows' windows can meet
+    a.window_pages = w > 0 && w < (1 << 30) ? (w + kRows + kPage - 2) / kPage + 1 : 0;
     if (c.head_dim == 64)
-        launch_rows<64>(a, p.units, l);
+        launch_rows<64>(a, units, l);
     else if (c.head_dim == 128)
-        launch_rows<128>(a, p.units, l);
+        launch_rows<128>(a, units, l);
     else
-        launch_rows<256>(a, p.units, l);
+        launch_rows<256>(a, units, l);
     return launch_status("engram cache_attend kernel");
 }
 
