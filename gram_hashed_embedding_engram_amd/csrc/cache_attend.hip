@@ -37,56 +37,57 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const Seq &q)
     return (int)(((int64_t)q.n * a.g + kRows - 1) / kRows);
 }
 
-// A place in the row of pages.
-struct Place {
-    int b, unit;              // the sequence, its unit (tile * kv_heads + head)
-    int64_t first;            // where the sequence's pages begin
-    int64_t total;            // pages of all sequences
-};
-// The place of page `at` (BY_UNIT false) or of unit number `at` (true); b = -1
-// past the end.  Called by whole wavefronts.
-template <bool BY_UNIT>
-__device__ __forceinline__ Place find_place(const AttendArgs &a, int64_t at)
+// Inclusive sum over the wavefront's lanes, in data-parallel moves: within
+// rows of 16 lanes by shifts of 1, 2, 4, 8, then rows 0 and 2 into 1 and 3 and
+// row 1 into 2 and 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_iadd(int v)
 {
-    const int lane = threadIdx.x & 63;
-    Place p{-1, 0, 0, 0};
-    int64_t units_before = 0;
-    for (int base = 0; base < a.s.B; base += 64) {
-        int64_t units = 0, pages = 0;
-        int each = 0;
-        if (base + lane < a.s.B) {
-            const Seq q = seq_at(a.s, base + lane);
-            each = unit_pages(a, q);
-            units = (int64_t)unit_tiles(a, q) * a.c.kv_heads;
-            pages = units * each;
-        }
-        int64_t sum_p = pages, sum_u = units;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t up = __shfl_up(sum_p, d), uu = __shfl_up(sum_u, d);
-            sum_p += lane >= d ? up : 0;
-            sum_u += lane >= d ? uu : 0;
-        }
-        const int64_t key = BY_UNIT ? units_before + sum_u : p.total + sum_p;
-        const uint64_t over = __ballot(key > at);
-        if (over && p.b < 0) {
-            const int l = __builtin_ctzll(over);
-            p.b = base + l;
-            p.first = p.total + __shfl(sum_p - pages, l);
-            const int n = __builtin_amdgcn_readlane(each, l);
-            p.unit = BY_UNIT ? (int)(at - (units_before + __shfl(sum_u - units, l)))
-                             : (int)((at - p.first) / (n > 0 ? n : 1));
-        }
-        p.total += __shfl(sum_p, 63);
-        units_before += __shfl(sum_u, 63);
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v = dpp_iadd<0x111, 0xF>(v);
+    v = dpp_iadd<0x112, 0xF>(v);
+    v = dpp_iadd<0x114, 0xF>(v);
+    v = dpp_iadd<0x118, 0xF>(v);
+    v = dpp_iadd<0x142, 0xA>(v);
+    v = dpp_iadd<0x143, 0xC>(v);
+    return v;
+}
+
+// Sequences base .. base+63, one a lane, with their units and pages and the
+// sums of both up to and with them (a call's units x pages stay below 2^31).
+struct Lanes {
+    Seq q;
+    int each, units, pages, sum_u, sum_p;
+    __device__ __forceinline__ int all_units() const { return __builtin_amdgcn_readlane(sum_u, 63); }
+    __device__ __forceinline__ int all_pages() const { return __builtin_amdgcn_readlane(sum_p, 63); }
+    __device__ __forceinline__ Seq seq(int l) const
+    {
+        return Seq{__builtin_amdgcn_readlane(q.t0, l), __builtin_amdgcn_readlane(q.n, l),
+                   __builtin_amdgcn_readlane(q.start, l), (bool)__builtin_amdgcn_readlane(q.bad, l)};
     }
-    return p;
+};
+__device__ __forceinline__ Lanes lanes_at(const AttendArgs &a, int base)
+{
+    const int b = base + (threadIdx.x & 63);
+    Lanes c{{0, 0, 0, false}, 0, 0, 0, 0, 0};
+    if (b < a.s.B) {
+        c.q = seq_at(a.s, b);
+        c.each = unit_pages(a, c.q);
+        c.units = unit_tiles(a, c.q) * a.c.kv_heads;
+        c.pages = c.units * c.each;
+    }
+    c.sum_u = wave_scan(c.units);
+    c.sum_p = wave_scan(c.pages);
+    return c;
 }
 
 // Pages a workgroup takes.
-__device__ __forceinline__ int64_t share_of(const AttendArgs &a, int64_t total)
+__device__ __forceinline__ int share_of(const AttendArgs &a, int total)
 {
-    const int64_t per = (total + a.parts - 1) / a.parts;
+    const int per = (total + a.parts - 1) / a.parts;
     return per > a.least ? per : a.least;
 }
 
@@ -189,7 +190,11 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
 {
     constexpr int KS = D == 64 ? 1 : D / 128;     // 128-value steps of the logits
     constexpr int VW = D / 64;                    // dwords of a token's values a lane holds
-    const int tid = threadIdx.x, lane = tid & 63;
+    int tid = threadIdx.x;
+    // opaque, so that what is derived from it is not kept in registers over
+    // the caller's loop
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q4 = lane >> 4;
 
@@ -246,20 +251,6 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
     for (int i = 0; i < D / 16; i++)
         o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int32_t *table = a.s.pages + (int64_t)t.b * a.s.max_pages;
-    int ids = 0;
-    // the wavefront's i-th page; -1 past the last or outside the cache
-    const auto page_id = [&](int i) {
-        if ((i & 63) == 0) {
-            const int at = first + w + W * (i + lane);
-            ids = at < last ? table[at] : -1;
-            if (at < last && (ids < 0 || ids >= a.c.n_pages)) {
-                raise(a.s.err, ENGRAM_DEVERR_PAGE);
-                ids = -1;
-            }
-        }
-        return __builtin_amdgcn_readlane(ids, i & 63);
-    };
     i32x8 kf[4][KS];
     uint32_t vf[4][4][VW];
     float ks = 0.0f, vs = 0.0f, vs_next = 0.0f;
@@ -304,29 +295,13 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
             }
     };
 
-    const int mine = last - first - w > 0 ? (last - first - w + W - 1) / W : 0;
-    int next = mine > 0 ? page_id(0) : -1;
-    if (next >= 0) {
-        const int64_t at = (int64_t)next * a.c.kv_heads + t.h;
-        load_k(at);
-        load_v(at);
-    }
-    for (int i = 0; i < mine; i++) {
-        const int page = next;
-        next = i + 1 < mine ? page_id(i + 1) : -1;
+    // One page.  FULL: every row sees all of it, and the next such page is
+    // loaded meanwhile: its keys once this one's are used, its values likewise
+    // (the barriers keep the compiler from loading into other registers and
+    // waiting for them in order to copy).
+    const auto step = [&](auto full_c, int page, int base, int next) {
+        constexpr bool edge = !decltype(full_c)::value;
         const int64_t at_next = (int64_t)next * a.c.kv_heads + t.h;
-        if (page < 0) {
-            if (next >= 0) {
-                load_k(at_next);
-                load_v(at_next);
-            }
-            continue;
-        }
-        const int base = (first + w + W * i) * kPage;
-        // pages that some row does not see whole take the masks, and no loads
-        // ahead (which would not fit the registers beside the masks)
-        const auto step = [&](auto edge_c) {
-        constexpr bool edge = decltype(edge_c)::value;
         // ---- logits
         f32x4 s[4];
 #pragma unroll
@@ -343,8 +318,12 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
         }
         const float f = qs * ks;
         vs = vs_next;
-        if (!edge && next >= 0)
-            load_k(at_next);                     // in flight during the rest
+        if (!edge) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (next >= 0)
+                load_k(at_next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; j++)
@@ -436,16 +415,52 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
                     o[u][e] = n[e] > 0.0f ? __uint_as_float(0x7FC00000u) : o[u][e];
             });
         }
-        if (next >= 0) {
-            if (edge)
-                load_k(at_next);
-            load_v(at_next);
+        if (!edge) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (next >= 0)
+                load_v(at_next);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        };
-        if (base + kPage - 1 > pos_lo || base < all_lo)
-            step(std::true_type{});
-        else
-            step(std::false_type{});
+    };
+
+    // The wavefront's pages, 64 at a time and one a lane: first those that
+    // every row sees whole, then the others.
+    const int32_t *table = a.s.pages + (int64_t)t.b * a.s.max_pages;
+    for (int p = first + w; p < last; p += 64 * W) {
+        const int mine = p + W * lane;
+        int id = -1;
+        if (mine < last) {
+            id = table[mine];
+            if (id < 0 || id >= a.c.n_pages) {
+                raise(a.s.err, ENGRAM_DEVERR_PAGE);
+                id = -1;
+            }
+        }
+        const bool whole = mine * kPage + kPage - 1 <= pos_lo && mine * kPage >= all_lo;
+        uint64_t todo = __ballot(id >= 0 && whole);
+        if (todo) {
+            int i = __builtin_ctzll(todo);
+            int page = __builtin_amdgcn_readlane(id, i);
+            load_k((int64_t)page * a.c.kv_heads + t.h);
+            load_v((int64_t)page * a.c.kv_heads + t.h);
+            while (todo) {
+                todo &= todo - 1;
+                const int j = todo ? __builtin_ctzll(todo) : 0;
+                const int next = todo ? __builtin_amdgcn_readlane(id, j) : -1;
+                step(std::true_type{}, page, (p + W * i) * kPage, next);
+                i = j;
+                page = next;
+            }
+        }
+        todo = __ballot(id >= 0 && !whole);
+        while (todo) {
+            const int i = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const int page = __builtin_amdgcn_readlane(id, i);
+            load_k((int64_t)page * a.c.kv_heads + t.h);
+            load_v((int64_t)page * a.c.kv_heads + t.h);
+            step(std::false_type{}, page, (p + W * i) * kPage, -1);
+        }
     }
 
     // ---- the wavefronts' sums
@@ -509,13 +524,21 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : W / 4) void attend_unit_kern
         b = blockIdx.x / units;
         unit = blockIdx.x % units;
     } else {
-        const Place p = find_place<true>(a, blockIdx.x);
-        if (p.b < 0) {
-            raise_bad(a);
-            return;
+        unit = blockIdx.x;
+        Lanes c = lanes_at(a, 0);
+        int base = 0;
+        while (unit >= c.all_units()) {
+            unit -= c.all_units();
+            base += 64;
+            if (base >= a.s.B) {
+                raise_bad(a);
+                return;
+            }
+            c = lanes_at(a, base);
         }
-        b = p.b;
-        unit = p.unit;
+        const int l = __builtin_ctzll(__ballot(c.sum_u > unit));
+        b = base + l;
+        unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
     }
     raise_bad(a);
     const RowTile t = tile_at(a, b, unit, seq_at(a.s, b));
@@ -527,69 +550,132 @@ template <int D, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(AttendArgs a)
 {
     __shared__ Reduce<D, W> red;
+    __shared__ Seq seqs[64];
+    __shared__ int each_s[64], units_s[64];
     raise_bad(a);
-    const Place all = find_place<false>(a, 0);
-    const int64_t share = share_of(a, all.total);
-    int64_t at = blockIdx.x * share;
-    const int64_t end = min(at + share, all.total);
-    if (at >= end)
+    Lanes c = lanes_at(a, 0);
+    int total = c.all_pages();
+    for (int base = 64; base < a.s.B; base += 64)
+        total += lanes_at(a, base).all_pages();
+    const int share = share_of(a, total);
+    if ((int64_t)blockIdx.x * share >= total)
         return;
-    const Place p = find_place<false>(a, at);
-    int b = p.b, unit = p.unit;
-    Seq q = seq_at(a.s, b);
-    int each = unit_pages(a, q);
-    int p0 = (int)(at - p.first - (int64_t)unit * each);
-    for (bool lead = true;; lead = false) {
-        const int np = (int)min((int64_t)(each - p0), end - at);
-        const RowTile t = tile_at(a, b, unit, q);
-        float *part = np == each ? nullptr
-                                 : a.part + (2 * (int64_t)blockIdx.x + (lead ? 0 : 1)) * part_floats(D);
-        attend_unit<D, W>(a, t, p0, np, part, red);
+    int at = blockIdx.x * share;
+    const int end = min((int64_t)at + share, (int64_t)total);
+    // the sequence, unit and page that the share begins with; the sequences
+    // wait in LDS while a unit is at work (its registers are all taken)
+    int base = 0, before = 0;
+    while (before + c.all_pages() <= at) {
+        before += c.all_pages();
+        base += 64;
+        c = lanes_at(a, base);
+    }
+    int l = __builtin_ctzll(__ballot(before + c.sum_p > at));
+    int p0 = at - before - __builtin_amdgcn_readlane(c.sum_p - c.pages, l);
+    int unit = p0 / __builtin_amdgcn_readlane(c.each, l);
+    p0 -= unit * __builtin_amdgcn_readlane(c.each, l);
+    const auto keep = [&] {
+        if (threadIdx.x < 64) {
+            seqs[threadIdx.x] = c.q;
+            each_s[threadIdx.x] = c.each;
+            units_s[threadIdx.x] = c.pages ? c.units : 0;
+        }
+        __syncthreads();
+    };
+    keep();
+    float *part = a.part + 2 * (int64_t)blockIdx.x * part_floats(D);
+    int place = 0;
+    while (true) {
+        const int each = __builtin_amdgcn_readfirstlane(each_s[l]);
+        const int np = min(each - p0, end - at);
+        const Seq q{__builtin_amdgcn_readfirstlane(seqs[l].t0), __builtin_amdgcn_readfirstlane(seqs[l].n),
+                    __builtin_amdgcn_readfirstlane(seqs[l].start),
+                    (bool)__builtin_amdgcn_readfirstlane(seqs[l].bad)};
+        attend_unit<D, W>(a, tile_at(a, base + l, unit, q), p0, np,
+                          np == each ? nullptr : part + place * part_floats(D), red);
         at += np;
         if (at >= end)
             return;
+        place = 1;
         p0 = 0;
-        if (++unit == unit_tiles(a, q) * a.c.kv_heads) {
-            unit = 0;
-            do {
-                q = seq_at(a.s, ++b);           // (at < end: there is one)
-                each = unit_pages(a, q);
-            } while (each == 0);
-        }
         __syncthreads();                        // the sums in LDS have been read
+        if (++unit == __builtin_amdgcn_readfirstlane(units_s[l])) {
+            unit = 0;
+            do {                                // (at < end: there is one)
+                if (++l == 64) {
+                    l = 0;
+                    base += 64;
+                    const Lanes next = lanes_at(a, base);
+                    c = next;
+                    keep();
+                }
+            } while (__builtin_amdgcn_readfirstlane(units_s[l]) == 0);
+        }
     }
 }
 
-// Joins the parts of a unit's rows: a workgroup per unit and row, a thread
-// group of D/4 for every (512 / (D/4))th part.
-template <int D>
+// Joins the parts of a unit's rows.  A workgroup takes a unit, or, with
+// SPLIT, where units are few and their parts many, a unit's row; G thread
+// groups of D/4 then take parts in turn.
+template <int D, bool SPLIT>
 __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
 {
     constexpr int QUADS = D / 4, GROUPS = 512 / QUADS;
     __shared__ f32x4 acc_s[GROUPS][QUADS];
     __shared__ float l_s[GROUPS], m_s[8];
     const int tid = threadIdx.x;
-    const int r = blockIdx.x % a.join_rows;
-    const Place p = find_place<true>(a, blockIdx.x / a.join_rows);
-    if (p.b < 0)
-        return;
-    const Seq q = seq_at(a.s, p.b);
-    const RowTile t = tile_at(a, p.b, p.unit, q);
-    if (t.row0 + r >= t.rows)
-        return;
-    const int each = unit_pages(a, q);
-    const int64_t begin = p.first + (int64_t)p.unit * each, share = share_of(a, p.total);
-    const int64_t i0 = begin / share;
-    const int n = (int)((begin + each - 1) / share - i0) + 1;
-    if (n == 1)
+    const int r0 = SPLIT ? blockIdx.x % a.join_rows : 0;
+    int unit = SPLIT ? blockIdx.x / a.join_rows : blockIdx.x;
+    Lanes c = lanes_at(a, 0);
+    int total = c.all_pages();
+    for (int base = 64; base < a.s.B; base += 64)
+        total += lanes_at(a, base).all_pages();
+    int base = 0, before = 0;
+    while (unit >= c.all_units()) {
+        unit -= c.all_units();
+        before += c.all_pages();
+        base += 64;
+        if (base >= a.s.B)
+            return;
+        c = lanes_at(a, base);
+    }
+    const int l = __builtin_ctzll(__ballot(c.sum_u > unit));
+    unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
+    const RowTile t = tile_at(a, base + l, unit, c.seq(l));
+    const int each = __builtin_amdgcn_readlane(c.each, l), share = share_of(a, total);
+    const int begin = before + __builtin_amdgcn_readlane(c.sum_p - c.pages, l) + unit * each;
+    const int i0 = begin / share;
+    const int n = (begin + each - 1) / share - i0 + 1;
+    const int rows = min(kRows, t.rows - t.row0);
+    if (n == 1 || r0 >= rows)
         return;
     // part i of the unit
     const auto place = [&](int i) {
-        return a.part + (2 * (i0 + i) + ((i0 + i) * share >= begin ? 0 : 1)) * part_floats(D);
+        return a.part + (2 * (int64_t)(i0 + i) + ((i0 + i) * share >= begin ? 0 : 1)) * part_floats(D);
     };
+    const int g = tid / QUADS, d = tid % QUADS;
+    if (!SPLIT) {
+        for (int r = g; r < rows; r += GROUPS) {
+            float m = -INFINITY;
+            for (int i = 0; i < n; i++)
+                m = fmaxf(m, place(i)[r]);
+            const float zero = m == -INFINITY ? 0.0f : m;
+            float sum = 0.0f;
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+            for (int i = 0; i < n; i++) {
+                const float *x = place(i);
+                const float k = __builtin_amdgcn_exp2f(x[r] - zero);
+                sum += k * x[kRows + r];
+                acc += k * *(const f32x4 *)(x + 2 * kRows + r * D + 4 * d);
+            }
+            store_row<D>(a, t, t.row0 + r, 4 * d, acc, sum);
+        }
+        return;
+    }
     float m = -INFINITY;
     for (int i = tid; i < n; i += 512)
-        m = fmaxf(m, place(i)[r]);
+        m = fmaxf(m, place(i)[r0]);
     m = max_x16(m);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1)
@@ -601,27 +687,26 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
     for (int i = 0; i < 8; i++)
         m = fmaxf(m, m_s[i]);
     const float zero = m == -INFINITY ? 0.0f : m;
-    const int g = tid / QUADS, d = tid % QUADS;
-    float l = 0.0f;
+    float sum = 0.0f;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int i = g; i < n; i += GROUPS) {
         const float *x = place(i);
-        const float k = __builtin_amdgcn_exp2f(x[r] - zero);
-        l += k * x[kRows + r];
-        acc += k * *(const f32x4 *)(x + 2 * kRows + r * D + 4 * d);
+        const float k = __builtin_amdgcn_exp2f(x[r0] - zero);
+        sum += k * x[kRows + r0];
+        acc += k * *(const f32x4 *)(x + 2 * kRows + r0 * D + 4 * d);
     }
     acc_s[g][d] = acc;
     if (d == 0)
-        l_s[g] = l;
+        l_s[g] = sum;
     __syncthreads();
     if (g == 0) {
         const int groups = min(n, GROUPS);
         for (int u = 1; u < groups; u++) {
             acc += acc_s[u][d];
-            l += l_s[u];
+            sum += l_s[u];
         }
-        store_row<D>(a, t, t.row0 + r, 4 * d, acc, l);
+        store_row<D>(a, t, t.row0 + r0, 4 * d, acc, sum);
     }
 }
 
@@ -641,7 +726,7 @@ int64_t row_units(const engram_cache &c, const Seqs &s, int32_t g)
 
 // Tables of so few pages are read by one workgroup a unit.
 constexpr int kShortPages = 16;
-constexpr int kLeastShare = 8;
+constexpr int kLeastShare = 4;
 
 // Workgroups that share the pages out: two a CU, one with 256-wide heads
 // (whose wavefronts need a SIMD's registers alone).
@@ -668,8 +753,12 @@ static void launch_rows(const AttendArgs &a, int64_t units, const Launch &l)
         return;
     }
     dispatch(attend_share_kernel<D, 4>, dim3((unsigned)a.parts), dim3(256), l, true, false, a);
-    dispatch(attend_join_kernel<D>, dim3((unsigned)(units * a.join_rows)), dim3(512), l, false,
-             true, a);
+    if (units < a.parts / 2)
+        dispatch(attend_join_kernel<D, true>, dim3((unsigned)(units * a.join_rows)), dim3(512), l,
+                 false, true, a);
+    else
+        dispatch(attend_join_kernel<D, false>, dim3((unsigned)units), dim3(512), l, false, true,
+                 a);
 }
 
 int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint16_t *out,
@@ -684,6 +773,10 @@ int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint
     if (units * (many ? 1 : a.join_rows) >= ((int64_t)1 << 23))
         return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
                     (long long)units);
+    if (!many && units * s.max_pages >= ((int64_t)1 << 31))
+        return fail(ENGRAM_E_RANGE,
+                    "engram cache_attend: %lld row tiles of up to %d pages exceed 2^31 in one call",
+                    (long long)units, s.max_pages);
     if (many)
         return launch_attend_prompt(a, l);
     a.parts = parts_of(c);
