@@ -89,29 +89,43 @@ __device__ __forceinline__ void raise(int32_t *err, int32_t bits)
         atomicOr(err, bits);
 }
 
+// Inclusive sum over the wavefront's lanes, in data-parallel moves: within
+// rows of 16 lanes by shifts of 1, 2, 4, 8, then rows 0 and 2 into 1 and 3 and
+// row 1 into 2 and 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_iadd(int v)
+{
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v = dpp_iadd<0x111, 0xF>(v);
+    v = dpp_iadd<0x112, 0xF>(v);
+    v = dpp_iadd<0x114, 0xF>(v);
+    v = dpp_iadd<0x118, 0xF>(v);
+    v = dpp_iadd<0x142, 0xA>(v);
+    v = dpp_iadd<0x143, 0xC>(v);
+    return v;
+}
+
 // Work item i of a grid laid over the sequences: finds the sequence b and the
 // piece of it, where sequence b has pieces(b) of them, in order.  Called by
 // whole wavefronts with a uniform i; false past the last item.
 template <class F>
-__device__ __forceinline__ bool find_piece(int64_t i, int B, F pieces, int &b, int &piece)
+__device__ __forceinline__ bool find_piece(int i, int B, F pieces, int &b, int &piece)
 {
     const int lane = threadIdx.x & 63;
     for (int base = 0; base < B; base += 64) {
-        int c = base + lane < B ? pieces(base + lane) : 0;
-        const int own = c;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(c, d);
-            c += lane >= d ? up : 0;
-        }
-        const int64_t total = __builtin_amdgcn_readlane(c, 63);
-        if (i < total) {
-            const int at = __builtin_ctzll(__ballot((int64_t)c > i));
+        const int own = base + lane < B ? pieces(base + lane) : 0;
+        const int sum = wave_scan(own);
+        const uint64_t over = __ballot(sum > i);
+        if (over) {
+            const int at = __builtin_ctzll(over);
             b = base + at;
-            piece = (int)i - (__builtin_amdgcn_readlane(c, at) - __builtin_amdgcn_readlane(own, at));
+            piece = i - __builtin_amdgcn_readlane(sum - own, at);
             return true;
         }
-        i -= total;
+        i -= __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
 }

@@ -1,11 +1,10 @@
 // The position rotation of a step's queries and keys, and the append of its
 // keys and values to the paged 8-bit cache.
 //
-// One launch with two kinds of workgroup: a page of one sequence (all its key
-// heads in turn, keys and values, so that an angle is formed once a token and
-// pair), or a run of tokens' queries.  Bound by memory: a key or value is read
-// once as bf16 and written once as a code, and stays in registers between the
-// page's maximum and the codes.
+// One launch with two kinds of workgroup: the keys or the values of one page
+// and head, or a run of tokens' queries.  Bound by memory: a key or value is
+// read once as bf16 and written once as a code, and stays in registers between
+// the page's maximum and the codes; a query's angles are formed once a token.
 #include "attention.h"
 
 namespace engram {
@@ -96,114 +95,116 @@ __device__ __forceinline__ void turn8(float (&v)[8], const Place &at, bool halve
     }
 }
 
+constexpr int kRunTokens = 8;       // tokens a queries' workgroup takes at most
+
 struct AppendArgs {
     engram_cache c;
     Seqs s;
     Heads k, v, q;
     uint16_t *q_out;
     Rotation r;
-    int32_t q_heads, pieces;    // grid: `pieces` x kv_heads page workgroups, then queries
-    int32_t q_blocks;
+    int32_t q_heads, pieces;    // grid: keys and values of `pieces` x kv_heads pages,
+    int32_t run;                // then queries, `run` tokens a workgroup
 };
 
-// One page of one sequence and key head: keys, then values.
+// The keys (z 0) or values (z 1) of one page and key head.
 template <int D, bool HALVES>
 __device__ __forceinline__ void append_page(const AppendArgs &a, const Seq &q, int blk,
-                                            int32_t page, int h)
+                                            int32_t page, int h, bool z)
 {
     constexpr int E = D / 8;                    // threads a token
     constexpr int TOK = kThreads / E;           // tokens at a time
     constexpr int N = kPage / TOK;
-    __shared__ float part[2][kThreads / 64];
+    __shared__ float part[kThreads / 64];
     const int tid = threadIdx.x, e = tid % E, g = tid / E;
     const int page0 = blk * kPage;
     const int older = max(q.start - page0, 0);
     const int last = min(q.start + q.n - page0, kPage);
     const int64_t at = (int64_t)page * a.c.kv_heads + h;
+    const Heads &src = z ? a.v : a.k;
+    uint8_t *codes = (z ? a.c.d_v : a.c.d_k) + at * kPage * D;
+    float *scale = (z ? a.c.d_v_scales : a.c.d_k_scales) + at;
+    Rotation r = a.r;
+    r.halves = HALVES;
+    if (z)
+        r.rot = 0;
+    const Place pl = place_of<D>(e, r);
+    float v[N][8];
+    float amax = 0.0f;
 #pragma unroll
-    for (int z = 0; z < 2; z++) {
-        const Heads &src = z ? a.v : a.k;
-        uint8_t *codes = (z ? a.c.d_v : a.c.d_k) + at * kPage * D;
-        float *scale = (z ? a.c.d_v_scales : a.c.d_k_scales) + at;
-        Rotation r = a.r;
-        r.halves = HALVES;
-        if (z)
-            r.rot = 0;
-        const Place pl = place_of<D>(e, r);
-        float v[N][8];
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int slot = g + TOK * i;
-            if (slot >= older && slot < last) {
-                const int pos = page0 + slot;
-                load8(src.p + (q.t0 + (int64_t)(pos - q.start)) * src.token + h * src.head, pl, v[i]);
-            }
+    for (int i = 0; i < N; i++) {
+        const int slot = g + TOK * i;
+        if (slot >= older && slot < last) {
+            const int pos = page0 + slot;
+            load8(src.p + (q.t0 + (int64_t)(pos - q.start)) * src.token + h * src.head, pl, v[i]);
         }
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int slot = g + TOK * i;
-            if (slot >= older && slot < last) {
-                if (!z && pl.pair >= 0) {
-                    Turn t[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        t[j] = turn_of(page0 + slot, r.freq[pl.pair + j]);
-                    turn8(v[i], pl, HALVES, t);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    amax = fmaxf(amax, finite_abs(v[i][j]));
-            }
-        }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1)
-            amax = fmaxf(amax, __shfl_xor(amax, m));
-        if ((tid & 63) == 0)
-            part[z][tid >> 6] = amax;
-        const float had = older > 0 ? *scale : 0.0f;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kThreads / 64; i++)
-            amax = fmaxf(amax, part[z][i]);
-        const float need = exp2_int(e4m3_scale_exp(amax));
-        const float now = fmaxf(had, need);
-        if (now != had) {                       // (never where the page is new)
-            const float ratio = had / now;
-            for (int i = tid; i < older * (D / 4); i += kThreads) {
-                uint32_t *p = (uint32_t *)codes + i;
-                const uint32_t x = *p;
-                *p = e4m3x4(e4m3_at<0>(x) * ratio, e4m3_at<1>(x) * ratio, e4m3_at<2>(x) * ratio,
-                            e4m3_at<3>(x) * ratio);
-            }
-        }
-        const float inv = 1.0f / now;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int slot = g + TOK * i;
-            if (slot >= older && slot < last) {
-                uint8_t *p = codes + slot * D;
-                *(uint32_t *)(p + pl.i0) = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-                *(uint32_t *)(p + pl.i1) = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-            }
-        }
-        if (tid == 0)                           // all have read it before the barrier
-            *scale = now;
     }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int slot = g + TOK * i;
+        if (slot >= older && slot < last) {
+            if (!z && pl.pair >= 0) {
+                Turn t[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    t[j] = turn_of(page0 + slot, r.freq[pl.pair + j]);
+                turn8(v[i], pl, HALVES, t);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                amax = fmaxf(amax, finite_abs(v[i][j]));
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+        amax = fmaxf(amax, __shfl_xor(amax, m));
+    if ((tid & 63) == 0)
+        part[tid >> 6] = amax;
+    const float had = older > 0 ? *scale : 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; i++)
+        amax = fmaxf(amax, part[i]);
+    const float need = exp2_int(e4m3_scale_exp(amax));
+    const float now = fmaxf(had, need);
+    if (now != had) {                       // (never where the page is new)
+        const float ratio = had / now;
+        for (int i = tid; i < older * (D / 4); i += kThreads) {
+            uint32_t *p = (uint32_t *)codes + i;
+            const uint32_t x = *p;
+            *p = e4m3x4(e4m3_at<0>(x) * ratio, e4m3_at<1>(x) * ratio, e4m3_at<2>(x) * ratio,
+                        e4m3_at<3>(x) * ratio);
+        }
+    }
+    const float inv = 1.0f / now;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int slot = g + TOK * i;
+        if (slot >= older && slot < last) {
+            uint8_t *p = codes + slot * D;
+            *(uint32_t *)(p + pl.i0) = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+            *(uint32_t *)(p + pl.i1) = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+        }
+    }
+    if (tid == 0)                           // all have read it before the barrier
+        *scale = now;
 }
 
 template <int D, bool HALVES>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
 {
+    __shared__ int tok_s[kRunTokens], pos_s[kRunTokens];
+    __shared__ Turn turn_s[kRunTokens][D / 2];
     const int tid = threadIdx.x;
-    const int pages = a.pieces * a.c.kv_heads;
+    const int pages = 2 * a.pieces * a.c.kv_heads;
     if (blockIdx.x == 0)
         for (int i = tid; i < a.s.B; i += kThreads)
             if (seq_at(a.s, i).bad)
                 raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
     if ((int)blockIdx.x < pages) {
-        const int h = blockIdx.x % a.c.kv_heads;
-        int i = blockIdx.x / a.c.kv_heads, b, piece;
+        const bool z = blockIdx.x & 1;
+        const int h = blockIdx.x / 2 % a.c.kv_heads;
+        int i = blockIdx.x / 2 / a.c.kv_heads, b, piece;
         const auto touched = [&](int x) {
             const Seq q = seq_at(a.s, x);
             return q.bad || q.n == 0 ? 0 : (q.start + q.n - 1) / kPage - q.start / kPage + 1;
@@ -225,56 +226,84 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
                 raise(a.s.err, ENGRAM_DEVERR_PAGE);
             return;
         }
-        append_page<D, HALVES>(a, q, blk, page, h);
+        append_page<D, HALVES>(a, q, blk, page, h, z);
         return;
     }
-    // queries: a thread takes eight values of a token's head, heads in turn
-    constexpr int E = D / 8, ROWS = kThreads / E;
-    const int e = tid % E, g = tid / E;
-    const int t = blockIdx.x - pages;
-    int b, piece;
-    if (!a.s.cu) {
-        b = t / a.s.each;
-        piece = t % a.s.each;
-    } else if (!find_piece(t, a.s.B,
-                           [&](int x) {
-                               const Seq q = seq_at(a.s, x);
-                               return q.bad ? 0 : q.n;
-                           },
-                           b, piece)) {
-        return;
+    // queries: where the run's tokens lie, their angles, then eight values a thread
+    const int t0 = (blockIdx.x - pages) * a.run;
+    for (int i = tid >> 6; i < a.run; i += kThreads / 64) {
+        int b = 0, piece = 0;
+        bool found;
+        if (!a.s.cu) {
+            b = (t0 + i) / a.s.each;
+            piece = (t0 + i) % a.s.each;
+            found = t0 + i < a.s.T;
+        } else {
+            found = find_piece(t0 + i, a.s.B,
+                               [&](int x) {
+                                   const Seq q = seq_at(a.s, x);
+                                   return q.bad ? 0 : q.n;
+                               },
+                               b, piece);
+        }
+        if ((tid & 63) == 0) {
+            const Seq q = found ? seq_at(a.s, b) : Seq{0, 0, 0, true};
+            tok_s[i] = q.bad ? -1 : q.t0 + piece;
+            pos_s[i] = q.start + piece;
+        }
     }
-    const Seq q = seq_at(a.s, b);
-    if (q.bad)
-        return;
-    const int64_t tok = q.t0 + piece;
+    __syncthreads();
+    for (int i = tid; i < a.run * (a.r.rot / 2); i += kThreads) {
+        const int t = i / (a.r.rot / 2), p = i % (a.r.rot / 2);
+        if (tok_s[t] >= 0)
+            turn_s[t][p] = turn_of(pos_s[t], a.r.freq[p]);
+    }
+    __syncthreads();
+    constexpr int E = D / 8, ROWS = kThreads / E, AT_ONCE = 4;
+    const int e = tid % E;
     Rotation r = a.r;
     r.halves = HALVES;
     const Place pl = place_of<D>(e, r);
-    Turn turn[4];
-    if (pl.pair >= 0)
+    for (int row0 = tid / E; row0 < a.run * a.q_heads; row0 += ROWS * AT_ONCE) {
+        float v[AT_ONCE][8];
+        int tok[AT_ONCE], head[AT_ONCE], run[AT_ONCE];
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            turn[j] = turn_of(q.start + piece, r.freq[pl.pair + j]);
-    for (int h = g; h < a.q_heads; h += ROWS) {
-        float v[8];
-        load8(a.q.p + tok * a.q.token + h * a.q.head, pl, v);
-        turn8(v, pl, HALVES, turn);
-        uint16_t *o = a.q_out + (tok * a.q_heads + h) * D;
-        u32x2 lo, hi;
-        lo.x = pack_bf16x2(v[0], v[1]);
-        lo.y = pack_bf16x2(v[2], v[3]);
-        hi.x = pack_bf16x2(v[4], v[5]);
-        hi.y = pack_bf16x2(v[6], v[7]);
-        *(u32x2 *)(o + pl.i0) = lo;
-        *(u32x2 *)(o + pl.i1) = hi;
+        for (int i = 0; i < AT_ONCE; i++) {
+            const int row = row0 + ROWS * i;
+            run[i] = row / a.q_heads;
+            head[i] = row - run[i] * a.q_heads;
+            tok[i] = row < a.run * a.q_heads ? tok_s[run[i]] : -1;
+            if (tok[i] >= 0)
+                load8(a.q.p + (int64_t)tok[i] * a.q.token + head[i] * a.q.head, pl, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++) {
+            if (tok[i] < 0)
+                continue;
+            if (pl.pair >= 0) {
+                Turn t[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    t[j] = turn_s[run[i]][pl.pair + j];
+                turn8(v[i], pl, HALVES, t);
+            }
+            uint16_t *o = a.q_out + ((int64_t)tok[i] * a.q_heads + head[i]) * D;
+            u32x2 lo, hi;
+            lo.x = pack_bf16x2(v[i][0], v[i][1]);
+            lo.y = pack_bf16x2(v[i][2], v[i][3]);
+            hi.x = pack_bf16x2(v[i][4], v[i][5]);
+            hi.y = pack_bf16x2(v[i][6], v[i][7]);
+            *(u32x2 *)(o + pl.i0) = lo;
+            *(u32x2 *)(o + pl.i1) = hi;
+        }
     }
 }
 
 template <int D>
 void launch_dim(const AppendArgs &a, const Launch &l)
 {
-    const dim3 grid((unsigned)((int64_t)a.pieces * a.c.kv_heads + a.q_blocks)), block(kThreads);
+    const unsigned runs = a.q_heads ? (a.s.T + a.run - 1) / a.run : 0;
+    const dim3 grid(2u * a.pieces * a.c.kv_heads + runs), block(kThreads);
     if (a.r.halves)
         dispatch(append_kernel<D, true>, grid, block, l, true, true, a);
     else
@@ -290,10 +319,13 @@ int32_t launch_append(const engram_cache &c, const Seqs &s, const Heads &k, cons
     // pages a call can touch: n tokens meet (n + 62) / 64 + 1 at most
     const int64_t pieces = s.cu ? s.T / kPage + 2 * (int64_t)s.B
                                 : (int64_t)s.B * ((s.each + kPage - 2) / kPage + 1);
-    if (pieces * c.kv_heads + s.T >= ((int64_t)1 << 24))
+    if (2 * pieces * c.kv_heads + s.T >= ((int64_t)1 << 24))
         return fail(ENGRAM_E_RANGE, "engram cache_append: %lld pages of %d heads in one call",
                     (long long)pieces, c.kv_heads);
-    const AppendArgs a{c, s, k, v, q, q_out, r, q_heads, (int32_t)pieces, q_heads ? s.T : 0};
+    // several tokens a workgroup once there are enough of them
+    const int64_t run = s.T / (4 * device_cus());
+    const AppendArgs a{c, s, k, v, q, q_out, r, q_heads, (int32_t)pieces,
+                       (int32_t)(run < 1 ? 1 : run > kRunTokens ? kRunTokens : run)};
     if (c.head_dim == 64)
         launch_dim<64>(a, l);
     else if (c.head_dim == 128)

@@ -37,25 +37,6 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const Seq &q)
     return (int)(((int64_t)q.n * a.g + kRows - 1) / kRows);
 }
 
-// Inclusive sum over the wavefront's lanes, in data-parallel moves: within
-// rows of 16 lanes by shifts of 1, 2, 4, 8, then rows 0 and 2 into 1 and 3 and
-// row 1 into 2 and 3.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_iadd(int v)
-{
-    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v)
-{
-    v = dpp_iadd<0x111, 0xF>(v);
-    v = dpp_iadd<0x112, 0xF>(v);
-    v = dpp_iadd<0x114, 0xF>(v);
-    v = dpp_iadd<0x118, 0xF>(v);
-    v = dpp_iadd<0x142, 0xA>(v);
-    v = dpp_iadd<0x143, 0xC>(v);
-    return v;
-}
-
 // Sequences base .. base+63, one a lane, with their units and pages and the
 // sums of both up to and with them (a call's units x pages stay below 2^31).
 struct Lanes {
@@ -264,8 +245,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
 #pragma unroll
             for (int s = 0; s < KS; s++) {
                 const uint8_t *p = kp + 16 * i * D + 128 * s;
-                const u32x4 u = *(const u32x4 *)(p + k_off);
-                const u32x4 v = D == 64 ? u : *(const u32x4 *)(p + 16 + k_off);
+                const u32x4 u = __builtin_nontemporal_load((const u32x4 *)(p + k_off));
+                const u32x4 v = D == 64 ? u : __builtin_nontemporal_load((const u32x4 *)(p + 16 + k_off));
                 kf[i][s] = i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w,
                                  (int)v.x, (int)v.y, (int)v.z, (int)v.w};
             }
@@ -280,13 +261,13 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
             for (int e = 0; e < 4; e++) {
                 const uint8_t *p = vp + (16 * i + e) * D + v_off;
                 if (VW == 1) {
-                    vf[i][e][0] = *(const uint32_t *)p;
+                    vf[i][e][0] = __builtin_nontemporal_load((const uint32_t *)p);
                 } else if (VW == 2) {
-                    const u32x2 u = *(const u32x2 *)p;
+                    const u32x2 u = __builtin_nontemporal_load((const u32x2 *)p);
                     vf[i][e][0] = u.x;
                     vf[i][e][1] = u.y;
                 } else {
-                    const u32x4 u = *(const u32x4 *)p;
+                    const u32x4 u = __builtin_nontemporal_load((const u32x4 *)p);
                     vf[i][e][0] = u.x;
                     vf[i][e][1] = u.y;
                     vf[i][e][2 % VW] = u.z;

@@ -1,14 +1,19 @@
 // The projection of few tokens through 4-bit weights with a power-of-two
 // scale per 32 values: y[t][n] = bf16(sum_k x[t][k] * w[n][k]).
 //
-// One pass over the weights, as a stream: a workgroup owns 16*RT output rows
-// for up to 64 tokens, its four wavefronts take chunks of 512 k in turn and
-// their sums meet in LDS.  The weights are the matrix instructions' first
-// operand as they lie in memory (lane l: row l % 16, the 16 bytes of 32 values
-// from 32(l / 16) on, four rows' worth of 64 contiguous bytes an instruction).
-// e4m3 activations go in as codes beside their scales (the instruction applies
-// both scales per 32 values); for bf16 activations the weights are widened to
-// bf16 in registers, which holds a code times its power of two exactly.
+// One pass over the weights, laid out so that a whole CU's share is in flight
+// at once: a workgroup a CU owns 16*RT output rows for up to 64 tokens, its
+// eight wavefronts split K into equal runs of 256 values, load ahead of the
+// matrix instructions, and their sums meet in LDS.
+//
+// A matrix instruction wants neighbouring lanes in different rows, memory wants
+// them side by side (each row's 16 bytes is a lookup of its own: loaded that
+// way, 63 MB of weights took 25 us however many loads were in flight).  So
+// weights and activations are loaded as whole 128-byte lines, eight lanes a
+// row, and turned in the wavefront's own 4 KiB of LDS.  e4m3 activations go in
+// as codes beside their scales (the instruction applies both scales per 32
+// values); for bf16 activations the weights are widened to bf16 in registers,
+// which holds a code times its power of two exactly.
 #include "attention.h"
 
 namespace engram {
@@ -18,18 +23,10 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
-constexpr int kW4Waves = 4;
 constexpr int kW4Tokens = 64;       // tokens a workgroup takes
 constexpr int kFp4 = 4;             // the instruction's format numbers
 constexpr int kFp8 = 0;
-
-// A dword of scale bytes -> the float 2^(s - 127) of byte q.
-__device__ __forceinline__ float scale_f32(uint32_t bytes, int q)
-{
-    return __uint_as_float(((bytes >> (8 * q)) & 0xFFu) << 23);
-}
 
 // Eight e2m1 codes (a dword) times `scale` as eight bf16.
 __device__ __forceinline__ u32x4 widen8(uint32_t c, float scale)
@@ -41,34 +38,94 @@ __device__ __forceinline__ u32x4 widen8(uint32_t c, float scale)
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3))};
 }
 
+constexpr int kW4Waves = 8;
+
+// Registers for loads ahead, beside the sums: runs of 256 values whose weights
+// are loaded at once, and steps of 128 whose activations are.
+constexpr int regs_left(int rt, int mt) { return (mt == 1 ? 212 : rt * mt < 20 ? 196 : 166) - 4 * rt * mt; }
+constexpr int runs_ahead(bool fp8, int rt, int mt)
+{
+    const int u = regs_left(rt, mt) / (9 * rt + (fp8 ? 17 : 32) * mt);
+    return u < 1 ? 1 : u > 3 ? 3 : u;
+}
+constexpr int steps_ahead(bool fp8, int rt, int mt)
+{
+    return runs_ahead(fp8, rt, mt) > 1 || regs_left(rt, mt) >= 9 * rt + (fp8 ? 17 : 32) * mt
+               ? 2 * runs_ahead(fp8, rt, mt) : 1;
+}
+
+// Sixteen rows of 128 bytes, loaded eight lanes a row (a: rows 0-7, b: rows
+// 8-15), into pieces q and 4 + q of row l % 16 in lane l.  The 16-byte pieces
+// of a row are swapped by its number, so that eight lanes that write a row or
+// read eight rows meet all banks.  Only this wavefront touches `stage`, and its
+// LDS accesses execute in order.
+__device__ __forceinline__ void turn_rows(uint8_t *stage, int lane, u32x4 &a, u32x4 &b)
+{
+    const int r = lane >> 3, p = lane & 7, r16 = lane & 15, q = lane >> 4;
+    *(u32x4 *)(stage + 128 * r + 16 * (p ^ r)) = a;
+    *(u32x4 *)(stage + 128 * (8 + r) + 16 * (p ^ r)) = b;
+    a = *(const u32x4 *)(stage + 128 * r16 + 16 * (q ^ (r16 & 7)));
+    b = *(const u32x4 *)(stage + 128 * r16 + 16 * ((4 + q) ^ (r16 & 7)));
+}
+
+// Sixteen rows of 256 bytes, sixteen lanes a row (x[i]: rows 4i + l / 16), into
+// pieces 4q + i of row l % 16.
+__device__ __forceinline__ void turn_long_rows(uint8_t *stage, int lane, u32x4 (&x)[4])
+{
+    const int r16 = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = 4 * i + q;
+        *(u32x4 *)(stage + 256 * r + 16 * (r16 ^ (r & 7))) = x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        x[i] = *(const u32x4 *)(stage + 256 * r16 + 16 * ((4 * q + i) ^ (r16 & 7)));
+}
+
 template <bool FP8, int RT, int MT>
-__global__ __launch_bounds__(64 * kW4Waves, RT *MT > 8 ? 2 : 3) void w4_kernel(
+__global__ __launch_bounds__(64 * kW4Waves, 1) void w4_kernel(
     const uint8_t *__restrict__ x, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ w,
     const uint8_t *__restrict__ ws, uint16_t *__restrict__ y, int T, int K, int N)
 {
-    __shared__ f32x4 red[kW4Waves][RT][MT][64];
+    constexpr int W = kW4Waves, U = runs_ahead(FP8, RT, MT), XS = steps_ahead(FP8, RT, MT);
+    constexpr int XL = FP8 ? 2 : 4;                 // loads of a token tile's step
+    __shared__ __attribute__((aligned(16))) uint8_t stage_s[W][4096];
+    __shared__ f32x4 red[W / 2][RT][MT][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q = lane >> 4;
     const int n0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * kW4Tokens;
-    const int kg = K / 32;
+    const int kg = K / 32, kb = K / 2;
+    uint8_t *stage = stage_s[wv];
 
-    // rows past N read the last tile's (never stored), tokens past T the last token
-    const uint8_t *wrow[RT], *wsrow[RT];
+    // The weights are read through a buffer descriptor of the workgroup's own
+    // rows: what lies past its end (rows past N, values past K or the run's
+    // end) comes back as zeros, so no load hangs on a branch.
+    const int rows = min(16 * RT, N - n0);
+    const __amdgpu_buffer_rsrc_t wb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(w + (int64_t)n0 * kb), 0, rows * kb, 0x00027000);
+    const __amdgpu_buffer_rsrc_t wsb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(ws + (int64_t)n0 * kg), 0, rows * kg, 0x00027000);
+    constexpr uint32_t kPast = 0xFFFFFF00u;
+    constexpr int kStream = 2;                      // non-temporal
+    const int p = lane & 7;
+    const uint32_t w_off = (lane >> 3) * kb + 16 * p;
+    // scales: lane l loads four steps' bytes of row l / 4
+    const uint32_t ws_off = (lane >> 2) * kg;
+    // tokens past T read the last one (never stored)
+    const uint8_t *xt = x + (FP8 ? (int64_t)t0 * K : 2 * (int64_t)t0 * K);
+    const uint8_t *xst = FP8 ? xs + (int64_t)t0 * kg : nullptr;
+    uint32_t x_off[MT][XL], xs_off[MT];
 #pragma unroll
-    for (int i = 0; i < RT; i++) {
-        const int64_t n = min(n0 + 16 * i, N - 16) + r16;
-        wrow[i] = w + n * (K / 2) + 16 * q;
-        wsrow[i] = ws + n * kg;
-    }
-    const uint8_t *xrow[MT], *xsrow[MT];
+    for (int j = 0; j < MT; j++) {
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-        const int64_t t = min(t0 + 16 * i + r16, T - 1);
-        // e4m3: the operand's lane l holds values 16(l / 16) and 64 + 16(l / 16)
-        // on of a 128-value step; bf16: 32(l / 16) on, eight an instruction
-        xrow[i] = x + (FP8 ? t * K + 16 * q : 2 * (t * K + 32 * q));
-        xsrow[i] = FP8 ? xs + t * kg : nullptr;
+        for (int z = 0; z < XL; z++) {
+            const int r = FP8 ? 8 * z + (lane >> 3) : 4 * z + q;
+            const uint32_t t = min(t0 + 16 * j + r, T - 1) - t0;
+            x_off[j][z] = FP8 ? t * K + 16 * p : 2 * t * K + 16 * r16;
+        }
+        xs_off[j] = (min(t0 + 16 * j + r16, T - 1) - t0) * kg;
     }
     f32x4 acc[RT][MT];
 #pragma unroll
@@ -77,98 +134,123 @@ __global__ __launch_bounds__(64 * kW4Waves, RT *MT > 8 ? 2 : 3) void w4_kernel(
         for (int j = 0; j < MT; j++)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // one 128-value step from value k on
-    const auto step = [&](const u32x4 (&wr)[RT], const uint32_t (&wsc)[RT],
-                          const uint32_t (&xsc)[MT], int64_t k) {
-        if (FP8) {
+    const int steps = K / 128, runs = (steps + 1) / 2;
+    const int begin = (int)((int64_t)runs * wv / W), end = (int)((int64_t)runs * (wv + 1) / W);
+    u32x4 xr[XS][MT][XL];
+    uint32_t xsc[XS][MT];
+    const auto load_x = [&](int k0) {               // XS steps from step k0 on
+#pragma unroll
+        for (int u = 0; u < XS; u++) {
+            const int k = min(k0 + u, steps - 1);
 #pragma unroll
             for (int j = 0; j < MT; j++) {
-                const u32x4 a = *(const u32x4 *)(xrow[j] + k);
-                const u32x4 b = *(const u32x4 *)(xrow[j] + k + 64);
-                const i32x8 xf = {(int)a.x, (int)a.y, (int)a.z, (int)a.w,
-                                  (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 #pragma unroll
-                for (int i = 0; i < RT; i++) {
-                    const i32x8 wf = {(int)wr[i].x, (int)wr[i].y, (int)wr[i].z, (int)wr[i].w,
-                                      0, 0, 0, 0};
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        wf, xf, acc[i][j], kFp4, kFp8, 0, (int)(wsc[i] >> (8 * q)), 0,
-                        (int)(xsc[j] >> (8 * q)));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                u32x4 xf[MT];
-#pragma unroll
-                for (int j = 0; j < MT; j++)
-                    xf[j] = *(const u32x4 *)(xrow[j] + 2 * k + 16 * u);
-#pragma unroll
-                for (int i = 0; i < RT; i++) {
-                    const u32x4 wf = widen8(wr[i][u], scale_f32(wsc[i], q));
-#pragma unroll
-                    for (int j = 0; j < MT; j++)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, wf), __builtin_bit_cast(bf16x8, xf[j]),
-                            acc[i][j], 0, 0, 0);
-                }
+                for (int z = 0; z < XL; z++)
+                    xr[u][j][z] = *(const u32x4 *)(xt + (FP8 ? 128 : 256) * (int64_t)k + x_off[j][z]);
+                xsc[u][j] = FP8 ? *(const uint32_t *)(xst + 4 * k + xs_off[j]) : 0;
             }
         }
     };
-
-    const int chunks = K / 512;
-    for (int c = wv; c < chunks; c += kW4Waves) {
-        u32x4 wr[4][RT], wsc[RT], xsc[MT];
+    for (int k0 = begin; k0 < end; k0 += U) {
+        u32x4 wr[U][RT][2];
+        uint32_t wsc[(U + 1) / 2][RT];
 #pragma unroll
-        for (int i = 0; i < RT; i++) {
-#pragma unroll
-            for (int s = 0; s < 4; s++)
-                wr[s][i] = __builtin_nontemporal_load((const u32x4 *)(wrow[i] + 256 * c + 64 * s));
-            wsc[i] = *(const u32x4_a4 *)(wsrow[i] + 16 * c);
-        }
-#pragma unroll
-        for (int j = 0; j < MT; j++)
-            if (FP8)
-                xsc[j] = *(const u32x4_a4 *)(xsrow[j] + 16 * c);
-#pragma unroll
-        for (int s = 0; s < 4; s++) {
-            uint32_t a[RT], b[MT];
+        for (int u = 0; u < U; u++)
 #pragma unroll
             for (int i = 0; i < RT; i++)
-                a[i] = wsc[i][s];
 #pragma unroll
-            for (int j = 0; j < MT; j++)
-                b[j] = FP8 ? xsc[j][s] : 0;
-            step(wr[s], a, b, 512 * (int64_t)c + 128 * s);
+                for (int z = 0; z < 2; z++)
+                    wr[u][i][z] = __builtin_amdgcn_raw_buffer_load_b128(
+                        wb, k0 + u < end && 128 * (k0 + u) + 16 * p < kb
+                                ? w_off + (16 * i + 8 * z) * kb + 128 * (k0 + u) : kPast,
+                        0, kStream);
+#pragma unroll
+        for (int u = 0; u < (U + 1) / 2; u++)
+#pragma unroll
+            for (int i = 0; i < RT; i++) {
+                const int at = 8 * k0 + 16 * u + 4 * (lane & 3);
+                wsc[u][i] = __builtin_amdgcn_raw_buffer_load_b32(
+                    wsb, at < kg ? ws_off + 16 * i * kg + at : kPast, 0, 0);
+            }
+        if (XS > 1)
+            load_x(2 * k0);
+        // all loads are under way before the first is waited for
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+#pragma unroll
+            for (int i = 0; i < RT; i++)
+                turn_rows(stage, lane, wr[u][i][0], wr[u][i][1]);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {           // step 2(k0 + u) + h
+                if (XS == 1)
+                    load_x(2 * (k0 + u) + h);
+                const int xu = XS == 1 ? 0 : 2 * u + h;
+                uint32_t sc[RT];                    // of row l % 16, group l / 16
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+                    sc[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(
+                                4 * (4 * r16 + 2 * (u & 1) + h), (int)wsc[u / 2][i]) >> (8 * q);
+#pragma unroll
+                for (int j = 0; j < MT; j++) {
+                    if constexpr (FP8) {
+                        turn_rows(stage, lane, xr[xu][j][0], xr[xu][j][1]);
+                        const u32x4 a = xr[xu][j][0], b = xr[xu][j][1];
+                        const i32x8 xf = {(int)a.x, (int)a.y, (int)a.z, (int)a.w,
+                                          (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+#pragma unroll
+                        for (int i = 0; i < RT; i++) {
+                            const u32x4 c = wr[u][i][h];
+                            const i32x8 wf = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                wf, xf, acc[i][j], kFp4, kFp8, 0, (int)sc[i], 0,
+                                (int)(xsc[xu][j] >> (8 * q)));
+                        }
+                    } else {
+                        turn_long_rows(stage, lane, xr[xu][j]);
+                    }
+                }
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int i = 0; i < RT; i++)
+#pragma unroll
+                        for (int z = 0; z < 4; z++) {
+                            const u32x4 wf = widen8(wr[u][i][h][z],
+                                                    __uint_as_float((sc[i] & 0xFFu) << 23));
+#pragma unroll
+                            for (int j = 0; j < MT; j++)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8, wf),
+                                    __builtin_bit_cast(bf16x8, xr[xu][j][z]), acc[i][j], 0, 0, 0);
+                        }
+                }
+            }
         }
-    }
-    // the last K % 512: up to three steps, one a wavefront
-    for (int u = 4 * chunks + wv; u < K / 128; u += kW4Waves) {
-        u32x4 wr[RT];
-        uint32_t a[RT], b[MT];
-#pragma unroll
-        for (int i = 0; i < RT; i++) {
-            wr[i] = __builtin_nontemporal_load((const u32x4 *)(wrow[i] + 64 * u));
-            a[i] = *(const uint32_t *)(wsrow[i] + 4 * u);
-        }
-#pragma unroll
-        for (int j = 0; j < MT; j++)
-            b[j] = FP8 ? *(const uint32_t *)(xsrow[j] + 4 * u) : 0;
-        step(wr, a, b, 128 * (int64_t)u);
     }
 
+    // the wavefronts' sums, halved until four are left
 #pragma unroll
     for (int i = 0; i < RT; i++)
 #pragma unroll
         for (int j = 0; j < MT; j++)
-            red[wv][i][j][lane] = acc[i][j];
+            if (wv >= W / 2)
+                red[wv - W / 2][i][j][lane] = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int j = 0; j < MT; j++)
+            if (wv < W / 2) {
+                acc[i][j] += red[wv][i][j][lane];
+                red[wv][i][j][lane] = acc[i][j];
+            }
     __syncthreads();
     // accumulator e of lane l: output 16i + 4(l / 16) + e, token 16j + l % 16
-    for (int u = wv; u < RT * MT; u += kW4Waves) {
+    for (int u = wv; u < RT * MT; u += W) {
         const int i = u / MT, j = u - i * MT;
         f32x4 v = red[0][i][j][lane];
 #pragma unroll
-        for (int z = 1; z < kW4Waves; z++)
+        for (int z = 1; z < W / 2; z++)
             v += red[z][i][j][lane];
         const int t = t0 + 16 * j + r16, n = n0 + 16 * i + 4 * q;
         if (t < T && n < N) {
@@ -180,35 +262,45 @@ __global__ __launch_bounds__(64 * kW4Waves, RT *MT > 8 ? 2 : 3) void w4_kernel(
     }
 }
 
+struct Args {
+    const void *x;
+    const uint8_t *xs, *w, *ws;
+    uint16_t *y;
+    int64_t T, K, N;
+};
+
 template <bool FP8, int RT, int MT>
-void launch_one(const void *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws, uint16_t *y,
-                int64_t T, int64_t K, int64_t N, const Launch &l)
+void launch_one(const Args &a, const Launch &l)
 {
-    const dim3 grid((unsigned)((N / 16 + RT - 1) / RT),
-                    (unsigned)((T + kW4Tokens - 1) / kW4Tokens));
-    dispatch(w4_kernel<FP8, RT, MT>, grid, dim3(64 * kW4Waves), l, true, true, (const uint8_t *)x,
-             xs, w, ws, y, (int)T, (int)K, (int)N);
+    const dim3 grid((unsigned)((a.N / 16 + RT - 1) / RT),
+                    (unsigned)((a.T + kW4Tokens - 1) / kW4Tokens));
+    dispatch(w4_kernel<FP8, RT, MT>, grid, dim3(64 * kW4Waves), l, true, true, (const uint8_t *)a.x,
+             a.xs, a.w, a.ws, a.y, (int)a.T, (int)a.K, (int)a.N);
+}
+
+// Row tiles a workgroup: at most five (whose sums and loads fill the
+// registers), as many as give every CU the same number of workgroups.  Every
+// workgroup reads all its tokens' values, so fewer, wider ones are better.
+template <bool FP8, int MT>
+void launch_rows(const Args &a, const Launch &l)
+{
+    const int64_t tiles = a.N / 16, cus = device_cus();
+    const int64_t rounds = (tiles + 5 * cus - 1) / (5 * cus);
+    const int64_t rt = (tiles + rounds * cus - 1) / (rounds * cus);
+    rt <= 1   ? launch_one<FP8, 1, MT>(a, l)
+    : rt == 2 ? launch_one<FP8, 2, MT>(a, l)
+    : rt == 3 ? launch_one<FP8, 3, MT>(a, l)
+    : rt == 4 ? launch_one<FP8, 4, MT>(a, l)
+              : launch_one<FP8, 5, MT>(a, l);
 }
 
 template <bool FP8>
-void launch_tokens(const void *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws,
-                   uint16_t *y, int64_t T, int64_t K, int64_t N, const Launch &l)
+void launch_tokens(const Args &a, const Launch &l)
 {
-    // every workgroup reads all its tokens' values, so more rows a workgroup
-    // as the tokens grow, while there are enough row tiles to fill the chip
-    const bool wide = N / 16 >= 2 * (int64_t)device_cus();
-    if (T <= 16)
-        wide ? launch_one<FP8, 2, 1>(x, xs, w, ws, y, T, K, N, l)
-             : launch_one<FP8, 1, 1>(x, xs, w, ws, y, T, K, N, l);
-    else if (T <= 32)
-        wide ? launch_one<FP8, 2, 2>(x, xs, w, ws, y, T, K, N, l)
-             : launch_one<FP8, 1, 2>(x, xs, w, ws, y, T, K, N, l);
-    else if (T <= 48)
-        wide ? launch_one<FP8, 4, 3>(x, xs, w, ws, y, T, K, N, l)
-             : launch_one<FP8, 1, 3>(x, xs, w, ws, y, T, K, N, l);
-    else
-        wide ? launch_one<FP8, 4, 4>(x, xs, w, ws, y, T, K, N, l)
-             : launch_one<FP8, 1, 4>(x, xs, w, ws, y, T, K, N, l);
+    a.T <= 16   ? launch_rows<FP8, 1>(a, l)
+    : a.T <= 32 ? launch_rows<FP8, 2>(a, l)
+    : a.T <= 48 ? launch_rows<FP8, 3>(a, l)
+                : launch_rows<FP8, 4>(a, l);
 }
 
 }  // namespace
@@ -216,10 +308,11 @@ void launch_tokens(const void *x, const uint8_t *xs, const uint8_t *w, const uin
 int32_t launch_w4(const void *x, const uint8_t *xs, const uint8_t *w, const uint8_t *ws,
                   uint16_t *y, int64_t T, int64_t K, int64_t N, const Launch &l)
 {
+    const Args a{x, xs, w, ws, y, T, K, N};
     if (xs)
-        launch_tokens<true>(x, xs, w, ws, y, T, K, N, l);
+        launch_tokens<true>(a, l);
     else
-        launch_tokens<false>(x, xs, w, ws, y, T, K, N, l);
+        launch_tokens<false>(a, l);
     return launch_status("engram w4 kernel");
 }
 
