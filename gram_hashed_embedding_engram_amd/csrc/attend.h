@@ -7,7 +7,6 @@
 namespace engram {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -17,39 +16,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // E8M0 scale of a query's second part, which is held 2^4 times larger: the
 // residual of e4m3's four bits is at most 2^-4 of the value.
 constexpr int kOne = 127, kLoScale = 127 - 4;
-
-__device__ __forceinline__ uint32_t cvt_bf16x2(float a, float b)
-{
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, b2));
-}
-
-// max / sum over lanes l and l ^ 32 (both get it)
-__device__ __forceinline__ float max_x32(float v)
-{
-    const uint32_t u = __float_as_uint(v);
-    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float add_x32(float v)
-{
-    const uint32_t u = __float_as_uint(v);
-    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-// max / sum over lanes l, l ^ 16, l ^ 32, l ^ 48
-__device__ __forceinline__ float max_x16(float v)
-{
-    const uint32_t u = __float_as_uint(v);
-    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    return max_x32(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
-}
-__device__ __forceinline__ float add_x16(float v)
-{
-    const uint32_t u = __float_as_uint(v);
-    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    return add_x32(__uint_as_float(r[0]) + __uint_as_float(r[1]));
-}
 
 // Thirty-two bf16 query values as two e4m3 parts, q = 2^k (hi + lo / 16):
 // bf16 has eight significant bits and each part four, so the sum is exact

@@ -41,11 +41,47 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 
+// Two f32 -> two bf16, first in the low half (the hardware's rounding, to
+// nearest even; NaN stays NaN).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t cvt_bf16x2(float a, float b)
+{
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, b2));
+}
+
 // Byte I of a dword of e4m3 codes as f32.
 template <int I>
 __device__ __forceinline__ float e4m3_at(uint32_t w)
 {
     return __builtin_amdgcn_cvt_f32_fp8((int)w, I);
+}
+
+// max / sum over lanes l and l ^ 32 (both get it)
+__device__ __forceinline__ float max_x32(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_x32(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// max / sum over lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float max_x16(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return max_x32(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float add_x16(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return add_x32(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 // The sequences of a step, as the kernels see them: T tokens, `each` tokens a

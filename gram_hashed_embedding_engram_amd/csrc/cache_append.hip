@@ -1,21 +1,26 @@
 // The position rotation of a step's queries and keys, and the append of its
 // keys and values to the paged 8-bit cache.
 //
-// One launch with two kinds of workgroup: the keys or the values of one page
-// and head, or a run of tokens' queries.  Bound by memory: a key or value is
+// One launch with two kinds of workgroup: the keys or the values of one page,
+// of one or several heads in turn, or a run of tokens' queries.  Bound by memory: a key or value is
 // read once as bf16 and written once as a code, and stays in registers between
-// the page's maximum and the codes; a query's angles are formed once a token.
+// the page's maximum and the codes.  Angles, whose 64-bit reduction and series
+// are most of the arithmetic, are formed once a workgroup and token and wait in
+// LDS.
 #include "attention.h"
 
 namespace engram {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads a workgroup: twice as many where a page's angles take 64 KiB of LDS.
+template <int D>
+constexpr int threads_of = D == 256 ? 512 : 256;
 
 // cos and sin of a 64-bit angle, rounded to f32.  The angle less the nearest
 // multiple n of pi/2 (pi/2 as the sum of two doubles, so the remainder keeps
-// an absolute error below 2^-60 n), then the Taylor series to x^13 and x^14
-// on [-pi/4, pi/4] (next term below 2^-44), swapped and signed by n mod 4.
+// an absolute error below 2^-60 n), then the Taylor series to x^11 and x^10
+// on [-pi/4, pi/4] (next terms below 2^-33, far under f32's half step),
+// swapped and signed by n mod 4.
 struct Turn {
     float c, s;
 };
@@ -25,11 +30,8 @@ __device__ __forceinline__ Turn turn_of(int pos, float freq)
     const double n = rint(a * 0.63661977236758134308);
     const double x = fma(-n, 6.123233995736766036e-17, fma(-n, 1.57079632679489661923, a));
     const double z = x * x;
-    double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
-    s = fma(s, z, -1.0 / 39916800.0);
-    c = fma(c, z, 1.0 / 479001600.0);
+    double s = -1.0 / 39916800.0, c = -1.0 / 3628800.0;
     s = fma(s, z, 1.0 / 362880.0);
-    c = fma(c, z, -1.0 / 3628800.0);
     s = fma(s, z, -1.0 / 5040.0);
     c = fma(c, z, 1.0 / 40320.0);
     s = fma(s, z, 1.0 / 120.0);
@@ -69,33 +71,84 @@ __device__ __forceinline__ Place place_of(int e, const Rotation &r)
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// A thread's values, as one access where they lie side by side for all.
+template <bool HALVES>
 __device__ __forceinline__ void load8(const uint16_t *p, const Place &at, float (&v)[8])
 {
-    const u32x2 a = *(const u32x2 *)(p + at.i0), b = *(const u32x2 *)(p + at.i1);
-    v[0] = bf16_lo(a.x);
-    v[1] = bf16_hi(a.x);
-    v[2] = bf16_lo(a.y);
-    v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(b.x);
-    v[5] = bf16_hi(b.x);
-    v[6] = bf16_lo(b.y);
-    v[7] = bf16_hi(b.y);
+    u32x4 x;
+    if (HALVES) {
+        const u32x2 a = *(const u32x2 *)(p + at.i0), b = *(const u32x2 *)(p + at.i1);
+        x = u32x4{a.x, a.y, b.x, b.y};
+    } else {
+        x = *(const u32x4 *)(p + at.i0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[2 * i] = bf16_lo(x[i]);
+        v[2 * i + 1] = bf16_hi(x[i]);
+    }
 }
 
-__device__ __forceinline__ void turn8(float (&v)[8], const Place &at, bool halves, const Turn (&t)[4])
+template <bool HALVES>
+__device__ __forceinline__ void store8(uint16_t *p, const Place &at, const float (&v)[8])
 {
-    if (at.pair < 0)
-        return;
+    const u32x2 a = {cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+    const u32x2 b = {cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
+    if (HALVES) {
+        *(u32x2 *)(p + at.i0) = a;
+        *(u32x2 *)(p + at.i1) = b;
+    } else {
+        *(u32x4 *)(p + at.i0) = u32x4{a.x, a.y, b.x, b.y};
+    }
+}
+
+template <bool HALVES>
+__device__ __forceinline__ void store8_codes(uint8_t *p, const Place &at, const float (&v)[8], float f)
+{
+    const uint32_t a = e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+    const uint32_t b = e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);
+    if (HALVES) {
+        *(uint32_t *)(p + at.i0) = a;
+        *(uint32_t *)(p + at.i1) = b;
+    } else {
+        *(u32x2 *)(p + at.i0) = u32x2{a, b};
+    }
+}
+
+// The values' four pairs by t[0..3].
+__device__ __forceinline__ void turn8(float (&v)[8], bool halves, const Turn *t)
+{
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         float &a = v[halves ? i : 2 * i], &b = v[halves ? 4 + i : 2 * i + 1];
-        const float x = a, y = b;
-        a = x * t[i].c - y * t[i].s;
-        b = x * t[i].s + y * t[i].c;
+        const float x = a, y = b, c = t[i].c, s = t[i].s;
+        a = x * c - y * s;
+        b = x * s + y * c;
+    }
+}
+
+// f(t, p) for tokens t < n and pairs p < half, shared out over the threads (one
+// division a thread).
+template <int THREADS, class F>
+__device__ __forceinline__ void each_turn(int half, int n, F f)
+{
+    if (half == 0)
+        return;
+    const int dt = THREADS / half, dp = THREADS - dt * half;
+    int t = threadIdx.x / half, p = threadIdx.x - t * half;
+    while (t < n) {
+        f(t, p);
+        t += dt;
+        p += dp;
+        if (p >= half) {
+            p -= half;
+            t++;
+        }
     }
 }
 
 constexpr int kRunTokens = 8;       // tokens a queries' workgroup takes at most
+constexpr int kRunHeads = 8;        // heads a page's workgroup takes at most
 
 struct AppendArgs {
     engram_cache c;
@@ -103,108 +156,115 @@ struct AppendArgs {
     Heads k, v, q;
     uint16_t *q_out;
     Rotation r;
-    int32_t q_heads, pieces;    // grid: keys and values of `pieces` x kv_heads pages,
-    int32_t run;                // then queries, `run` tokens a workgroup
+    int32_t q_heads, pieces;    // grid: keys and values of `pieces` pages, `heads` heads a
+    int32_t run, heads;         // workgroup, then queries, `run` tokens a workgroup
 };
 
-// The keys (z 0) or values (z 1) of one page and key head.
+// The keys (z 0) or values (z 1) of heads h0 .. h1-1 of one page.
 template <int D, bool HALVES>
 __device__ __forceinline__ void append_page(const AppendArgs &a, const Seq &q, int blk,
-                                            int32_t page, int h, bool z)
+                                            int32_t page, int h0, int h1, bool z,
+                                            Turn (*turns)[D / 2])
 {
+    constexpr int kThreads = threads_of<D>;
     constexpr int E = D / 8;                    // threads a token
     constexpr int TOK = kThreads / E;           // tokens at a time
     constexpr int N = kPage / TOK;
-    __shared__ float part[kThreads / 64];
+    __shared__ float part[2][kThreads / 64];
     const int tid = threadIdx.x, e = tid % E, g = tid / E;
     const int page0 = blk * kPage;
     const int older = max(q.start - page0, 0);
     const int last = min(q.start + q.n - page0, kPage);
-    const int64_t at = (int64_t)page * a.c.kv_heads + h;
     const Heads &src = z ? a.v : a.k;
-    uint8_t *codes = (z ? a.c.d_v : a.c.d_k) + at * kPage * D;
-    float *scale = (z ? a.c.d_v_scales : a.c.d_k_scales) + at;
     Rotation r = a.r;
     r.halves = HALVES;
     if (z)
         r.rot = 0;
     const Place pl = place_of<D>(e, r);
-    float v[N][8];
-    float amax = 0.0f;
+    const uint16_t *row[N];
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int slot = g + TOK * i;
-        if (slot >= older && slot < last) {
-            const int pos = page0 + slot;
-            load8(src.p + (q.t0 + (int64_t)(pos - q.start)) * src.token + h * src.head, pl, v[i]);
-        }
+    for (int i = 0; i < N; i++)
+        row[i] = src.p + (q.t0 + (int64_t)(page0 + g + TOK * i - q.start)) * src.token;
+    const int half = r.rot / 2;
+    if (half) {
+        each_turn<kThreads>(half, last - older, [&](int t, int p) {
+            turns[older + t][p] = turn_of(page0 + older + t, r.freq[p]);
+        });
+        __syncthreads();
     }
+    for (int h = h0; h < h1; h++) {
+        const int64_t at = (int64_t)page * a.c.kv_heads + h;
+        uint8_t *codes = (z ? a.c.d_v : a.c.d_k) + at * kPage * D;
+        float *scale = (z ? a.c.d_v_scales : a.c.d_k_scales) + at;
+        const float had = older > 0 ? *scale : 0.0f;
+        float v[N][8];
+        float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int slot = g + TOK * i;
-        if (slot >= older && slot < last) {
-            if (!z && pl.pair >= 0) {
-                Turn t[4];
+        for (int i = 0; i < N; i++) {
+            const int slot = g + TOK * i;
+            if (slot >= older && slot < last)
+                load8<HALVES>(row[i] + h * src.head, pl, v[i]);
+        }
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    t[j] = turn_of(page0 + slot, r.freq[pl.pair + j]);
-                turn8(v[i], pl, HALVES, t);
+        for (int i = 0; i < N; i++) {
+            const int slot = g + TOK * i;
+            if (slot >= older && slot < last) {
+                if (pl.pair >= 0)
+                    turn8(v[i], HALVES, &turns[slot][pl.pair]);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    amax = fmaxf(amax, finite_abs(v[i][j]));
             }
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                amax = fmaxf(amax, finite_abs(v[i][j]));
         }
-    }
+        amax = max_x16(amax);
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        amax = fmaxf(amax, __shfl_xor(amax, m));
-    if ((tid & 63) == 0)
-        part[tid >> 6] = amax;
-    const float had = older > 0 ? *scale : 0.0f;
-    __syncthreads();
+        for (int m = 1; m < 16; m <<= 1)
+            amax = fmaxf(amax, __shfl_xor(amax, m));
+        if ((tid & 63) == 0)
+            part[h & 1][tid >> 6] = amax;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; i++)
-        amax = fmaxf(amax, part[i]);
-    const float need = exp2_int(e4m3_scale_exp(amax));
-    const float now = fmaxf(had, need);
-    if (now != had) {                       // (never where the page is new)
-        const float ratio = had / now;
-        for (int i = tid; i < older * (D / 4); i += kThreads) {
-            uint32_t *p = (uint32_t *)codes + i;
-            const uint32_t x = *p;
-            *p = e4m3x4(e4m3_at<0>(x) * ratio, e4m3_at<1>(x) * ratio, e4m3_at<2>(x) * ratio,
-                        e4m3_at<3>(x) * ratio);
+        for (int i = 0; i < kThreads / 64; i++)
+            amax = fmaxf(amax, part[h & 1][i]);
+        const float now = fmaxf(had, exp2_int(e4m3_scale_exp(amax)));
+        if (now != had) {                       // (never where the page is new)
+            const float ratio = had / now;
+            for (int i = tid; i < older * (D / 4); i += kThreads) {
+                uint32_t *p = (uint32_t *)codes + i;
+                const uint32_t x = *p;
+                *p = e4m3x4(e4m3_at<0>(x) * ratio, e4m3_at<1>(x) * ratio, e4m3_at<2>(x) * ratio,
+                            e4m3_at<3>(x) * ratio);
+            }
         }
-    }
-    const float inv = 1.0f / now;
+        const float inv = 1.0f / now;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int slot = g + TOK * i;
-        if (slot >= older && slot < last) {
-            uint8_t *p = codes + slot * D;
-            *(uint32_t *)(p + pl.i0) = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-            *(uint32_t *)(p + pl.i1) = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+        for (int i = 0; i < N; i++) {
+            const int slot = g + TOK * i;
+            if (slot >= older && slot < last)
+                store8_codes<HALVES>(codes + slot * D, pl, v[i], inv);
         }
+        if (tid == 0)                           // all have read it before the barrier
+            *scale = now;
     }
-    if (tid == 0)                           // all have read it before the barrier
-        *scale = now;
 }
 
 template <int D, bool HALVES>
-__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
+__global__ __launch_bounds__(threads_of<D>) void append_kernel(AppendArgs a)
 {
+    constexpr int kThreads = threads_of<D>;
     __shared__ int tok_s[kRunTokens], pos_s[kRunTokens];
-    __shared__ Turn turn_s[kRunTokens][D / 2];
+    __shared__ Turn turn_s[kPage][D / 2];
     const int tid = threadIdx.x;
-    const int pages = 2 * a.pieces * a.c.kv_heads;
+    const int groups = (a.c.kv_heads + a.heads - 1) / a.heads;
+    const int pages = 2 * a.pieces * groups;
     if (blockIdx.x == 0)
         for (int i = tid; i < a.s.B; i += kThreads)
             if (seq_at(a.s, i).bad)
                 raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
     if ((int)blockIdx.x < pages) {
         const bool z = blockIdx.x & 1;
-        const int h = blockIdx.x / 2 % a.c.kv_heads;
-        int i = blockIdx.x / 2 / a.c.kv_heads, b, piece;
+        const int h = blockIdx.x / 2 % groups * a.heads;
+        int i = blockIdx.x / 2 / groups, b, piece;
         const auto touched = [&](int x) {
             const Seq q = seq_at(a.s, x);
             return q.bad || q.n == 0 ? 0 : (q.start + q.n - 1) / kPage - q.start / kPage + 1;
@@ -226,7 +286,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
                 raise(a.s.err, ENGRAM_DEVERR_PAGE);
             return;
         }
-        append_page<D, HALVES>(a, q, blk, page, h, z);
+        append_page<D, HALVES>(a, q, blk, page, h, min(h + a.heads, a.c.kv_heads), z, turn_s);
         return;
     }
     // queries: where the run's tokens lie, their angles, then eight values a thread
@@ -253,12 +313,13 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
         }
     }
     __syncthreads();
-    for (int i = tid; i < a.run * (a.r.rot / 2); i += kThreads) {
-        const int t = i / (a.r.rot / 2), p = i % (a.r.rot / 2);
+    const int half = a.r.rot / 2;
+    each_turn<kThreads>(half, a.run, [&](int t, int p) {
         if (tok_s[t] >= 0)
             turn_s[t][p] = turn_of(pos_s[t], a.r.freq[p]);
-    }
+    });
     __syncthreads();
+    const float per_head = 1.0f / (float)a.q_heads;
     constexpr int E = D / 8, ROWS = kThreads / E, AT_ONCE = 4;
     const int e = tid % E;
     Rotation r = a.r;
@@ -270,31 +331,20 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a)
 #pragma unroll
         for (int i = 0; i < AT_ONCE; i++) {
             const int row = row0 + ROWS * i;
-            run[i] = row / a.q_heads;
+            run[i] = (int)(((float)row + 0.5f) * per_head);      // row / q_heads, both below 2^14
             head[i] = row - run[i] * a.q_heads;
             tok[i] = row < a.run * a.q_heads ? tok_s[run[i]] : -1;
             if (tok[i] >= 0)
-                load8(a.q.p + (int64_t)tok[i] * a.q.token + head[i] * a.q.head, pl, v[i]);
+                load8<HALVES>(a.q.p + (int64_t)tok[i] * a.q.token + head[i] * a.q.head, pl, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; i++) {
             if (tok[i] < 0)
                 continue;
-            if (pl.pair >= 0) {
-                Turn t[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    t[j] = turn_s[run[i]][pl.pair + j];
-                turn8(v[i], pl, HALVES, t);
-            }
+            if (pl.pair >= 0)
+                turn8(v[i], HALVES, &turn_s[run[i]][pl.pair]);
             uint16_t *o = a.q_out + ((int64_t)tok[i] * a.q_heads + head[i]) * D;
-            u32x2 lo, hi;
-            lo.x = pack_bf16x2(v[i][0], v[i][1]);
-            lo.y = pack_bf16x2(v[i][2], v[i][3]);
-            hi.x = pack_bf16x2(v[i][4], v[i][5]);
-            hi.y = pack_bf16x2(v[i][6], v[i][7]);
-            *(u32x2 *)(o + pl.i0) = lo;
-            *(u32x2 *)(o + pl.i1) = hi;
+            store8<HALVES>(o, pl, v[i]);
         }
     }
 }
@@ -303,7 +353,8 @@ template <int D>
 void launch_dim(const AppendArgs &a, const Launch &l)
 {
     const unsigned runs = a.q_heads ? (a.s.T + a.run - 1) / a.run : 0;
-    const dim3 grid(2u * a.pieces * a.c.kv_heads + runs), block(kThreads);
+    const unsigned groups = (a.c.kv_heads + a.heads - 1) / a.heads;
+    const dim3 grid(2u * a.pieces * groups + runs), block(threads_of<D>);
     if (a.r.halves)
         dispatch(append_kernel<D, true>, grid, block, l, true, true, a);
     else
@@ -325,7 +376,8 @@ int32_t launch_append(const engram_cache &c, const Seqs &s, const Heads &k, cons
     // several tokens a workgroup once there are enough of them
     const int64_t run = s.T / (4 * device_cus());
     const AppendArgs a{c, s, k, v, q, q_out, r, q_heads, (int32_t)pieces,
-                       (int32_t)(run < 1 ? 1 : run > kRunTokens ? kRunTokens : run)};
+                       (int32_t)(run < 1 ? 1 : run > kRunTokens ? kRunTokens : run),
+                       run < 2 ? 1 : kRunHeads};
     if (c.head_dim == 64)
         launch_dim<64>(a, l);
     else if (c.head_dim == 128)

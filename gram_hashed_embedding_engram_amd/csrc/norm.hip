@@ -59,7 +59,7 @@ __global__ __launch_bounds__(THREADS) void add_norm_kernel(
                 u32x4 o;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    o[j] = pack_bf16x2(s[2 * j], s[2 * j + 1]);
+                    o[j] = cvt_bf16x2(s[2 * j], s[2 * j + 1]);
                     s[2 * j] = bf16_lo(o[j]);          // the norm is that of the sum as kept
                     s[2 * j + 1] = bf16_hi(o[j]);
                 }

@@ -255,8 +255,8 @@ __global__ __launch_bounds__(64 * kW4Waves, 1) void w4_kernel(
         const int t = t0 + 16 * j + r16, n = n0 + 16 * i + 4 * q;
         if (t < T && n < N) {
             u32x2 o;
-            o.x = pack_bf16x2(v.x, v.y);
-            o.y = pack_bf16x2(v.z, v.w);
+            o.x = cvt_bf16x2(v.x, v.y);
+            o.y = cvt_bf16x2(v.z, v.w);
             *(u32x2 *)(y + (int64_t)t * N + n) = o;
         }
     }
