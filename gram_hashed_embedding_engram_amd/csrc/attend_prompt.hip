@@ -6,6 +6,7 @@ namespace engram {
 namespace {
 
 constexpr int kTileWaves = 4;
+constexpr float kSlack = 8.0f;
 constexpr int kTileRows = 32 * kTileWaves;
 
 // 16-byte chunk of a staged row, moved so that eight lanes reading (or
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     constexpr int VL = D / 128 > 0 ? D / 128 : 1; // 8-token x 4-value blocks of values
     __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][KB];
     __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][VB];
-    __shared__ int poison_s[2];       // the staged page that holds a noted NaN
+    __shared__ int poison_s;          // some page held a NaN that only some rows see
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r32 = lane & 31, h = lane >> 5;
@@ -92,10 +93,11 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
             amax = fmaxf(amax, amax_bf16(x[s]));
         }
         const int k = e4m3_scale_exp(max_x32(amax));
-        qs = exp2_int(k) * a.scale;
+        qs = exp2_int(k) * fabsf(a.scale);
+        const float inv = a.scale < 0.0f ? -exp2_int(-k) : exp2_int(-k);
 #pragma unroll
         for (int s = 0; s < KS; s++)
-            split_query(x[s], exp2_int(-k), qh[s], ql[s]);
+            split_query(x[s], inv, qh[s], ql[s]);
     }
 
     float m = -INFINITY, l = 0.0f;
@@ -128,9 +130,14 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                 for (int e = 0; e < 8; e++)
                     vr[i][e] = *(const uint32_t *)(vp + (uint32_t)(v_token(i, e) * D + 4 * quad));
     };
-    // blk: the page's place in the sequence; edge: some row of the workgroup
-    // does not see it whole (what no row sees is zeroed; a NaN that only some
-    // see is zeroed and noted)
+    // whether some row of the workgroup does not see page blk whole
+    const auto cut = [&](int blk) {
+        return blk * kPage + kPage - 1 > pos_lo ||
+               (a.window > 0 && blk * kPage < pos_hi - a.window + 1);
+    };
+    // Stages page blk of the sequence.  Of a cut page, values that no row sees
+    // are zeroed (0 * NaN is NaN), and a NaN that only some rows see is zeroed
+    // and noted: those rows get it at the end.
     const auto stage = [&](int buf, int blk) {
 #pragma unroll
         for (int i = 0; i < KL; i++) {
@@ -139,9 +146,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
         }
         if (!v_on)
             return;
-        const bool edge = blk * kPage + kPage - 1 > pos_lo ||
-                          (a.window > 0 && blk * kPage < max(pos_hi - a.window + 1, 0));
-        if (edge) {
+        if (cut(blk)) {
             uint32_t any = 0;
 #pragma unroll
             for (int i = 0; i < VL; i++)
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                     vr[i][e] = x & ~nan;
                 }
             if (any)
-                poison_s[buf] = blk;
+                poison_s = 1;
         }
 #pragma unroll
         for (int i = 0; i < VL; i++) {
@@ -194,8 +199,8 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     };
 
     int page = 0, blk = seek(first, page), buf = 0;
-    if (tid < 2)
-        poison_s[tid] = -1;
+    if (tid == 0)
+        poison_s = 0;
     __syncthreads();
     if (blk < last) {
         fetch(page);
@@ -205,6 +210,11 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     while (blk < last) {
         const int64_t at = (int64_t)page * kv + head;
         const float ks = a.c.d_k_scales[at], vs = a.c.d_v_scales[at];
+        const bool plain = vs >= 0x1p-100f && vs <= 0x1p100f;
+        const int v_bits = (int)(__float_as_uint(vs) >> 23) - 127;
+        const float v_exp = plain ? (float)v_bits : 0.0f;
+        const float v_inv = plain ? exp2_int(-v_bits) : 1.0f;
+        const float v_rest = plain ? vs * v_inv : vs;
         int next_page = 0;
         const int next = seek(blk + 1, next_page);
         if (next < last)
@@ -230,6 +240,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                     s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[u], s[t], 0, 0, 0, kOne, 0, kLoScale);
                 }
             }
+            // logits are s * f, f >= 0 (the scale's sign went into the queries)
             const float f = qs * ks;
             const bool edge = base + kPage - 1 > my_lo || base < my_all;
             if (edge) {
@@ -238,14 +249,8 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
 #pragma unroll
                     for (int e = 0; e < 16; e++) {
                         const int p = base + 32 * t + 8 * (e / 4) + 4 * h + e % 4;
-                        s[t][e] = p <= pos && p >= lo ? s[t][e] * f : -INFINITY;
+                        s[t][e] = p <= pos && p >= lo ? s[t][e] : -INFINITY;
                     }
-            } else {
-#pragma unroll
-                for (int t = 0; t < 2; t++)
-#pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        s[t][e] *= f;
             }
             float top = -INFINITY;
 #pragma unroll
@@ -253,31 +258,51 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
 #pragma unroll
                 for (int e = 0; e < 16; e++)
                     top = fmaxf(top, s[t][e]);
-            top = fmaxf(max_x32(top), m);
-            const float zero = top == -INFINITY ? 0.0f : top;
-            if (__any(top != m)) {
-                const float keep = __builtin_amdgcn_exp2f(m - zero);
-                m = top;
+            top = max_x32(top);
+            top = top == -INFINITY ? top : top * f;
+            // the base m follows the maximum once that is 2^8 past it: sums and
+            // probabilities stay far inside f32's and bf16's range
+            if (__any(top > m + kSlack)) {
+                const float now = fmaxf(m, top);
+                const float keep = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+                m = now;
                 l *= keep;
 #pragma unroll
                 for (int i = 0; i < DT; i++)
                     o[i] *= keep;
             }
+            // probabilities times the page's value scale: its power of two
+            // joins the exponent, what is left (1 but for scales that
+            // cache_append does not write) multiplies
+            const float zero = (m == -INFINITY ? 0.0f : m) - v_exp;
+            float sum = 0.0f;
             u32x4 pb[4];
+            if (!edge && v_rest == 1.0f) {
 #pragma unroll
-            for (int t = 0; t < 2; t++)
+                for (int t = 0; t < 2; t++)
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float p0 = __builtin_amdgcn_exp2f(s[t][e] - zero);
-                    const float p1 = __builtin_amdgcn_exp2f(s[t][e + 1] - zero);
-                    l += p0 + p1;
-                    float v0 = p0 * vs, v1 = p1 * vs;
-                    if (edge) {
-                        v0 = s[t][e] == -INFINITY ? 0.0f : v0;
-                        v1 = s[t][e + 1] == -INFINITY ? 0.0f : v1;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e], f, -zero));
+                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e + 1], f, -zero));
+                        sum += p0 + p1;
+                        pb[2 * t + e / 8][(e % 8) / 2] = cvt_bf16x2(p0, p1);
                     }
-                    pb[2 * t + e / 8][(e % 8) / 2] = cvt_bf16x2(v0, v1);
-                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e], f, -zero));
+                        float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e + 1], f, -zero));
+                        p0 = s[t][e] == -INFINITY ? 0.0f : p0;
+                        p1 = s[t][e + 1] == -INFINITY ? 0.0f : p1;
+                        sum += p0 + p1;
+                        p0 = s[t][e] == -INFINITY ? 0.0f : p0 * v_rest;
+                        p1 = s[t][e + 1] == -INFINITY ? 0.0f : p1 * v_rest;
+                        pb[2 * t + e / 8][(e % 8) / 2] = cvt_bf16x2(p0, p1);
+                    }
+            }
+            l += sum * v_inv;
             // ---- values
 #pragma unroll
             for (int i = 0; i < DT; i++)
@@ -288,52 +313,6 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                     o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
                                                                    __builtin_bit_cast(bf16x8, pb[c]), o[i], 0, 0, 0);
                 }
-            if (poison_s[buf] == blk) {
-                // how many NaN codes each row sees, by the same product
-#pragma unroll
-                for (int t = 0; t < 2; t++)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const int p = base + 32 * t + 8 * (e / 4) + 4 * h + e % 4;
-                        pb[2 * t + e / 8][(e % 8) / 2] =
-                            cvt_bf16x2(p <= pos && p >= lo ? 1.0f : 0.0f,
-                                       p + 1 <= pos && p + 1 >= lo ? 1.0f : 0.0f);
-                    }
-                const uint8_t *vp = a.c.d_v + at * KB;
-#pragma unroll 1
-                for (int c = 0; c < 4; c++)
-#pragma unroll
-                    for (int i = 0; i < DT; i++) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const int p = 16 * c + 4 * h + (2 * e & 3) + 8 * (e >> 1);
-                            x[e] = 0;
-#pragma unroll
-                            for (int z = 0; z < 2; z++)
-                                if (base + p + z <= pos_hi && base + p + z >= see_lo &&
-                                    (vp[(p + z) * D + 32 * i + r32] & 0x7F) == 0x7F)
-                                    x[e] |= 0x3F80u << (16 * z);
-                        }
-                        u32x4 pc = pb[0];
-                        if (c == 1)
-                            pc = pb[1];
-                        if (c == 2)
-                            pc = pb[2];
-                        if (c == 3)
-                            pc = pb[3];
-                        f32x16 n;
-#pragma unroll
-                        for (int e = 0; e < 16; e++)
-                            n[e] = 0.0f;
-                        n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(bf16x8, (u32x4){x[0], x[1], x[2], x[3]}),
-                            __builtin_bit_cast(bf16x8, pc), n, 0, 0, 0);
-#pragma unroll
-                        for (int e = 0; e < 16; e++)
-                            o[i][e] = n[e] > 0.0f ? __uint_as_float(0x7FC00000u) : o[i][e];
-                    }
-            }
         }
         if (next < last) {
             stage(buf ^ 1, next);       // its last readers passed the previous barrier
@@ -344,6 +323,46 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
         page = next_page;
     }
 
+    if (poison_s) {
+        // how many NaN codes of the cut pages each row sees, by the values'
+        // product with ones for both
+        for (int i = first; i < last; i++) {
+            const int32_t id = __builtin_amdgcn_readfirstlane(table[i]);
+            if (!cut(i) || id < 0 || id >= a.c.n_pages)
+                continue;
+            const uint8_t *vp = a.c.d_v + ((int64_t)id * kv + head) * KB;
+            for (int c = 0; c < 4; c++) {
+                const int t0 = i * kPage + 16 * c + 4 * h;
+                u32x4 see;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int p = t0 + (2 * e & 3) + 8 * (e >> 1);
+                    see[e] = cvt_bf16x2(p <= pos && p >= lo ? 1.0f : 0.0f,
+                                        p + 1 <= pos && p + 1 >= lo ? 1.0f : 0.0f);
+                }
+#pragma unroll
+                for (int d = 0; d < DT; d++) {
+                    u32x4 nan = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int p = t0 + (e & 3) + 8 * (e >> 2);
+                        if (p <= pos_hi && p >= see_lo &&
+                            (vp[(p - i * kPage) * D + 32 * d + r32] & 0x7F) == 0x7F)
+                            nan[e / 2] |= 0x3F80u << (16 * (e & 1));
+                    }
+                    f32x16 n;
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        n[e] = 0.0f;
+                    n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, nan), __builtin_bit_cast(bf16x8, see), n, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        o[d][e] = n[e] > 0.0f ? __uint_as_float(0x7FC00000u) : o[d][e];
+                }
+            }
+        }
+    }
     l = add_x32(l);
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     if (!valid)
