@@ -1,12 +1,13 @@
 // Attention over the paged 8-bit cache for many rows a sequence (prompt
 // chunks): tiles of 128 rows against 64-token pages staged through LDS.
+#include <type_traits>
+
 #include "attend.h"
 
 namespace engram {
 namespace {
 
 constexpr int kTileWaves = 4;
-constexpr float kSlack = 8.0f;
 constexpr int kTileRows = 32 * kTileWaves;
 
 // 16-byte chunk of a staged row, moved so that eight lanes reading (or
@@ -26,6 +27,14 @@ __device__ __forceinline__ int v_chunk(int d, int c) { return c ^ ((d ^ (d >> 2)
 // {0..3}, are the second operand of O^T = V^T P^T as they stand.  Keys are
 // staged as codes, values transposed and widened to bf16 with their tokens in
 // that order.
+//
+// Bound by the matrix and the vector units together, which only overlap where
+// their instructions alternate (a wavefront issues in order), and by the
+// latency of LDS where little is in flight.  So the pages that every row sees
+// whole go through a pipeline of half pages: while a half's probabilities are
+// formed, the logits of the next half are multiplied and the values that the
+// half needs are read.  One barrier a page; pages are loaded two ahead.  The
+// pages with masks come after, one by one.
 template <int D>
 __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs a)
 {
@@ -34,7 +43,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     constexpr int KL = KB / 16 / 256;             // 16-byte chunks of keys a thread stages
     constexpr int VL = D / 128 > 0 ? D / 128 : 1; // 8-token x 4-value blocks of values
     __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][KB];
-    __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][VB];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_v[3][VB];
     __shared__ int poison_s;          // some page held a NaN that only some rows see
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -74,7 +83,6 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     const int my_lo = q.start + min(row0 + 32 * w, rows - 1) / a.g;
     const int my_hi = q.start + min(row0 + 32 * w + 31, rows - 1) / a.g;
     const int my_see = a.window > 0 ? max(my_lo - a.window + 1, 0) : 0;
-    const int my_all = a.window > 0 ? max(my_hi - a.window + 1, 0) : 0;
     const int first = see_lo / kPage, last = q.bad ? first : pos_hi / kPage + 1;
 
     // ---- queries
@@ -117,50 +125,32 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     const int quad = tid % (D / 4);
     const auto v_group = [&](int i) { return tid / (D / 4) + i * (1024 / D); };
     const auto v_token = [&](int i, int e) { return 16 * (v_group(i) >> 1) + 4 * (v_group(i) & 1) + (e & 3) + 8 * (e >> 2); };
+    const uint32_t k_off = 16 * tid;
+    const uint32_t v_off = (16 * (v_group(0) >> 1) + 4 * (v_group(0) & 1)) * D + 4 * quad;
     const auto fetch = [&](int page) {
-        const int64_t at = (int64_t)page * kv + head;
-        const uint8_t *kp = a.c.d_k + at * KB, *vp = a.c.d_v + at * KB;
+        const int64_t at = ((int64_t)page * kv + head) * KB;
+        const __amdgpu_buffer_rsrc_t kp = __builtin_amdgcn_make_buffer_rsrc(a.c.d_k + at, 0, KB, 0x00027000);
+        const __amdgpu_buffer_rsrc_t vp = __builtin_amdgcn_make_buffer_rsrc(a.c.d_v + at, 0, KB, 0x00027000);
 #pragma unroll
         for (int i = 0; i < KL; i++)
-            kr[i] = *(const u32x4 *)(kp + (uint32_t)(16 * (tid + 256 * i)));
-        if (v_on)
+            kr[i] = __builtin_amdgcn_raw_buffer_load_b128(kp, k_off + 4096 * i, 0, 0);
 #pragma unroll
-            for (int i = 0; i < VL; i++)
+        for (int i = 0; i < VL; i++)
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    vr[i][e] = *(const uint32_t *)(vp + (uint32_t)(v_token(i, e) * D + 4 * quad));
+            for (int e = 0; e < 8; e++)      // (groups are 1024 / D apart: whole 16-token steps)
+                vr[i][e] = __builtin_amdgcn_raw_buffer_load_b32(
+                    vp, v_off + (16 * (i * (1024 / D) / 2) + (e & 3) + 8 * (e >> 2)) * D, 0, 0);
     };
-    // whether some row of the workgroup does not see page blk whole
-    const auto cut = [&](int blk) {
-        return blk * kPage + kPage - 1 > pos_lo ||
-               (a.window > 0 && blk * kPage < pos_hi - a.window + 1);
-    };
-    // Stages page blk of the sequence.  Of a cut page, values that no row sees
-    // are zeroed (0 * NaN is NaN), and a NaN that only some rows see is zeroed
-    // and noted: those rows get it at the end.
-    const auto stage = [&](int buf, int blk) {
+    const auto stage_k = [&](int slot) {
 #pragma unroll
         for (int i = 0; i < KL; i++) {
             const int c = tid + 256 * i, r = c / CH;
-            *(u32x4 *)(lds_k[buf] + 16 * (r * CH + k_chunk<D>(r, c % CH))) = kr[i];
+            *(u32x4 *)(lds_k[slot] + 16 * (r * CH + k_chunk<D>(r, c % CH))) = kr[i];
         }
+    };
+    const auto stage_v = [&](int slot) {
         if (!v_on)
             return;
-        if (cut(blk)) {
-            uint32_t any = 0;
-#pragma unroll
-            for (int i = 0; i < VL; i++)
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const int p = blk * kPage + v_token(i, e);
-                    uint32_t x = p <= pos_hi && p >= see_lo ? vr[i][e] : 0u;
-                    const uint32_t nan = nan_bytes(x);
-                    any |= nan;
-                    vr[i][e] = x & ~nan;
-                }
-            if (any)
-                poison_s = 1;
-        }
 #pragma unroll
         for (int i = 0; i < VL; i++) {
             uint32_t ab[2][2], cd[2][2];
@@ -182,147 +172,279 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                                       : u32x4{widen2<false>(ab[0][n]), widen2<false>(cd[0][n]),
                                               widen2<false>(ab[1][n]), widen2<false>(cd[1][n])};
                 const int r = 4 * quad + d;
-                *(u32x4 *)(lds_v[buf] + 128 * r + 16 * v_chunk(r, g)) = y;
+                *(u32x4 *)(lds_v[slot] + 128 * r + 16 * v_chunk(r, g)) = y;
             }
         }
     };
-    // the next page from blk on that lies in the cache (last if none)
-    const auto seek = [&](int blk, int &page) {
-        for (; blk < last; blk++) {
-            page = __builtin_amdgcn_readfirstlane(table[blk]);
-            if (page >= 0 && page < a.c.n_pages)
-                return blk;
-            if (tid == 0)
-                raise(a.s.err, ENGRAM_DEVERR_PAGE);
-        }
-        return last;
+    // whether some row of the workgroup does not see page blk whole
+    const auto cut = [&](int blk) {
+        return blk * kPage + kPage - 1 > pos_lo ||
+               (a.window > 0 && blk * kPage < pos_hi - a.window + 1);
     };
 
-    int page = 0, blk = seek(first, page), buf = 0;
-    if (tid == 0)
-        poison_s = 0;
-    __syncthreads();
-    if (blk < last) {
-        fetch(page);
-        stage(0, blk);
-    }
-    __syncthreads();
-    while (blk < last) {
-        const int64_t at = (int64_t)page * kv + head;
-        const float ks = a.c.d_k_scales[at], vs = a.c.d_v_scales[at];
-        const bool plain = vs >= 0x1p-100f && vs <= 0x1p100f;
-        const int v_bits = (int)(__float_as_uint(vs) >> 23) - 127;
-        const float v_exp = plain ? (float)v_bits : 0.0f;
-        const float v_inv = plain ? exp2_int(-v_bits) : 1.0f;
-        const float v_rest = plain ? vs * v_inv : vs;
-        int next_page = 0;
-        const int next = seek(blk + 1, next_page);
-        if (next < last)
-            fetch(next_page);
-        const int base = blk * kPage;
-        // a wavefront whose rows see none of the page passes it by
-        if (row0 + 32 * w < rows && base <= my_hi && base + kPage > my_see) {
-            // ---- logits
-            f32x16 s[2];
+    // ---- the sequence's pages, 64 at a time and one a lane: id and scales
+    int from = first, id = -1;
+    float ks_lane = 0.0f, vs_lane = 0.0f;
+    uint64_t todo = 0;
+    // FAST: pages seen whole whose value scale is a power of two (what
+    // cache_append writes); else the other pages of the cache
+    const auto look = [&](auto fast_c) {
+        constexpr bool fast = decltype(fast_c)::value;
+        const int blk = from + lane;
+        id = blk < last ? table[blk] : -1;
+        if (id < 0 || id >= a.c.n_pages) {
+            if (fast && blk < last)
+                raise(a.s.err, ENGRAM_DEVERR_PAGE);
+            id = -1;
+        } else {
+            ks_lane = a.c.d_k_scales[(int64_t)id * kv + head];
+            vs_lane = a.c.d_v_scales[(int64_t)id * kv + head];
+        }
+        const bool plain = vs_lane >= 0x1p-100f && vs_lane <= 0x1p100f &&
+                           (__float_as_uint(vs_lane) & 0x7FFFFFu) == 0;
+        todo = __ballot(id >= 0 && fast == (plain && !cut(blk)));
+    };
+    struct Page {
+        int id, blk;
+        float f, vs;
+    };
+    const auto next_page = [&](auto fast_c) {
+        while (!todo && from + 64 < last) {
+            from += 64;
+            look(fast_c);
+        }
+        if (!todo)
+            return Page{-1, 0, 0.0f, 0.0f};
+        const int i = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        return Page{__builtin_amdgcn_readlane(id, i), from + i,
+                    __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_lane), i)),
+                    __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_lane), i))};
+    };
+
+    // ---- the steps of half a page (32 tokens)
+    uint32_t k_at[KS][2], v_at[4];             // a lane's pieces of row l % 32
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
+    for (int u = 0; u < KS; u++)
 #pragma unroll
-                for (int e = 0; e < 16; e++)
-                    s[t][e] = 0.0f;
+        for (int i = 0; i < 2; i++)
+            k_at[u][i] = 16 * (r32 * CH + k_chunk<D>(r32, 4 * u + 2 * h + i));
 #pragma unroll
-                for (int u = 0; u < KS; u++) {
-                    const int r = 32 * t + r32;
-                    const u32x4 x = *(const u32x4 *)(lds_k[buf] + 16 * (r * CH + k_chunk<D>(r, 4 * u + 2 * h)));
-                    const u32x4 y = *(const u32x4 *)(lds_k[buf] + 16 * (r * CH + k_chunk<D>(r, 4 * u + 2 * h + 1)));
-                    const i32x8 kf = {(int)x.x, (int)x.y, (int)x.z, (int)x.w,
-                                      (int)y.x, (int)y.y, (int)y.z, (int)y.w};
-                    s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[u], s[t], 0, 0, 0, kOne, 0, kOne);
-                    s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[u], s[t], 0, 0, 0, kOne, 0, kLoScale);
-                }
-            }
-            // logits are s * f, f >= 0 (the scale's sign went into the queries)
-            const float f = qs * ks;
-            const bool edge = base + kPage - 1 > my_lo || base < my_all;
-            if (edge) {
+    for (int c = 0; c < 4; c++)
+        v_at[c] = 128 * r32 + 16 * v_chunk(r32, 2 * c + h);
+    const auto logits = [&](const uint8_t *kp, int t, f32x16 &s) {
 #pragma unroll
-                for (int t = 0; t < 2; t++)
+        for (int e = 0; e < 16; e++)
+            s[e] = 0.0f;
+        i32x8 kf[KS];
 #pragma unroll
-                    for (int e = 0; e < 16; e++) {
-                        const int p = base + 32 * t + 8 * (e / 4) + 4 * h + e % 4;
-                        s[t][e] = p <= pos && p >= lo ? s[t][e] : -INFINITY;
-                    }
-            }
-            float top = -INFINITY;
+        for (int u = 0; u < KS; u++) {
+            const u32x4 x = *(const u32x4 *)(kp + k_at[u][0] + 32 * D * t);
+            const u32x4 y = *(const u32x4 *)(kp + k_at[u][1] + 32 * D * t);
+            kf[u] = i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w,
+                          (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+        }
 #pragma unroll
-            for (int t = 0; t < 2; t++)
+        for (int u = 0; u < KS; u++) {
+            s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf[u], qh[u], s, 0, 0, 0, kOne, 0, kOne);
+            s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf[u], ql[u], s, 0, 0, 0, kOne, 0, kLoScale);
+        }
+    };
+    // Logits are s * f, f >= 0 (the scale's sign went into the queries).  Moves
+    // the base m to their maximum.
+    const auto rebase = [&](const f32x16 &s, float f) {
+        float top[4];
 #pragma unroll
-                for (int e = 0; e < 16; e++)
-                    top = fmaxf(top, s[t][e]);
-            top = max_x32(top);
-            top = top == -INFINITY ? top : top * f;
-            // the base m follows the maximum once that is 2^8 past it: sums and
-            // probabilities stay far inside f32's and bf16's range
-            if (__any(top > m + kSlack)) {
-                const float now = fmaxf(m, top);
-                const float keep = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - now);
-                m = now;
-                l *= keep;
+        for (int i = 0; i < 4; i++)
+            top[i] = s[i];
 #pragma unroll
-                for (int i = 0; i < DT; i++)
-                    o[i] *= keep;
-            }
-            // probabilities times the page's value scale: its power of two
-            // joins the exponent, what is left (1 but for scales that
-            // cache_append does not write) multiplies
-            const float zero = (m == -INFINITY ? 0.0f : m) - v_exp;
-            float sum = 0.0f;
-            u32x4 pb[4];
-            if (!edge && v_rest == 1.0f) {
+        for (int e = 4; e < 16; e += 4)
 #pragma unroll
-                for (int t = 0; t < 2; t++)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e], f, -zero));
-                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e + 1], f, -zero));
-                        sum += p0 + p1;
-                        pb[2 * t + e / 8][(e % 8) / 2] = cvt_bf16x2(p0, p1);
-                    }
-            } else {
-#pragma unroll
-                for (int t = 0; t < 2; t++)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e], f, -zero));
-                        float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e + 1], f, -zero));
-                        p0 = s[t][e] == -INFINITY ? 0.0f : p0;
-                        p1 = s[t][e + 1] == -INFINITY ? 0.0f : p1;
-                        sum += p0 + p1;
-                        p0 = s[t][e] == -INFINITY ? 0.0f : p0 * v_rest;
-                        p1 = s[t][e + 1] == -INFINITY ? 0.0f : p1 * v_rest;
-                        pb[2 * t + e / 8][(e % 8) / 2] = cvt_bf16x2(p0, p1);
-                    }
-            }
-            l += sum * v_inv;
-            // ---- values
+            for (int i = 0; i < 4; i++)
+                top[i] = __builtin_elementwise_maximum(top[i], s[e + i]);
+        // (a NaN passes through, and makes its row NaN whatever the base)
+        float t = max_x32(__builtin_elementwise_maximum(__builtin_elementwise_maximum(top[0], top[1]),
+                                                        __builtin_elementwise_maximum(top[2], top[3])));
+        t = t == -INFINITY ? t : t * f;
+        if (__any(t > m)) {
+            const float now = fmaxf(m, t);
+            const float keep = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+            m = now;
+            l *= keep;
 #pragma unroll
             for (int i = 0; i < DT; i++)
+                o[i] *= keep;
+        }
+    };
+    const auto read_values = [&](const uint8_t *vp, int t, u32x4 (&vf)[2][DT]) {
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    const int r = 32 * i + r32;
-                    const u32x4 x = *(const u32x4 *)(lds_v[buf] + 128 * r + 16 * v_chunk(r, 2 * c + h));
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
-                                                                   __builtin_bit_cast(bf16x8, pb[c]), o[i], 0, 0, 0);
-                }
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int i = 0; i < DT; i++)
+                vf[c][i] = *(const u32x4 *)(vp + v_at[2 * t + c] + 4096 * i);
+    };
+    const auto values = [&](const u32x4 (&vf)[2][DT], const u32x4 (&pb)[2]) {
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int i = 0; i < DT; i++)
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[c][i]),
+                                                               __builtin_bit_cast(bf16x8, pb[c]), o[i], 0, 0, 0);
+    };
+    // 2^(s f - m) times 2^v, a power of two that joins the exponent
+    const auto weights = [&](const f32x16 &s, float f, float v, u32x4 (&pb)[2]) {
+        const float zero = m - v;
+        float sum[4] = {};
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], f, -zero));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + 1], f, -zero));
+            sum[e % 4] += p0;
+            sum[e % 4 + 1] += p1;
+            pb[e / 8][(e % 8) / 2] = cvt_bf16x2(p0, p1);
         }
-        if (next < last) {
-            stage(buf ^ 1, next);       // its last readers passed the previous barrier
+        return sum[0] + sum[1] + (sum[2] + sum[3]);
+    };
+    // A step of the pipeline: half t of the page with values at vp, whose logits
+    // are s, while those of the next half, half 1-t of the keys at kp, go to
+    // s_next.  The base stays where it is until a sum passes 2^40: sums and
+    // probabilities are floating point and lose nothing below that.
+    const auto half_turn = [&](const Page &cur, const uint8_t *vp, int t, f32x16 &s, const uint8_t *kp,
+                               f32x16 &s_next) {
+        const float f = qs * cur.f;
+        const int v_bits = (int)(__float_as_uint(cur.vs) >> 23) - 127;
+        u32x4 pb[2], vf[2][DT];
+        logits(kp, 1 - t, s_next);
+        read_values(vp, t, vf);
+        float sum = weights(s, f, (float)v_bits, pb);
+        // the instructions in turn: a matrix instruction, then what the vector
+        // unit does meanwhile
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * KS, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * KS; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, DT / KS, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 40 / (2 * KS), 0);
+            __builtin_amdgcn_sched_group_barrier(0x400, 16 / (2 * KS), 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const float one = exp2_int(-v_bits);
+        if (__any(sum * one > 0x1p40f)) {
+            rebase(s, f);
+            sum = weights(s, f, (float)v_bits, pb);
+        }
+        l += sum * one;
+        values(vf, pb);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    if (tid == 0)
+        poison_s = 0;
+    look(std::true_type{});
+    {
+        // p[0]: at work, its values in slot v_slot of three and its keys in slot
+        // k_slot of two; p[1]: staged; p[2]: in the registers
+        Page p[3];
+        p[0] = next_page(std::true_type{});
+        if (p[0].id >= 0) {
+            for (int i = 1; i < 3; i++)
+                p[i] = p[i - 1].id >= 0 ? next_page(std::true_type{}) : p[i - 1];
+            // (past the last page p[0] is loaded again, and not used)
+            const auto load = [&](const Page &x) { fetch(x.id >= 0 ? x.id : p[0].id); };
+            load(p[0]);
+            stage_k(0);
+            stage_v(0);
+            load(p[1]);
+            stage_k(1);
+            stage_v(1);
+            load(p[2]);
             __syncthreads();
+            int k_slot = 0, v_slot = 0;
+            f32x16 sa, sb;
+            logits(lds_k[0], 0, sa);
+            rebase(sa, qs * p[0].f);
+            while (true) {
+                const uint8_t *vp = lds_v[v_slot];
+                half_turn(p[0], vp, 0, sa, lds_k[k_slot], sb);
+                __syncthreads();                // p[0]'s keys are used, p[1] is staged
+                half_turn(p[0], vp, 1, sb, lds_k[k_slot ^ 1], sa);
+                if (p[1].id < 0)
+                    break;
+                stage_k(k_slot);
+                v_slot = v_slot == 2 ? 0 : v_slot + 1;
+                stage_v(v_slot == 2 ? 0 : v_slot + 1);
+                k_slot ^= 1;
+                p[0] = p[1];
+                p[1] = p[2];
+                p[2] = p[1].id >= 0 ? next_page(std::true_type{}) : p[1];
+                load(p[2]);
+            }
         }
-        buf ^= 1;
-        blk = next;
-        page = next_page;
     }
 
+    // ---- the pages that some row does not see whole
+    from = first;
+    look(std::false_type{});
+    while (true) {
+        const Page cur = next_page(std::false_type{});
+        if (cur.id < 0)
+            break;
+        const int base = cur.blk * kPage;
+        fetch(cur.id);
+        __syncthreads();                        // the slots' last readers are done
+        // values that no row sees are zeroed (0 * NaN is NaN); a NaN that only
+        // some rows see is zeroed and noted: those rows get it at the end
+        if (v_on && cut(cur.blk)) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int i = 0; i < VL; i++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const int p = base + v_token(i, e);
+                    const uint32_t x = p <= pos_hi && p >= see_lo ? vr[i][e] : 0u;
+                    const uint32_t nan = nan_bytes(x);
+                    any |= nan;
+                    vr[i][e] = x & ~nan;
+                }
+            if (any)
+                poison_s = 1;
+        }
+        stage_k(0);
+        stage_v(0);
+        __syncthreads();
+        // a wavefront whose rows see none of the page passes it by
+        if (row0 + 32 * w < rows && base <= my_hi && base + kPage > my_see) {
+            const float f = qs * cur.f;
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                f32x16 s;
+                logits(lds_k[0], t, s);
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const int p = base + 32 * t + 8 * (e / 4) + 4 * h + e % 4;
+                    s[e] = p <= pos && p >= lo ? s[e] : -INFINITY;
+                }
+                rebase(s, f);
+                const float zero = m == -INFINITY ? 0.0f : m;
+                u32x4 pb[2], vf[2][DT];
+                read_values(lds_v[0], t, vf);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    float p[2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {     // (f may be 0, and 0 * -inf NaN)
+                        const bool masked = s[e + i] == -INFINITY;
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + i], f, -zero));
+                        l += masked ? 0.0f : p[i];
+                        p[i] = masked ? 0.0f : p[i] * cur.vs;
+                    }
+                    pb[e / 8][(e % 8) / 2] = cvt_bf16x2(p[0], p[1]);
+                }
+                values(vf, pb);
+            }
+        }
+    }
+    __syncthreads();                            // poison_s
     if (poison_s) {
         // how many NaN codes of the cut pages each row sees, by the values'
         // product with ones for both
