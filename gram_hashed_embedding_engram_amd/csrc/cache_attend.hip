@@ -179,44 +179,10 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q4 = lane >> 4;
 
-    // ---- the queries
+    // ---- what the rows see
     const int row = t.row0 + r16;
     const bool valid = row < t.rows;
     const int tok = valid ? row / a.g : 0;
-    i32x8 qh[KS], ql[KS];
-    float qs = 0.0f;
-    {
-        const uint16_t *qp = a.q.p + (int64_t)(t.q.t0 + tok) * a.q.token +
-                             (int64_t)(t.h * a.g + (valid ? row % a.g : 0)) * a.q.head;
-        u32x4 x[KS][4];
-        float amax = 0.0f;
-#pragma unroll
-        for (int s = 0; s < KS; s++) {
-            const int at = D == 64 ? 16 * q4 : 128 * s + 32 * q4;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                x[s][i] = *(const u32x4 *)(qp + at + 8 * (D == 64 ? i & 1 : i));
-                if (!valid)
-                    x[s][i] = u32x4{0u, 0u, 0u, 0u};
-            }
-            amax = fmaxf(amax, amax_bf16(x[s]));
-        }
-        const int k = e4m3_scale_exp(max_x16(amax));
-        qs = exp2_int(k) * a.scale;
-#pragma unroll
-        for (int s = 0; s < KS; s++)
-            split_query(x[s], exp2_int(-k), qh[s], ql[s]);
-    }
-    // head_dim 64: one instruction takes both parts.  A lane's first 16 codes
-    // are the contraction's indices 16(l / 16) on, under the scales of lanes
-    // 0-31, its last 16 those from 64 on, under the scales of lanes 32-63.
-    const int sel_scale = D == 64 && q4 >= 2 ? kLoScale : kOne;
-    if (D == 64)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            qh[0][4 + i] = ql[0][i];
-
-    // ---- what the rows see
     const int pos = t.q.start + tok;
     const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
     const int pos_lo = t.q.start + t.row0 / a.g;          // the tile's first and last position
@@ -275,6 +241,77 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
                 }
             }
     };
+
+    // The wavefront's pages, 64 at a time and one a lane: first those that
+    // every row sees whole, then the others.  The first is on its way before
+    // the queries are looked at.
+    const int32_t *table = a.s.pages + (int64_t)t.b * a.s.max_pages;
+    uint64_t whole = 0, rest = 0;
+    int id = -1;
+    const auto entry = [&](int p) { return p + W * lane < last ? table[p + W * lane] : -1; };
+    const auto sort = [&](int p, int entry_id) {
+        const int mine = p + W * lane;
+        id = entry_id;
+        if (id < 0 || id >= a.c.n_pages) {
+            if (mine < last)
+                raise(a.s.err, ENGRAM_DEVERR_PAGE);
+            id = -1;
+        }
+        const bool full = mine * kPage + kPage - 1 <= pos_lo && mine * kPage >= all_lo;
+        whole = __ballot(id >= 0 && full);
+        rest = __ballot(id >= 0 && !full);
+    };
+    // the place of the page to come next, -1 past the last
+    const auto ahead = [&] { return whole ? __builtin_ctzll(whole) : rest ? __builtin_ctzll(rest) : -1; };
+    const auto load = [&](int i) {
+        const int64_t at = (int64_t)__builtin_amdgcn_readlane(id, i) * a.c.kv_heads + t.h;
+        load_k(at);
+        load_v(at);
+    };
+
+    // ---- the queries
+    const int entry_0 = entry(first + w);
+    u32x4 x[KS][4];
+    const uint16_t *qp = a.q.p + (int64_t)(t.q.t0 + tok) * a.q.token +
+                         (int64_t)(t.h * a.g + (valid ? row % a.g : 0)) * a.q.head;
+#pragma unroll
+    for (int s = 0; s < KS; s++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            x[s][i] = *(const u32x4 *)(qp + (D == 64 ? 16 * q4 : 128 * s + 32 * q4) +
+                                       8 * (D == 64 ? i & 1 : i));
+    sort(first + w, entry_0);
+    int i = ahead();
+    if (i >= 0)
+        load(i);
+    __builtin_amdgcn_sched_barrier(0);
+
+    i32x8 qh[KS], ql[KS];
+    float qs = 0.0f;
+    {
+        float amax = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (!valid)
+                    x[s][i] = u32x4{0u, 0u, 0u, 0u};
+            amax = fmaxf(amax, amax_bf16(x[s]));
+        }
+        const int k = e4m3_scale_exp(max_x16(amax));
+        qs = exp2_int(k) * a.scale;
+#pragma unroll
+        for (int s = 0; s < KS; s++)
+            split_query(x[s], exp2_int(-k), qh[s], ql[s]);
+    }
+    // head_dim 64: one instruction takes both parts.  A lane's first 16 codes
+    // are the contraction's indices 16(l / 16) on, under the scales of lanes
+    // 0-31, its last 16 those from 64 on, under the scales of lanes 32-63.
+    const int sel_scale = D == 64 && q4 >= 2 ? kLoScale : kOne;
+    if (D == 64)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            qh[0][4 + i] = ql[0][i];
 
     // One page.  FULL: every row sees all of it, and the next such page is
     // loaded meanwhile: its keys once this one's are used, its values likewise
@@ -404,43 +441,25 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
         }
     };
 
-    // The wavefront's pages, 64 at a time and one a lane: first those that
-    // every row sees whole, then the others.
-    const int32_t *table = a.s.pages + (int64_t)t.b * a.s.max_pages;
     for (int p = first + w; p < last; p += 64 * W) {
-        const int mine = p + W * lane;
-        int id = -1;
-        if (mine < last) {
-            id = table[mine];
-            if (id < 0 || id >= a.c.n_pages) {
-                raise(a.s.err, ENGRAM_DEVERR_PAGE);
-                id = -1;
-            }
+        if (p != first + w) {
+            sort(p, entry(p));
+            i = ahead();
+            if (i >= 0)
+                load(i);
         }
-        const bool whole = mine * kPage + kPage - 1 <= pos_lo && mine * kPage >= all_lo;
-        uint64_t todo = __ballot(id >= 0 && whole);
-        if (todo) {
-            int i = __builtin_ctzll(todo);
-            int page = __builtin_amdgcn_readlane(id, i);
-            load_k((int64_t)page * a.c.kv_heads + t.h);
-            load_v((int64_t)page * a.c.kv_heads + t.h);
-            while (todo) {
-                todo &= todo - 1;
-                const int j = todo ? __builtin_ctzll(todo) : 0;
-                const int next = todo ? __builtin_amdgcn_readlane(id, j) : -1;
-                step(std::true_type{}, page, (p + W * i) * kPage, next);
-                i = j;
-                page = next;
-            }
+        while (whole) {
+            whole &= whole - 1;
+            const int page = __builtin_amdgcn_readlane(id, i), base = (p + W * i) * kPage;
+            i = ahead();
+            step(std::true_type{}, page, base, i >= 0 ? __builtin_amdgcn_readlane(id, i) : -1);
         }
-        todo = __ballot(id >= 0 && !whole);
-        while (todo) {
-            const int i = __builtin_ctzll(todo);
-            todo &= todo - 1;
-            const int page = __builtin_amdgcn_readlane(id, i);
-            load_k((int64_t)page * a.c.kv_heads + t.h);
-            load_v((int64_t)page * a.c.kv_heads + t.h);
-            step(std::false_type{}, page, (p + W * i) * kPage, -1);
+        while (rest) {
+            rest &= rest - 1;
+            step(std::false_type{}, __builtin_amdgcn_readlane(id, i), (p + W * i) * kPage, -1);
+            i = ahead();
+            if (i >= 0)
+                load(i);
         }
     }
 
@@ -521,9 +540,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : W / 4) void attend_unit_kern
         b = base + l;
         unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
     }
-    raise_bad(a);
     const RowTile t = tile_at(a, b, unit, seq_at(a.s, b));
     attend_unit<D, W>(a, t, 0, 1 << 26, nullptr, red);
+    raise_bad(a);                               // last: nothing waits for it
 }
 
 // Long tables: a workgroup a share of the row of pages.
@@ -533,14 +552,15 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
     __shared__ Reduce<D, W> red;
     __shared__ Seq seqs[64];
     __shared__ int each_s[64], units_s[64];
-    raise_bad(a);
     Lanes c = lanes_at(a, 0);
     int total = c.all_pages();
     for (int base = 64; base < a.s.B; base += 64)
         total += lanes_at(a, base).all_pages();
     const int share = share_of(a, total);
-    if ((int64_t)blockIdx.x * share >= total)
+    if ((int64_t)blockIdx.x * share >= total) {
+        raise_bad(a);
         return;
+    }
     int at = blockIdx.x * share;
     const int end = min((int64_t)at + share, (int64_t)total);
     // the sequence, unit and page that the share begins with; the sequences
@@ -576,7 +596,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
                           np == each ? nullptr : part + place * part_floats(D), red);
         at += np;
         if (at >= end)
-            return;
+            break;
         place = 1;
         p0 = 0;
         __syncthreads();                        // the sums in LDS have been read
@@ -593,6 +613,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
             } while (__builtin_amdgcn_readfirstlane(units_s[l]) == 0);
         }
     }
+    raise_bad(a);
 }
 
 // Joins the parts of a unit's rows.  A workgroup takes a unit, or, with

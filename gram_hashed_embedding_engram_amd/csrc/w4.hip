@@ -178,11 +178,16 @@ __global__ __launch_bounds__(64 * kW4Waves, 1) void w4_kernel(
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; u++) {
+            if (k0 + u >= end)
+                break;
 #pragma unroll
             for (int i = 0; i < RT; i++)
                 turn_rows(stage, lane, wr[u][i][0], wr[u][i][1]);
 #pragma unroll
             for (int h = 0; h < 2; h++) {           // step 2(k0 + u) + h
+                // (not multiplied past the end, where an infinite x would meet zeros)
+                if (2 * (k0 + u) + h >= steps)
+                    break;
                 if (XS == 1)
                     load_x(2 * (k0 + u) + h);
                 const int xu = XS == 1 ? 0 : 2 * u + h;

@@ -174,6 +174,17 @@ def test_project_w4_nan(E, fp8):
     assert torch.equal(torch.isnan(y), bad)
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 128, 16), (20, 640, 64), (40, 1152, 80), (60, 4096, 1296)])
+def test_project_w4_infinite(E, T, K, N):
+    """An infinite value meets its own weights only, wherever in K it stands:
+    infinities of the weights' signs, NaN over zero weights."""
+    w, ws, x, xs, _ = w4_case(13 + K, T, K, N, False)
+    for t, at in ((0, K - 1), (1, K // 2), (2, 0)):
+        x[t, at] = math.inf
+    x[T - 1, K - 128] = -math.inf
+    check_w4(E, w, ws, x, xs, x.to(F64))
+
+
 # ----------------------------------------------------------------- append
 STEPS = [  # new tokens, older positions, kv heads, queries a key head, head_dim
     ([1], [0], 1, 1, 64), ([1], [63], 2, 4, 128), ([1], [64], 2, 3, 64), ([1, 1, 1], [5, 127, 300], 4, 8, 256),
@@ -423,6 +434,19 @@ def test_attend_peaked(E, d, n, kv):
     check_attend(E, st, q=q)
     check_attend(E, st, q=q * 2.0 ** -100)
     check_attend(E, st, q=q, scale=2.0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,kv", [(1, 2), (90, 2), (400, 4)])
+@pytest.mark.parametrize("far", [-100, -61, 61, 100])
+def test_attend_far_value_scales(E, far, d, n, kv):
+    """Values near both ends of f32's range, under large logits."""
+    st = R.Step(n + d + 1, [n, n], [700, 64], kv, 4, d)
+    st.fill_new()
+    st.scales[1] *= 2.0 ** far
+    q = st.heads()[0].contiguous()
+    q[:, ::2] *= 16
+    check_attend(E, st, q=q)
 
 
 @pytest.mark.parametrize("n,kv,d", [(1, 2, 128), (90, 2, 128), (90, 2, 64), (30, 2, 256), (600, 8, 128),
