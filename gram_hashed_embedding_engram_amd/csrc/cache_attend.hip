@@ -15,11 +15,13 @@ namespace {
 //
 // A unit is a row tile and a key head.  Every unit of a sequence counts the
 // same number of pages, and all units' pages lie in one row, sequence by
-// sequence; workgroup i takes pages i*share .. (i+1)*share-1 of it, whatever
-// the sequences' lengths are, so that all end together.  A unit that lies in
-// one workgroup is written out there; parts of a unit go to the workgroup's
-// two places in the workspace (0 for its first part, 1 for a last one that is
-// not its first) and are joined by a second kernel.
+// sequence, that the workgroups share out whatever the sequences' lengths are,
+// so that all end together.  Where units are fewer than workgroups, a unit's
+// pages are cut into equal pieces, one a workgroup; else workgroup i takes
+// pages i*share .. (i+1)*share-1 of the row.  A unit that lies in one workgroup
+// is written out there; parts of a unit go to the workgroup's two places in the
+// workspace (0 for its first part, 1 for a last one that is not its first) and
+// are joined by a second kernel.
 
 // Pages that each unit of sequence b counts: 0 where it brings no token.
 __device__ __forceinline__ int unit_pages(const AttendArgs &a, const Seq &q)
@@ -37,20 +39,28 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const Seq &q)
     return (int)(((int64_t)q.n * a.g + kRows - 1) / kRows);
 }
 
-// Sequences base .. base+63, one a lane, with their units and pages and the
-// sums of both up to and with them (a call's units x pages stay below 2^31).
+// Sequences base .. base+63, one a lane, with their units and pieces and the
+// sums of both up to and with them (a call's units x pages stay below 2^30).
+// A piece is a page, or, with most > 0, a run of `most` pages of a unit (the
+// last one what is left).
 struct Lanes {
     Seq q;
-    int each, units, pages, sum_u, sum_p;
+    int each, units, pieces, sum_u, sum_p;          // each: pieces a unit
     __device__ __forceinline__ int all_units() const { return __builtin_amdgcn_readlane(sum_u, 63); }
-    __device__ __forceinline__ int all_pages() const { return __builtin_amdgcn_readlane(sum_p, 63); }
+    __device__ __forceinline__ int all_pieces() const { return __builtin_amdgcn_readlane(sum_p, 63); }
     __device__ __forceinline__ Seq seq(int l) const
     {
         return Seq{__builtin_amdgcn_readlane(q.t0, l), __builtin_amdgcn_readlane(q.n, l),
                    __builtin_amdgcn_readlane(q.start, l), (bool)__builtin_amdgcn_readlane(q.bad, l)};
     }
+    __device__ __forceinline__ void cut(int most)
+    {
+        each = (int)((uint32_t)(each + most - 1) / (uint32_t)most);
+        pieces = units * each;
+        sum_p = wave_scan(pieces);
+    }
 };
-__device__ __forceinline__ Lanes lanes_at(const AttendArgs &a, int base)
+__device__ __forceinline__ Lanes lanes_at(const AttendArgs &a, int base, int most = 0)
 {
     const int b = base + (threadIdx.x & 63);
     Lanes c{{0, 0, 0, false}, 0, 0, 0, 0, 0};
@@ -58,26 +68,68 @@ __device__ __forceinline__ Lanes lanes_at(const AttendArgs &a, int base)
         c.q = seq_at(a.s, b);
         c.each = unit_pages(a, c.q);
         c.units = unit_tiles(a, c.q) * a.c.kv_heads;
-        c.pages = c.units * c.each;
+        c.pieces = c.units * c.each;
     }
     c.sum_u = wave_scan(c.units);
-    c.sum_p = wave_scan(c.pages);
+    if (most > 0)
+        c.cut(most);
+    else
+        c.sum_p = wave_scan(c.pieces);
     return c;
 }
 
-// Pages a workgroup takes.
-__device__ __forceinline__ int share_of(const AttendArgs &a, int total)
+// How a call's pages are shared out: pieces a workgroup, pieces in all, and the
+// pages a piece holds (0: pieces are pages).
+struct Plan {
+    int share, total, most;
+};
+
+// A workgroup whose share ends inside a unit and goes on in the next one begins
+// anew there, which takes as long as 16 pages of its four wavefronts (4 us; 16
+// sequences of 1180 positions with 256-wide heads took 18 us that way).  So
+// units are cut evenly unless the longest piece then passes a share by more.
+constexpr int kBeginPages = 16;
+
+// (c: the first sequences' lanes, cut as the plan says.)
+__device__ __forceinline__ Plan plan_of(const AttendArgs &a, Lanes &c)
 {
-    const int per = (total + a.parts - 1) / a.parts;
-    return per > a.least ? per : a.least;
+    int total = c.all_pieces(), units = c.all_units();
+    for (int base = 64; base < a.s.B; base += 64) {
+        const Lanes next = lanes_at(a, base);
+        total += next.all_pieces();
+        units += next.all_units();
+    }
+    const int share = max((int)(((uint32_t)total + a.parts - 1) / (uint32_t)a.parts), a.least);
+    if (units < a.parts) {
+        // pieces of a share's pages, if no more than workgroups come of it; else of
+        // so many that they are at most total / most + units <= parts
+        const int pages = c.each;
+        int most = share;
+#pragma unroll 1
+        do {
+            c.each = pages;
+            c.cut(most);
+            int pieces = c.all_pieces();
+            for (int base = 64; base < a.s.B; base += 64)
+                pieces += lanes_at(a, base, most).all_pieces();
+            if (pieces <= a.parts)
+                return Plan{1, pieces, most};
+            const uint32_t left = a.parts - units;
+            most = (int)(((uint32_t)total + left - 1) / left);      // > share: pieces were too many
+        } while (most <= share + kBeginPages);
+        c.each = pages;
+        c.cut(1);
+    }
+    return Plan{share, total, 0};
 }
 
 __device__ __forceinline__ RowTile tile_at(const AttendArgs &a, int b, int unit, const Seq &q)
 {
     RowTile t;
     t.b = b;
-    t.h = unit % a.c.kv_heads;
-    t.row0 = unit / a.c.kv_heads * kRows;
+    const int tile = (uint32_t)unit / (uint32_t)a.c.kv_heads;
+    t.h = unit - tile * a.c.kv_heads;
+    t.row0 = tile * kRows;
     t.q = q;
     t.rows = q.n * a.g;
     return t;
@@ -85,7 +137,8 @@ __device__ __forceinline__ RowTile tile_at(const AttendArgs &a, int b, int unit,
 
 __device__ __forceinline__ uint16_t *out_row(const AttendArgs &a, const RowTile &t, int row, int D)
 {
-    return a.out + ((int64_t)(t.q.t0 + row / a.g) * a.heads + t.h * a.g + row % a.g) * D;
+    const int tok = (uint32_t)row / (uint32_t)a.g;
+    return a.out + ((int64_t)(t.q.t0 + tok) * a.heads + t.h * a.g + row - tok * a.g) * D;
 }
 
 template <int D>
@@ -182,11 +235,11 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
     // ---- what the rows see
     const int row = t.row0 + r16;
     const bool valid = row < t.rows;
-    const int tok = valid ? row / a.g : 0;
+    const int tok = valid ? (uint32_t)row / (uint32_t)a.g : 0;
     const int pos = t.q.start + tok;
     const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    const int pos_lo = t.q.start + t.row0 / a.g;          // the tile's first and last position
-    const int pos_hi = t.q.start + min(t.row0 + kRows - 1, t.rows - 1) / a.g;
+    const int pos_lo = t.q.start + (uint32_t)t.row0 / (uint32_t)a.g;          // the tile's first and last position
+    const int pos_hi = t.q.start + (uint32_t)min(t.row0 + kRows - 1, t.rows - 1) / (uint32_t)a.g;
     const int see_lo = a.window > 0 ? max(pos_lo - a.window + 1, 0) : 0;     // seen by any row
     const int all_lo = a.window > 0 ? max(pos_hi - a.window + 1, 0) : 0;     // seen by every row
     const int first = see_lo / kPage + p0;
@@ -273,7 +326,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
     const int entry_0 = entry(first + w);
     u32x4 x[KS][4];
     const uint16_t *qp = a.q.p + (int64_t)(t.q.t0 + tok) * a.q.token +
-                         (int64_t)(t.h * a.g + (valid ? row % a.g : 0)) * a.q.head;
+                         (int64_t)(t.h * a.g + (valid ? row - tok * a.g : 0)) * a.q.head;
 #pragma unroll
     for (int s = 0; s < KS; s++)
 #pragma unroll
@@ -553,37 +606,35 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
     __shared__ Seq seqs[64];
     __shared__ int each_s[64], units_s[64];
     Lanes c = lanes_at(a, 0);
-    int total = c.all_pages();
-    for (int base = 64; base < a.s.B; base += 64)
-        total += lanes_at(a, base).all_pages();
-    const int share = share_of(a, total);
-    if ((int64_t)blockIdx.x * share >= total) {
+    const Plan plan = plan_of(a, c);
+    if ((int64_t)blockIdx.x * plan.share >= plan.total) {
         raise_bad(a);
         return;
     }
-    int at = blockIdx.x * share;
-    const int end = min((int64_t)at + share, (int64_t)total);
-    // the sequence, unit and page that the share begins with; the sequences
+    int at = blockIdx.x * plan.share;
+    const int end = min((int64_t)at + plan.share, (int64_t)plan.total);
+    // the sequence, unit and piece that the share begins with; the sequences
     // wait in LDS while a unit is at work (its registers are all taken)
     int base = 0, before = 0;
-    while (before + c.all_pages() <= at) {
-        before += c.all_pages();
+    while (before + c.all_pieces() <= at) {
+        before += c.all_pieces();
         base += 64;
-        c = lanes_at(a, base);
+        c = lanes_at(a, base, plan.most);
     }
     int l = __builtin_ctzll(__ballot(before + c.sum_p > at));
-    int p0 = at - before - __builtin_amdgcn_readlane(c.sum_p - c.pages, l);
-    int unit = p0 / __builtin_amdgcn_readlane(c.each, l);
+    int p0 = at - before - __builtin_amdgcn_readlane(c.sum_p - c.pieces, l);
+    int unit = (uint32_t)p0 / (uint32_t)__builtin_amdgcn_readlane(c.each, l);
     p0 -= unit * __builtin_amdgcn_readlane(c.each, l);
     const auto keep = [&] {
         if (threadIdx.x < 64) {
             seqs[threadIdx.x] = c.q;
             each_s[threadIdx.x] = c.each;
-            units_s[threadIdx.x] = c.pages ? c.units : 0;
+            units_s[threadIdx.x] = c.pieces ? c.units : 0;
         }
         __syncthreads();
     };
     keep();
+    const int step = plan.most > 0 ? plan.most : 1;
     float *part = a.part + 2 * (int64_t)blockIdx.x * part_floats(D);
     int place = 0;
     while (true) {
@@ -592,7 +643,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
         const Seq q{__builtin_amdgcn_readfirstlane(seqs[l].t0), __builtin_amdgcn_readfirstlane(seqs[l].n),
                     __builtin_amdgcn_readfirstlane(seqs[l].start),
                     (bool)__builtin_amdgcn_readfirstlane(seqs[l].bad)};
-        attend_unit<D, W>(a, tile_at(a, base + l, unit, q), p0, np,
+        attend_unit<D, W>(a, tile_at(a, base + l, unit, q), p0 * step, np * step,
                           np == each ? nullptr : part + place * part_floats(D), red);
         at += np;
         if (at >= end)
@@ -606,7 +657,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
                 if (++l == 64) {
                     l = 0;
                     base += 64;
-                    const Lanes next = lanes_at(a, base);
+                    const Lanes next = lanes_at(a, base, plan.most);
                     c = next;
                     keep();
                 }
@@ -614,6 +665,42 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
         }
     }
     raise_bad(a);
+}
+
+// A row's parts first, first + by, ... < n, joined for four output values: the
+// running maximum and sum again, U parts' loads under way at a time.
+struct Joined {
+    float m, l;
+    f32x4 acc;
+    __device__ __forceinline__ void add(float pm, float pl, const f32x4 &po)
+    {
+        const float top = fmaxf(m, pm), zero = top == -INFINITY ? 0.0f : top;
+        const float k = __builtin_amdgcn_exp2f(m - zero), pk = __builtin_amdgcn_exp2f(pm - zero);
+        m = top;
+        l = k * l + pk * pl;
+        acc = k * acc + pk * po;
+    }
+};
+template <int D, int U, class P>
+__device__ __forceinline__ Joined join_row(int first, int by, int n, int r, int d, P place)
+{
+    Joined j{-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int i = first; i < n; i += U * by) {
+        float m[U], l[U];
+        f32x4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const float *x = place(min(i + u * by, n - 1));
+            m[u] = x[r];
+            l[u] = x[kRows + r];
+            o[u] = *(const f32x4 *)(x + 2 * kRows + r * D + d);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (i + u * by < n)
+                j.add(m[u], l[u], o[u]);
+    }
+    return j;
 }
 
 // Joins the parts of a unit's rows.  A workgroup takes a unit, or, with
@@ -624,91 +711,59 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
 {
     constexpr int QUADS = D / 4, GROUPS = 512 / QUADS;
     __shared__ f32x4 acc_s[GROUPS][QUADS];
-    __shared__ float l_s[GROUPS], m_s[8];
+    __shared__ float l_s[GROUPS], m_s[GROUPS];
     const int tid = threadIdx.x;
     const int r0 = SPLIT ? blockIdx.x % a.join_rows : 0;
     int unit = SPLIT ? blockIdx.x / a.join_rows : blockIdx.x;
     Lanes c = lanes_at(a, 0);
-    int total = c.all_pages();
-    for (int base = 64; base < a.s.B; base += 64)
-        total += lanes_at(a, base).all_pages();
+    const Plan plan = plan_of(a, c);
     int base = 0, before = 0;
     while (unit >= c.all_units()) {
         unit -= c.all_units();
-        before += c.all_pages();
+        before += c.all_pieces();
         base += 64;
         if (base >= a.s.B)
             return;
-        c = lanes_at(a, base);
+        c = lanes_at(a, base, plan.most);
     }
     const int l = __builtin_ctzll(__ballot(c.sum_u > unit));
     unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
     const RowTile t = tile_at(a, base + l, unit, c.seq(l));
-    const int each = __builtin_amdgcn_readlane(c.each, l), share = share_of(a, total);
-    const int begin = before + __builtin_amdgcn_readlane(c.sum_p - c.pages, l) + unit * each;
-    const int i0 = begin / share;
-    const int n = (begin + each - 1) / share - i0 + 1;
+    const int each = __builtin_amdgcn_readlane(c.each, l);
+    const int begin = before + __builtin_amdgcn_readlane(c.sum_p - c.pieces, l) + unit * each;
+    int i0 = begin, n = each;
+    if (plan.share > 1) {
+        i0 = (uint32_t)begin / (uint32_t)plan.share;
+        n = (uint32_t)(begin + each - 1) / (uint32_t)plan.share - i0 + 1;
+    }
     const int rows = min(kRows, t.rows - t.row0);
     if (n == 1 || r0 >= rows)
         return;
     // part i of the unit
     const auto place = [&](int i) {
-        return a.part + (2 * (int64_t)(i0 + i) + ((i0 + i) * share >= begin ? 0 : 1)) * part_floats(D);
+        return a.part + (2 * (int64_t)(i0 + i) + ((i0 + i) * plan.share >= begin ? 0 : 1)) * part_floats(D);
     };
     const int g = tid / QUADS, d = tid % QUADS;
     if (!SPLIT) {
         for (int r = g; r < rows; r += GROUPS) {
-            float m = -INFINITY;
-            for (int i = 0; i < n; i++)
-                m = fmaxf(m, place(i)[r]);
-            const float zero = m == -INFINITY ? 0.0f : m;
-            float sum = 0.0f;
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-            for (int i = 0; i < n; i++) {
-                const float *x = place(i);
-                const float k = __builtin_amdgcn_exp2f(x[r] - zero);
-                sum += k * x[kRows + r];
-                acc += k * *(const f32x4 *)(x + 2 * kRows + r * D + 4 * d);
-            }
-            store_row<D>(a, t, t.row0 + r, 4 * d, acc, sum);
+            const Joined j = join_row<D, 2>(0, 1, n, r, 4 * d, place);
+            store_row<D>(a, t, t.row0 + r, 4 * d, j.acc, j.l);
         }
         return;
     }
-    float m = -INFINITY;
-    for (int i = tid; i < n; i += 512)
-        m = fmaxf(m, place(i)[r0]);
-    m = max_x16(m);
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1)
-        m = fmaxf(m, __shfl_xor(m, x));
-    if ((tid & 63) == 0)
-        m_s[tid >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-        m = fmaxf(m, m_s[i]);
-    const float zero = m == -INFINITY ? 0.0f : m;
-    float sum = 0.0f;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int i = g; i < n; i += GROUPS) {
-        const float *x = place(i);
-        const float k = __builtin_amdgcn_exp2f(x[r0] - zero);
-        sum += k * x[kRows + r0];
-        acc += k * *(const f32x4 *)(x + 2 * kRows + r0 * D + 4 * d);
+    Joined j = n <= GROUPS ? join_row<D, 1>(g, GROUPS, n, r0, 4 * d, place)
+                           : join_row<D, 8>(g, GROUPS, n, r0, 4 * d, place);
+    acc_s[g][d] = j.acc;
+    if (d == 0) {
+        m_s[g] = j.m;
+        l_s[g] = j.l;
     }
-    acc_s[g][d] = acc;
-    if (d == 0)
-        l_s[g] = sum;
     __syncthreads();
     if (g == 0) {
         const int groups = min(n, GROUPS);
-        for (int u = 1; u < groups; u++) {
-            acc += acc_s[u][d];
-            sum += l_s[u];
-        }
-        store_row<D>(a, t, t.row0 + r0, 4 * d, acc, sum);
+        for (int u = 1; u < groups; u++)
+            j.add(m_s[u], l_s[u], acc_s[u][d]);
+        store_row<D>(a, t, t.row0 + r0, 4 * d, j.acc, j.l);
     }
 }
 
@@ -775,9 +830,9 @@ int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint
     if (units * (many ? 1 : a.join_rows) >= ((int64_t)1 << 23))
         return fail(ENGRAM_E_RANGE, "engram cache_attend: %lld row tiles in one call",
                     (long long)units);
-    if (!many && units * s.max_pages >= ((int64_t)1 << 31))
+    if (!many && units * s.max_pages >= ((int64_t)1 << 30))
         return fail(ENGRAM_E_RANGE,
-                    "engram cache_attend: %lld row tiles of up to %d pages exceed 2^31 in one call",
+                    "engram cache_attend: %lld row tiles of up to %d pages exceed 2^30 in one call",
                     (long long)units, s.max_pages);
     if (many)
         return launch_attend_prompt(a, l);
