@@ -278,20 +278,26 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                 o[i] *= keep;
         }
     };
-    const auto read_values = [&](const uint8_t *vp, int t, u32x4 (&vf)[2][DT]) {
+    // 256-wide heads have registers for one of a half's two 16-token steps: the
+    // second takes the first's place as that is multiplied
+    constexpr int VC = D == 256 ? 1 : 2;
+    const auto read_values = [&](const uint8_t *vp, int t, u32x4 (&vf)[VC][DT]) {
 #pragma unroll
-        for (int c = 0; c < 2; c++)
+        for (int c = 0; c < VC; c++)
 #pragma unroll
             for (int i = 0; i < DT; i++)
                 vf[c][i] = *(const u32x4 *)(vp + v_at[2 * t + c] + 4096 * i);
     };
-    const auto values = [&](const u32x4 (&vf)[2][DT], const u32x4 (&pb)[2]) {
+    const auto values = [&](const uint8_t *vp, int t, u32x4 (&vf)[VC][DT], const u32x4 (&pb)[2]) {
 #pragma unroll
         for (int c = 0; c < 2; c++)
 #pragma unroll
-            for (int i = 0; i < DT; i++)
-                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[c][i]),
+            for (int i = 0; i < DT; i++) {
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[c % VC][i]),
                                                                __builtin_bit_cast(bf16x8, pb[c]), o[i], 0, 0, 0);
+                if (c + 1 == VC && VC == 1)
+                    vf[0][i] = *(const u32x4 *)(vp + v_at[2 * t + 1] + 4096 * i);
+            }
     };
     // 2^(s f - m) times 2^v, a power of two that joins the exponent
     const auto weights = [&](const f32x16 &s, float f, float v, u32x4 (&pb)[2]) {
@@ -315,7 +321,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                                f32x16 &s_next) {
         const float f = qs * cur.f;
         const int v_bits = (int)(__float_as_uint(cur.vs) >> 23) - 127;
-        u32x4 pb[2], vf[2][DT];
+        u32x4 pb[2], vf[VC][DT];
         logits(kp, 1 - t, s_next);
         read_values(vp, t, vf);
         float sum = weights(s, f, (float)v_bits, pb);
@@ -325,7 +331,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
 #pragma unroll
         for (int i = 0; i < 2 * KS; i++) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, DT / KS, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, VC * DT / (2 * KS), 0);
             __builtin_amdgcn_sched_group_barrier(0x002, 40 / (2 * KS), 0);
             __builtin_amdgcn_sched_group_barrier(0x400, 16 / (2 * KS), 0);
         }
@@ -336,7 +342,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
             sum = weights(s, f, (float)v_bits, pb);
         }
         l += sum * one;
-        values(vf, pb);
+        values(vp, t, vf, pb);
         __builtin_amdgcn_sched_barrier(0);
     };
 
@@ -428,7 +434,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                 }
                 rebase(s, f);
                 const float zero = m == -INFINITY ? 0.0f : m;
-                u32x4 pb[2], vf[2][DT];
+                u32x4 pb[2], vf[VC][DT];
                 read_values(lds_v[0], t, vf);
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
@@ -442,7 +448,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                     }
                     pb[e / 8][(e % 8) / 2] = cvt_bf16x2(p[0], p[1]);
                 }
-                values(vf, pb);
+                values(lds_v[0], t, vf, pb);
             }
         }
     }
