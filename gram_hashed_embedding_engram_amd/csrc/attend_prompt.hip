@@ -327,11 +327,11 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
         float sum = weights(s, f, (float)v_bits, pb);
         // the instructions in turn: a matrix instruction, then what the vector
         // unit does meanwhile
-        __builtin_amdgcn_sched_group_barrier(0x100, 2 * KS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, D == 256 ? 4 : 2 * KS, 0);
 #pragma unroll
         for (int i = 0; i < 2 * KS; i++) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, VC * DT / (2 * KS), 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, D == 256 ? 2 : DT / KS, 0);
             __builtin_amdgcn_sched_group_barrier(0x002, 40 / (2 * KS), 0);
             __builtin_amdgcn_sched_group_barrier(0x400, 16 / (2 * KS), 0);
         }
