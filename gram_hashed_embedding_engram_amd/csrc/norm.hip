@@ -4,7 +4,14 @@
 //
 // One pass over the row: a thread keeps its values in registers between the
 // sum of squares and the codes.  Bound by memory (11 bytes a value with an f32
-// residual, 7 with bf16).
+// residual, 7 with bf16): 16384 rows of 4096 f32 in 132 us (5.6 TB/s, where a
+// plain copy reaches 5.0), 777 rows of 7200 bf16 in 10.3 us; one row in 3 us,
+// which is a launch and one round trip to memory.
+//
+// Codes and bf16 sums stream past the caches (8160 x 4160 bf16: 52.8 -> 50.2
+// us); f32 sums do not, whose 16-byte halves of 32 bytes a lane would each be
+// written out (132 -> 137 us), nor do loads, whose data the kernel before has
+// just left there (1674 x 4640 f32: 18 -> 20 us).
 #include "attention.h"
 
 namespace engram {
@@ -64,7 +71,7 @@ __global__ __launch_bounds__(THREADS) void add_norm_kernel(
                     s[2 * j + 1] = bf16_hi(o[j]);
                 }
                 if (store)
-                    *(u32x4 *)((uint16_t *)sum + row + i) = o;
+                    __builtin_nontemporal_store(o, (u32x4 *)((uint16_t *)sum + row + i));
             } else if (store) {
                 *(f32x4 *)((float *)sum + row + i) = f32x4{s[0], s[1], s[2], s[3]};
                 *(f32x4 *)((float *)sum + row + i + 4) = f32x4{s[4], s[5], s[6], s[7]};
@@ -89,7 +96,7 @@ __global__ __launch_bounds__(THREADS) void add_norm_kernel(
             u32x2 o;
             o.x = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
             o.y = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
-            *(u32x2 *)(codes + row + i) = o;
+            __builtin_nontemporal_store(o, (u32x2 *)(codes + row + i));
             if ((tid & 3) == 0)
                 scales[(row + i) / 32] = (uint8_t)(k + 127);
         };
