@@ -400,6 +400,23 @@ def test_attend_long(E, new, old, kv, g, d, window):
 
 
 @pytest.mark.parametrize("new,old,kv,g,d,window", [
+    # units of even pieces, over more sequences than a wavefront's lanes
+    ([1] * 70, [1030 + 29 * (i % 7) for i in range(70)], 2, 4, 64, 0),
+    ([0, 1] * 50, [40 * i for i in range(100)], 1, 2, 64, 0),
+    ([1] * 66, [20000 if i in (3, 65) else 3 * i for i in range(66)], 2, 4, 128, 0),
+    # more units than workgroups; one long sequence among many short ones
+    ([1] * 150, [1100 + (i % 3) for i in range(150)], 4, 1, 64, 0),
+    ([1] * 40, [60000] + [70] * 39, 8, 2, 128, 0), ([1] * 90, [1500 + i for i in range(90)], 4, 2, 256, 300),
+    # units that end one page past, on and before a piece
+    ([1, 1, 1], [64 * 32, 64 * 32 - 1, 64 * 31 - 1], 1, 4, 256, 0), ([2, 1], [1020, 63], 3, 8, 256, 0)])
+def test_attend_shares(E, new, old, kv, g, d, window):
+    log(f"attend shares {len(new)} sequences, longest {max(old)}, kv {kv} g {g} d {d} window {window}")
+    st = R.Step(len(new) + d, new, old, kv, g, d)
+    st.fill_new()
+    check_attend(E, st, window)
+
+
+@pytest.mark.parametrize("new,old,kv,g,d,window", [
     ([300], [100], 2, 4, 128, 0), ([513, 60, 0, 129], [0, 700, 5, 63], 1, 4, 64, 0),
     ([200, 33], [77, 1000], 2, 3, 256, 0), ([400], [900], 1, 8, 128, 150), ([350, 90], [64, 300], 2, 1, 128, 0),
     ([150], [0], 8, 8, 64, 40), ([100], [1030], 1, 20, 128, 0), ([130], [70], 1, 6, 256, 1),
@@ -578,3 +595,17 @@ def test_stream_and_graph(E):
         x.copy_(rn(T, dim).bfloat16())               # another step between, eager
         step()
         want = out.clone()
+
+
+def test_example(E):
+    """The example's prompt and steps: finite, and the same bits again."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "attention_step.py")
+    spec = importlib.util.spec_from_file_location("attention_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    rows = example.run()
+    assert bool(torch.isfinite(rows).all())
+    assert torch.equal(rows, example.run())
