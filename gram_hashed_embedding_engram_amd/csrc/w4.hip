@@ -14,6 +14,14 @@
 // as codes beside their scales (the instruction applies both scales per 32
 // values); for bf16 activations the weights are widened to bf16 in registers,
 // which holds a code times its power of two exactly.
+//
+// 6144 x 20480, sixteen e4m3 tokens (67 MB): 15 us, 4.4 TB/s; of that 10 are the
+// bytes at a read-only stream's rate, the rest a launch, the first loads' way
+// and the last sums.  4096 x 6144, one token: 5.7 us, a launch and two trips to
+// memory.  4096 x 14336, 37 bf16 tokens: 13.8 us, bound by the activations that
+// every workgroup reads from L2 and turns in LDS (2.6 times the weights' bytes).
+// Weights a run ahead of the instructions, with registers loaded again as they
+// were used, took longer (64 bf16 tokens of 6144 x 20480: 28 -> 37 us).
 #include "attention.h"
 
 namespace engram {
