@@ -240,11 +240,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
 #pragma unroll
     for (int c = 0; c < 4; c++)
         v_at[c] = 128 * r32 + 16 * v_chunk(r32, 2 * c + h);
-    const auto logits = [&](const uint8_t *kp, int t, f32x16 &s) {
-#pragma unroll
-        for (int e = 0; e < 16; e++)
-            s[e] = 0.0f;
-        i32x8 kf[KS];
+    const auto read_keys = [&](const uint8_t *kp, int t, i32x8 (&kf)[KS]) {
 #pragma unroll
         for (int u = 0; u < KS; u++) {
             const u32x4 x = *(const u32x4 *)(kp + k_at[u][0] + 32 * D * t);
@@ -252,6 +248,13 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
             kf[u] = i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w,
                           (int)y.x, (int)y.y, (int)y.z, (int)y.w};
         }
+    };
+    const auto logits = [&](const uint8_t *kp, int t, f32x16 &s) {
+        i32x8 kf[KS];
+        read_keys(kp, t, kf);
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+            s[e] = 0.0f;
 #pragma unroll
         for (int u = 0; u < KS; u++) {
             s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf[u], qh[u], s, 0, 0, 0, kOne, 0, kOne);
@@ -327,20 +330,51 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
                                f32x16 &s_next) {
         const float f = qs * cur.f;
         const int v_bits = (int)(__float_as_uint(cur.vs) >> 23) - 127;
+        const float zero = m - (float)v_bits;
         u32x4 pb[2], vf[VC][DT];
-        logits(kp, 1 - t, s_next);
+        i32x8 kf[KS];
+        read_keys(kp, 1 - t, kf);
         read_values(vp, t, vf);
-        float sum = weights(s, f, (float)v_bits, pb);
-        // the instructions in turn: a matrix instruction, then what the vector
-        // unit does meanwhile
-        __builtin_amdgcn_sched_group_barrier(0x100, D == 256 ? 4 : 2 * KS, 0);
+        // the instructions in turn: what the vector unit does of these weights, then
+        // a matrix instruction of the next logits, which each wait for the last
+        constexpr int TURNS = 2 * KS, EACH = 16 / TURNS;
+        float part[4] = {};
 #pragma unroll
-        for (int i = 0; i < 2 * KS; i++) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, D == 256 ? 2 : DT / KS, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 40 / (2 * KS), 0);
-            __builtin_amdgcn_sched_group_barrier(0x400, 16 / (2 * KS), 0);
+        for (int e = 0; e < 16; e++)
+            s_next[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TURNS; i++) {
+#pragma unroll
+            for (int e = EACH * i; e < EACH * (i + 1); e += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], f, -zero));
+                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + 1], f, -zero));
+                part[e % 4] += p0;
+                part[e % 4 + 1] += p1;
+                pb[e / 8][(e % 8) / 2] = cvt_bf16x2(p0, p1);
+            }
+            if (D != 256)
+                __builtin_amdgcn_sched_barrier(0);
+            s_next = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                kf[i / 2], i & 1 ? ql[i / 2] : qh[i / 2], s_next, 0, 0, 0, kOne, 0, i & 1 ? kLoScale : kOne);
+            if (D != 256)
+                __builtin_amdgcn_sched_barrier(0);
         }
+        // (256-wide heads have no registers for all their keys at once: their reads
+        // take turns too)
+        if (D == 256) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+            for (int i = 0; i < TURNS; i++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 40 / TURNS, 0);
+                __builtin_amdgcn_sched_group_barrier(0x400, 16 / TURNS, 0);
+            }
+        }
+        float sum = part[0] + part[1] + (part[2] + part[3]);
+        // (a use of the logits here, or they would be multiplied past the branch,
+        // after the vector unit's work instead of beside it)
+        asm volatile("" : : "v"(s_next));
         __builtin_amdgcn_sched_barrier(0);
         const float one = exp2_int(-v_bits);
         if (__any(sum * one > 0x1p40f)) {
