@@ -361,6 +361,9 @@ def layer_static(tables: HashTables, hash_index, table: Table, d_wkv, d_qk, eps,
                                      _ptr(d_err), _stream(stream)))
 
 
+# The attention sub-layer's calls look at all their tensors in one condition and
+# go through _typed and _heads, one by one, only to name what is wrong: a call of
+# a function a tensor would cost as much as the launch.
 def _typed(t, name, dtypes, shape=None):
     """Refuse a tensor of another type, shape or, for the kernels that take
     rows back to back, a strided view."""
@@ -406,21 +409,26 @@ def add_norm(d_x, d_res, d_w, eps, d_codes, d_scales, d_sum=None, stream=None):
     k = _types or _kinds()
     shape = d_res.shape
     dim = shape[-1]
-    _typed(d_res, "res", k.res)
-    res = total = d_res.data_ptr()
-    if d_sum is not None and d_sum is not d_res:
-        _typed(d_sum, "sum", (d_res.dtype,), shape)
-        total = d_sum.data_ptr()
-    x = None
-    if d_x is not None:
-        _typed(d_x, "x", k.bf16, shape)
-        x = d_x.data_ptr()
-    _typed(d_w, "w", k.bf16, (dim,))
-    _typed(d_codes, "codes", k.e4m3, shape)
-    _typed(d_scales, "scales", k.e8m0, shape[:-1] + (dim // NORM_GROUP,))
+    groups = shape[:-1] + (dim // NORM_GROUP,)
+    total = d_res if d_sum is None else d_sum
+    if not (d_res.dtype in k.res and d_res.is_contiguous()
+            and (total is d_res or total.dtype is d_res.dtype and total.shape == shape
+                 and total.is_contiguous())
+            and (d_x is None or d_x.dtype in k.bf16 and d_x.shape == shape and d_x.is_contiguous())
+            and d_w.dtype in k.bf16 and d_w.shape == (dim,) and d_w.is_contiguous()
+            and d_codes.dtype in k.e4m3 and d_codes.shape == shape and d_codes.is_contiguous()
+            and d_scales.dtype in k.e8m0 and d_scales.shape == groups and d_scales.is_contiguous()):
+        _typed(d_res, "res", k.res)
+        _typed(total, "sum", (d_res.dtype,), shape)
+        if d_x is not None:
+            _typed(d_x, "x", k.bf16, shape)
+        _typed(d_w, "w", k.bf16, (dim,))
+        _typed(d_codes, "codes", k.e4m3, shape)
+        _typed(d_scales, "scales", k.e8m0, groups)
     rc = (_lib or lib()).engram_add_norm(
-        x, res, d_res.element_size() == 2, d_w.data_ptr(), eps, total, d_codes.data_ptr(),
-        d_scales.data_ptr(), d_res.numel() // dim if dim else 0, dim, _stream(stream))
+        None if d_x is None else d_x.data_ptr(), d_res.data_ptr(), d_res.dtype not in k.f32,
+        d_w.data_ptr(), eps, total.data_ptr(), d_codes.data_ptr(), d_scales.data_ptr(),
+        d_res.numel() // dim if dim else 0, dim, _stream(stream))
     if rc:
         _check(rc)
 
@@ -444,14 +452,16 @@ def project_w4(d_x, weights: W4, d_y, d_xs=None, stream=None):
     or e4m3 codes with d_xs [T, K/32]; d_y [T, N] bf16."""
     k = _types or _kinds()
     T, K, N = d_x.shape[0], weights.K, weights.N
-    xs = None
-    if d_xs is None:
-        _typed(d_x, "x", k.bf16, (T, K))
-    else:
-        _typed(d_x, "x", k.e4m3, (T, K))
-        _typed(d_xs, "x scales", k.e8m0, (T, weights.groups))
-        xs = d_xs.data_ptr()
-    _typed(d_y, "y", k.bf16, (T, N))
+    if not ((d_x.dtype in k.bf16 if d_xs is None else
+             d_x.dtype in k.e4m3 and d_xs.dtype in k.e8m0 and d_xs.shape == (T, weights.groups)
+             and d_xs.is_contiguous())
+            and d_x.shape == (T, K) and d_x.is_contiguous()
+            and d_y.dtype in k.bf16 and d_y.shape == (T, N) and d_y.is_contiguous()):
+        _typed(d_x, "x", k.bf16 if d_xs is None else k.e4m3, (T, K))
+        if d_xs is not None:
+            _typed(d_xs, "x scales", k.e8m0, (T, weights.groups))
+        _typed(d_y, "y", k.bf16, (T, N))
+    xs = None if d_xs is None else d_xs.data_ptr()
     w, ws = weights.at
     rc = (_lib or lib()).engram_project_w4(d_x.data_ptr(), xs, w, ws, d_y.data_ptr(), T, K, N,
                                            _stream(stream))

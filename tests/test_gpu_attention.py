@@ -543,6 +543,41 @@ def test_attend_bad_sequences(E, n, kv):
             assert torch.equal(out[2 * n:], good[2 * n:]) and bool((out[:2 * n] == 9).all())
 
 
+# ----------------------------------------------------- a cache past 32 bits
+@pytest.mark.parametrize("new,old", [([1, 1], [100, 900]), ([1, 1], [1500, 70]), ([300, 260], [200, 33])])
+def test_pages_past_4_gib(E, new, old):
+    """Pages behind 4 GiB of codes: the same bits as in a cache of their own."""
+    st = R.Step(60, new, old, 8, 4, 256)
+    freq = R.freq_of(256)
+
+    def step():
+        q, k, v = st.heads()
+        qo, out = (torch.empty(st.T, st.q, st.d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        cache, seqs = st.objects(E)
+        ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, st.T), dtype=torch.uint8, device="cuda")
+        E.cache_append(cache, seqs, k, v, freq, q, qo)
+        E.cache_attend(cache, seqs, qo, out, 1 / 16, 0, ws)
+        torch.cuda.synchronize()
+        assert int(st.err) == 0
+        return out
+
+    first = ((1 << 32) // (8 * 64 * 256)) + 5
+    codes, scales, n = [c.clone() for c in st.codes], [x.clone() for x in st.scales], st.n_pages
+    want = step()
+    appended = [c.clone() for c in st.codes] + [x.clone() for x in st.scales]
+    for which in (0, 1):
+        for kept, now in ((codes, st.codes), (scales, st.scales)):
+            big = torch.empty(first + n, *kept[which].shape[1:], dtype=kept[which].dtype, device="cuda")
+            big[first:] = kept[which]
+            now[which] = big
+    st.pages = (st.pages + first).int()
+    st.n_pages = first + n
+    assert torch.equal(step(), want)
+    for big, small in zip(st.codes + st.scales, appended):
+        assert torch.equal(big[first:].nan_to_num() if big.dtype == torch.float32 else big[first:],
+                           small.nan_to_num() if big.dtype == torch.float32 else small)
+
+
 # ------------------------------------------------------- streams and graphs
 def test_stream_and_graph(E):
     """The four operators on a stream of their own, and captured into a graph
