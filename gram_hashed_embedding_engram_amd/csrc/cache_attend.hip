@@ -221,19 +221,19 @@ __device__ __forceinline__ void values_product(const uint32_t (&vf)[4][4][D / 64
 // takes the tokens in that same order.  Keys go from memory into matrix
 // instructions as the codes they are (the query is split into two e4m3 parts);
 // values are paired by token with byte permutes and widened to bf16.  Nothing
-// of the cache passes through LDS.
-template <int D, int W>
+// of the cache passes through LDS.  Output values v0 .. v0+DV-1 of the head.
+template <int DV, int W>
 struct Reduce {
-    float o[W][kRows][D + 4];
+    float o[W][kRows][DV + 4];
     float m[W][kRows], l[W][kRows];
 };
 
-template <int D, int W>
+template <int D, int W, int DV>
 __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &t, int p0, int np,
-                                            float *part, Reduce<D, W> &red)
+                                            int v0, float *part, Reduce<DV, W> &red)
 {
     constexpr int KS = D == 64 ? 1 : D / 128;     // 128-value steps of the logits
-    constexpr int VW = D / 64;                    // dwords of a token's values a lane holds
+    constexpr int VW = DV / 64;                   // dwords of a token's values a lane holds
     int tid = threadIdx.x;
     // opaque, so that what is derived from it is not kept in registers over
     // the caller's loop
@@ -256,9 +256,9 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
     const int last = t.q.bad ? first : min(first + np, pos_hi / kPage + 1);
 
     float m = -INFINITY, l = 0.0f;
-    f32x4 o[D / 16];
+    f32x4 o[DV / 16];
 #pragma unroll
-    for (int i = 0; i < D / 16; i++)
+    for (int i = 0; i < DV / 16; i++)
         o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     i32x8 kf[4][KS];
@@ -266,7 +266,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
     float ks = 0.0f, vs = 0.0f, vs_next = 0.0f;
     // a lane's place in a page: 32 bits on top of the page's uniform address
     const uint32_t k_off = r16 * D + (D == 64 ? 16 : 32) * q4;
-    const uint32_t v_off = 4 * q4 * D + r16 * (4 * VW);
+    const uint32_t v_off = 4 * q4 * D + v0 + r16 * (4 * VW);
     const auto load_k = [&](int64_t at) {
         const uint8_t *kp = a.c.d_k + at * (kPage * D);
 #pragma unroll
@@ -424,7 +424,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
             m = top;
             l *= keep;
 #pragma unroll
-            for (int j = 0; j < D / 16; j++)
+            for (int j = 0; j < DV / 16; j++)
                 o[j] *= keep;
         }
         uint32_t pb[4][2];
@@ -470,8 +470,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
                 poison = __any(any != 0);
             }
         }
-        values_product<D>(vf, pb, [&](int u) { return o[u]; },
-                          [&](int u, const f32x4 &sum) { o[u] = sum; });
+        values_product<DV>(vf, pb, [&](int u) { return o[u]; },
+                           [&](int u, const f32x4 &sum) { o[u] = sum; });
         if (poison) {
             // how many NaN codes each row sees, by the same product
             load_v((int64_t)page * a.c.kv_heads + t.h);
@@ -489,8 +489,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
                 pb[j][0] = cvt_bf16x2(p[0], p[1]);
                 pb[j][1] = cvt_bf16x2(p[2], p[3]);
             }
-            values_product<D>(vf, pb, [&](int) { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; },
-                              [&](int u, const f32x4 &n) {
+            values_product<DV>(vf, pb, [&](int) { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; },
+                               [&](int u, const f32x4 &n) {
 #pragma unroll
                 for (int e = 0; e < 4; e++)
                     o[u][e] = n[e] > 0.0f ? __uint_as_float(0x7FC00000u) : o[u][e];
@@ -535,11 +535,11 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
 #pragma unroll
     for (int e = 0; e < 4; e++)
 #pragma unroll
-        for (int u = 0; u < D / 16; u += 4)
-            *(f32x4 *)&red.o[w][r16][(4 * q4 + e) * (D / 16) + u] =
+        for (int u = 0; u < DV / 16; u += 4)
+            *(f32x4 *)&red.o[w][r16][(4 * q4 + e) * (DV / 16) + u] =
                 f32x4{o[u][e], o[u + 1][e], o[u + 2][e], o[u + 3][e]};
     __syncthreads();
-    constexpr int QUADS = D / 4;
+    constexpr int QUADS = DV / 4;
     const int rows = min(kRows, t.rows - t.row0);
     for (int i = tid; i < rows * QUADS; i += 64 * W) {
         const int r = i / QUADS, d = 4 * (i % QUADS);
@@ -557,7 +557,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
             acc += k * *(const f32x4 *)&red.o[u][r][d];
         }
         if (!part) {
-            store_row<D>(a, t, t.row0 + r, d, acc, ll);
+            store_row<D>(a, t, t.row0 + r, v0 + d, acc, ll);
         } else {
             *(f32x4 *)(part + 2 * kRows + r * D + d) = acc;
             if (d == 0) {
@@ -576,18 +576,19 @@ __device__ __forceinline__ void raise_bad(const AttendArgs &a)
                 raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
 }
 
-// Short tables: a workgroup a unit, nothing to join.
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : W / 4) void attend_unit_kernel(AttendArgs a)
+// Short tables: a workgroup a unit and DV of its output values, nothing to join.
+template <int D, int W, int DV>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attend_unit_kernel(AttendArgs a)
 {
-    __shared__ Reduce<D, W> red;
+    __shared__ Reduce<DV, W> red;
+    const int v0 = DV * (blockIdx.x % (D / DV)), at = blockIdx.x / (D / DV);
     int b, unit;
     if (!a.s.cu) {
         const int units = (int)(((int64_t)a.s.each * a.g + kRows - 1) / kRows) * a.c.kv_heads;
-        b = blockIdx.x / units;
-        unit = blockIdx.x % units;
+        b = at / units;
+        unit = at % units;
     } else {
-        unit = blockIdx.x;
+        unit = at;
         Lanes c = lanes_at(a, 0);
         int base = 0;
         while (unit >= c.all_units()) {
@@ -604,7 +605,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : W / 4) void attend_unit_kern
         unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
     }
     const RowTile t = tile_at(a, b, unit, seq_at(a.s, b));
-    attend_unit<D, W>(a, t, 0, 1 << 26, nullptr, red);
+    attend_unit<D, W, DV>(a, t, 0, 1 << 26, v0, nullptr, red);
     raise_bad(a);                               // last: nothing waits for it
 }
 
@@ -653,8 +654,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
         const Seq q{__builtin_amdgcn_readfirstlane(seqs[l].t0), __builtin_amdgcn_readfirstlane(seqs[l].n),
                     __builtin_amdgcn_readfirstlane(seqs[l].start),
                     (bool)__builtin_amdgcn_readfirstlane(seqs[l].bad)};
-        attend_unit<D, W>(a, tile_at(a, base + l, unit, q), p0 * step, np * step,
-                          np == each ? nullptr : part + place * part_floats(D), red);
+        attend_unit<D, W, D>(a, tile_at(a, base + l, unit, q), p0 * step, np * step, 0,
+                             np == each ? nullptr : part + place * part_floats(D), red);
         at += np;
         if (at >= end)
             break;
@@ -820,8 +821,15 @@ template <int D>
 static void launch_rows(const AttendArgs &a, int64_t units, const Launch &l)
 {
     if (a.s.max_pages <= kShortPages) {
+        // Where units leave CUs idle, one takes a unit's keys and 64 of its values
+        // a workgroup: a CU takes in only so much (see above).
         constexpr int W = D == 256 ? 4 : 8;
-        dispatch(attend_unit_kernel<D, W>, dim3((unsigned)units), dim3(64 * W), l, true, true, a);
+        if (D > 64 && units * (D / 64) <= device_cus())
+            dispatch(attend_unit_kernel<D, 8, 64>, dim3((unsigned)(units * (D / 64))), dim3(512), l,
+                     true, true, a);
+        else
+            dispatch(attend_unit_kernel<D, W, D>, dim3((unsigned)units), dim3(64 * W), l, true, true,
+                     a);
         return;
     }
     dispatch(attend_share_kernel<D, 4>, dim3((unsigned)a.parts), dim3(256), l, true, false, a);
