@@ -13,7 +13,8 @@
 // (5.9 TB/s, where a stream that only reads reaches 6.6); one of 131072
 // positions with 256-wide heads (268 MB) in 52 us, 47 and 5 for the join.
 // Short calls are bound by latency: 4.4 us with no page to read, 5.9 with one,
-// and a CU takes in some 51 bytes a ns (8 pages of 128-wide heads: 8.4 us).
+// and a CU takes in some 51 bytes a ns (8 pages of 128-wide heads by a CU a unit:
+// 8.4 us; by two, each with half the values: 7.4).
 #include <type_traits>
 
 #include "attend.h"
@@ -795,9 +796,10 @@ int64_t row_units(const engram_cache &c, const Seqs &s, int32_t g)
                  : (((int64_t)s.each * g + kRows - 1) / kRows) * s.B) * c.kv_heads;
 }
 
-// Tables of so few pages are read by one workgroup a unit: 16 pages take 11 us
-// there, as long as a share of four pages (one a wavefront) and the join, whose
-// launch costs 4.7 us; fewer take less.
+// Tables of so few pages are read without a join: 16 pages take 11 us there, as
+// long as a share of four pages (one a wavefront) and the join, whose launch
+// costs 4.7 us; fewer take less, and 23 pages took 13.8 against 11.2, 32 17.8
+// against 11.6.
 constexpr int kShortPages = 16;
 constexpr int kLeastShare = 4;
 
