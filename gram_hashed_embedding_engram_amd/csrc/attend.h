@@ -71,7 +71,8 @@ struct AttendArgs {
     int32_t window_pages;     // pages a tile's windows meet at most, 0 = no bound
     int32_t parts, least;     // workgroups that share the pages; pages each takes at least
     int32_t join_rows;        // rows of a unit that the join provides for
-    float *part;              // partial results: two places a workgroup
+    int32_t splits;           // workgroups that share a 128-row tile's pages
+    float *part;              // partial results: two places a workgroup (128-row tiles: one)
 };
 
 // A partial result: kRows rows of m, of l, then of D output sums.
@@ -85,8 +86,47 @@ struct RowTile {
     Seq q;
 };
 
-// Row tiles of the many-row kernel (attend_prompt.hip) in a call, times heads.
+// A row's parts first, first + by, ... < n, joined for four output values: the
+// running maximum and sum again, U parts' loads under way at a time.  place(i)
+// is part i: ROWS rows of m, of l, then of D sums.
+struct Joined {
+    float m, l;
+    f32x4 acc;
+    __device__ __forceinline__ void add(float pm, float pl, const f32x4 &po)
+    {
+        const float top = fmaxf(m, pm), zero = top == -INFINITY ? 0.0f : top;
+        const float k = __builtin_amdgcn_exp2f(m - zero), pk = __builtin_amdgcn_exp2f(pm - zero);
+        m = top;
+        l = k * l + pk * pl;
+        acc = k * acc + pk * po;
+    }
+};
+template <int D, int ROWS, int U, class P>
+__device__ __forceinline__ Joined join_row(int first, int by, int n, int r, int d, P place)
+{
+    Joined j{-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int i = first; i < n; i += U * by) {
+        float m[U], l[U];
+        f32x4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const float *x = place(min(i + u * by, n - 1));
+            m[u] = x[r];
+            l[u] = x[ROWS + r];
+            o[u] = *(const f32x4 *)(x + 2 * ROWS + r * D + d);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (i + u * by < n)
+                j.add(m[u], l[u], o[u]);
+    }
+    return j;
+}
+
+// Row tiles of the many-row kernel (attend_prompt.hip) in a call, times heads,
+// and the workspace that it needs.
 int64_t prompt_tiles(const engram_cache &c, const Seqs &s, int32_t g);
+size_t prompt_bytes(const engram_cache &c, const Seqs &s, int32_t g);
 int32_t launch_attend_prompt(const AttendArgs &a, const Launch &l);
 
 }  // namespace engram

@@ -19,7 +19,39 @@ __device__ __forceinline__ int k_chunk(int row, int c)
 }
 __device__ __forceinline__ int v_chunk(int d, int c) { return c ^ ((d ^ (d >> 2)) & 7); }
 
-// A workgroup's four wavefronts take 32 rows each against the same pages.
+constexpr int64_t tile_floats(int d) { return kTileRows * (int64_t)(d + 2); }
+
+// Tile `item` of a call: rows row0 .. of sequence b's.
+struct Tile {
+    Seq q;
+    int b, row0, rows;
+    bool on;
+};
+__device__ __forceinline__ Tile prompt_tile(const AttendArgs &a, int item)
+{
+    Tile t{{0, 0, 0, false}, 0, 0, 0, true};
+    int piece;
+    if (!a.s.cu) {
+        const int each = (int)(((int64_t)a.s.each * a.g + kTileRows - 1) / kTileRows);
+        t.b = (uint32_t)item / (uint32_t)each;
+        piece = item - t.b * each;
+    } else {
+        t.on = find_piece(item, a.s.B,
+                          [&](int i) { return (int)(((int64_t)seq_at(a.s, i).n * a.g + kTileRows - 1) / kTileRows); },
+                          t.b, piece);
+        if (!t.on)
+            return t;
+    }
+    t.q = seq_at(a.s, t.b);
+    t.rows = t.q.n * a.g;
+    // those that see most keys first
+    t.row0 = ((t.rows + kTileRows - 1) / kTileRows - 1 - piece) * kTileRows;
+    return t;
+}
+
+// A workgroup's four wavefronts take 32 rows each against the same pages, all
+// that the rows see or, with SPLIT, one of a.splits equal runs of them, whose
+// maxima, sums and outputs go to the workspace.
 //
 // S^T = K Q^T: lane l holds query l % 32 and, of each 32 tokens, tokens
 // 8j + 4(l / 32) + e.  Maximum, sum and rescaling are per lane (and lane ^ 32),
@@ -41,7 +73,7 @@ __device__ __forceinline__ int v_chunk(int d, int c) { return c ^ ((d ^ (d >> 2)
 // runs at 1.22; pages one by one, without the pipeline, took 351 us).  4096
 // tokens after 4096: 64-wide heads 0.82 PFLOP/s, 256-wide ones 0.87 (their sums
 // and queries leave one wavefront a SIMD).
-template <int D>
+template <int D, bool SPLIT>
 __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs a)
 {
     constexpr int KS = D / 64, DT = D / 32, CH = D / 16;
@@ -57,26 +89,17 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
 
     // ---- which rows
     const int kv = a.c.kv_heads;
-    const int head = blockIdx.x % kv;
-    const int64_t item = blockIdx.x / kv;
-    int b, piece, tiles;
+    const int split = SPLIT ? blockIdx.x % a.splits : 0, at = SPLIT ? blockIdx.x / a.splits : blockIdx.x;
+    const int item = (uint32_t)at / (uint32_t)kv, head = at - item * kv;
     if (blockIdx.x == 0)
         for (int i = tid; i < a.s.B; i += 64 * kTileWaves)
             if (seq_at(a.s, i).bad)
                 raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
-    if (!a.s.cu) {
-        tiles = (int)(((int64_t)a.s.each * a.g + kTileRows - 1) / kTileRows);
-        b = (int)(item / tiles);
-        piece = (int)(item - (int64_t)b * tiles);
-    } else if (!find_piece(item, a.s.B,
-                           [&](int i) { return (int)(((int64_t)seq_at(a.s, i).n * a.g + kTileRows - 1) / kTileRows); },
-                           b, piece)) {
+    const Tile tile = prompt_tile(a, item);
+    if (!tile.on)
         return;
-    }
-    const Seq q = seq_at(a.s, b);
-    const int rows = q.n * a.g;
-    tiles = (rows + kTileRows - 1) / kTileRows;
-    const int row0 = (tiles - 1 - piece) * kTileRows;      // those that see most keys first
+    const Seq q = tile.q;
+    const int b = tile.b, rows = tile.rows, row0 = tile.row0;
     const int row = row0 + 32 * w + r32;
     const bool valid = row < rows;
     const int tok = min(row, rows - 1) / a.g;
@@ -89,7 +112,12 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     const int my_lo = q.start + min(row0 + 32 * w, rows - 1) / a.g;
     const int my_hi = q.start + min(row0 + 32 * w + 31, rows - 1) / a.g;
     const int my_see = a.window > 0 ? max(my_lo - a.window + 1, 0) : 0;
-    const int first = see_lo / kPage, last = q.bad ? first : pos_hi / kPage + 1;
+    int first = see_lo / kPage, last = q.bad ? first : pos_hi / kPage + 1;
+    if (SPLIT) {
+        const int each = (uint32_t)(last - first + a.splits - 1) / (uint32_t)a.splits;
+        first += split * each;
+        last = min(first + each, last);
+    }
 
     // ---- queries
     i32x8 qh[KS], ql[KS];
@@ -534,9 +562,24 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
         }
     }
     l = add_x32(l);
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     if (!valid)
         return;
+    if (SPLIT) {
+        float *part = a.part + (int64_t)blockIdx.x * tile_floats(D);
+        const int r = 32 * w + r32;
+        if (h == 0) {
+            part[r] = m;
+            part[kTileRows + r] = l;
+        }
+        part += 2 * kTileRows + r * D;
+#pragma unroll
+        for (int i = 0; i < DT; i++)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *(f32x4 *)(part + 32 * i + 2 * e + 4 * h) = f32x4{o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]};
+        return;
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     uint16_t *out = a.out + ((int64_t)(q.t0 + tok) * a.heads + head * a.g + row % a.g) * D;
 #pragma unroll
     for (int i = 0; i < DT; i++)
@@ -549,6 +592,64 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
         }
 }
 
+// Joins the runs of a tile's rows, 16 rows a workgroup.
+constexpr int kJoinRows = 16, kJoins = kTileRows / kJoinRows;
+
+template <int D>
+__global__ __launch_bounds__(256) void attend_tile_join_kernel(AttendArgs a)
+{
+    constexpr int QUADS = D / 4;
+    const int at = blockIdx.x / kJoins, group = blockIdx.x % kJoins;
+    const int item = (uint32_t)at / (uint32_t)a.c.kv_heads, head = at - item * a.c.kv_heads;
+    const Tile t = prompt_tile(a, item);
+    if (!t.on)
+        return;
+    const float *parts = a.part + (int64_t)at * a.splits * tile_floats(D);
+    const auto place = [&](int i) { return parts + i * tile_floats(D); };
+    for (int i = threadIdx.x; i < kJoinRows * QUADS; i += 256) {
+        const int r = kJoinRows * group + i / QUADS, d = 4 * (i % QUADS), row = t.row0 + r;
+        if (row >= t.rows)
+            continue;
+        const Joined j = join_row<D, kTileRows, 4>(0, 1, a.splits, r, d, place);
+        const float inv = j.l != 0.0f ? 1.0f / j.l : 0.0f;
+        const int tok = (uint32_t)row / (uint32_t)a.g;
+        u32x2 y;
+        y.x = cvt_bf16x2(j.acc.x * inv, j.acc.y * inv);
+        y.y = cvt_bf16x2(j.acc.z * inv, j.acc.w * inv);
+        *(u32x2 *)(a.out + ((int64_t)(t.q.t0 + tok) * a.heads + head * a.g + row - tok * a.g) * D + d) = y;
+    }
+}
+
+// Workgroups that share a tile's pages: as many as the chip holds beside each
+// other, while each has so many pages of the table's width to read that the time
+// it saves (1.2, 1.7 and 3-4 us a page of 64-, 128- and 256-wide heads) exceeds
+// the join's 5 us.  512 tokens after 30000, 32 heads of 128 over 8: 565 -> 245
+// us; 818 tokens of 6 heads of 64 after 227: 22 -> 18; 2 x 805 of 6 heads of 256
+// over 2 after 786: 71 -> 45.  With pieces of 4 pages 64-wide heads lost (750
+// tokens in three ragged chunks: 18 -> 21), with 6 256-wide ones (9 pages: 31 -> 36).
+int32_t splits_of(const engram_cache &c, const Seqs &s, int32_t g)
+{
+    constexpr int64_t kMost = 16;
+    const int64_t least = c.head_dim == 64 ? 8 : c.head_dim == 128 ? 6 : 4;
+    const int64_t resident = device_cus() * (c.head_dim == 256 ? 1 : 2);
+    int64_t n = resident / prompt_tiles(c, s, g);
+    n = n < s.max_pages / least ? n : s.max_pages / least;
+    return (int32_t)(n < 1 ? 1 : n > kMost ? kMost : n);
+}
+
+template <int D>
+void launch_dim(const AttendArgs &a, const Launch &l)
+{
+    const int64_t tiles = prompt_tiles(a.c, a.s, a.g);
+    const dim3 block(64 * kTileWaves);
+    if (a.splits == 1) {
+        dispatch(attend_tile_kernel<D, false>, dim3((unsigned)tiles), block, l, true, true, a);
+        return;
+    }
+    dispatch(attend_tile_kernel<D, true>, dim3((unsigned)(tiles * a.splits)), block, l, true, false, a);
+    dispatch(attend_tile_join_kernel<D>, dim3((unsigned)(tiles * kJoins)), dim3(256), l, false, true, a);
+}
+
 }  // namespace
 
 int64_t prompt_tiles(const engram_cache &c, const Seqs &s, int32_t g)
@@ -557,15 +658,22 @@ int64_t prompt_tiles(const engram_cache &c, const Seqs &s, int32_t g)
                  : (((int64_t)s.each * g + kTileRows - 1) / kTileRows) * s.B) * c.kv_heads;
 }
 
-int32_t launch_attend_prompt(const AttendArgs &a, const Launch &l)
+size_t prompt_bytes(const engram_cache &c, const Seqs &s, int32_t g)
 {
-    const dim3 grid((unsigned)prompt_tiles(a.c, a.s, a.g)), block(64 * kTileWaves);
+    const int32_t n = splits_of(c, s, g);
+    return n == 1 ? 0 : sizeof(float) * (size_t)(prompt_tiles(c, s, g) * n * tile_floats(c.head_dim));
+}
+
+int32_t launch_attend_prompt(const AttendArgs &args, const Launch &l)
+{
+    AttendArgs a = args;
+    a.splits = splits_of(a.c, a.s, a.g);
     if (a.c.head_dim == 64)
-        dispatch(attend_tile_kernel<64>, grid, block, l, true, true, a);
+        launch_dim<64>(a, l);
     else if (a.c.head_dim == 128)
-        dispatch(attend_tile_kernel<128>, grid, block, l, true, true, a);
+        launch_dim<128>(a, l);
     else
-        dispatch(attend_tile_kernel<256>, grid, block, l, true, true, a);
+        launch_dim<256>(a, l);
     return launch_status("engram cache_attend prompt kernel");
 }
 

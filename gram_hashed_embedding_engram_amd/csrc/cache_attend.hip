@@ -679,42 +679,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
     raise_bad(a);
 }
 
-// A row's parts first, first + by, ... < n, joined for four output values: the
-// running maximum and sum again, U parts' loads under way at a time.
-struct Joined {
-    float m, l;
-    f32x4 acc;
-    __device__ __forceinline__ void add(float pm, float pl, const f32x4 &po)
-    {
-        const float top = fmaxf(m, pm), zero = top == -INFINITY ? 0.0f : top;
-        const float k = __builtin_amdgcn_exp2f(m - zero), pk = __builtin_amdgcn_exp2f(pm - zero);
-        m = top;
-        l = k * l + pk * pl;
-        acc = k * acc + pk * po;
-    }
-};
-template <int D, int U, class P>
-__device__ __forceinline__ Joined join_row(int first, int by, int n, int r, int d, P place)
-{
-    Joined j{-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int i = first; i < n; i += U * by) {
-        float m[U], l[U];
-        f32x4 o[U];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const float *x = place(min(i + u * by, n - 1));
-            m[u] = x[r];
-            l[u] = x[kRows + r];
-            o[u] = *(const f32x4 *)(x + 2 * kRows + r * D + d);
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++)
-            if (i + u * by < n)
-                j.add(m[u], l[u], o[u]);
-    }
-    return j;
-}
-
 // Joins the parts of a unit's rows.  A workgroup takes a unit, or, with
 // SPLIT, where units are few and their parts many, a unit's row; G thread
 // groups of D/4 then take parts in turn.
@@ -758,13 +722,13 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
     const int g = tid / QUADS, d = tid % QUADS;
     if (!SPLIT) {
         for (int r = g; r < rows; r += GROUPS) {
-            const Joined j = join_row<D, 2>(0, 1, n, r, 4 * d, place);
+            const Joined j = join_row<D, kRows, 2>(0, 1, n, r, 4 * d, place);
             store_row<D>(a, t, t.row0 + r, 4 * d, j.acc, j.l);
         }
         return;
     }
-    Joined j = n <= GROUPS ? join_row<D, 1>(g, GROUPS, n, r0, 4 * d, place)
-                           : join_row<D, 8>(g, GROUPS, n, r0, 4 * d, place);
+    Joined j = n <= GROUPS ? join_row<D, kRows, 1>(g, GROUPS, n, r0, 4 * d, place)
+                           : join_row<D, kRows, 8>(g, GROUPS, n, r0, 4 * d, place);
     acc_s[g][d] = j.acc;
     if (d == 0) {
         m_s[g] = j.m;
@@ -783,7 +747,7 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
 // of them for every eighth CU, else tiles of 16 whose keys are shared out.  (In
 // us, 16-row tiles against 128-row ones: 534 tokens of 48 heads over 8 key heads
 // 43 and 18; 816 tokens of 16 heads over 2 27 and 16; 818 tokens of 6 heads
-// over 1, 39 tiles, 15 and 24; 2 x 4096 ragged tokens of 32 heads 1658 and 278.)
+// over 1, 39 tiles, 15 and 18; 2 x 4096 ragged tokens of 32 heads 1658 and 278.)
 bool many_rows(const engram_cache &c, const Seqs &s, int32_t g)
 {
     return (int64_t)s.T * g >= 64 * (int64_t)s.B && prompt_tiles(c, s, g) >= device_cus() / 8;
@@ -814,7 +778,9 @@ int32_t parts_of(const engram_cache &c)
 
 size_t attend_bytes(const engram_cache &c, const Seqs &s, int32_t q_heads)
 {
-    if (many_rows(c, s, q_heads / c.kv_heads) || s.max_pages <= kShortPages)
+    if (many_rows(c, s, q_heads / c.kv_heads))
+        return prompt_bytes(c, s, q_heads / c.kv_heads);
+    if (s.max_pages <= kShortPages)
         return 0;
     return sizeof(float) * 2 * (size_t)parts_of(c) * (size_t)part_floats(c.head_dim);
 }
@@ -848,7 +814,7 @@ int32_t launch_attend(const engram_cache &c, const Seqs &s, const Heads &q, uint
 {
     const int32_t g = q_heads / c.kv_heads;
     const int32_t w = window < ((int64_t)1 << 31) ? (int32_t)window : 0;
-    AttendArgs a{c, s, q, out, q_heads, g, scale * kLog2e, w, 0, 0, 0, 0, (float *)ws};
+    AttendArgs a{c, s, q, out, q_heads, g, scale * kLog2e, w, 0, 0, 0, 0, 1, (float *)ws};
     const bool many = many_rows(c, s, g);
     const int64_t units = many ? prompt_tiles(c, s, g) : row_units(c, s, g);
     a.join_rows = !s.cu && (int64_t)s.each * g < kRows ? s.each * g : kRows;

@@ -422,7 +422,10 @@ def test_attend_shares(E, new, old, kv, g, d, window):
     ([150], [0], 8, 8, 64, 40), ([100], [1030], 1, 20, 128, 0), ([130], [70], 1, 6, 256, 1),
     ([1100], [33], 2, 4, 128, 0), ([700, 300], [77, 200], 4, 3, 256, 0), ([600], [64], 4, 8, 64, 90),
     ([700], [300], 4, 4, 256, 64), ([800, 3], [5, 90], 4, 6, 64, 0), ([600], [130], 8, 3, 128, 33),
-    ([90] * 5, [11 * i for i in range(5)], 2, 4, 128, 0)])
+    ([90] * 5, [11 * i for i in range(5)], 2, 4, 128, 0),
+    # tiles whose pages are shared out: long caches, short ones among them, windows
+    ([300], [3000], 8, 2, 128, 0), ([520, 64], [2500, 3], 4, 4, 64, 700), ([200, 129, 0], [2000, 1, 9], 8, 3, 256, 0),
+    ([257], [6000], 8, 4, 128, 100), ([150], [1200], 8, 8, 256, 0), ([1, 600], [4000, 2100], 4, 4, 64, 0)])
 def test_attend_prompt(E, new, old, kv, g, d, window):
     log(f"attend prompt {new} after {old} kv {kv} g {g} d {d} window {window}")
     st = R.Step(sum(old) + 1, new, old, kv, g, d)
