@@ -638,6 +638,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
     int unit = (uint32_t)p0 / (uint32_t)__builtin_amdgcn_readlane(c.each, l);
     p0 -= unit * __builtin_amdgcn_readlane(c.each, l);
     const auto keep = [&] {
+        __syncthreads();                        // the sequences before these have been read
         if (threadIdx.x < 64) {
             seqs[threadIdx.x] = c.q;
             each_s[threadIdx.x] = c.each;

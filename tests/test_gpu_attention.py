@@ -416,6 +416,26 @@ def test_attend_shares(E, new, old, kv, g, d, window):
     check_attend(E, st, window)
 
 
+def empty_run(B, lo, hi, past):
+    """One token for each of B sequences, none for sequences lo .. hi-1."""
+    return ([0 if lo <= i < hi else 1 for i in range(B)],
+            [70 if lo <= i < hi else past + 5 * (i % 9) for i in range(B)])
+
+
+@pytest.mark.parametrize("B,lo,hi,past,kv,g,d", [
+    (140, 40, 64, 1100, 8, 1, 64), (140, 40, 65, 1100, 8, 4, 128), (140, 63, 66, 1100, 8, 2, 64),
+    (140, 10, 64, 1100, 4, 1, 256), (230, 50, 130, 1100, 8, 2, 64), (260, 30, 200, 1100, 8, 1, 128),
+    (300, 1, 299, 40000, 2, 4, 64), (200, 64, 128, 1090, 4, 2, 256)])
+def test_attend_shares_over_empty_sequences(E, B, lo, hi, past, kv, g, d):
+    """Workgroups whose share walks on over runs of sequences without tokens,
+    inside and across groups of 64 sequences."""
+    log(f"attend over empty sequences {lo}..{hi} of {B}, kv {kv} g {g} d {d}")
+    new, old = empty_run(B, lo, hi, past)
+    st = R.Step(B + lo, new, old, kv, g, d)
+    st.fill_new()
+    check_attend(E, st)
+
+
 @pytest.mark.parametrize("new,old,kv,g,d,window", [
     ([300], [100], 2, 4, 128, 0), ([513, 60, 0, 129], [0, 700, 5, 63], 1, 4, 64, 0),
     ([200, 33], [77, 1000], 2, 3, 256, 0), ([400], [900], 1, 8, 128, 150), ([350, 90], [64, 300], 2, 1, 128, 0),
