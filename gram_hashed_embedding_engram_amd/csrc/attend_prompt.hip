@@ -35,14 +35,14 @@ __device__ __forceinline__ Tile prompt_tile(const AttendArgs &a, int item)
         const int each = (int)(((int64_t)a.s.each * a.g + kTileRows - 1) / kTileRows);
         t.b = (uint32_t)item / (uint32_t)each;
         piece = item - t.b * each;
+        t.q = even_seq(a.s, t.b);
     } else {
-        t.on = find_piece(item, a.s.B,
-                          [&](int i) { return (int)(((int64_t)seq_at(a.s, i).n * a.g + kTileRows - 1) / kTileRows); },
-                          t.b, piece);
+        t.on = find_piece(item, a.s,
+                          [&](const Seq &q) { return (int)(((int64_t)q.n * a.g + kTileRows - 1) / kTileRows); },
+                          t.b, piece, t.q);
         if (!t.on)
             return t;
     }
-    t.q = seq_at(a.s, t.b);
     t.rows = t.q.n * a.g;
     // those that see most keys first
     t.row0 = ((t.rows + kTileRows - 1) / kTileRows - 1 - piece) * kTileRows;
@@ -92,9 +92,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     const int split = SPLIT ? blockIdx.x % a.splits : 0, at = SPLIT ? blockIdx.x / a.splits : blockIdx.x;
     const int item = (uint32_t)at / (uint32_t)kv, head = at - item * kv;
     if (blockIdx.x == 0)
-        for (int i = tid; i < a.s.B; i += 64 * kTileWaves)
-            if (seq_at(a.s, i).bad)
-                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
+        raise_bad(a.s);
     const Tile tile = prompt_tile(a, item);
     if (!tile.on)
         return;

@@ -93,30 +93,25 @@ struct Seqs {
     int32_t T, each;
 };
 
-// Sequence b: its first token, how many it brings and the position of the
-// first; n = 0 with `bad` set where its bounds do not hold.
+// A sequence: its first token, how many it brings and the position of the
+// first; n = 0 with `bad` set where its token bounds do not hold.
 struct Seq {
     int32_t t0, n, start;
     bool bad;
 };
 
-__device__ __forceinline__ Seq seq_at(const Seqs &s, int b)
+__device__ __forceinline__ Seq make_seq(const Seqs &s, int32_t t0, int32_t n, int32_t start,
+                                        bool tokens)
 {
-    Seq q;
-    int32_t t1;
-    if (s.cu) {
-        q.t0 = s.cu[b];
-        t1 = s.cu[b + 1];
-    } else {
-        q.t0 = b * s.each;
-        t1 = q.t0 + s.each;
-    }
-    q.start = s.start[b];
-    const bool tokens = q.t0 >= 0 && t1 >= q.t0 && t1 <= s.T;
-    q.n = tokens ? t1 - q.t0 : 0;
-    q.bad = !tokens || q.start < 0 ||
-            (int64_t)q.start + q.n > (int64_t)s.max_pages * kPage;
+    Seq q{t0, tokens ? n : 0, start, false};
+    q.bad = !tokens || start < 0 || (int64_t)start + q.n > (int64_t)s.max_pages * kPage;
     return q;
+}
+
+// Sequence b of a call without token bounds.
+__device__ __forceinline__ Seq even_seq(const Seqs &s, int b)
+{
+    return make_seq(s, b * s.each, s.each, s.start[b], true);
 }
 
 __device__ __forceinline__ void raise(int32_t *err, int32_t bits)
@@ -125,40 +120,95 @@ __device__ __forceinline__ void raise(int32_t *err, int32_t bits)
         atomicOr(err, bits);
 }
 
-// Inclusive sum over the wavefront's lanes, in data-parallel moves: within
-// rows of 16 lanes by shifts of 1, 2, 4, 8, then rows 0 and 2 into 1 and 3 and
-// row 1 into 2 and 3.
+// Inclusive sum (or, of values >= 0, maximum) over the wavefront's lanes, in
+// data-parallel moves: within rows of 16 lanes by shifts of 1, 2, 4, 8, then
+// rows 0 and 2 into 1 and 3 and row 1 into 2 and 3.
 template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_iadd(int v)
+__device__ __forceinline__ int dpp_from(int v)
 {
-    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
 }
 __device__ __forceinline__ int wave_scan(int v)
 {
-    v = dpp_iadd<0x111, 0xF>(v);
-    v = dpp_iadd<0x112, 0xF>(v);
-    v = dpp_iadd<0x114, 0xF>(v);
-    v = dpp_iadd<0x118, 0xF>(v);
-    v = dpp_iadd<0x142, 0xA>(v);
-    v = dpp_iadd<0x143, 0xC>(v);
+    v += dpp_from<0x111, 0xF>(v);
+    v += dpp_from<0x112, 0xF>(v);
+    v += dpp_from<0x114, 0xF>(v);
+    v += dpp_from<0x118, 0xF>(v);
+    v += dpp_from<0x142, 0xA>(v);
+    v += dpp_from<0x143, 0xC>(v);
+    return v;
+}
+__device__ __forceinline__ int wave_max_scan(int v)
+{
+    v = max(v, dpp_from<0x111, 0xF>(v));
+    v = max(v, dpp_from<0x112, 0xF>(v));
+    v = max(v, dpp_from<0x114, 0xF>(v));
+    v = max(v, dpp_from<0x118, 0xF>(v));
+    v = max(v, dpp_from<0x142, 0xA>(v));
+    v = max(v, dpp_from<0x143, 0xC>(v));
     return v;
 }
 
-// Work item i of a grid laid over the sequences: finds the sequence b and the
-// piece of it, where sequence b has pieces(b) of them, in order.  Called by
-// whole wavefronts with a uniform i; false past the last item.
-template <class F>
-__device__ __forceinline__ bool find_piece(int i, int B, F pieces, int &b, int &piece)
+// Sequences base .. base+63, one a lane (no tokens past the last).  With token
+// bounds a sequence may not begin before the end of an earlier one: no token
+// counts twice, so that a call's sequences never bring more than its T tokens,
+// which its grid, its workspace and 32-bit counts are laid out for.  reach: the
+// furthest end of the sequences before base, moved on past these.
+__device__ __forceinline__ Seq seqs_at(const Seqs &s, int base, int32_t &reach)
 {
-    const int lane = threadIdx.x & 63;
-    for (int base = 0; base < B; base += 64) {
-        const int own = base + lane < B ? pieces(base + lane) : 0;
+    const int b = base + (threadIdx.x & 63);
+    const Seq none{0, 0, 0, false};
+    if (!s.cu)
+        return b < s.B ? even_seq(s, b) : none;
+    const bool in = b < s.B;
+    const int32_t t0 = in ? s.cu[b] : 0, t1 = in ? s.cu[b + 1] : 0, start = in ? s.start[b] : 0;
+    const bool own = t0 >= 0 && t1 >= t0 && t1 <= s.T;
+    const int ends = wave_max_scan(own ? t1 : 0);
+    const int before = max((int)reach, dpp_from<0x138, 0xF>(ends));     // up to lane l - 1
+    reach = max((int)reach, __builtin_amdgcn_readlane(ends, 63));
+    return in ? make_seq(s, t0, t1 - t0, start, own && t0 >= before) : none;
+}
+
+__device__ __forceinline__ Seq lane_seq(const Seq &q, int l)
+{
+    return Seq{__builtin_amdgcn_readlane(q.t0, l), __builtin_amdgcn_readlane(q.n, l),
+               __builtin_amdgcn_readlane(q.start, l), (bool)__builtin_amdgcn_readlane(q.bad, l)};
+}
+
+// Sequences whose bounds do not hold set their error bit (one workgroup of a
+// call; whole wavefronts).
+__device__ __forceinline__ void raise_bad(const Seqs &s)
+{
+    if (!s.cu) {
+        for (int b = threadIdx.x; b < s.B; b += blockDim.x)
+            if (even_seq(s, b).bad)
+                raise(s.err, ENGRAM_DEVERR_SEQUENCE);
+    } else if (threadIdx.x < 64) {
+        int32_t reach = 0;
+        for (int base = 0; base < s.B; base += 64)
+            if (seqs_at(s, base, reach).bad)
+                raise(s.err, ENGRAM_DEVERR_SEQUENCE);
+    }
+}
+
+// Work item i of a grid laid over sequences with token bounds: finds the
+// sequence b, which is q, and the piece of it, where a sequence has pieces(q) of
+// them (none if it brings no token), in order.  Called by whole wavefronts with
+// a uniform i; false past the last item.
+template <class F>
+__device__ __forceinline__ bool find_piece(int i, const Seqs &s, F pieces, int &b, int &piece, Seq &q)
+{
+    int32_t reach = 0;
+    for (int base = 0; base < s.B; base += 64) {
+        const Seq lane = seqs_at(s, base, reach);
+        const int own = pieces(lane);
         const int sum = wave_scan(own);
         const uint64_t over = __ballot(sum > i);
         if (over) {
             const int at = __builtin_ctzll(over);
             b = base + at;
             piece = i - __builtin_amdgcn_readlane(sum - own, at);
+            q = lane_seq(lane, at);
             return true;
         }
         i -= __builtin_amdgcn_readlane(sum, 63);

@@ -267,27 +267,25 @@ __global__ __launch_bounds__(threads_of<D>) void append_kernel(AppendArgs a)
     const int groups = (a.c.kv_heads + a.heads - 1) / a.heads;
     const int pages = 2 * a.pieces * groups;
     if (blockIdx.x == 0)
-        for (int i = tid; i < a.s.B; i += kThreads)
-            if (seq_at(a.s, i).bad)
-                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
+        raise_bad(a.s);
     if ((int)blockIdx.x < pages) {
         const bool z = blockIdx.x & 1;
         const int h = blockIdx.x / 2 % groups * a.heads;
         int i = blockIdx.x / 2 / groups, b, piece;
-        const auto touched = [&](int x) {
-            const Seq q = seq_at(a.s, x);
-            return q.bad || q.n == 0 ? 0 : (q.start + q.n - 1) / kPage - q.start / kPage + 1;
+        Seq q;
+        const auto touched = [](const Seq &x) {
+            return x.bad || x.n == 0 ? 0 : (x.start + x.n - 1) / kPage - x.start / kPage + 1;
         };
         if (!a.s.cu) {                          // every sequence has room for as many pages
             const int each = a.pieces / a.s.B;
             b = i / each;
             piece = i % each;
-            if (piece >= touched(b))
+            q = even_seq(a.s, b);
+            if (piece >= touched(q))
                 return;
-        } else if (!find_piece(i, a.s.B, touched, b, piece)) {
+        } else if (!find_piece(i, a.s, touched, b, piece, q)) {
             return;
         }
-        const Seq q = seq_at(a.s, b);
         const int blk = q.start / kPage + piece;
         const int32_t page = a.s.pages[(int64_t)b * a.s.max_pages + blk];
         if (page < 0 || page >= a.c.n_pages) {
@@ -302,21 +300,15 @@ __global__ __launch_bounds__(threads_of<D>) void append_kernel(AppendArgs a)
     const int t0 = (blockIdx.x - pages) * a.run;
     for (int i = tid >> 6; i < a.run; i += kThreads / 64) {
         int b = 0, piece = 0;
-        bool found;
+        Seq q{0, 0, 0, true};
         if (!a.s.cu) {
-            b = (t0 + i) / a.s.each;
             piece = (t0 + i) % a.s.each;
-            found = t0 + i < a.s.T;
+            if (t0 + i < a.s.T)
+                q = even_seq(a.s, (t0 + i) / a.s.each);
         } else {
-            found = find_piece(t0 + i, a.s.B,
-                               [&](int x) {
-                                   const Seq q = seq_at(a.s, x);
-                                   return q.bad ? 0 : q.n;
-                               },
-                               b, piece);
+            find_piece(t0 + i, a.s, [](const Seq &x) { return x.bad ? 0 : x.n; }, b, piece, q);
         }
         if ((tid & 63) == 0) {
-            const Seq q = found ? seq_at(a.s, b) : Seq{0, 0, 0, true};
             tok_s[i] = q.bad ? -1 : q.t0 + piece;
             pos_s[i] = q.start + piece;
         }

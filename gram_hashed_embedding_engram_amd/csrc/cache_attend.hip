@@ -57,13 +57,9 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const Seq &q)
 struct Lanes {
     Seq q;
     int each, units, pieces, sum_u, sum_p;          // each: pieces a unit
+    int32_t reach;                                  // the furthest token up to and with them
     __device__ __forceinline__ int all_units() const { return __builtin_amdgcn_readlane(sum_u, 63); }
     __device__ __forceinline__ int all_pieces() const { return __builtin_amdgcn_readlane(sum_p, 63); }
-    __device__ __forceinline__ Seq seq(int l) const
-    {
-        return Seq{__builtin_amdgcn_readlane(q.t0, l), __builtin_amdgcn_readlane(q.n, l),
-                   __builtin_amdgcn_readlane(q.start, l), (bool)__builtin_amdgcn_readlane(q.bad, l)};
-    }
     __device__ __forceinline__ void cut(int most)
     {
         each = (int)((uint32_t)(each + most - 1) / (uint32_t)most);
@@ -71,16 +67,15 @@ struct Lanes {
         sum_p = wave_scan(pieces);
     }
 };
-__device__ __forceinline__ Lanes lanes_at(const AttendArgs &a, int base, int most = 0)
+// (reach: that of the sequences before base.)
+__device__ __forceinline__ Lanes lanes_at(const AttendArgs &a, int base, int32_t reach, int most = 0)
 {
-    const int b = base + (threadIdx.x & 63);
-    Lanes c{{0, 0, 0, false}, 0, 0, 0, 0, 0};
-    if (b < a.s.B) {
-        c.q = seq_at(a.s, b);
-        c.each = unit_pages(a, c.q);
-        c.units = unit_tiles(a, c.q) * a.c.kv_heads;
-        c.pieces = c.units * c.each;
-    }
+    Lanes c;
+    c.reach = reach;
+    c.q = seqs_at(a.s, base, c.reach);
+    c.each = unit_pages(a, c.q);
+    c.units = unit_tiles(a, c.q) * a.c.kv_heads;
+    c.pieces = c.units * c.each;
     c.sum_u = wave_scan(c.units);
     if (most > 0)
         c.cut(most);
@@ -105,10 +100,12 @@ constexpr int kBeginPages = 16;
 __device__ __forceinline__ Plan plan_of(const AttendArgs &a, Lanes &c)
 {
     int total = c.all_pieces(), units = c.all_units();
+    int32_t reach = c.reach;
     for (int base = 64; base < a.s.B; base += 64) {
-        const Lanes next = lanes_at(a, base);
+        const Lanes next = lanes_at(a, base, reach);
         total += next.all_pieces();
         units += next.all_units();
+        reach = next.reach;
     }
     const int share = max((int)(((uint32_t)total + a.parts - 1) / (uint32_t)a.parts), a.least);
     if (units < a.parts) {
@@ -121,8 +118,12 @@ __device__ __forceinline__ Plan plan_of(const AttendArgs &a, Lanes &c)
             c.each = pages;
             c.cut(most);
             int pieces = c.all_pieces();
-            for (int base = 64; base < a.s.B; base += 64)
-                pieces += lanes_at(a, base, most).all_pieces();
+            reach = c.reach;
+            for (int base = 64; base < a.s.B; base += 64) {
+                const Lanes next = lanes_at(a, base, reach, most);
+                pieces += next.all_pieces();
+                reach = next.reach;
+            }
             if (pieces <= a.parts)
                 return Plan{1, pieces, most};
             const uint32_t left = a.parts - units;
@@ -572,9 +573,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs &a, const RowTile &
 __device__ __forceinline__ void raise_bad(const AttendArgs &a)
 {
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.s.B; b += blockDim.x)
-            if (seq_at(a.s, b).bad)
-                raise(a.s.err, ENGRAM_DEVERR_SEQUENCE);
+        raise_bad(a.s);
 }
 
 // Short tables: a workgroup a unit and DV of its output values, nothing to join.
@@ -584,13 +583,15 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attend_unit_kernel(Att
     __shared__ Reduce<DV, W> red;
     const int v0 = DV * (blockIdx.x % (D / DV)), at = blockIdx.x / (D / DV);
     int b, unit;
+    Seq q;
     if (!a.s.cu) {
         const int units = (int)(((int64_t)a.s.each * a.g + kRows - 1) / kRows) * a.c.kv_heads;
         b = at / units;
         unit = at % units;
+        q = even_seq(a.s, b);
     } else {
         unit = at;
-        Lanes c = lanes_at(a, 0);
+        Lanes c = lanes_at(a, 0, 0);
         int base = 0;
         while (unit >= c.all_units()) {
             unit -= c.all_units();
@@ -599,13 +600,14 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 1) void attend_unit_kernel(Att
                 raise_bad(a);
                 return;
             }
-            c = lanes_at(a, base);
+            c = lanes_at(a, base, c.reach);
         }
         const int l = __builtin_ctzll(__ballot(c.sum_u > unit));
         b = base + l;
         unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
+        q = lane_seq(c.q, l);
     }
-    const RowTile t = tile_at(a, b, unit, seq_at(a.s, b));
+    const RowTile t = tile_at(a, b, unit, q);
     attend_unit<D, W, DV>(a, t, 0, 1 << 26, v0, nullptr, red);
     raise_bad(a);                               // last: nothing waits for it
 }
@@ -617,7 +619,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
     __shared__ Reduce<D, W> red;
     __shared__ Seq seqs[64];
     __shared__ int each_s[64], units_s[64];
-    Lanes c = lanes_at(a, 0);
+    Lanes c = lanes_at(a, 0, 0);
     const Plan plan = plan_of(a, c);
     if ((int64_t)blockIdx.x * plan.share >= plan.total) {
         raise_bad(a);
@@ -631,7 +633,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
     while (before + c.all_pieces() <= at) {
         before += c.all_pieces();
         base += 64;
-        c = lanes_at(a, base, plan.most);
+        c = lanes_at(a, base, c.reach, plan.most);
     }
     int l = __builtin_ctzll(__ballot(before + c.sum_p > at));
     int p0 = at - before - __builtin_amdgcn_readlane(c.sum_p - c.pieces, l);
@@ -670,7 +672,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_share_kernel(
                 if (++l == 64) {
                     l = 0;
                     base += 64;
-                    const Lanes next = lanes_at(a, base, plan.most);
+                    const Lanes next = lanes_at(a, base, c.reach, plan.most);
                     c = next;
                     keep();
                 }
@@ -692,7 +694,7 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
     const int tid = threadIdx.x;
     const int r0 = SPLIT ? blockIdx.x % a.join_rows : 0;
     int unit = SPLIT ? blockIdx.x / a.join_rows : blockIdx.x;
-    Lanes c = lanes_at(a, 0);
+    Lanes c = lanes_at(a, 0, 0);
     const Plan plan = plan_of(a, c);
     int base = 0, before = 0;
     while (unit >= c.all_units()) {
@@ -701,11 +703,11 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
         base += 64;
         if (base >= a.s.B)
             return;
-        c = lanes_at(a, base, plan.most);
+        c = lanes_at(a, base, c.reach, plan.most);
     }
     const int l = __builtin_ctzll(__ballot(c.sum_u > unit));
     unit -= __builtin_amdgcn_readlane(c.sum_u - c.units, l);
-    const RowTile t = tile_at(a, base + l, unit, c.seq(l));
+    const RowTile t = tile_at(a, base + l, unit, lane_seq(c.q, l));
     const int each = __builtin_amdgcn_readlane(c.each, l);
     const int begin = before + __builtin_amdgcn_readlane(c.sum_p - c.pieces, l) + unit * each;
     int i0 = begin, n = each;

@@ -484,12 +484,13 @@ typedef struct engram_cache {
  * d_pages[b][p/64].  d_cu [batch+1], non-decreasing within 0..T; NULL gives
  * every sequence T/batch tokens.  A sequence may bring no token.
  *   batch 1..65536;  d_pages [batch][max_pages] int32, max_pages below 2^25;
- *   d_err   nullable.  A sequence with a negative start, token bounds outside
- *           0..T or in falling order, or positions past its max_pages pages
- *           sets ENGRAM_DEVERR_SEQUENCE: nothing of it is appended, and its
- *           attention rows are zeros.  A page id outside the cache sets
- *           ENGRAM_DEVERR_PAGE: its positions are not written and are masked
- *           for attention.
+ *   d_err   nullable.  A sequence with a negative start or positions past its
+ *           max_pages pages sets ENGRAM_DEVERR_SEQUENCE: nothing of it is
+ *           appended, and its attention rows are zeros.  So does one whose
+ *           token bounds lie outside 0..T, fall, or begin before an earlier
+ *           sequence's end: it counts as bringing no token.  A page id outside
+ *           the cache sets ENGRAM_DEVERR_PAGE: its positions are not written
+ *           and are masked for attention.
  * Pages that a call appends to belong to one sequence each. */
 typedef struct engram_seqs {
     int32_t batch;

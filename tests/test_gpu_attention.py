@@ -566,6 +566,39 @@ def test_attend_bad_sequences(E, n, kv):
             assert torch.equal(out[2 * n:], good[2 * n:]) and bool((out[:2 * n] == 9).all())
 
 
+# ------------------------------------------- token bounds that are not in order
+def overlapping(B, first, last):
+    """Bounds whose first sequence brings tokens 0 .. first-1 and whose last
+    brings the `last` after them; those between begin again at 0, or fall."""
+    return [0] + [first if i % 2 else 0 for i in range(1, B)] + [first + last]
+
+
+@pytest.mark.parametrize("B,first,last,old,kv,g,d", [
+    (4, 6, 3, 10, 2, 2, 64), (4, 1, 1, 1100, 2, 4, 128), (200, 16, 3, 1100, 8, 2, 64),
+    (66, 2, 1, 1500, 1, 1, 256), (4, 600, 90, 70, 8, 2, 128), (130, 400, 300, 5, 8, 4, 64)])
+def test_overlapping_bounds(E, B, first, last, old, kv, g, d):
+    """A sequence that begins before an earlier one's end is bad: its tokens
+    count once, whatever the bounds between say."""
+    log(f"overlapping bounds, {B} sequences, {first} + {last} tokens after {old}, kv {kv} g {g} d {d}")
+    new, olds = [first] + [0] * (B - 2) + [last], [old] + [9] * (B - 2) + [old // 2]
+    good, st = (R.Step(B + first, new, olds, kv, g, d) for _ in range(2))
+    bounds = overlapping(B, first, last)
+    st.cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    outs = []
+    for s in (good, st):
+        q, k, v = s.heads()
+        cache, seqs = s.objects(E)
+        outs.append(torch.full((s.T, s.q, s.d), 9.0, dtype=torch.bfloat16, device="cuda"))
+        E.cache_append(cache, seqs, k, v, R.freq_of(d), q, outs[-1])
+    torch.cuda.synchronize()
+    assert int(good.err) == 0 and int(st.err) == 16
+    assert torch.equal(*outs)
+    for x, y in zip(st.codes + st.scales, good.codes + good.scales):
+        assert torch.equal(x.nan_to_num(), y.nan_to_num())
+    st.err.zero_()
+    check_attend(E, st, bits=16)
+
+
 # ----------------------------------------------------- a cache past 32 bits
 @pytest.mark.parametrize("new,old", [([1, 1], [100, 900]), ([1, 1], [1500, 70]), ([300, 260], [200, 33])])
 def test_pages_past_4_gib(E, new, old):
