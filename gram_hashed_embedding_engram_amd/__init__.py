@@ -376,6 +376,27 @@ def _typed(t, name, dtypes, shape=None):
         raise EngramError(E_ARG, f"{name}: a contiguous tensor is needed")
 
 
+def _on_gpu(t, name):
+    """Refuse a tensor in host memory, whose address a kernel cannot read."""
+    if not t.is_cuda:
+        raise EngramError(E_ARG, f"{name}: a tensor on the GPU is needed, this one is on {t.device}")
+
+
+def _host_name(**tensors):
+    """The name of the first of these tensors that is in host memory, or None:
+    what W4, Cache and Sequences keep, so that a call need not look again."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            return name.replace("_", " ")
+    return None
+
+
+def _refuse_host(*names):
+    for name in names:
+        if name is not None:
+            raise EngramError(E_ARG, f"{name}: a tensor on the GPU is needed, this one is not")
+
+
 class _Types:
     """Element types the attention sub-layer's tensors may have (torch is
     imported by the first call that needs it)."""
@@ -411,13 +432,16 @@ def add_norm(d_x, d_res, d_w, eps, d_codes, d_scales, d_sum=None, stream=None):
     dim = shape[-1]
     groups = shape[:-1] + (dim // NORM_GROUP,)
     total = d_res if d_sum is None else d_sum
-    if not (d_res.dtype in k.res and d_res.is_contiguous()
-            and (total is d_res or total.dtype is d_res.dtype and total.shape == shape
-                 and total.is_contiguous())
-            and (d_x is None or d_x.dtype in k.bf16 and d_x.shape == shape and d_x.is_contiguous())
-            and d_w.dtype in k.bf16 and d_w.shape == (dim,) and d_w.is_contiguous()
-            and d_codes.dtype in k.e4m3 and d_codes.shape == shape and d_codes.is_contiguous()
-            and d_scales.dtype in k.e8m0 and d_scales.shape == groups and d_scales.is_contiguous()):
+    if not (d_res.dtype in k.res and d_res.is_cuda and d_res.is_contiguous()
+            and (total is d_res or total.dtype is d_res.dtype and total.is_cuda
+                 and total.shape == shape and total.is_contiguous())
+            and (d_x is None or d_x.dtype in k.bf16 and d_x.is_cuda and d_x.shape == shape
+                 and d_x.is_contiguous())
+            and d_w.dtype in k.bf16 and d_w.is_cuda and d_w.shape == (dim,) and d_w.is_contiguous()
+            and d_codes.dtype in k.e4m3 and d_codes.is_cuda and d_codes.shape == shape
+            and d_codes.is_contiguous()
+            and d_scales.dtype in k.e8m0 and d_scales.is_cuda and d_scales.shape == groups
+            and d_scales.is_contiguous()):
         _typed(d_res, "res", k.res)
         _typed(total, "sum", (d_res.dtype,), shape)
         if d_x is not None:
@@ -425,6 +449,10 @@ def add_norm(d_x, d_res, d_w, eps, d_codes, d_scales, d_sum=None, stream=None):
         _typed(d_w, "w", k.bf16, (dim,))
         _typed(d_codes, "codes", k.e4m3, shape)
         _typed(d_scales, "scales", k.e8m0, groups)
+        for t, name in ((d_res, "res"), (total, "sum"), (d_x, "x"), (d_w, "w"), (d_codes, "codes"),
+                        (d_scales, "scales")):
+            if t is not None:
+                _on_gpu(t, name)
     rc = (_lib or lib()).engram_add_norm(
         None if d_x is None else d_x.data_ptr(), d_res.data_ptr(), d_res.dtype not in k.f32,
         d_w.data_ptr(), eps, total.data_ptr(), d_codes.data_ptr(), d_scales.data_ptr(),
@@ -445,6 +473,7 @@ class W4:
         self.w, self.scales = d_w, d_scales
         self.N, self.K, self.groups = N, 2 * half, 2 * half // NORM_GROUP
         self.at = (d_w.data_ptr(), d_scales.data_ptr())
+        self.host = _host_name(w=d_w, w_scales=d_scales)
 
 
 def project_w4(d_x, weights: W4, d_y, d_xs=None, stream=None):
@@ -453,14 +482,19 @@ def project_w4(d_x, weights: W4, d_y, d_xs=None, stream=None):
     k = _types or _kinds()
     T, K, N = d_x.shape[0], weights.K, weights.N
     if not ((d_x.dtype in k.bf16 if d_xs is None else
-             d_x.dtype in k.e4m3 and d_xs.dtype in k.e8m0 and d_xs.shape == (T, weights.groups)
-             and d_xs.is_contiguous())
-            and d_x.shape == (T, K) and d_x.is_contiguous()
-            and d_y.dtype in k.bf16 and d_y.shape == (T, N) and d_y.is_contiguous()):
+             d_x.dtype in k.e4m3 and d_xs.dtype in k.e8m0 and d_xs.is_cuda
+             and d_xs.shape == (T, weights.groups) and d_xs.is_contiguous())
+            and d_x.is_cuda and d_x.shape == (T, K) and d_x.is_contiguous()
+            and d_y.dtype in k.bf16 and d_y.is_cuda and d_y.shape == (T, N) and d_y.is_contiguous()
+            and weights.host is None):
         _typed(d_x, "x", k.bf16 if d_xs is None else k.e4m3, (T, K))
         if d_xs is not None:
             _typed(d_xs, "x scales", k.e8m0, (T, weights.groups))
         _typed(d_y, "y", k.bf16, (T, N))
+        _refuse_host(weights.host)
+        for t, name in ((d_x, "x"), (d_xs, "x scales"), (d_y, "y")):
+            if t is not None:
+                _on_gpu(t, name)
     xs = None if d_xs is None else d_xs.data_ptr()
     w, ws = weights.at
     rc = (_lib or lib()).engram_project_w4(d_x.data_ptr(), xs, w, ws, d_y.data_ptr(), T, K, N,
@@ -481,6 +515,7 @@ class Cache:
         _typed(d_k_scales, "k scales", k.f32, (n_pages, kv_heads))
         _typed(d_v_scales, "v scales", k.f32, (n_pages, kv_heads))
         self.keep = (d_k, d_v, d_k_scales, d_v_scales)
+        self.host = _host_name(k=d_k, v=d_v, k_scales=d_k_scales, v_scales=d_v_scales)
         self.kv_heads, self.head_dim, self.n_pages = kv_heads, head_dim, n_pages
         self.c = CacheC(kv_heads, head_dim, n_pages, d_k.data_ptr(), d_v.data_ptr(),
                         d_k_scales.data_ptr(), d_v_scales.data_ptr())
@@ -503,6 +538,7 @@ class Sequences:
             _typed(d_err, "err", i32)
             _need(d_err, "err", 4)
         self.keep = (d_pages, d_start, d_cu, d_err)
+        self.host = _host_name(pages=d_pages, start=d_start, cu=d_cu, err=d_err)
         self.B = B
         self.c = SequencesC(B, width, d_pages.data_ptr(), d_start.data_ptr(), _ptr(d_cu),
                             _ptr(d_err))
@@ -519,6 +555,8 @@ def _heads(t, name, T, heads, head_dim):
     token, head, one = t.stride()
     if one != 1:
         raise EngramError(E_ARG, f"{name}: a head's values must lie side by side")
+    if not t.is_cuda:
+        _on_gpu(t, name)
     return t.data_ptr(), token, head
 
 
@@ -529,6 +567,8 @@ def cache_append(cache: Cache, seqs: Sequences, d_k, d_v, d_freq, d_q=None, d_q_
     [T, q_heads, head_dim] bf16, as views of one projection's output if need
     be; d_freq [rot/2] f32 or None (no rotation); d_q_out as d_q, contiguous."""
     T, kv, d = d_k.shape[0], cache.kv_heads, cache.head_dim
+    if cache.host is not None or seqs.host is not None:
+        _refuse_host(cache.host, seqs.host)
     kp, kt, kh = _heads(d_k, "k", T, kv, d)
     vp, vt, vh = _heads(d_v, "v", T, kv, d)
     qp = qt = qh = q_heads = qo = 0
@@ -538,10 +578,12 @@ def cache_append(cache: Cache, seqs: Sequences, d_k, d_v, d_freq, d_q=None, d_q_
         if d_q_out is None:
             raise EngramError(E_ARG, "q_out: queries are given and no place for them")
         _typed(d_q_out, "q_out", _types.bf16, (T, q_heads, d))
+        _on_gpu(d_q_out, "q_out")
         qo = d_q_out.data_ptr()
     rot = fp = 0
     if d_freq is not None:
         _typed(d_freq, "freq", _types.f32)
+        _on_gpu(d_freq, "freq")
         rot, fp = 2 * d_freq.numel(), d_freq.data_ptr()
     rc = (_lib or lib()).engram_cache_append(cache.ref, seqs.ref, kp, kt, kh, vp, vt, vh, qp, qt, qh, qo,
                                   q_heads, fp, rot, halves, T, _stream(stream))
@@ -560,11 +602,15 @@ def cache_attend(cache: Cache, seqs: Sequences, d_q, d_out, scale, window=0, d_w
     d_q [T, q_heads, head_dim] bf16 (a view if need be), d_out contiguous of
     that shape, d_ws a uint8 tensor of cache_attend_bytes bytes or None."""
     T, q_heads, _ = shape = d_q.shape
+    if cache.host is not None or seqs.host is not None:
+        _refuse_host(cache.host, seqs.host)
     qp, qt, qh = _heads(d_q, "q", T, q_heads, cache.head_dim)
     _typed(d_out, "out", _types.bf16, shape)
+    _on_gpu(d_out, "out")
     ws, nws = 0, 0
     if d_ws is not None:
         _typed(d_ws, "ws", _types.u8)
+        _on_gpu(d_ws, "ws")
         ws, nws = d_ws.data_ptr(), d_ws.numel()
     rc = (_lib or lib()).engram_cache_attend(cache.ref, seqs.ref, qp, qt, qh, d_out.data_ptr(), q_heads, T,
                                   scale, window, ws, nws, _stream(stream))

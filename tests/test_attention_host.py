@@ -215,3 +215,28 @@ def test_binding_refusals():
         E.cache_attend(c, s, z(4, 4, 64), z(4, 4, 32), 1.0)
     with bad:
         E.cache_attend(c, s, z(4, 4, 64, dt=f32), z(4, 4, 64), 1.0)
+
+
+def test_host_tensors_are_refused():
+    """A tensor in host memory, right in type and shape, ends in the binding."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    cache = E.Cache(z(3, 2, 64, 64, dt=u8), z(3, 2, 64, 64, dt=u8), z(3, 2, dt=f32), z(3, 2, dt=f32))
+    seqs = E.Sequences(z(2, 3, dt=i32), z(2, dt=i32))
+    weights = E.W4(z(16, 64, dt=u8), z(16, 4, dt=u8))
+    assert cache.host == "k" and seqs.host == "pages" and weights.host == "w"
+    calls = [
+        lambda: E.add_norm(z(4, 64), z(4, 64, dt=f32), z(64), 1e-6, z(4, 64, dt=u8), z(4, 2, dt=u8),
+                           stream=0),
+        lambda: E.project_w4(z(2, 128), weights, z(2, 16), stream=0),
+        lambda: E.project_w4(z(2, 128, dt=u8), weights, z(2, 16), z(2, 4, dt=u8), stream=0),
+        lambda: E.cache_append(cache, seqs, z(4, 2, 64), z(4, 2, 64), z(32, dt=f32), stream=0),
+        lambda: E.cache_attend(cache, seqs, z(4, 4, 64), z(4, 4, 64), 1.0, stream=0)]
+    for call in calls:
+        with pytest.raises(E.EngramError, match="on the GPU is needed"):
+            call()
+    # the step's own tensors, where what the program keeps is on the GPU
+    cache.host = seqs.host = weights.host = None
+    for call in calls:
+        with pytest.raises(E.EngramError, match="on the GPU is needed"):
+            call()

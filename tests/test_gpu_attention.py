@@ -566,6 +566,43 @@ def test_attend_bad_sequences(E, n, kv):
             assert torch.equal(out[2 * n:], good[2 * n:]) and bool((out[:2 * n] == 9).all())
 
 
+# ------------------------------------------------------- tensors in host memory
+def test_one_host_tensor(E):
+    """Each tensor of each call alone in host memory is refused, by name."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    norm = dict(d_x=z(4, 64), d_res=z(4, 64, dt=f32), d_w=z(64), d_codes=z(4, 64, dt=u8),
+                d_scales=z(4, 2, dt=u8), d_sum=z(4, 64, dt=f32))
+    w4 = dict(d_w=z(16, 64, dt=u8), d_scales=z(16, 4, dt=u8))
+    project = dict(d_x=z(2, 128, dt=u8), d_xs=z(2, 4, dt=u8), d_y=z(2, 16))
+    keys = dict(d_k=z(3, 1, 64, 64, dt=u8), d_v=z(3, 1, 64, 64, dt=u8), d_k_scales=z(3, 1, dt=f32),
+                d_v_scales=z(3, 1, dt=f32))
+    seqs = dict(d_pages=z(2, 1, dt=i32), d_start=z(2, dt=i32), d_cu=z(3, dt=i32), d_err=z(1, dt=i32))
+    append = dict(d_k=z(4, 1, 64), d_v=z(4, 1, 64), d_freq=z(32, dt=f32), d_q=z(4, 2, 64), d_q_out=z(4, 2, 64))
+    attend = dict(d_q=z(4, 2, 64), d_out=z(4, 2, 64), d_ws=z(1 << 20, dt=u8))
+    seqs["d_cu"] += torch.tensor([0, 2, 4], dtype=i32, device="cuda")
+
+    def calls(norm=norm, w4=w4, project=project, keys=keys, seqs=seqs, append=append, attend=attend):
+        s, c = E.Sequences(**seqs), E.Cache(**keys)
+        return {"norm": lambda: E.add_norm(eps=1e-6, **norm),
+                "project": lambda: E.project_w4(weights=E.W4(**w4), **project),
+                "append": lambda: E.cache_append(c, s, **append),
+                "attend": lambda: E.cache_attend(c, s, scale=1.0, **attend)}
+
+    for call in calls().values():
+        call()
+    torch.cuda.synchronize()
+    uses = dict(norm=["norm"], w4=["project"], project=["project"], keys=["append", "attend"],
+                seqs=["append", "attend"], append=["append"], attend=["attend"])
+    for group, names in uses.items():
+        have = dict(norm=norm, w4=w4, project=project, keys=keys, seqs=seqs, append=append, attend=attend)[group]
+        for name in have:
+            bad = calls(**{group: {**have, name: have[name].cpu()}})
+            for call in names:
+                with pytest.raises(E.EngramError, match="on the GPU is needed"):
+                    bad[call]()
+
+
 # ------------------------------------------- token bounds that are not in order
 def overlapping(B, first, last):
     """Bounds whose first sequence brings tokens 0 .. first-1 and whose last
