@@ -135,14 +135,18 @@ def lib():
             "engram_cache_attend": (i32, [p, p, p, i64, i64, p, i32, i64, ctypes.c_float, i64, p,
                                           ctypes.c_size_t, p]),
         }
+        # a library built before this binding: another version, or, as additions
+        # alone leave the version as it is, one that lacks an entry point
+        rebuild = "rebuild it (python -m gram_hashed_embedding_engram_amd.build)"
+        if L.engram_abi_version() != ABI_VERSION:
+            raise RuntimeError(f"{LIB_PATH} has ABI version {L.engram_abi_version()}, this "
+                               f"binding {ABI_VERSION}: {rebuild}")
         for name, (res, args) in sig.items():
+            if not hasattr(L, name):
+                raise RuntimeError(f"{LIB_PATH} has no {name}: {rebuild}")
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        if L.engram_abi_version() != ABI_VERSION:
-            raise RuntimeError(f"{LIB_PATH} has ABI version {L.engram_abi_version()}, this "
-                               f"binding {ABI_VERSION}: rebuild it (python -m "
-                               "gram_hashed_embedding_engram_amd.build)")
         _lib = L
     return _lib
 

@@ -2,6 +2,7 @@
 they refuse, before any launch (fake device addresses are never read)."""
 import ctypes
 import os
+import subprocess
 
 import pytest
 
@@ -240,3 +241,18 @@ def test_host_tensors_are_refused():
     for call in calls:
         with pytest.raises(E.EngramError, match="on the GPU is needed"):
             call()
+
+
+@pytest.mark.parametrize("version,message", [(E.ABI_VERSION - 1, "ABI version"), (E.ABI_VERSION, "has no engram_")])
+def test_stale_library(tmp_path, monkeypatch, version, message):
+    """A library built before this binding is named as that, whether its
+    version differs or entry points were only added since."""
+    src, so = tmp_path / "stale.c", tmp_path / "stale.so"
+    src.write_text(f"int engram_abi_version(void) {{ return {version}; }}\n"
+                   "const char *engram_last_error(void) { return \"\"; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    monkeypatch.setattr(E, "_lib", None)
+    monkeypatch.setattr(E, "LIB_PATH", str(so))
+    with pytest.raises(RuntimeError, match=f"{message}.*rebuild"):
+        E.lib()
+    assert E._lib is None
