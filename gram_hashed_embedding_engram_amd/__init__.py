@@ -201,9 +201,14 @@ def _stream(stream):
         if _current is None:
             import torch
             first = torch.cuda.current_stream().cuda_stream      # initialises the device
-            # the same address without a Stream object a call (0.2 us, not 3)
-            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            _current = lambda: raw(device())  # noqa: E731
+            # the same address without a Stream object a call (0.2 us, not 3), where
+            # torch has these two functions of its own
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", None)
+            if raw and device:
+                _current = lambda: raw(device())  # noqa: E731
+            else:
+                _current = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
             return first
         return _current()
     if isinstance(stream, int):

@@ -256,3 +256,18 @@ def test_stale_library(tmp_path, monkeypatch, version, message):
     with pytest.raises(RuntimeError, match=f"{message}.*rebuild"):
         E.lib()
     assert E._lib is None
+
+
+@pytest.mark.parametrize("gone", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_current_stream_by_the_public_way(monkeypatch, gone):
+    """Without torch's own short cut the current stream is asked for publicly."""
+    asked = []
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: asked.append(1) or Stream)
+    monkeypatch.delattr(torch._C, gone, raising=False)
+    monkeypatch.setattr(E, "_current", None)
+    assert [E._stream(None) for _ in range(3)] == [77] * 3 and len(asked) == 3
+    assert E._stream(5) == 5 and E._stream(Stream) == 77
