@@ -21,6 +21,14 @@ constexpr int32_t kMaxHeads = 1024;
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Whether an input and an output share memory: several workgroups read what
+// one of them would already have written.
+bool overlap(const void *in, uint64_t in_bytes, const void *out, uint64_t out_bytes)
+{
+    const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
+    return a < b ? b - a < in_bytes : a - b < out_bytes;
+}
+
 Launch on(void *stream)
 {
     Launch l;
@@ -133,6 +141,8 @@ int32_t engram_project_w4(const void *d_x, const uint8_t *d_x_scales, const uint
               aligned(d_w_scales, 4) && aligned(d_y, 8),
           ENGRAM_E_ARG,
           "engram project_w4: x and w must be 16-byte, y 8-byte, scales 4-byte aligned");
+    CHECK(!overlap(d_x, (uint64_t)(T * K) * (d_x_scales ? 1 : 2), d_y, (uint64_t)(T * N) * 2),
+          ENGRAM_E_ARG, "engram project_w4: y overlaps x");
     return launch_w4(d_x, d_x_scales, d_w, d_w_scales, d_y, T, K, N, on(stream));
 }
 
@@ -217,6 +227,10 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
           "engram cache_attend: a workspace of %zu bytes, %zu needed", ws_bytes, need);
     CHECK(need == 0 || (d_ws && aligned(d_ws, 256)), ENGRAM_E_ARG,
           "engram cache_attend: NULL or unaligned workspace (256 bytes)");
+    const uint64_t q_values = (uint64_t)(T - 1) * (uint64_t)q_token_stride +
+                              (uint64_t)(q_heads - 1) * (uint64_t)q_head_stride + cache->head_dim;
+    CHECK(!overlap(d_q, 2 * q_values, d_out, (uint64_t)T * q_heads * cache->head_dim * 2),
+          ENGRAM_E_ARG, "engram cache_attend: out overlaps q");
     return launch_attend(*cache, s, Heads{d_q, q_token_stride, q_head_stride}, d_out, q_heads,
                          scale, window, d_ws, on(stream));
 }

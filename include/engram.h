@@ -424,6 +424,8 @@ void engram_ctx_destroy(engram_ctx *ctx);
  * with the append to a paged 8-bit cache (engram_cache_append), and attention
  * over that cache (engram_cache_attend).  None of them allocates, keeps state
  * between calls or uses atomics on results: equal inputs give equal bits.
+ * Outputs do not overlap inputs, except where a call says that they may
+ * (engram_project_w4 and engram_cache_attend refuse it).
  *
  * 8-bit values are e4m3fn codes under power-of-two scales: the scale of a
  * group is the least 2^k, k >= -126, with amax <= 448 * 2^k over the group's

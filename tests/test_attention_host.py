@@ -271,3 +271,14 @@ def test_current_stream_by_the_public_way(monkeypatch, gone):
     monkeypatch.setattr(E, "_current", None)
     assert [E._stream(None) for _ in range(3)] == [77] * 3 and len(asked) == 3
     assert E._stream(5) == 5 and E._stream(Stream) == 77
+
+
+def test_outputs_over_inputs_are_refused(L):
+    """Workgroups read what another would have written: refused, in place or
+    shifted by a few bytes (a call that starts where the other ends is not)."""
+    for shift in (-256, 0, 8, 1024):
+        assert w4(L, T=4, K=256, N=64, xs=None, y=FAKE + shift) == E.E_ARG and "overlaps" in E.last_error()
+        # q spans 5 strides of 1024 values, 3 of 128 and a head
+        assert attend(L, out=FAKE + shift) == E.E_ARG and "overlaps" in E.last_error()
+    assert attend(L, out=FAKE + 2 * (5 * 1024 + 3 * 128 + 128) - 16) == E.E_ARG and "overlaps" in E.last_error()
+    assert attend(L, out=FAKE - 6 * 4 * 128 * 2 + 16) == E.E_ARG and "overlaps" in E.last_error()

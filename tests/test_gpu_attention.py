@@ -603,6 +603,37 @@ def test_one_host_tensor(E):
                     bad[call]()
 
 
+def test_outputs_beside_inputs(E):
+    """An output that begins where its input ends, or ends where it begins, is
+    no overlap: the same bits as in a buffer of its own."""
+    st = R.Step(81, [3, 2], [70, 1200], 2, 4, 128)
+    st.fill_new()
+    n = st.T * st.q * st.d
+    cache, seqs = st.objects(E)
+    ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, st.T), dtype=torch.uint8, device="cuda")
+    q = st.heads()[0].contiguous()
+    want = torch.empty_like(q)
+    E.cache_attend(cache, seqs, q, want, 0.1, 0, ws)
+    for at in (0, n):
+        both = torch.empty(2 * n, dtype=torch.bfloat16, device="cuda")
+        x, out = both[at:at + n].view_as(q), both[n - at:2 * n - at].view_as(q)
+        x.copy_(q)
+        E.cache_attend(cache, seqs, x, out, 0.1, 0, ws)
+        assert torch.equal(out, want) and torch.equal(x, q)
+        with pytest.raises(E.EngramError, match="overlaps"):
+            E.cache_attend(cache, seqs, x, x, 0.1, 0, ws)
+    w, ws4, x, xs, _ = w4_case(82, 5, 256, 256, False)
+    want = torch.empty(5, 256, dtype=torch.bfloat16, device="cuda")
+    E.project_w4(x, E.W4(w, ws4), want)
+    for at in (0, 1):
+        both = torch.empty(2, 5, 256, dtype=torch.bfloat16, device="cuda")
+        both[at].copy_(x)
+        E.project_w4(both[at], E.W4(w, ws4), both[1 - at])
+        assert torch.equal(both[1 - at], want)
+        with pytest.raises(E.EngramError, match="overlaps"):
+            E.project_w4(both[at], E.W4(w, ws4), both[at])
+
+
 # ------------------------------------------- token bounds that are not in order
 def overlapping(B, first, last):
     """Bounds whose first sequence brings tokens 0 .. first-1 and whose last
