@@ -282,3 +282,17 @@ def test_outputs_over_inputs_are_refused(L):
         assert attend(L, out=FAKE + shift) == E.E_ARG and "overlaps" in E.last_error()
     assert attend(L, out=FAKE + 2 * (5 * 1024 + 3 * 128 + 128) - 16) == E.E_ARG and "overlaps" in E.last_error()
     assert attend(L, out=FAKE - 6 * 4 * 128 * 2 + 16) == E.E_ARG and "overlaps" in E.last_error()
+
+
+def test_attend_asks_for_a_workspace(L):
+    """A long table of few rows has its keys split over workgroups, on any
+    device: never 0 bytes, and one byte less is refused."""
+    for dim in (64, 128, 256):
+        cache, seqs = cache_c(head_dim=dim), seqs_c(batch=1, max_pages=4096)
+        need = L.engram_cache_attend_bytes(ctypes.byref(cache), ctypes.byref(seqs), 4, 1)
+        assert need > 0
+        call = dict(cache=cache, seqs=seqs, T=1, qh=dim)
+        assert attend(L, nws=need - 1, **call) == E.E_RANGE and E.last_error()
+        assert attend(L, ws=None, nws=need, **call) == E.E_ARG and E.last_error()
+        assert attend(L, ws=FAKE + 16, nws=need, **call) == E.E_ARG and E.last_error()
+    assert L.engram_cache_attend_bytes(ctypes.byref(cache_c()), ctypes.byref(seqs_c(batch=1, max_pages=16)), 4, 1) == 0

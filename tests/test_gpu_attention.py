@@ -566,6 +566,144 @@ def test_attend_bad_sequences(E, n, kv):
             assert torch.equal(out[2 * n:], good[2 * n:]) and bool((out[:2 * n] == 9).all())
 
 
+# -------------------------------------------- every page and position, once each
+def visible(st, b, window):
+    """[new, positions] of sequence b: what each of its tokens sees."""
+    n, o = st.new[b], st.old[b]
+    i, j = torch.arange(o, o + n, device="cuda"), torch.arange(o + n, device="cuda")
+    seen = j[None] <= i[:, None]
+    return seen & (j[None] > i[:, None] - window) if window else seen
+
+
+def page_marks(d, step):
+    """Each page's positions mark one dimension; pages d apart share it (at
+    most 32 of the longest cache's), and another step pairs other pages."""
+    def dims(st, b, j):
+        blk = j // 64
+        return (blk * step + (blk // d if step > 1 else 0)) % d
+    return dims
+
+
+def position_marks(d, window):
+    """Up to d single positions, each in a dimension of its own: both ends of
+    pages, cache and windows, and others between; the rest mark none (-1)."""
+    def dims(st, b, j):
+        L, o = len(j), st.old[b]
+        at = [0, 1, 63, 64, 65, L - 1, L - 2, o, o - 1, o + 1, L // 2, L // 64 * 64, L // 64 * 64 - 1,
+              o // 64 * 64, o // 64 * 64 - 1]
+        at += [x - window + k for x in (o, L - 1) for k in (-1, 0, 1) if window]
+        at += [64 * k + (7 * k) % 64 for k in range(0, L // 64 + 1, max(1, L // 64 // (d // 3)))]
+        at = sorted({x for x in at if 0 <= x < L})[:d]
+        out = torch.full((L,), -1, dtype=torch.long, device="cuda")
+        out[torch.tensor(at, device="cuda")] = torch.arange(len(at), device="cuda")
+        return out
+    return dims
+
+
+def check_marks(E, st, window, dims):
+    """Zero queries weigh what they see evenly, and the values are zeros but for
+    the marks: an output is a count over the positions seen, so a page or a
+    position that is lost, doubled, another sequence's or another head's is off
+    by 2^-5 of it and more.  Weights, products and sums are exact in f32; the
+    quotient's two roundings (2^-24) and the result's (bf16, 2^-8) remain."""
+    d = st.d
+    want = torch.zeros(st.T, st.q, d, dtype=F64, device="cuda")
+    at = 0
+    for b, (n, o) in enumerate(zip(st.new, st.old)):
+        L = o + n
+        j = torch.arange(L, device="cuda")
+        pg, slot = st.pages[b].long()[j // 64], j % 64
+        size = 1 + b % 4 / 4                                     # an e4m3 value, 0x38 is 1
+        code = 0x38 + 2 * (b % 4)
+        at_d = dims(st, b, j) if L else j
+        st.codes[1][pg, :, slot] = 0
+        on = at_d >= 0
+        st.codes[1][pg[on], :, slot[on], at_d[on]] = code
+        for h in range(st.kv):
+            st.scales[1][pg, h] = 2.0 ** (h % 4)
+        if n == 0:
+            continue
+        marks = torch.zeros(L, d, dtype=F64, device="cuda")
+        marks[j[on], at_d[on]] = size
+        seen = visible(st, b, window).to(F64)
+        mean = (seen @ marks) / seen.sum(1, keepdim=True)
+        for h in range(st.kv):
+            want[at:at + n, h * st.g:(h + 1) * st.g] = mean[:, None] * 2.0 ** (h % 4)
+        at += n
+    q = torch.zeros(st.T, st.q, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 9.0)
+    cache, seqs = st.objects(E)
+    ws = torch.full((E.cache_attend_bytes(cache, seqs, st.q, st.T),), 0xFF, dtype=torch.uint8, device="cuda")
+    E.cache_attend(cache, seqs, q, out, 0.7, window, ws)
+    torch.cuda.synchronize()
+    assert int(st.err) == 0
+    within(out, want, (2.0 ** -8 + 2.0 ** -22) * want, "out")
+
+
+def check_all_marks(E, new, old, kv, g, d, window, width=None):
+    st = R.Step(len(new) + sum(old) % 1000, new, old, kv, g, d, width=width)
+    st.fill_new()
+    for dims in (page_marks(d, 1), page_marks(d, 5), position_marks(d, window)):
+        check_marks(E, st, window, dims)
+
+
+@pytest.mark.parametrize("window", [0, 1, 7, 64, 100])
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_marks_short(E, case, window):
+    new, old, kv, g, d = STEPS[case]
+    log(f"marks {new[:6]} after {old[:6]} kv {kv} g {g} d {d} window {window}")
+    check_all_marks(E, new, old, kv, g, d, window)
+
+
+MARKED = [
+    # short tables: many units, whose values one workgroup takes
+    ([1] * 300, [900 - (i % 40) for i in range(300)], 4, 2, 128, 0), ([1] * 90, [1000 - i for i in range(90)], 4, 1, 256, 0),
+    ([2] * 200, [7 * i % 900 for i in range(200)], 2, 16, 64, 0), ([1] * 150, [1000 - i for i in range(150)], 8, 1, 64, 200),
+    # one or few sequences: even pieces, joined by rows
+    ([1], [131071], 1, 3, 64, 0), ([1], [40000], 2, 8, 256, 0), ([1], [20000], 1, 32, 128, 0), ([1], [1025], 1, 1, 64, 0),
+    ([1] * 9, [4096 + 511 * i for i in range(9)], 4, 4, 128, 0), ([4, 1], [9000, 3], 2, 8, 64, 500), ([3], [6000], 2, 5, 64, 0),
+    ([1, 1], [30000, 5], 1, 1, 256, 1000), ([17], [3000], 1, 20, 128, 0),
+    ([1, 1, 1], [64 * 32, 64 * 32 - 1, 64 * 31 - 1], 1, 4, 256, 0), ([1] * 70, [1030 + 29 * (i % 7) for i in range(70)], 2, 4, 64, 0),
+    # shares that cross units, groups of 64 sequences and sequences without tokens
+    ([1] * 150, [1100 + (i % 3) for i in range(150)], 4, 1, 64, 0), ([1] * 200, [1030 + 90 * (i % 5) for i in range(200)], 8, 2, 128, 0),
+    ([1] * 40, [60000] + [70] * 39, 8, 2, 128, 0), ([1] * 90, [1500 + i for i in range(90)], 4, 2, 256, 300),
+    ([1] * 66, [20000 if i in (3, 65) else 3 * i for i in range(66)], 2, 4, 128, 0), (*empty_run(230, 50, 130, 1100), 8, 2, 64, 0),
+    ([1] * 51, [1113] * 51, 8, 4, 128, 0),
+    # tiles of 128 rows, whole and with their pages shared out
+    ([300], [100], 2, 4, 128, 0), ([513, 60, 0, 129], [0, 700, 5, 63], 1, 4, 64, 0), ([700, 300], [77, 200], 4, 3, 256, 0),
+    ([400], [900], 1, 8, 128, 150), ([600], [64], 4, 8, 64, 90), ([700], [300], 4, 4, 256, 64), ([1100], [33], 2, 4, 128, 0),
+    ([300], [3000], 8, 2, 128, 0), ([520, 64], [2500, 3], 4, 4, 64, 700), ([200, 129, 0], [2000, 1, 9], 8, 3, 256, 0),
+    ([257], [6000], 8, 4, 128, 100), ([1, 600], [4000, 2100], 4, 4, 64, 0), ([512], [30000], 8, 4, 128, 0),
+    # prompts and single tokens in one step, by either kind of tile
+    ([700] + [1] * 63, [50] + [1200 + 31 * i for i in range(63)], 8, 4, 128, 0), ([1] * 40 + [500], [300] * 40 + [2000], 4, 8, 64, 0),
+    ([130] + [1] * 63, [900] + [40 * i for i in range(63)], 2, 4, 128, 0), ([100] + [1] * 90, [1500] + [1100] * 90, 4, 4, 256, 0)]
+
+
+@pytest.mark.parametrize("case", range(len(MARKED)))
+def test_marks(E, case):
+    new, old, kv, g, d, window = MARKED[case]
+    log(f"marks {len(new)} sequences of up to {max(new)} after up to {max(old)}, kv {kv} g {g} d {d} window {window}")
+    check_all_marks(E, new, old, kv, g, d, window)
+
+
+@pytest.mark.parametrize("new,old,kv,g,d,window", [
+    ([1], [500], 8, 4, 128, 0), ([1] * 20, [800 - i for i in range(20)], 4, 4, 256, 0), ([3, 1], [62, 10], 2, 4, 64, 0),
+    ([600], [130], 4, 4, 128, 0), ([300, 40], [0, 64], 4, 4, 256, 90), ([90] * 5, [11 * i for i in range(5)], 8, 4, 64, 0)])
+def test_marks_wide_table(E, new, old, kv, g, d, window):
+    """Tables of many more columns than the sequences fill, as a server keeps
+    them: other kernels than a tight table's, the same outputs."""
+    log(f"marks {new[:6]} after {old[:6]} kv {kv} g {g} d {d} in a table of 2048 columns")
+    check_all_marks(E, new, old, kv, g, d, window, width=2048)
+
+
+def test_workspace_is_asked_for(E):
+    """What splits its pages needs a workspace; what does not needs none."""
+    for new, old, kv, g, d, some in (([1], [5000], 2, 4, 128, True), ([1], [500], 2, 4, 128, False),
+                                     ([512], [30000], 8, 4, 128, True), ([4096], [100], 8, 4, 128, False)):
+        st = R.Step(1, new, old, kv, g, d)
+        assert (E.cache_attend_bytes(*st.objects(E), st.q, st.T) > 0) == some
+
+
 # ------------------------------------------------------- tensors in host memory
 def test_one_host_tensor(E):
     """Each tensor of each call alone in host memory is refused, by name."""
