@@ -18,9 +18,15 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kOne = 127, kLoScale = 127 - 4;
 
 // Thirty-two bf16 query values as two e4m3 parts, q = 2^k (hi + lo / 16):
-// bf16 has eight significant bits and each part four, so the sum is exact
-// down to 2^-15 of the row's largest value and off by at most 2^-19 of it
-// below.  The matrix instructions then take keys as the codes they are.
+// bf16 has eight significant bits and each part four.  The row's largest value
+// lies in (224, 448] and lo's finest step is 2^-9 / 16 = 2^-13, so eight bits
+// fit down to values of 2^-6, which is 2^-13.8 of the largest or less; below, a
+// value is off by at most 2^-14, 2^-21.8 of the largest.  The matrix
+// instructions then take keys as the codes they are.  They cut the products of
+// eight neighbours towards zero below 2^-13 of the largest one's power of two
+// and add in f32: some 2^-16 of a logit's size for normal values, little beside
+// the keys' four bits, where bf16 products would need every key widened and
+// staged at twice its bytes.
 __device__ __forceinline__ void split_query(const u32x4 (&x)[4], float inv, i32x8 &hi, i32x8 &lo)
 {
 #pragma unroll

@@ -3,10 +3,11 @@
 //
 // One pass over the keys with a running maximum m and sum l of the softmax
 // (in base 2): a page's logits s give p = 2^(s - m), and what was summed under
-// an older m is multiplied by 2^(m_old - m).  m, l and the sums are f32; the
-// only roundings to fewer bits are those of p (to bf16, the matrix
-// instructions' type for values: at most 2^-8 of a term, in either
-// direction) and of the result.
+// an older m is multiplied by 2^(m_old - m).  m, l and the sums are f32.
+// Roundings to fewer bits: those of p (to bf16, the matrix instructions' type
+// for values: at most 2^-8 of a term, in either direction; l sums p as it was,
+// which leaves the term's rounding alone in the result), of the result, and in
+// the logits those of split_query.
 //
 // Single tokens are bound by memory, the cache's bytes: 64 sequences of up to
 // 8192 positions (581 MB) in 103 us, 99 of them in the kernel that reads

@@ -448,7 +448,7 @@ int32_t engram_add_norm(const uint16_t *d_x, const void *d_res, int32_t res_bf16
                         const uint16_t *d_w, float eps, void *d_sum, uint8_t *d_codes,
                         uint8_t *d_scales, int64_t rows, int64_t dim, void *stream);
 
-/* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ), f32 sums, w in 4 bits:
+/* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ), w in 4 bits:
  *   d_w        [N][K/2]: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  *              negatives), the even k in the low nibble;
  *   d_w_scales [N][K/32]: exponents + 127 of a power of two per 32 values
@@ -457,6 +457,11 @@ int32_t engram_add_norm(const uint16_t *d_x, const void *d_res, int32_t res_bf16
  *   d_x        [T][K] e4m3 codes with d_x_scales [T][K/32] of the same kind
  *              (engram_add_norm's outputs), or bf16 with d_x_scales = NULL;
  *   d_y        [T][N] bf16.
+ * Sums are f32.  With e4m3 x the matrix instruction takes the products of eight
+ * neighbours (k = 8i .. 8i+7) together and cuts them towards zero below 2^-13
+ * of the largest one's power of two before it adds them: for normally
+ * distributed values that moves a sum by about 2^-16 of its size, a hundredth
+ * of the result's rounding; with bf16 x nothing is cut.
  * K a positive multiple of 128 up to 2^20, N a positive multiple of 16 up to
  * 2^24, T up to 2^22; made for few tokens (the weights are read once per 64 tokens).
  * d_x and d_w 16-byte, scales 4-byte, d_y 8-byte aligned.  T = 0 is a no-op. */
@@ -530,9 +535,19 @@ int32_t engram_cache_append(const engram_cache *cache, const engram_seqs *seqs,
 /* Attention of the step's queries over the cache (append first): query head h
  * of a token at position p reads key head h / (q_heads/kv_heads) at positions
  * j <= p, and j > p - window where window > 0:
- *   out = softmax_j(scale * q . k_j) v_j, in f32, rounded once to bf16.
+ *   out = softmax_j(scale * q . k_j) v_j, rounded to bf16.
  * Queries with no position left to read give zeros.  Tokens of no sequence
  * are left as they are.
+ * Maxima, sums and outputs are f32.  Fewer bits are kept in three places:
+ *   - a weight e^(..) is rounded to bf16 (2^-8 of itself at most) where it meets
+ *     its value, and not where it is summed, so the weights of a row add up to
+ *     one only to that precision;
+ *   - a query is taken as two e4m3 parts: exact down to 2^-13.8 of its largest
+ *     value, off by at most 2^-21.8 of that below;
+ *   - of a logit's products, those of eight neighbours are cut as in
+ *     engram_project_w4: by about 2^-16 of its size for normal values.
+ * For normal inputs an output is 0.0019 to 0.0023 of its size (rms) from the
+ * exact one, of which the result's rounding alone is 0.0017.
  *   d_q as for engram_cache_append; d_out [T][q_heads][head_dim] bf16,
  *   8-byte aligned; q_heads a multiple of kv_heads; scale finite;
  *   d_ws (256-byte aligned, caller-owned) of engram_cache_attend_bytes bytes:

@@ -185,6 +185,49 @@ def test_project_w4_infinite(E, T, K, N):
     check_w4(E, w, ws, x, xs, x.to(F64))
 
 
+def cut_products(x, w):
+    """Sums over k of products x[t][k] w[n][k] as the scaled 8-bit instruction
+    forms them: the products of eight neighbours are cut towards zero below
+    2^-13 of the largest one's power of two (the operands' exponents added;
+    zeros have none), then everything is added in f32 (here exactly)."""
+    T, K, N = x.shape[0], x.shape[1], w.shape[0]
+    low = torch.full((), -1000.0, dtype=F64, device=x.device)
+    ex = torch.where(x == 0, low, x.abs().clamp(min=2.0 ** -6).log2().floor())
+    ew = torch.where(w == 0, low, w.abs().clamp(min=1.0).log2().floor())
+    p = (x[:, None, :] * w[None]).view(T, N, K // 8, 8)
+    top = (ex[:, None, :] + ew[None]).view(T, N, K // 8, 8).amax(-1, keepdim=True)
+    unit = torch.exp2(top.clamp(min=-100) - 13)
+    return (torch.trunc(p / unit) * unit).sum((-1, -2)), p.abs().sum((-1, -2))
+
+
+@pytest.mark.parametrize("spread", [0, 8, 14])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_project_w4_sums(E, fp8, spread):
+    """What a sum keeps beside large values that cancel: with bf16 activations
+    what f32 keeps, with 8-bit ones what the instruction does."""
+    T, K, N = 32, 128, 256
+    g = seeded(spread + 17)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    w[:, 0::4] = 0xF7                                   # 6 and -6 for the first two of every eight
+    ws = torch.full((N, K // 32), 127, device="cuda", dtype=torch.uint8)
+    x = torch.randn(T, K, generator=g, device="cuda")
+    x *= torch.exp2(torch.rand(T, K, generator=g, device="cuda") * spread - spread + 6)
+    x = x.clamp(-448, 448)
+    x[:, 0::8] = x[:, 1::8] = 448
+    x = x.to(torch.float8_e4m3fn)
+    w64, x64 = R.e2m1(w), x.float().to(F64)
+    cut, size = cut_products(x64, w64)
+    exact = x64 @ w64.t()
+    assert bool(((cut - exact).abs() <= K / 8 * 7 * 2.0 ** -13 * 448 * 6).all())
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    if fp8:
+        E.project_w4(x.view(torch.uint8), E.W4(w, ws), y, torch.full((T, K // 32), 127, device="cuda", dtype=torch.uint8))
+    else:
+        E.project_w4(x.to(torch.bfloat16), E.W4(w, ws), y)
+    want = cut if fp8 else exact
+    within(y, want, 2.0 ** -8 * want.abs() + K * 2.0 ** -24 * size, "y")
+
+
 # ----------------------------------------------------------------- append
 STEPS = [  # new tokens, older positions, kv heads, queries a key head, head_dim
     ([1], [0], 1, 1, 64), ([1], [63], 2, 4, 128), ([1], [64], 2, 3, 64), ([1, 1, 1], [5, 127, 300], 4, 8, 256),
@@ -474,6 +517,44 @@ def test_attend_peaked(E, d, n, kv):
     check_attend(E, st, q=q)
     check_attend(E, st, q=q * 2.0 ** -100)
     check_attend(E, st, q=q, scale=2.0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,kv", [([1, 1], 2), ([20, 30], 2), ([300, 90], 8)])
+@pytest.mark.parametrize("loud", [1, 8])
+def test_attend_logits(E, loud, new, kv, d):
+    """Logits within what the 8-bit instructions keep: of each eight neighbours'
+    products, seven may lose up to 2^-13 of the largest, for the query's first
+    part (at most 1 + 2^-4 of it) and its second (2^-4 of that)."""
+    st = R.Step(d + loud, new, [200, 70], kv, 2, d)
+    st.fill_new()
+    q = (st.heads()[0] * loud).contiguous()
+    scale = 1 / math.sqrt(d)
+    out = torch.empty_like(q)
+    cache, seqs = st.objects(E)
+    ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, st.T), dtype=torch.uint8, device="cuda")
+    E.cache_attend(cache, seqs, q, out, scale, 0, ws)
+    torch.cuda.synchronize()
+    at = 0
+    for b, (n, o) in enumerate(zip(st.new, st.old)):
+        L = o + n
+        pg = st.pages[b, :(L + 63) // 64].long()
+        seen = visible(st, b, 0)
+        for u in range(st.q):
+            k, v = ((R.e4m3(c[pg, u // st.g]) * s[pg, u // st.g].to(F64)[:, None, None]).reshape(-1, d)[:L]
+                    for c, s in zip(st.codes, st.scales))
+            x = q[at:at + n, u].to(F64)
+            a = torch.where(seen, x @ k.t() * scale, torch.full((), -math.inf, dtype=F64, device="cuda"))
+            p = torch.softmax(a, 1)
+            largest = (x[:, None, :] * k[None]).abs().view(n, L, d // 8, 8).amax(-1).sum(-1)
+            off = 7 * 2.0 ** -13 * (1 + 2.0 ** -4) ** 2 * largest           # what is cut
+            # the query's parts (2^-21 of its largest value), f32 sums of 2d products
+            off += 2.0 ** -21 * x.abs().amax(1, keepdim=True) * k.abs().sum(1)[None] + 2 * d * 2.0 ** -24 * (x.abs() @ k.abs().t())
+            off = torch.where(seen, off, torch.zeros_like(off)).amax(1, keepdim=True) * scale + 2.0 ** -16
+            want = p @ v
+            tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + torch.expm1(2 * off) + L * 2.0 ** -24) * (p @ v.abs())
+            within(out[at:at + n, u], want, tol, f"out of head {u}")
+        at += n
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
