@@ -350,12 +350,17 @@ __global__ __launch_bounds__(threads_of<D>) void append_kernel(AppendArgs a)
     }
 }
 
+int64_t blocks_of(const AppendArgs &a)
+{
+    const int64_t runs = a.q_heads ? (a.s.T + a.run - 1) / a.run : 0;
+    const int64_t groups = (a.c.kv_heads + a.heads - 1) / a.heads;
+    return 2 * (int64_t)a.pieces * groups + runs;
+}
+
 template <int D>
 void launch_dim(const AppendArgs &a, const Launch &l)
 {
-    const unsigned runs = a.q_heads ? (a.s.T + a.run - 1) / a.run : 0;
-    const unsigned groups = (a.c.kv_heads + a.heads - 1) / a.heads;
-    const dim3 grid(2u * a.pieces * groups + runs), block(threads_of<D>);
+    const dim3 grid((unsigned)blocks_of(a)), block(threads_of<D>);
     if (a.r.halves)
         dispatch(append_kernel<D, true>, grid, block, l, true, true, a);
     else
@@ -379,6 +384,11 @@ int32_t launch_append(const engram_cache &c, const Seqs &s, const Heads &k, cons
     const AppendArgs a{c, s, k, v, q, q_out, r, q_heads, (int32_t)pieces,
                        (int32_t)(run < 1 ? 1 : run > kRunTokens ? kRunTokens : run),
                        run < 2 ? 1 : kRunHeads};
+    // (a grid's threads are counted in 32 bits)
+    const int64_t threads = c.head_dim == 256 ? threads_of<256> : threads_of<64>;
+    if (blocks_of(a) * threads >= ((int64_t)1 << 32))
+        return fail(ENGRAM_E_RANGE, "engram cache_append: %lld workgroups of %lld threads in one call",
+                    (long long)blocks_of(a), (long long)threads);
     if (c.head_dim == 64)
         launch_dim<64>(a, l);
     else if (c.head_dim == 128)

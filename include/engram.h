@@ -524,7 +524,9 @@ typedef struct engram_seqs {
  * scale of a page and head covers the new tokens and, where the page already
  * holds older positions, is at least its old one; where it rises, the older
  * codes are rounded again under it.  Slots past the last token keep their
- * bytes.  T up to 2^22; T = 0 is a no-op. */
+ * bytes.  T up to 2^22, and twice the pages that T tokens of batch sequences can
+ * touch, times kv_heads, plus T below 2^24 (2^23 with head_dim 256);
+ * ENGRAM_E_RANGE past that.  T = 0 is a no-op. */
 int32_t engram_cache_append(const engram_cache *cache, const engram_seqs *seqs,
                             const uint16_t *d_k, int64_t k_token_stride, int64_t k_head_stride,
                             const uint16_t *d_v, int64_t v_token_stride, int64_t v_head_stride,
@@ -538,6 +540,10 @@ int32_t engram_cache_append(const engram_cache *cache, const engram_seqs *seqs,
  *   out = softmax_j(scale * q . k_j) v_j, rounded to bf16.
  * Queries with no position left to read give zeros.  Tokens of no sequence
  * are left as they are.
+ * Limits of one call, ENGRAM_E_RANGE past them: T up to 2^22; where rows are
+ * taken by 16 (few tokens a sequence) such tiles below 2^19, and below 2^30
+ * times max_pages; where they are taken by 128 (prompts) tiles below 2^23.  A
+ * tile's rows are one sequence's tokens times one key head's query heads.
  * Maxima, sums and outputs are f32.  Fewer bits are kept in three places:
  *   - a weight e^(..) is rounded to bf16 (2^-8 of itself at most) where it meets
  *     its value, and not where it is summed, so the weights of a row add up to

@@ -296,3 +296,12 @@ def test_attend_asks_for_a_workspace(L):
         assert attend(L, ws=None, nws=need, **call) == E.E_ARG and E.last_error()
         assert attend(L, ws=FAKE + 16, nws=need, **call) == E.E_ARG and E.last_error()
     assert L.engram_cache_attend_bytes(ctypes.byref(cache_c()), ctypes.byref(seqs_c(batch=1, max_pages=16)), 4, 1) == 0
+
+
+def test_append_grid_is_checked(L):
+    """More workgroups than a grid holds threads for: refused before a launch."""
+    cache, seqs = cache_c(head_dim=256, kv_heads=32), seqs_c(batch=65536)
+    strides = dict(kt=32 * 256, kh=256, vt=32 * 256, vh=256, q=None, heads=0, rot=0, freq=None)
+    assert append(L, cache=cache, seqs=seqs, T=1024, **strides) == E.E_RANGE
+    assert "workgroups" in E.last_error()
+    assert append(L, cache=cache_c(head_dim=256, kv_heads=64), seqs=seqs, T=1024, **dict(strides, kt=64 * 256, vt=64 * 256)) == E.E_RANGE
