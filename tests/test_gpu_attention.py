@@ -921,6 +921,145 @@ def test_pages_past_4_gib(E, new, old):
                            small.nan_to_num() if big.dtype == torch.float32 else small)
 
 
+# ------------------------------------------------------ the far end of the sizes
+@pytest.mark.parametrize("dim,bf16", [(32, False), (544, True)])
+def test_add_norm_many_rows(E, dim, bf16):
+    """More rows than workgroups: each takes rows in turn.  The same bits as in
+    calls of fewer."""
+    rows, some = (1 << 20) + 1037, 4096
+    t = torch.bfloat16 if bf16 else torch.float32
+    g = seeded(dim)
+    few = torch.randn(some, dim, generator=g, device="cuda")
+    w = (1 + 0.3 * torch.randn(dim, generator=g, device="cuda")).bfloat16()
+    at = torch.arange(rows, device="cuda") % some
+    x = (0.3 * few).bfloat16()
+
+    def call(res, x):
+        total, codes = torch.empty_like(res), torch.zeros(res.shape, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(res.shape[0], dim // 32, dtype=torch.uint8, device="cuda")
+        E.add_norm(x, res, w, 1e-6, codes, scales, d_sum=total)
+        return total, codes, scales
+
+    want = call(few.to(t), x)
+    for got, one in zip(call(few.to(t)[at], x[at]), want):
+        assert torch.equal(got, one[at])
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_project_w4_most_tokens(E, fp8):
+    """2^22 tokens, which repeat sixty-four: the same bits for each."""
+    T, K, N = 1 << 22, 128, 16
+    w, ws, x, xs, x64 = w4_case(91, 64, K, N, fp8)
+    want = check_w4(E, w, ws, x, xs, x64)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    E.project_w4(x.repeat(T // 64, 1), E.W4(w, ws), y, None if xs is None else xs.repeat(T // 64, 1))
+    assert bool((y.view(T // 64, 64, N) == want).all())
+
+
+def test_append_most_tokens(E):
+    """2^22 tokens of one sequence at once, and in two calls that meet at a page's
+    border: the same bytes (each page has all its tokens in one call)."""
+    n, d = 1 << 22, 64
+    pages = torch.randperm(n // 64, device="cuda").int().view(1, -1)
+    k, v = (torch.randn(n, 1, d, generator=seeded(s), device="cuda", dtype=torch.bfloat16) for s in (1, 2))
+    freq = R.freq_of(d)
+    made = []
+    for cuts in ((0, n), (0, n // 2 + 64 * 77, n)):
+        codes = [torch.zeros(n // 64, 1, 64, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros(n // 64, 1, device="cuda") for _ in range(2)]
+        cache, err = E.Cache(*codes, *scales), torch.zeros(1, dtype=torch.int32, device="cuda")
+        for lo, hi in zip(cuts, cuts[1:]):
+            start = torch.tensor([lo], dtype=torch.int32, device="cuda")
+            E.cache_append(cache, E.Sequences(pages, start, d_err=err), k[lo:hi], v[lo:hi], freq)
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        made.append(codes + scales)
+    for x, y in zip(*made):
+        assert torch.equal(x, y)
+    # the last page against the formula
+    at = slice(n - 64, n)
+    want, _ = R.rotate(k[at], torch.arange(n - 64, n, device="cuda"), freq, True)
+    p = int(pages[0, -1])
+    got = R.e4m3(made[0][0][p, 0]) * made[0][2][p].to(F64)
+    within(got, want[:, 0], 2.0 ** -4 * want[:, 0].abs() + 2.0 ** -10 * made[0][2][p].to(F64) + 2.0 ** -20 * 8, "keys")
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_project_w4_lowest_scale(E, fp8):
+    """Scale byte 0 is 2^-127, below f32's normal numbers."""
+    w, ws, x, xs, x64 = w4_case(19, 5, 256, 32, fp8, 0, 1)
+    if fp8:
+        xs = (254 - xs.int()).to(torch.uint8)
+        x64 = R.grouped(R.e4m3(x), xs)
+    else:
+        x = (x.float() * 2.0 ** 120).bfloat16()
+        x64 = x.to(F64)
+    check_w4(E, w, ws, x, xs, x64)
+
+
+FORMS = [([1], [500], 2, 4, 128), ([1, 1], [1500, 70], 2, 8, 256), ([3], [5000], 1, 4, 64), ([300, 7], [90, 64], 4, 4, 128),
+         ([90, 60], [700, 3], 8, 4, 256), ([260], [2500], 8, 4, 64)]      # short, even pieces, tiles, split tiles
+
+
+@pytest.mark.parametrize("case", range(len(FORMS)))
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30])
+def test_attend_scales(E, scale, case):
+    """Negative scales turn the order of the logits round, zero ones level it."""
+    st = R.Step(70 + case, *FORMS[case])
+    st.fill_new()
+    q = st.heads()[0]
+    out = torch.empty(st.T, st.q, st.d, dtype=torch.bfloat16, device="cuda")
+    cache, seqs = st.objects(E)
+    ws = torch.empty(E.cache_attend_bytes(cache, seqs, st.q, st.T), dtype=torch.uint8, device="cuda")
+    E.cache_attend(cache, seqs, q, out, scale, 0, ws)
+    want, tol = R.attend(st, q, scale, 0)
+    within(out, want, tol, "out")
+
+
+@pytest.mark.parametrize("case", range(len(FORMS)))
+def test_attend_any_page_scale(E, case):
+    """Page scales that are no powers of two, as a caller's own cache may have."""
+    st = R.Step(80 + case, *FORMS[case])
+    st.fill_new()
+    for i in (0, 1):
+        st.scales[i] *= 1 + torch.rand(st.scales[i].shape, generator=st.gen, device="cuda")
+    check_attend(E, st)
+    check_attend(E, st, window=77)
+
+
+@pytest.mark.parametrize("case", range(len(FORMS)))
+def test_attend_far_windows(E, case):
+    """A window past every position is none, however large it is."""
+    st = R.Step(90 + case, *FORMS[case])
+    st.fill_new()
+    none = check_attend(E, st)
+    for window in (max(st.old) + max(st.new), (1 << 30) + 5, (1 << 31) - 1, 1 << 31, (1 << 40) + 1):
+        out = check_attend(E, st, window)
+        if window > 1 << 30:                            # shared out as without one: the same bits
+            assert torch.equal(out, none)
+
+
+@pytest.mark.parametrize("case", range(len(FORMS)))
+def test_heads_side_by_token(E, case):
+    """Queries, keys and values whose tokens lie side by side within a head."""
+    st, same = (R.Step(100 + case, *FORMS[case]) for _ in range(2))
+    freq, outs = R.freq_of(st.d), []
+    for s, far in ((st, True), (same, False)):
+        heads = [x.transpose(0, 1).contiguous().transpose(0, 1) if far else x for x in s.heads()]
+        q, k, v = heads
+        assert not far or s.T == 1 or q.stride(0) == s.d
+        qo, out = (torch.empty(s.T, s.q, s.d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        cache, seqs = s.objects(E)
+        E.cache_append(cache, seqs, k, v, freq, q, qo)
+        ws = torch.empty(E.cache_attend_bytes(cache, seqs, s.q, s.T), dtype=torch.uint8, device="cuda")
+        E.cache_attend(cache, seqs, qo.transpose(0, 1).contiguous().transpose(0, 1) if far else qo, out, 0.1, 0, ws)
+        outs += [qo, out]
+        assert int(s.err) == 0
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    for x, y in zip(st.codes + st.scales, same.codes + same.scales):
+        assert torch.equal(x.nan_to_num(), y.nan_to_num())
+
+
 # ------------------------------------------------------- streams and graphs
 def test_stream_and_graph(E):
     """The four operators on a stream of their own, and captured into a graph
