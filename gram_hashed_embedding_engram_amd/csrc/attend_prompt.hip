@@ -70,9 +70,11 @@ __device__ __forceinline__ Tile prompt_tile(const AttendArgs &a, int item)
 //
 // Two ragged chunks of 4096 tokens at most, 32 heads of 128 over 1500 cached
 // positions: 268-280 us, 0.98-1.02 PFLOP/s (a library's bf16 product of 8192^3
-// runs at 1.22; pages one by one, without the pipeline, took 351 us).  4096
-// tokens after 4096: 64-wide heads 0.82 PFLOP/s, 256-wide ones 0.87 (their sums
-// and queries leave one wavefront a SIMD).
+// runs at 1.22; pages one by one, without the pipeline, took 351 us), matrix
+// units busy 43% of the time and vector units 48%.  4096 tokens after 4096:
+// 64-wide heads 243 us, 0.85 PFLOP/s (the vector work of a logit is the same
+// beside half the matrix work: 59% and 35%), 256-wide ones 929 us, 0.89 (their
+// sums and queries leave one wavefront a SIMD).
 template <int D, bool SPLIT>
 __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs a)
 {
@@ -625,6 +627,8 @@ __global__ __launch_bounds__(256) void attend_tile_join_kernel(AttendArgs a)
 // us; 818 tokens of 6 heads of 64 after 227: 22 -> 18; 2 x 805 of 6 heads of 256
 // over 2 after 786: 71 -> 45.  With pieces of 4 pages 64-wide heads lost (750
 // tokens in three ragged chunks: 18 -> 21), with 6 256-wide ones (9 pages: 31 -> 36).
+// A table much wider than its sequences is cut for its width (256 tokens of 32
+// heads without a cache: 13 us, 24 with a table of 2048 columns).
 int32_t splits_of(const engram_cache &c, const Seqs &s, int32_t g)
 {
     constexpr int64_t kMost = 16;

@@ -749,9 +749,15 @@ __global__ __launch_bounds__(512) void attend_join_kernel(AttendArgs a)
 
 // Which kernel a call takes: tiles of 128 rows where the call has a workgroup
 // of them for every eighth CU, else tiles of 16 whose keys are shared out.  (In
-// us, 16-row tiles against 128-row ones: 534 tokens of 48 heads over 8 key heads
-// 43 and 18; 816 tokens of 16 heads over 2 27 and 16; 818 tokens of 6 heads
-// over 1, 39 tiles, 15 and 18; 2 x 4096 ragged tokens of 32 heads 1658 and 278.)
+// us, 16-row tiles against 128-row ones with their pages shared out: 534 tokens
+// of 48 heads over 8 key heads 53 and 20; 816 tokens of 16 heads over 2 35 and
+// 23; 818 tokens of 6 64-wide heads over 1 after 227, 39 tiles, 15 and 18; 2 x
+// 4096 ragged tokens of 32 heads 1662 and 279; 64 tokens of 32 heads over 8, 16
+// tiles, 9 and 20 after 500, 29 and 25 after 4000; 3 x 16 tokens of 64 64-wide
+// heads over 8 after 834 8 and 19.)  It holds for the whole call: single tokens
+// beside a prompt go through its tiles, one workgroup a key head each where the
+// prompt's tiles fill the chip (4096 tokens and one over 131000: 2527 us, 168 and
+// 56 in two calls).
 bool many_rows(const engram_cache &c, const Seqs &s, int32_t g)
 {
     return (int64_t)s.T * g >= 64 * (int64_t)s.B && prompt_tiles(c, s, g) >= device_cus() / 8;
@@ -764,10 +770,13 @@ int64_t row_units(const engram_cache &c, const Seqs &s, int32_t g)
                  : (((int64_t)s.each * g + kRows - 1) / kRows) * s.B) * c.kv_heads;
 }
 
-// Tables of so few pages are read without a join: 16 pages take 11 us there, as
-// long as a share of four pages (one a wavefront) and the join, whose launch
-// costs 4.7 us; fewer take less, and 23 pages took 13.8 against 11.2, 32 17.8
-// against 11.6.
+// Tables of so few pages are read without a join, whose launch costs 4.7 us.
+// In us, without and with it, for 8 units of 128-wide heads: 8 pages 8.4 and 10.4,
+// 16 11.4 and 10.7, 24 14.7 and 11.0; 64-wide heads: 16 pages 8.1 and 9.0, 24
+// 10.4 and 9.3; 256-wide: 8 pages 12.1 and 14.0, 12 15.4 and 14.6, 16 18.4 and
+// 14.9.  With 512 units it is faster up to 32 pages at least (128-wide: 39.6 and
+// 45.0).  The table's width counts, not the sequences': the host does not see
+// their lengths.
 constexpr int kShortPages = 16;
 constexpr int kLeastShare = 4;
 

@@ -442,7 +442,8 @@ void engram_ctx_destroy(engram_ctx *ctx);
  * dim a multiple of 32 up to 65536, rows below 2^31; d_x, d_res, d_w and
  * d_sum 16-byte, d_codes 8-byte aligned.  A NaN makes its row NaN codes; an
  * infinity (or squares that sum past f32's range) makes the norm infinite,
- * so its row zeros and itself NaN.  rows = 0 is a no-op. */
+ * so its row zeros and itself NaN; with eps = 0 a row whose squares vanish in
+ * f32 (below 2^-75 throughout) is NaN codes.  rows = 0 is a no-op. */
 #define ENGRAM_NORM_GROUP 32
 int32_t engram_add_norm(const uint16_t *d_x, const void *d_res, int32_t res_bf16,
                         const uint16_t *d_w, float eps, void *d_sum, uint8_t *d_codes,
@@ -544,6 +545,10 @@ int32_t engram_cache_append(const engram_cache *cache, const engram_seqs *seqs,
  * taken by 16 (few tokens a sequence) such tiles below 2^19, and below 2^30
  * times max_pages; where they are taken by 128 (prompts) tiles below 2^23.  A
  * tile's rows are one sequence's tokens times one key head's query heads.
+ * How a call is divided follows its sizes and max_pages alone, so that it can be
+ * captured: a table much wider than its sequences costs up to 10 us, and a
+ * prompt and single tokens over long caches are faster as two calls (each with
+ * its own sequences and token bounds; the other's tokens are left alone).
  * Maxima, sums and outputs are f32.  Fewer bits are kept in three places:
  *   - a weight e^(..) is rounded to bf16 (2^-8 of itself at most) where it meets
  *     its value, and not where it is summed, so the weights of a row add up to
@@ -552,7 +557,7 @@ int32_t engram_cache_append(const engram_cache *cache, const engram_seqs *seqs,
  *     value, off by at most 2^-21.8 of that below;
  *   - of a logit's products, those of eight neighbours are cut as in
  *     engram_project_w4: by about 2^-16 of its size for normal values.
- * For normal inputs an output is 0.0019 to 0.0023 of its size (rms) from the
+ * For normal inputs an output is 0.0018 to 0.0023 of its size (rms) from the
  * exact one, of which the result's rounding alone is 0.0017.
  *   d_q as for engram_cache_append; d_out [T][q_heads][head_dim] bf16,
  *   8-byte aligned; q_heads a multiple of kv_heads; scale finite;

@@ -81,6 +81,26 @@ def test_add_norm(E, rows, dim, add, bf16):
     within(R.e4m3(codes) * wide, y, tol, "codes")
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_add_norm_without_eps(E, bf16):
+    """eps = 0: rows whose squares f32 holds are normed whatever their size;
+    where all vanish in f32 the norm is nothing to divide by."""
+    t = torch.bfloat16 if bf16 else torch.float32
+    size = torch.tensor([1.0, 2.0 ** -60, 2.0 ** 50, 2.0 ** -90, 0.0], device="cuda")
+    res = (torch.randn(5, 96, generator=seeded(33), device="cuda") * size[:, None]).to(t)
+    w = torch.ones(96, dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros(5, 96, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(5, 3, dtype=torch.uint8, device="cuda")
+    E.add_norm(None, res, w, 0.0, codes, scales)
+    got = R.grouped(R.e4m3(codes), scales)
+    assert bool(torch.isnan(got[3:]).all())
+    r = res[:3].to(F64)
+    y = r / (r * r).mean(1, keepdim=True).sqrt()
+    # squares of 2^-120 and their sum keep 24 bits in f32
+    wide = torch.exp2(scales[:3].to(F64) - 127).repeat_interleave(32, 1)
+    within(got[:3], y, y.abs() * (2.0 ** -4 + 2.0 ** -18) + 2.0 ** -10 * wide, "codes")
+
+
 # --------------------------------------------------------------------- w4
 def w4_case(seed, T, K, N, fp8, lo=110, hi=130):
     g = seeded(seed)
