@@ -73,7 +73,7 @@ __device__ __forceinline__ Tile prompt_tile(const AttendArgs &a, int item)
 // runs at 1.22; pages one by one, without the pipeline, took 351 us), matrix
 // units busy 43% of the time and vector units 48%.  4096 tokens after 4096:
 // 64-wide heads 243 us, 0.85 PFLOP/s (the vector work of a logit is the same
-// beside half the matrix work: 59% and 35%), 256-wide ones 929 us, 0.89 (their
+// beside half the matrix work: 59% and 35%), 256-wide ones 918 us, 0.90 (their
 // sums and queries leave one wavefront a SIMD).
 template <int D, bool SPLIT>
 __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs a)
@@ -93,11 +93,12 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
     const int kv = a.c.kv_heads;
     const int split = SPLIT ? blockIdx.x % a.splits : 0, at = SPLIT ? blockIdx.x / a.splits : blockIdx.x;
     const int item = (uint32_t)at / (uint32_t)kv, head = at - item * kv;
-    if (blockIdx.x == 0)
-        raise_bad(a.s);
     const Tile tile = prompt_tile(a, item);
-    if (!tile.on)
+    if (!tile.on) {
+        if (blockIdx.x == 0)
+            raise_bad(a.s);
         return;
+    }
     const Seq q = tile.q;
     const int b = tile.b, rows = tile.rows, row0 = tile.row0;
     const int row = row0 + 32 * w + r32;
@@ -561,6 +562,8 @@ __global__ __launch_bounds__(64 * kTileWaves, D == 256 ? 1 : 2) void attend_tile
             }
         }
     }
+    if (blockIdx.x == 0)            // last: nothing waits for it
+        raise_bad(a.s);
     l = add_x32(l);
     if (!valid)
         return;
