@@ -17,6 +17,7 @@ OK = 0
 E_ARG, E_RANGE, E_UNSUPPORTED, E_STATE, E_HIP, E_DEVICE = -1, -2, -3, -4, -5, -6
 DEVERR_TOKEN, DEVERR_ROW, DEVERR_POSITION = 1, 2, 4
 DEVERR_PAGE, DEVERR_SEQUENCE = 8, 16
+DEVERR_ROUTE = 32
 FMT_Q2K, FMT_E4M3 = 0, 1
 Q2K_ROW_BYTES = 84
 STREAM_ROW_BYTES = 12288      # engram_stream_read's row (ENGRAM_STREAM_ROW_BYTES)
@@ -24,6 +25,7 @@ STREAM_SINK_WORDS = 8192      # its sink (ENGRAM_STREAM_SINK_WORDS)
 STATIC_SCRATCH_BYTES = 32 << 20   # engram_layer_static's scratch (ENGRAM_STATIC_SCRATCH_BYTES)
 PAGE_TOKENS = 64              # positions a cache page holds (ENGRAM_PAGE_TOKENS)
 NORM_GROUP = 32               # values a scale of 8- and 4-bit rows covers (ENGRAM_NORM_GROUP)
+F8_BLOCK = 128                # weights and values a scale of 8-bit weights covers each way (ENGRAM_F8_BLOCK)
 STAGES = ("hash", "gather", "project", "gate")
 
 # Every symbol include/engram.h declares.
@@ -40,6 +42,8 @@ EXPORTS = (
     "engram_ctx_set_graph_mode", "engram_ctx_set_position", "engram_layer_static",
     "engram_add_norm", "engram_project_w4", "engram_cache_append", "engram_cache_attend_bytes",
     "engram_cache_attend",
+    "engram_project_f8", "engram_route_bytes", "engram_route", "engram_experts_up",
+    "engram_experts_down_bytes", "engram_experts_down",
 )
 
 
@@ -81,6 +85,13 @@ class SequencesC(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("d_pages", ctypes.c_void_p), ("d_start", ctypes.c_void_p),
                 ("d_cu", ctypes.c_void_p), ("d_err", ctypes.c_void_p)]
+
+
+class RoutesC(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("chosen", ctypes.c_int32),
+                ("tokens", ctypes.c_int64), ("d_ids", ctypes.c_void_p),
+                ("d_weights", ctypes.c_void_p), ("d_offsets", ctypes.c_void_p),
+                ("d_order", ctypes.c_void_p), ("d_err", ctypes.c_void_p)]
 
 
 _lib = None
@@ -134,6 +145,13 @@ def lib():
             "engram_cache_attend_bytes": (ctypes.c_size_t, [p, p, i32, i64]),
             "engram_cache_attend": (i32, [p, p, p, i64, i64, p, i32, i64, ctypes.c_float, i64, p,
                                           ctypes.c_size_t, p]),
+            "engram_project_f8": (i32, [p, p, i32, p, p, p, i64, i64, i64, p]),
+            "engram_route_bytes": (ctypes.c_size_t, [p]),
+            "engram_route": (i32, [p, p, i32, i64, p, i32, i32, i32, i32, i32, ctypes.c_float, p,
+                                   ctypes.c_size_t, p]),
+            "engram_experts_up": (i32, [p, p, p, i32, p, p, p, p, i64, i64, p]),
+            "engram_experts_down_bytes": (ctypes.c_size_t, [p, i64]),
+            "engram_experts_down": (i32, [p, p, p, i32, p, p, p, i64, i64, p, ctypes.c_size_t, p]),
         }
         # a library built before this binding: another version, or, as additions
         # alone leave the version as it is, one that lacks an entry point
@@ -623,6 +641,243 @@ def cache_attend(cache: Cache, seqs: Sequences, d_q, d_out, scale, window=0, d_w
         ws, nws = d_ws.data_ptr(), d_ws.numel()
     rc = (_lib or lib()).engram_cache_attend(cache.ref, seqs.ref, qp, qt, qh, d_out.data_ptr(), q_heads, T,
                                   scale, window, ws, nws, _stream(stream))
+    if rc:
+        _check(rc)
+
+
+# The experts' sub-layer's calls, as the attention sub-layer's, look at all their
+# tensors in one condition.
+class F8:
+    """Weight matrices in 8 bits: d_w [..., N, K] e4m3 codes, d_scales
+    [..., ceil(N/128), K/128] f32, one per block of 128 x 128."""
+
+    def __init__(self, d_w, d_scales):
+        *lead, N, K = d_w.shape
+        k = _kinds()
+        _typed(d_w, "w", k.e4m3)
+        _typed(d_scales, "w scales", k.f32, (*lead, -(-N // F8_BLOCK), -(-K // F8_BLOCK)))
+        self.w, self.scales, self.lead = d_w, d_scales, tuple(lead)
+        self.N, self.K = N, K
+        self.scale_shapes = (K // NORM_GROUP, K // F8_BLOCK)
+        self.at = (d_w.data_ptr(), d_scales.data_ptr())
+        self.host = _host_name(w=d_w, w_scales=d_scales)
+        self.device = _one_device(w=d_w, w_scales=d_scales)
+
+
+class Routes:
+    """Where a step's tokens go (engram_routes): d_ids [T, k] int32 and
+    d_weights [T, k] f32, the experts of each token; d_offsets [experts+1] and
+    d_order [T*k] int32, their slots sorted by expert; d_err an int32 error
+    word or None.  route fills the first four."""
+
+    def __init__(self, d_ids, d_weights, d_offsets, d_order, d_err=None):
+        T, chosen = d_ids.shape
+        k = _kinds()
+        _typed(d_ids, "ids", k.i32)
+        _typed(d_weights, "weights", k.f32, (T, chosen))
+        _typed(d_offsets, "offsets", k.i32)
+        _typed(d_order, "order", k.i32, (T * chosen,))
+        if d_offsets.dim() != 1 or d_offsets.numel() < 2:
+            raise EngramError(E_ARG, f"offsets: shape {tuple(d_offsets.shape)}, (experts + 1,) is needed")
+        if d_err is not None:
+            _typed(d_err, "err", k.i32)
+            _need(d_err, "err", 4)
+        self.keep = (d_ids, d_weights, d_offsets, d_order, d_err)
+        self.host = _host_name(ids=d_ids, weights=d_weights, offsets=d_offsets, order=d_order,
+                               err=d_err)
+        self.device = _one_device(ids=d_ids, weights=d_weights, offsets=d_offsets, order=d_order,
+                                  err=d_err)
+        self.T, self.k, self.experts = T, chosen, d_offsets.numel() - 1
+        self.c = RoutesC(self.experts, chosen, T, d_ids.data_ptr(), d_weights.data_ptr(),
+                         d_offsets.data_ptr(), d_order.data_ptr(), _ptr(d_err))
+        self.ref = ctypes.byref(self.c)
+
+
+def _one_device(**tensors):
+    """The index of the device that these tensors share (-1: host memory)."""
+    first = None
+    for name, t in tensors.items():
+        if t is not None:
+            if first is None:
+                first = t.get_device()
+            elif t.get_device() != first:
+                raise EngramError(E_ARG, f"{name.replace('_', ' ')}: on {t.device}, the others are not")
+    return first
+
+
+_device = None
+
+
+def _here(device):
+    """Refuse a call whose tensors are on another device than the current one,
+    whose stream it would be enqueued on."""
+    global _device
+    if _device is None:
+        import torch
+        torch.cuda.current_stream()                          # initialises the device
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if device != _device():
+        raise EngramError(E_ARG, f"the tensors are on device {device}, the current one is {_device()}")
+
+
+def _rows8(k, x, xs, rows, weights):
+    """Whether x and xs are such rows: 0 with E8M0 scales, 1 with f32 ones, -1 neither."""
+    if not (x.dtype in k.e4m3 and x.shape == (rows, weights.K) and x.is_contiguous()
+            and xs.is_contiguous()):
+        return -1
+    if xs.dtype in k.f32:
+        return 1 if xs.shape == (rows, weights.scale_shapes[1]) else -1
+    return 0 if xs.dtype in k.e8m0 and xs.shape == (rows, weights.scale_shapes[0]) else -1
+
+
+def _refuse_rows8(k, x, xs, name, rows, weights):
+    _typed(x, name, k.e4m3, (rows, weights.K))
+    _typed(xs, name + " scales", k.e8m0 | k.f32,
+           (rows, weights.scale_shapes[xs.dtype in k.f32]))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            _on_gpu(t, name.replace("_", " "))
+            if t.get_device() != device:
+                raise EngramError(E_ARG, f"{name.replace('_', ' ')}: on {t.device}, not on the "
+                                         f"call's device {device}")
+
+
+def project_f8(d_x, weights: F8, d_y, d_xs, stream=None):
+    """y = x w^T through 8-bit weights (engram_project_f8): d_x [T, K] e4m3
+    codes with d_xs [T, K/32] (powers of two, as add_norm gives them) or
+    [T, K/128] f32; d_y [T, N] bf16."""
+    k = _types or _kinds()
+    T, dev = d_x.shape[0], weights.device
+    kind = _rows8(k, d_x, d_xs, T, weights)
+    if not (kind >= 0 and dev >= 0 and weights.lead == () and weights.host is None
+            and d_y.dtype in k.bf16 and d_y.shape == (T, weights.N) and d_y.is_contiguous()
+            and d_x.get_device() == dev and d_xs.get_device() == dev and d_y.get_device() == dev):
+        if weights.lead:
+            raise EngramError(E_ARG, f"w: {weights.lead} matrices, one is needed")
+        _refuse_rows8(k, d_x, d_xs, "x", T, weights)
+        _typed(d_y, "y", k.bf16, (T, weights.N))
+        _refuse_host(weights.host)
+        _same_device(dev, x=d_x, x_scales=d_xs, y=d_y)
+    _here(dev)
+    w, ws = weights.at
+    rc = (_lib or lib()).engram_project_f8(d_x.data_ptr(), d_xs.data_ptr(), kind, w, ws,
+                                           d_y.data_ptr(), T, weights.K, weights.N,
+                                           _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def route_bytes(routes: Routes):
+    """Workspace bytes a route of these sizes needs (may be 0)."""
+    return lib().engram_route_bytes(routes.ref)
+
+
+def route(d_logits, routes: Routes, d_bias=None, softmax=False, groups=1, top_groups=1,
+          group_best=2, renorm=True, factor=1.0, d_ws=None, stream=None):
+    """Routing to experts (engram_route): d_logits [T, experts] f32 or bf16 (a
+    view of wider rows if need be), d_bias [experts] f32 or None; fills
+    routes.  Scores are sigmoids, or with softmax=True softmaxes; of `groups`
+    runs of experts the top_groups with the largest sum of their group_best
+    best are kept.  d_ws a uint8 tensor of route_bytes bytes or None."""
+    k = _types or _kinds()
+    dev = routes.device
+    if not (d_logits.dtype in k.res and d_logits.shape == (routes.T, routes.experts)
+            and routes.host is None and dev >= 0 and d_logits.get_device() == dev
+            and (d_logits.stride(1) == 1 or routes.experts == 1)
+            and (d_bias is None or d_bias.dtype in k.f32 and d_bias.shape == (routes.experts,)
+                 and d_bias.is_contiguous() and d_bias.get_device() == dev)
+            and (d_ws is None or d_ws.dtype in k.u8 and d_ws.is_contiguous()
+                 and d_ws.get_device() == dev)):
+        if d_logits.dtype not in k.res:
+            _typed(d_logits, "logits", k.res)
+        if d_logits.shape != (routes.T, routes.experts):
+            raise EngramError(E_ARG, f"logits: shape {tuple(d_logits.shape)}, "
+                                     f"{(routes.T, routes.experts)} is needed")
+        if routes.experts > 1 and d_logits.stride(1) != 1:
+            raise EngramError(E_ARG, "logits: a row's values must lie side by side")
+        if d_bias is not None:
+            _typed(d_bias, "bias", k.f32, (routes.experts,))
+        if d_ws is not None:
+            _typed(d_ws, "ws", k.u8)
+        _refuse_host(routes.host)
+        _same_device(dev, logits=d_logits, bias=d_bias, ws=d_ws)
+    _here(dev)
+    stride = d_logits.stride(0) if routes.T > 1 else routes.experts
+    ws, nws = (0, 0) if d_ws is None else (d_ws.data_ptr(), d_ws.numel())
+    rc = (_lib or lib()).engram_route(
+        routes.ref, d_logits.data_ptr(), d_logits.dtype not in k.f32, stride,
+        None if d_bias is None else d_bias.data_ptr(), softmax, groups, top_groups, group_best,
+        renorm, factor, ws, nws, _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def experts_up(d_x, d_xs, weights: F8, routes: Routes, d_h, d_hs, stream=None):
+    """The experts' gated up projection (engram_experts_up): d_x [T, K] e4m3
+    codes with scales d_xs as for project_f8; weights [experts, 2, I, K], the
+    gate's and the up matrix; d_h [T*k, I] codes and d_hs [T*k, I/32] in the
+    plan's order."""
+    k = _types or _kinds()
+    T, R, I, dev = routes.T, routes.T * routes.k, weights.N, weights.device
+    kind = _rows8(k, d_x, d_xs, T, weights)
+    if not (kind >= 0 and dev >= 0 and weights.lead == (routes.experts, 2) and weights.host is None
+            and routes.host is None and routes.device == dev
+            and d_h.dtype in k.e4m3 and d_h.shape == (R, I) and d_h.is_contiguous()
+            and d_hs.dtype in k.e8m0 and d_hs.shape == (R, I // NORM_GROUP) and d_hs.is_contiguous()
+            and d_x.get_device() == dev and d_xs.get_device() == dev
+            and d_h.get_device() == dev and d_hs.get_device() == dev):
+        if weights.lead != (routes.experts, 2):
+            raise EngramError(E_ARG, f"w: {weights.lead} matrices, {(routes.experts, 2)} are needed")
+        _refuse_rows8(k, d_x, d_xs, "x", T, weights)
+        _typed(d_h, "h", k.e4m3, (R, I))
+        _typed(d_hs, "h scales", k.e8m0, (R, I // NORM_GROUP))
+        _refuse_host(weights.host, routes.host)
+        _same_device(dev, x=d_x, x_scales=d_xs, h=d_h, h_scales=d_hs, ids=routes.keep[0])
+    _here(dev)
+    w, ws = weights.at
+    rc = (_lib or lib()).engram_experts_up(routes.ref, d_x.data_ptr(), d_xs.data_ptr(), kind, w, ws,
+                                           d_h.data_ptr(), d_hs.data_ptr(), weights.K, I,
+                                           _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def experts_down_bytes(weights: F8, routes: Routes):
+    """Workspace bytes an experts_down of these sizes needs (may be 0)."""
+    return lib().engram_experts_down_bytes(routes.ref, weights.N)
+
+
+def experts_down(d_h, d_hs, weights: F8, routes: Routes, d_y, d_ws=None, stream=None):
+    """The experts' down projection and the weighted sum over a token's experts
+    (engram_experts_down): d_h [T*k, K] in the plan's order with scales d_hs as
+    for project_f8; weights [experts, N, K]; d_y [T, N] bf16; d_ws a uint8
+    tensor of experts_down_bytes bytes or None."""
+    k = _types or _kinds()
+    T, dev = routes.T, weights.device
+    kind = _rows8(k, d_h, d_hs, T * routes.k, weights)
+    if not (kind >= 0 and dev >= 0 and weights.lead == (routes.experts,) and weights.host is None
+            and routes.host is None and routes.device == dev
+            and d_y.dtype in k.bf16 and d_y.shape == (T, weights.N) and d_y.is_contiguous()
+            and d_h.get_device() == dev and d_hs.get_device() == dev and d_y.get_device() == dev
+            and (d_ws is None or d_ws.dtype in k.u8 and d_ws.is_contiguous()
+                 and d_ws.get_device() == dev)):
+        if weights.lead != (routes.experts,):
+            raise EngramError(E_ARG, f"w: {weights.lead} matrices, {(routes.experts,)} are needed")
+        _refuse_rows8(k, d_h, d_hs, "h", T * routes.k, weights)
+        _typed(d_y, "y", k.bf16, (T, weights.N))
+        if d_ws is not None:
+            _typed(d_ws, "ws", k.u8)
+        _refuse_host(weights.host, routes.host)
+        _same_device(dev, h=d_h, h_scales=d_hs, y=d_y, ws=d_ws, ids=routes.keep[0])
+    _here(dev)
+    w, ws = weights.at
+    space, nws = (0, 0) if d_ws is None else (d_ws.data_ptr(), d_ws.numel())
+    rc = (_lib or lib()).engram_experts_down(routes.ref, d_h.data_ptr(), d_hs.data_ptr(), kind, w,
+                                             ws, d_y.data_ptr(), weights.K, weights.N, space, nws,
+                                             _stream(stream))
     if rc:
         _check(rc)
 

@@ -56,6 +56,7 @@ extern "C" {
 #define ENGRAM_DEVERR_POSITION 4   /* graph mode: a step past max_seq              */
 #define ENGRAM_DEVERR_PAGE 8       /* page id < 0 or >= the cache's page count     */
 #define ENGRAM_DEVERR_SEQUENCE 16  /* a sequence's start or token bounds           */
+#define ENGRAM_DEVERR_ROUTE 32     /* a logit, bias or plan of the experts          */
 
 /* limits of the hash geometry (the hash constants travel as kernel arguments) */
 #define ENGRAM_MAX_LAYERS 4
@@ -570,6 +571,112 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
                             const uint16_t *d_q, int64_t q_token_stride, int64_t q_head_stride,
                             uint16_t *d_out, int32_t q_heads, int64_t T, float scale,
                             int64_t window, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------- the experts' sub-layer beside it
+ *
+ * What a served token goes through after attention: routing to experts
+ * (engram_route), their gated up projection (engram_experts_up), and their down
+ * projection with the weighted sum over a token's experts
+ * (engram_experts_down).  engram_project_f8 is the plain product with weights of
+ * the same kind.  As above none of them allocates, keeps state between calls or
+ * lets the order of atomics show: equal inputs give equal bits; outputs do not
+ * overlap inputs.
+ *
+ * Weights are e4m3 codes [N][K] with one f32 scale per block of 128 x 128,
+ * [ceil(N/128)][K/128]: a weight is its code times its block's scale (whatever
+ * its sign or power).  Rows are e4m3 codes [rows][K] with scales of either kind:
+ *   x_f32 = 0:  [rows][K/32] exponents + 127 of a power of two per 32 values
+ *               (engram_add_norm's and engram_experts_up's outputs; 255 is NaN);
+ *   x_f32 != 0: [rows][K/128] f32.
+ * Within a block of 128 the matrix instruction takes the products of eight
+ * neighbours together, as engram_project_w4's does; blocks are added in f32. */
+#define ENGRAM_F8_BLOCK 128
+
+/* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ).
+ *   d_x, d_x_scales  T rows;  d_w, d_w_scales  weights;  d_y [T][N] bf16.
+ * K a positive multiple of 128 up to 2^20, N a positive multiple of 16 up to
+ * 2^24, T up to 2^22.  d_x and d_w 16-byte, d_y 8-byte, scales 4-byte aligned.
+ * T = 0 is a no-op. */
+int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_f32,
+                          const uint8_t *d_w, const float *d_w_scales, uint16_t *d_y, int64_t T,
+                          int64_t K, int64_t N, void *stream);
+
+/* Where a call's tokens go.  Slot t*chosen + j is token t's j-th expert.
+ *   experts  1..1024;  chosen  experts a token, 1..32 and up to experts;
+ *   tokens   up to 2^22, tokens * chosen up to 2^24;
+ *   d_ids     [tokens][chosen] int32, -1 = a slot without an expert;
+ *   d_weights [tokens][chosen] f32;
+ *   d_offsets [experts+1] int32 and d_order [tokens*chosen] int32, the plan:
+ *             d_order[d_offsets[e] .. d_offsets[e+1]-1] are the slots of
+ *             expert e, ascending; rows past d_offsets[experts] belong to none;
+ *   d_err     nullable.
+ * engram_route writes all but d_err; the products read them.  A plan made
+ * elsewhere may order an expert's slots as it likes, each slot at most once.
+ * Offsets outside 0..tokens*chosen or falling, and slots out of range, set
+ * ENGRAM_DEVERR_ROUTE; their rows are not computed. */
+typedef struct engram_routes {
+    int32_t experts;
+    int32_t chosen;
+    int64_t tokens;
+    int32_t *d_ids;
+    float *d_weights;
+    int32_t *d_offsets;
+    int32_t *d_order;
+    int32_t *d_err;
+} engram_routes;
+
+/* Chooses each token's experts and weights, and makes the plan.
+ *   d_logits  [tokens][experts] f32, or bf16 with logits_bf16 != 0, rows
+ *             logits_stride values apart;  d_bias [experts] f32, nullable.
+ * An expert is open to a token where its logit and its bias are finite (a logit
+ * or bias that is NaN or +inf also sets ENGRAM_DEVERR_ROUTE); only open experts
+ * count.  score = 1 / (1 + e^-x), or with softmax != 0 e^x over the sum of e^x.
+ * groups > 1 (experts in equal runs, up to 64 of them): only the experts of the
+ * top_groups groups with the largest sum of their group_best (1 or 2) largest
+ * score + bias are left.  Of those left the `chosen` with the largest score +
+ * bias are taken, largest first (without a bias: the largest logits); among
+ * equals the lower index, for groups too.  Sums and differences that decide are
+ * good to 64 bits.  weight = score, divided by the sum of the token's chosen
+ * scores with renorm != 0 (0 where that sum is 0), times factor.
+ * A token with fewer open experts than `chosen` has id -1 and weight 0 in its
+ * last slots, which are not in the plan; a row of -inf goes nowhere.
+ *   d_ws  (256-byte aligned, caller-owned) of engram_route_bytes bytes; may be
+ *         NULL where that is 0.  Calls that share it must not overlap.
+ * tokens = 0 is a no-op (the plan is not written). */
+size_t engram_route_bytes(const engram_routes *routes);
+int32_t engram_route(const engram_routes *routes, const void *d_logits, int32_t logits_bf16,
+                     int64_t logits_stride, const float *d_bias, int32_t softmax, int32_t groups,
+                     int32_t top_groups, int32_t group_best, int32_t renorm, float factor,
+                     void *d_ws, size_t ws_bytes, void *stream);
+
+/* h[p][i] = silu(g) * u for every row p of the plan, with g = x[t] . w[e][0][i]
+ * and u = x[t] . w[e][1][i] of its expert e and its slot's token t; h leaves as
+ * e4m3 codes under a power of two per 32 values (engram_add_norm's kind), from
+ * f32.
+ *   d_x, d_x_scales  tokens rows of K values;
+ *   d_w     [experts][2][I][K];  d_w_scales [experts][2][I/128][K/128];
+ *   d_h     [tokens*chosen][I];  d_h_scales [tokens*chosen][I/32].
+ * Rows of h past the plan's are left as they are.  K and I multiples of 128 up
+ * to 2^20, tokens * K below 2^31.  d_x, d_w and d_h 16-byte, scales 4-byte
+ * aligned. */
+int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const void *d_x_scales,
+                          int32_t x_f32, const uint8_t *d_w, const float *d_w_scales, uint8_t *d_h,
+                          uint8_t *d_h_scales, int64_t K, int64_t I, void *stream);
+
+/* y[t] = bf16( sum_j weight[t][j] * (w[e_j] h[p_j]) ) over the token's slots
+ * that have an expert, in f32; a token without one gets zeros.
+ *   d_h, d_h_scales  tokens*chosen rows of K values in the plan's order;
+ *   d_w     [experts][N][K];  d_w_scales [experts][ceil(N/128)][K/128];
+ *   d_y     [tokens][N] bf16;
+ *   d_ws    (256-byte aligned, caller-owned) of engram_experts_down_bytes bytes;
+ *           may be NULL where that is 0.  Calls that share it must not overlap.
+ * K a multiple of 128 up to 2^20, N of 16 up to 2^24.  d_h and d_w 16-byte, d_y
+ * 8-byte, scales 4-byte aligned. */
+size_t engram_experts_down_bytes(const engram_routes *routes, int64_t N);
+int32_t engram_experts_down(const engram_routes *routes, const uint8_t *d_h,
+                            const void *d_h_scales, int32_t h_f32, const uint8_t *d_w,
+                            const float *d_w_scales, uint16_t *d_y, int64_t K, int64_t N,
+                            void *d_ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------ measurement */
 
