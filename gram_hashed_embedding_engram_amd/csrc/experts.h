@@ -56,6 +56,17 @@ __device__ __forceinline__ bool find_expert(int i, const Plan &p, F pieces, int 
     return false;
 }
 
+// How many items find_expert finds.
+template <class F>
+__device__ __forceinline__ int all_pieces(const Plan &p, F pieces)
+{
+    const int lane = threadIdx.x & 63;
+    int sum = 0;
+    for (int base = 0; base < p.E; base += 64)
+        sum += base + lane < p.E ? pieces(span_of(p, base + lane).n) : 0;
+    return __builtin_amdgcn_readlane(wave_scan(sum), 63);
+}
+
 // Spans that do not hold set the error bit (one workgroup of a call).
 __device__ __forceinline__ void raise_bad_plan(const Plan &p)
 {

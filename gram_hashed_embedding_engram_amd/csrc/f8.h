@@ -1,0 +1,39 @@
+// Shared pieces of the products with block-scaled 8-bit weights (f8_rows.hip,
+// f8_tiles.hip).  Internal to the library.
+#pragma once
+
+#include "experts.h"
+
+namespace engram {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kFp8 = 0;                 // the matrix instruction's format number
+constexpr int kOne = 0x7F7F7F7F;        // E8M0 of 1
+
+// y = x w^T; h = silu(x gate^T) * (x up^T); products of the plan's rows
+enum F8Mode { kDense, kUp, kDown };
+
+struct F8Args {
+    Plan p;
+    const uint8_t *x;
+    const void *xs;                     // E8M0 per 32 values, or f32 per 128
+    const uint8_t *w;
+    const float *ws;
+    void *y;                            // bf16; e4m3 codes; f32 products by slot
+    uint8_t *hs;
+    int T, K, N;                        // N: outputs, for kUp those of one half
+};
+
+// tiles of `rows` rows that any plan of the call can ask for
+inline int64_t f8_most_tiles(const Plan &p, int64_t rows)
+{
+    return p.slots / rows + (p.slots < p.E ? p.slots : p.E);
+}
+
+template <F8Mode MODE>
+void launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l);
+
+}  // namespace engram

@@ -1,29 +1,9 @@
 // Products of 8-bit rows with 8-bit weights that carry an f32 scale per
 // 128 x 128 block.
-#include "experts.h"
+#include "f8.h"
 
 namespace engram {
 namespace {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kFp8 = 0;
-constexpr int kOne = 0x7F7F7F7F;        // E8M0 of 1
-
-enum Mode { kDense, kUp, kDown };
-
-struct Args {
-    Plan p;
-    const uint8_t *x;
-    const void *xs;
-    const uint8_t *w;
-    const float *ws;
-    void *y;
-    uint8_t *hs;
-    int T, K, N;                        // N: outputs, for kUp those of one half
-};
 
 // lane l's operand of a 16 x 128 tile: row l % 16, bytes 16(l / 16) and 64 on
 __device__ __forceinline__ i32x8 operand(const uint8_t *p)
@@ -33,8 +13,8 @@ __device__ __forceinline__ i32x8 operand(const uint8_t *p)
 }
 
 // A wavefront a tile of 16 rows and 32 outputs.
-template <Mode MODE, bool XF32>
-__global__ __launch_bounds__(64) void tile_kernel(Args a)
+template <F8Mode MODE, bool XF32>
+__global__ __launch_bounds__(64) void tile_kernel(F8Args a)
 {
     const int lane = threadIdx.x, r16 = lane & 15, q = lane >> 4;
     const int n0 = blockIdx.x * 32, KB = a.K / 128, NB = (a.N + 127) / 128;
@@ -135,8 +115,8 @@ __global__ __launch_bounds__(256) void sum_kernel(const float *__restrict__ v,
     }
 }
 
-template <Mode MODE>
-void launch_tiles(const Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
+template <F8Mode MODE>
+void launch_tiles(const F8Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
 {
     const dim3 grid((unsigned)((a.N + 31) / 32), (unsigned)tiles);
     if (f32)
@@ -145,28 +125,27 @@ void launch_tiles(const Args &a, bool f32, int64_t tiles, bool last, const Launc
         dispatch(tile_kernel<MODE, false>, grid, dim3(64), l, true, last, a);
 }
 
-// tiles of 16 rows that any plan of the call can ask for
-int64_t most_tiles(const Plan &p)
-{
-    const int64_t s = p.slots;
-    return s / 16 + (s < p.E ? s : p.E);
-}
-
 }  // namespace
 
 int32_t launch_project_f8(const Rows8 &x, const Blocks8 &w, uint16_t *y, int64_t T, int64_t K,
                           int64_t N, const Launch &l)
 {
-    const Args a{Plan{}, x.x, x.s, w.w, w.s, y, nullptr, (int)T, (int)K, (int)N};
-    launch_tiles<kDense>(a, x.f32, (T + 15) / 16, true, l);
+    const F8Args a{Plan{}, x.x, x.s, w.w, w.s, y, nullptr, (int)T, (int)K, (int)N};
+    if (T > 128)
+        launch_f8_tiles<kDense>(a, x.f32, true, l);
+    else
+        launch_tiles<kDense>(a, x.f32, (T + 15) / 16, true, l);
     return launch_status("engram project_f8 kernel");
 }
 
 int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8_t *h, uint8_t *hs,
                           int64_t K, int64_t I, const Launch &l)
 {
-    const Args a{p, x.x, x.s, w.w, w.s, h, hs, p.T, (int)K, (int)I};
-    launch_tiles<kUp>(a, x.f32, most_tiles(p), true, l);
+    const F8Args a{p, x.x, x.s, w.w, w.s, h, hs, p.T, (int)K, (int)I};
+    if (p.slots / p.E >= 48)
+        launch_f8_tiles<kUp>(a, x.f32, true, l);
+    else
+        launch_tiles<kUp>(a, x.f32, f8_most_tiles(p, 16), true, l);
     return launch_status("engram experts_up kernel");
 }
 
@@ -175,8 +154,11 @@ size_t experts_down_bytes(const Plan &p, int64_t N) { return (size_t)p.slots * N
 int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uint16_t *y, int64_t K,
                             int64_t N, void *ws, const Launch &l)
 {
-    const Args a{p, h.x, h.s, w.w, w.s, ws, nullptr, p.T, (int)K, (int)N};
-    launch_tiles<kDown>(a, h.f32, most_tiles(p), false, l);
+    const F8Args a{p, h.x, h.s, w.w, w.s, ws, nullptr, p.T, (int)K, (int)N};
+    if (p.slots / p.E >= 48)
+        launch_f8_tiles<kDown>(a, h.f32, false, l);
+    else
+        launch_tiles<kDown>(a, h.f32, f8_most_tiles(p, 16), false, l);
     dispatch(sum_kernel, dim3((unsigned)((N / 4 + 255) / 256), (unsigned)(p.T < 65535 ? p.T : 65535)),
              dim3(256), l, false, true, (const float *)ws, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     return launch_status("engram experts_down kernels");

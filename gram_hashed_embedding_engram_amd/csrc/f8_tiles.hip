@@ -1,0 +1,286 @@
+// Products of many 8-bit rows with 8-bit weights that carry an f32 scale per
+// 128 x 128 block: a plain projection, the experts' gated up projection, and
+// their down projection, as tiles of one matrix kernel.
+#include "f8.h"
+
+namespace engram {
+namespace {
+
+constexpr int BN = 256;            // weight rows a tile (kUp: 128 of the gate, 128 of the up matrix)
+constexpr int XCDS = 8;
+constexpr int WB = 4;              // 16-row weight blocks a wavefront
+
+typedef __attribute__((address_space(3))) void *lptr_t;
+
+// chunk c of an LDS row of 128 bytes sits at c ^ swizzle(r): any 8 or 16
+// neighbouring rows read at one chunk meet all banks
+__device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
+
+template <int TB>
+struct Stage {
+    u32x4 tok[32 * TB * 8];
+    u32x4 w[BN * 8];
+    uint32_t xs[32 * TB];
+};
+
+template <F8Mode MODE, bool XF32, int TB>
+__global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
+{
+    constexpr int BM = 32 * TB, LT = BM / 64, LW = BN / 64;
+    __shared__ Stage<TB> stage[2];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int th = (wave >> 2), oq = wave & 3;       // token half, output quarter
+    const int r16 = lane & 15, q = lane >> 4;
+    const int KB = a.K / 128;
+    constexpr int NT = MODE == kUp ? BN / 2 : BN;    // outputs a tile
+    const int tiles_n = (a.N + NT - 1) / NT;
+
+    // ---- this workgroup's tile: each XCD takes a contiguous run of them
+    int expert = 0, tm, tn;
+    Span span{0, a.T};
+    const auto mine = [&](int total) {
+        const int b = blockIdx.x, xcd = b % XCDS, per = total / XCDS, rem = total % XCDS;
+        return xcd * per + min(xcd, rem) + b / XCDS;
+    };
+    if (MODE == kDense) {
+        constexpr int GROUP_M = 8;
+        const int tiles_m = (a.T + BM - 1) / BM, L = mine(tiles_m * tiles_n);
+        const int in_group = GROUP_M * tiles_n, first = L / in_group * GROUP_M;
+        const int size = min(tiles_m - first, GROUP_M);
+        tm = first + L % in_group % size;
+        tn = L % in_group / size;
+    } else {
+        if (blockIdx.x == 0)
+            raise_bad_plan(a.p);
+        const auto pieces = [&](int n) { return (n + BM - 1) / BM * tiles_n; };
+        const int total = all_pieces(a.p, pieces);
+        int piece;
+        if ((int)blockIdx.x >= total || !find_expert(mine(total), a.p, pieces, expert, piece, span))
+            return;
+        const int tiles_m = (span.n + BM - 1) / BM;
+        tn = piece / tiles_m;
+        tm = piece - tn * tiles_m;
+    }
+    const int n0 = tn * NT, m0 = tm * BM, rows = min(BM, span.n - m0);
+    const int64_t p0 = span.from + m0;               // first row of the plan (or token)
+
+    // ---- loader.  A load of 1 KiB fills eight LDS rows; lane l brings to slot
+    // l % 8 of row l / 8 the chunk that belongs there.
+    constexpr int H = MODE == kUp ? 2 : 1;
+    const int half = MODE == kUp ? wave & 1 : 0;
+    const int64_t mat = (int64_t)expert * H + half;
+    // (kUp: LDS rows 64u .. 64u+31 are gate rows 32u .., 64u+32 .. their up rows)
+    const int w_first = MODE == kUp ? n0 + 32 * (wave >> 1) : n0 + 32 * wave;
+    // (a descriptor bounds a lane's own offset, not the scalar one, which stays
+    // within a row: rows past N read as zeros)
+    const uint8_t *w_from = a.w + (mat * a.N + w_first) * a.K;
+    const __amdgpu_buffer_rsrc_t rw0 = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)w_from, 0, max(0, min(16, a.N - w_first)) * a.K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rw1 = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(w_from + 16 * (int64_t)a.K), 0, max(0, min(16, a.N - w_first - 16)) * a.K, 0x00020000);
+    const int64_t x_first = MODE == kUp ? 0 : p0;
+    const uint32_t x_rows = MODE == kUp ? a.T : rows;
+    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(a.x + x_first * a.K), 0, (int)(x_rows * (uint32_t)a.K), 0x00020000);
+    const int xs_pitch = XF32 ? 4 * KB : a.K / 32;   // the same: a dword a row and block
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)((const uint8_t *)a.xs + x_first * xs_pitch), 0, (int)(x_rows * (uint32_t)xs_pitch),
+        0x00020000);
+    const int lr = lane >> 3, ls = lane & 7;
+    // the row of x behind tile row r (past the tile's end: its last one)
+    const auto x_row = [&](int r) {
+        r = min(r, rows - 1);
+        if (MODE != kUp)
+            return (uint32_t)r;
+        const int slot = a.p.order[p0 + r];
+        return (uint32_t)slot < (uint32_t)a.p.slots ? (uint32_t)slot / (uint32_t)a.p.k : 0u;
+    };
+    uint32_t w_at[2], x_at[4];           // (of x_at, LT are used)
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+        w_at[j] = (uint32_t)(8 * j + lr) * a.K + 16 * (ls ^ swizzle(8 * j + lr));
+#pragma unroll
+    for (int j = 0; j < LT; j++) {
+        const int r = wave * (BM / 8) + 8 * j + lr;
+        x_at[j] = x_row(r) * (uint32_t)a.K + 16 * (ls ^ swizzle(r));
+    }
+    const int s_row = wave % (BM / 64) * 64;
+    const uint32_t s_at = x_row(s_row + lane) * (uint32_t)xs_pitch;
+    const auto issue = [&](int kt, Stage<TB> &s) {
+#pragma unroll
+        for (int j = 0; j < LW; j++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 ? rw0 : rw1,
+                                                     (lptr_t)&s.w[(32 * wave + 8 * j) * 8], 16,
+                                                     w_at[j & 1], 128 * kt, 0, 0);
+#pragma unroll
+        for (int j = 0; j < LT; j++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rx, (lptr_t)&s.tok[(wave * (BM / 8) + 8 * j) * 8], 16, x_at[j], 128 * kt, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lptr_t)&s.xs[s_row], 4, s_at, 4 * kt, 0, 0);
+    };
+
+    // ---- block scales: kept a block a lane, 64 at a time
+    const float *ws[H];
+#pragma unroll
+    for (int h = 0; h < H; h++)
+        ws[h] = a.ws + (((int64_t)expert * H + h) * ((a.N + 127) / 128) +
+                        min(MODE == kUp ? n0 : n0 + 64 * oq, a.N - 1) / 128) * KB;
+    float wsv[H];
+
+    f32x4 acc[WB][TB];
+#pragma unroll
+    for (int i = 0; i < WB; i++)
+#pragma unroll
+        for (int j = 0; j < TB; j++)
+            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // a fragment's two pieces of row r16: at these offsets from its first row
+    const int at0 = 128 * r16 + 16 * (q ^ swizzle(r16)), at1 = at0 ^ 64;
+    const auto fragment = [&](const char *p0_, const char *p1_, int r) {
+        const u32x4 x = *(const u32x4 *)(p0_ + 128 * r), y = *(const u32x4 *)(p1_ + 128 * r);
+        return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+    };
+    const auto compute = [&](int kt, const Stage<TB> &s) {
+        const char *t0 = (const char *)s.tok + th * (BM / 2) * 128 + at0, *t1 = t0 - at0 + at1;
+        const char *w0 = (const char *)s.w + oq * 64 * 128 + at0, *w1 = w0 - at0 + at1;
+        const char *xs0 = (const char *)s.xs + 4 * (th * (BM / 2) + r16) + (XF32 ? 0 : q);
+        float f[H];
+#pragma unroll
+        for (int h = 0; h < H; h++)
+            f[h] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+                (int)__float_as_uint(wsv[h]), kt & 63));
+        i32x8 wf[WB];
+#pragma unroll
+        for (int i = 0; i < WB; i++)
+            wf[i] = fragment(w0, w1, 16 * i);
+#pragma unroll
+        for (int j = 0; j < TB; j++) {
+            const i32x8 xf = fragment(t0, t1, 16 * j);
+            const uint32_t xs = XF32 ? *(const uint32_t *)(xs0 + 64 * j) : *(const uint8_t *)(xs0 + 64 * j);
+            float g[H];
+#pragma unroll
+            for (int h = 0; h < H; h++)
+                g[h] = XF32 ? f[h] * __uint_as_float(xs) : f[h];
+#pragma unroll
+            for (int i = 0; i < WB; i++) {
+                const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    wf[i], xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp8, kFp8, 0, kOne, 0,
+                    XF32 ? kOne : (int)xs);
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    acc[i][j][e] = __builtin_fmaf(v[e], g[MODE == kUp ? i >> 1 : 0], acc[i][j][e]);
+            }
+        }
+    };
+
+    issue(0, stage[0]);
+    for (int kt = 0; kt < KB; kt++) {
+        if ((kt & 63) == 0)
+#pragma unroll
+            for (int h = 0; h < H; h++) {
+                wsv[h] = ws[h][min(kt + lane, KB - 1)];
+                asm volatile("" : "+v"(wsv[h]));    // waited for here, not at each use
+            }
+        // this wavefront's loads of the tile are in; then everybody's are, and
+        // everybody has read the last tile, whose stage the next one takes
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (kt + 1 < KB)
+            issue(kt + 1, stage[(kt + 1) & 1]);
+        compute(kt, stage[kt & 1]);
+    }
+
+    // ---- out: accumulator e of block (i, j) is weight row 16i + 4q + e, token
+    // 16j + lane % 16 of the wavefront's
+#pragma unroll
+    for (int j = 0; j < TB; j++) {
+        const int r = th * (BM / 2) + 16 * j + r16;
+        const bool in = r < rows;
+        const int64_t p = p0 + r;
+        int slot = 0;
+        if (MODE != kDense && in)
+            slot = a.p.order[p];
+        const bool fine = in && (uint32_t)slot < (uint32_t)(MODE == kDense ? 1 : a.p.slots);
+        if (MODE != kDense && in && !fine)
+            raise(a.p.err, ENGRAM_DEVERR_ROUTE);
+        if (MODE == kUp) {
+            float v[2][4], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    v[i][e] = gated(acc[i][j][e], acc[2 + i][j][e]);
+                    amax = fmaxf(amax, finite_abs(v[i][e]));
+                }
+            const int k = e4m3_scale_exp(max_x16(amax));
+            const float inv = exp2_int(-k);
+            if (!fine)
+                continue;
+            const int n = n0 + 32 * oq;
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                *(uint32_t *)((uint8_t *)a.y + p * a.N + n + 16 * i + 4 * q) =
+                    e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+            if (q == 0)
+                a.hs[p * (a.N / 32) + n / 32] = (uint8_t)(k + 127);
+            continue;
+        }
+        if (!fine)
+            continue;
+#pragma unroll
+        for (int i = 0; i < WB; i++) {
+            const int n = n0 + 64 * oq + 16 * i + 4 * q;
+            if (n >= a.N)
+                continue;
+            const f32x4 v = acc[i][j];
+            if (MODE == kDense)
+                *(u32x2 *)((uint16_t *)a.y + p * a.N + n) =
+                    u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+            else
+                *(f32x4 *)((float *)a.y + (int64_t)slot * a.N + n) = v;
+        }
+    }
+}
+
+template <F8Mode MODE, bool XF32>
+void launch_kind(const F8Args &a, int64_t grid8, int64_t grid4, bool big, bool last, const Launch &l)
+{
+    if (big)
+        dispatch(tiles_kernel<MODE, XF32, 8>, dim3((unsigned)grid8), dim3(512), l, true, last, a);
+    else
+        dispatch(tiles_kernel<MODE, XF32, 4>, dim3((unsigned)grid4), dim3(512), l, true, last, a);
+}
+
+}  // namespace
+
+template <F8Mode MODE>
+void launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
+{
+    const int64_t NT = MODE == kUp ? BN / 2 : BN, tiles_n = (a.N + NT - 1) / NT;
+    int64_t g8, g4;
+    bool big;
+    if (MODE == kDense) {
+        const int64_t m8 = (a.T + 255) / 256, m4 = (a.T + 127) / 128;
+        g8 = m8 * tiles_n;
+        g4 = m4 * tiles_n;
+        const int cus = device_cus();
+        big = !(g8 < cus && g4 <= cus);
+    } else {
+        // tiles that any plan of the call can ask for
+        g8 = f8_most_tiles(a.p, 256) * tiles_n;
+        g4 = f8_most_tiles(a.p, 128) * tiles_n;
+        big = a.p.slots / a.p.E >= 192;
+    }
+    if (f32)
+        launch_kind<MODE, true>(a, g8, g4, big, last, l);
+    else
+        launch_kind<MODE, false>(a, g8, g4, big, last, l);
+}
+
+template void launch_f8_tiles<kDense>(const F8Args &, bool, bool, const Launch &);
+template void launch_f8_tiles<kUp>(const F8Args &, bool, bool, const Launch &);
+template void launch_f8_tiles<kDown>(const F8Args &, bool, bool, const Launch &);
+
+}  // namespace engram
