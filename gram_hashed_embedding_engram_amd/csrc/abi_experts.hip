@@ -235,8 +235,8 @@ int32_t engram_experts_down(const engram_routes *routes, const uint8_t *d_h,
         rc = check_operands(d_h, d_h_scales, d_w, d_w_scales, "experts_down");
     if (rc != ENGRAM_OK)
         return rc;
-    CHECK(d_y && aligned(d_y, 8), ENGRAM_E_ARG,
-          "engram experts_down: NULL or unaligned y (8 bytes)");
+    CHECK(d_y && aligned(d_y, 16), ENGRAM_E_ARG,
+          "engram experts_down: NULL or unaligned y (16 bytes)");
     const Plan p = plan_of(routes);
     const size_t need = experts_down_bytes(p, N);
     CHECK(ws_bytes >= need, ENGRAM_E_RANGE,

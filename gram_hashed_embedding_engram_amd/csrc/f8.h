@@ -22,10 +22,25 @@ struct F8Args {
     const void *xs;                     // E8M0 per 32 values, or f32 per 128
     const uint8_t *w;
     const float *ws;
-    void *y;                            // bf16; e4m3 codes; f32 products by slot
-    uint8_t *hs;
+    void *y;                            // bf16; e4m3 codes; f16 products by slot
+    uint8_t *hs;                        // the codes' exponents + 127; the products' exponents
     int T, K, N;                        // N: outputs, for kUp those of one half
 };
+
+// Exponent k >= -126 with amax < 2^15 * 2^k, amax >= 2^14 * 2^k above the floor.
+__device__ __forceinline__ int f16_scale_exp(float amax)
+{
+    const int k = (int)(__float_as_uint(amax) >> 23) - 127 - 14;
+    return k < -126 ? -126 : k;
+}
+
+// Two f32 -> two f16, first in the low half (to nearest even; NaN and
+// infinities stay).
+__device__ __forceinline__ uint32_t cvt_f16x2(float a, float b)
+{
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, (h2){(_Float16)a, (_Float16)b});
+}
 
 // tiles of `rows` rows that any plan of the call can ask for
 inline int64_t f8_most_tiles(const Plan &p, int64_t rows)

@@ -82,6 +82,15 @@ __global__ __launch_bounds__(64) void tile_kernel(F8Args a)
         }
         return;
     }
+    int k16 = 0;
+    if (MODE == kDown) {
+        float amax = 0.0f;
+        for (int i = 0; i < 2; i++)
+            for (int e = 0; e < 4; e++)
+                amax = fmaxf(amax, finite_abs(acc[0][i][e]));
+        k16 = f16_scale_exp(max_x16(amax));
+    }
+    const float to_f16 = exp2_int(-k16);
     for (int i = 0; i < 2; i++) {
         const int n = n0 + 16 * i + 4 * q;
         if (r16 >= rows || n >= a.N || !fine)
@@ -91,27 +100,41 @@ __global__ __launch_bounds__(64) void tile_kernel(F8Args a)
             *(u32x2 *)((uint16_t *)a.y + (int64_t)p * a.N + n) =
                 u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
         else
-            *(f32x4 *)((float *)a.y + (int64_t)slot * a.N + n) = v;
+            *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
+                u32x2{cvt_f16x2(v[0] * to_f16, v[1] * to_f16), cvt_f16x2(v[2] * to_f16, v[3] * to_f16)};
+        if (MODE == kDown && q == 0 && i == 0)
+            a.hs[(int64_t)slot * ((a.N + 31) / 32) + n0 / 32] = (uint8_t)k16;
     }
 }
 
-// y[t] = sum_j weight[t][j] * product[t * k + j], in j's order
-__global__ __launch_bounds__(256) void sum_kernel(const float *__restrict__ v,
+// y[t] = sum_j weight[t][j] * product[t * k + j], in j's order; GROUP outputs
+// of a product share an exponent
+template <int GROUP>
+__global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v,
+                                                  const int8_t *__restrict__ exps,
                                                   const int32_t *__restrict__ ids,
                                                   const float *__restrict__ weights,
                                                   uint16_t *__restrict__ y, int T, int N, int k, int E)
 {
-    const int n = 4 * (blockIdx.x * 256 + threadIdx.x);
-    if (n >= N)
-        return;
-    for (int t = blockIdx.y; t < T; t += gridDim.y) {
-        f32x4 s = {};
+    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+    const int groups = (N + GROUP - 1) / GROUP;
+    const int64_t pieces = N / 8, all = T * pieces;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
+        const int t = (int)(i / pieces), n = 8 * (int)(i - t * pieces);
+        float s[8] = {};
+#pragma unroll 4
         for (int j = 0; j < k; j++) {
             const int64_t slot = (int64_t)t * k + j;
-            if ((uint32_t)ids[slot] < (uint32_t)E)
-                s += *(const f32x4 *)(v + slot * N + n) * weights[slot];
+            if ((uint32_t)ids[slot] >= (uint32_t)E)
+                continue;
+            const h8 x = __builtin_bit_cast(h8, *(const u32x4 *)(v + slot * N + n));
+            const float f = exp2_int(exps[slot * groups + n / GROUP]) ;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                s[e] += (float)x[e] * f * weights[slot];
         }
-        *(u32x2 *)(y + (int64_t)t * N + n) = u32x2{cvt_bf16x2(s[0], s[1]), cvt_bf16x2(s[2], s[3])};
+        *(u32x4 *)(y + (int64_t)t * N + n) = u32x4{cvt_bf16x2(s[0], s[1]), cvt_bf16x2(s[2], s[3]),
+                                                   cvt_bf16x2(s[4], s[5]), cvt_bf16x2(s[6], s[7])};
     }
 }
 
@@ -149,18 +172,28 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
     return launch_status("engram experts_up kernel");
 }
 
-size_t experts_down_bytes(const Plan &p, int64_t N) { return (size_t)p.slots * N * sizeof(float); }
+size_t experts_down_bytes(const Plan &p, int64_t N)
+{
+    return (size_t)p.slots * (2 * N + (N + 31) / 32);
+}
 
 int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uint16_t *y, int64_t K,
                             int64_t N, void *ws, const Launch &l)
 {
-    const F8Args a{p, h.x, h.s, w.w, w.s, ws, nullptr, p.T, (int)K, (int)N};
-    if (p.slots / p.E >= 48)
+    uint16_t *products = (uint16_t *)ws;
+    uint8_t *exps = (uint8_t *)(products + (int64_t)p.slots * N);
+    const F8Args a{p, h.x, h.s, w.w, w.s, products, exps, p.T, (int)K, (int)N};
+    const int64_t blocks = (p.T * (N / 8) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
+    if (p.slots / p.E >= 48) {
         launch_f8_tiles<kDown>(a, h.f32, false, l);
-    else
+        dispatch(sum_kernel<64>, grid, dim3(256), l, false, true, (const uint16_t *)products,
+                 (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
+    } else {
         launch_tiles<kDown>(a, h.f32, f8_most_tiles(p, 16), false, l);
-    dispatch(sum_kernel, dim3((unsigned)((N / 4 + 255) / 256), (unsigned)(p.T < 65535 ? p.T : 65535)),
-             dim3(256), l, false, true, (const float *)ws, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
+        dispatch(sum_kernel<32>, grid, dim3(256), l, false, true, (const uint16_t *)products,
+                 (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
+    }
     return launch_status("engram experts_down kernels");
 }
 

@@ -1,6 +1,8 @@
 // Products of many 8-bit rows with 8-bit weights that carry an f32 scale per
 // 128 x 128 block: a plain projection, the experts' gated up projection, and
 // their down projection, as tiles of one matrix kernel.
+#include <type_traits>
+
 #include "f8.h"
 
 namespace engram {
@@ -16,18 +18,39 @@ typedef __attribute__((address_space(3))) void *lptr_t;
 // neighbouring rows read at one chunk meet all banks
 __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 
+// a pointer that all lanes share, in scalar registers
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
+{
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint8_t *)((uint64_t)hi << 32 | lo);
+}
+
+// scales of the rows for this many blocks of K are loaded at once: a dword a row
+// and block, loaded block by block, would ask for as many lines as the codes
+constexpr int SB = 8;
+
 template <int TB>
 struct Stage {
     u32x4 tok[32 * TB * 8];
     u32x4 w[BN * 8];
-    uint32_t xs[32 * TB];
+};
+
+// (one object: of several, the compiler would wait for all loads in flight to
+// one before each read of another)
+template <int TB>
+struct Shared {
+    Stage<TB> stage[2];
+    uint32_t xs[2][32 * TB * SB];
 };
 
 template <F8Mode MODE, bool XF32, int TB>
 __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 {
     constexpr int BM = 32 * TB, LT = BM / 64, LW = BN / 64;
-    __shared__ Stage<TB> stage[2];
+    __shared__ Shared<TB> sh;
+    Stage<TB> *const stage = sh.stage;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int th = (wave >> 2), oq = wave & 3;       // token half, output quarter
@@ -62,6 +85,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         tn = piece / tiles_m;
         tm = piece - tn * tiles_m;
     }
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
     const int n0 = tn * NT, m0 = tm * BM, rows = min(BM, span.n - m0);
     const int64_t p0 = span.from + m0;               // first row of the plan (or token)
 
@@ -74,11 +99,13 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     const int w_first = MODE == kUp ? n0 + 32 * (wave >> 1) : n0 + 32 * wave;
     // (a descriptor bounds a lane's own offset, not the scalar one, which stays
     // within a row: rows past N read as zeros)
-    const uint8_t *w_from = a.w + (mat * a.N + w_first) * a.K;
+    const uint8_t *const w_from = uniform(a.w + (mat * a.N + w_first) * a.K);
+    const int w_bytes0 = __builtin_amdgcn_readfirstlane(max(0, min(16, a.N - w_first)) * a.K);
+    const int w_bytes1 = __builtin_amdgcn_readfirstlane(max(0, min(16, a.N - w_first - 16)) * a.K);
     const __amdgpu_buffer_rsrc_t rw0 = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)w_from, 0, max(0, min(16, a.N - w_first)) * a.K, 0x00020000);
+        (void *)w_from, 0, w_bytes0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rw1 = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(w_from + 16 * (int64_t)a.K), 0, max(0, min(16, a.N - w_first - 16)) * a.K, 0x00020000);
+        (void *)uniform(w_from + 16 * (int64_t)a.K), 0, w_bytes1, 0x00020000);
     const int64_t x_first = MODE == kUp ? 0 : p0;
     const uint32_t x_rows = MODE == kUp ? a.T : rows;
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
@@ -100,24 +127,37 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 #pragma unroll
     for (int j = 0; j < 2; j++)
         w_at[j] = (uint32_t)(8 * j + lr) * a.K + 16 * (ls ^ swizzle(8 * j + lr));
+    // this wavefront's rows of the first half of the tokens, then of the second
+    const auto t_row = [&](int j) { return (j >= LT / 2) * (BM / 2) + wave * (BM / 16) + 8 * (j % (LT / 2)); };
 #pragma unroll
     for (int j = 0; j < LT; j++) {
-        const int r = wave * (BM / 8) + 8 * j + lr;
+        const int r = t_row(j) + lr;
         x_at[j] = x_row(r) * (uint32_t)a.K + 16 * (ls ^ swizzle(r));
     }
-    const int s_row = wave % (BM / 64) * 64;
-    const uint32_t s_at = x_row(s_row + lane) * (uint32_t)xs_pitch;
-    const auto issue = [&](int kt, Stage<TB> &s) {
+    uint32_t s_at[4];                    // (LT are used) rows 8j .. of this wavefront's eighth
+#pragma unroll
+    for (int j = 0; j < LT; j++)
+        s_at[j] = x_row(wave * (BM / 8) + 8 * j + lr) * (uint32_t)xs_pitch + 4 * ls;
+    const auto issue_w = [&](int kt, Stage<TB> &s) {
+        const int k = min(kt, KB - 1);
 #pragma unroll
         for (int j = 0; j < LW; j++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 ? rw0 : rw1,
                                                      (lptr_t)&s.w[(32 * wave + 8 * j) * 8], 16,
-                                                     w_at[j & 1], 128 * kt, 0, 0);
+                                                     w_at[j & 1], 128 * k, 0, 0);
+    };
+    const auto issue_s = [&](int part) {
 #pragma unroll
         for (int j = 0; j < LT; j++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rx, (lptr_t)&s.tok[(wave * (BM / 8) + 8 * j) * 8], 16, x_at[j], 128 * kt, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lptr_t)&s.xs[s_row], 4, s_at, 4 * kt, 0, 0);
+                rs, (lptr_t)&sh.xs[part & 1][(wave * (BM / 8) + 8 * j) * SB], 4,
+                s_at[j] + 4 * SB * part, 0, 0, 0);
+    };
+    const auto issue_x = [&](int kt, Stage<TB> &s) {
+        const int k = min(kt, KB - 1);
+#pragma unroll
+        for (int j = 0; j < LT; j++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lptr_t)&s.tok[t_row(j) * 8], 16, x_at[j], 128 * k, 0, 0);
     };
 
     // ---- block scales: kept a block a lane, 64 at a time
@@ -140,23 +180,24 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         const u32x4 x = *(const u32x4 *)(p0_ + 128 * r), y = *(const u32x4 *)(p1_ + 128 * r);
         return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
     };
-    const auto compute = [&](int kt, const Stage<TB> &s) {
-        const char *t0 = (const char *)s.tok + th * (BM / 2) * 128 + at0, *t1 = t0 - at0 + at1;
+    i32x8 wf[WB];
+    float f[H];
+    const auto read_w = [&](const Stage<TB> &s) {
         const char *w0 = (const char *)s.w + oq * 64 * 128 + at0, *w1 = w0 - at0 + at1;
-        const char *xs0 = (const char *)s.xs + 4 * (th * (BM / 2) + r16) + (XF32 ? 0 : q);
-        float f[H];
-#pragma unroll
-        for (int h = 0; h < H; h++)
-            f[h] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
-                (int)__float_as_uint(wsv[h]), kt & 63));
-        i32x8 wf[WB];
 #pragma unroll
         for (int i = 0; i < WB; i++)
             wf[i] = fragment(w0, w1, 16 * i);
+    };
+    // blocks J0 .. J0 + NJ - 1 of the wavefront's tokens
+    const auto some = [&](int kt, const Stage<TB> &s, auto j0, auto nj) {
+        const char *t0 = (const char *)s.tok + th * 16 * 128 + at0, *t1 = t0 - at0 + at1;
+        const char *xs0 = (const char *)&sh.xs[kt / SB & 1][(th * 16 + r16) * SB + kt % SB] + (XF32 ? 0 : q);
+        constexpr int J0 = decltype(j0)::value, NJ = decltype(nj)::value;
 #pragma unroll
-        for (int j = 0; j < TB; j++) {
-            const i32x8 xf = fragment(t0, t1, 16 * j);
-            const uint32_t xs = XF32 ? *(const uint32_t *)(xs0 + 64 * j) : *(const uint8_t *)(xs0 + 64 * j);
+        for (int j = J0; j < J0 + NJ; j++) {
+            const i32x8 xf = fragment(t0, t1, 32 * j);
+            const uint32_t xs = XF32 ? *(const uint32_t *)(xs0 + 128 * SB * j)
+                                     : *(const uint8_t *)(xs0 + 128 * SB * j);
             float g[H];
 #pragma unroll
             for (int h = 0; h < H; h++)
@@ -172,8 +213,26 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             }
         }
     };
-
-    issue(0, stage[0]);
+    // the half of the tile from block J0 on; of an expert's last rows only what
+    // there is, to 64 (or 32) rows
+    const auto half_tile = [&](int kt, const Stage<TB> &s, auto j0) {
+        constexpr int J0 = decltype(j0)::value;
+        if (MODE == kDense || rows > 32 * (J0 + TB / 4))
+            some(kt, s, j0, std::integral_constant<int, TB / 2>{});
+        else if (rows > 32 * J0)
+            some(kt, s, j0, std::integral_constant<int, TB / 4>{});
+    };
+    const auto meet = [&](auto n) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    issue_s(0);
+    issue_w(0, stage[0]);
+    issue_x(0, stage[0]);
+    issue_w(1, stage[1]);
+    meet(std::integral_constant<int, LT + LW>{});
+    read_w(stage[0]);
     for (int kt = 0; kt < KB; kt++) {
         if ((kt & 63) == 0)
 #pragma unroll
@@ -181,22 +240,28 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
                 wsv[h] = ws[h][min(kt + lane, KB - 1)];
                 asm volatile("" : "+v"(wsv[h]));    // waited for here, not at each use
             }
-        // this wavefront's loads of the tile are in; then everybody's are, and
-        // everybody has read the last tile, whose stage the next one takes
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        if (kt + 1 < KB)
-            issue(kt + 1, stage[(kt + 1) & 1]);
-        compute(kt, stage[kt & 1]);
+        Stage<TB> &s = stage[kt & 1], &o = stage[(kt + 1) & 1];
+#pragma unroll
+        for (int h = 0; h < H; h++)
+            f[h] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(wsv[h]),
+                                                                       kt & 63));
+        meet(std::integral_constant<int, LT / 2 + LW>{});
+        if (kt % SB == 0)
+            issue_s(kt / SB + 1);
+        issue_x(kt + 1, o);
+        half_tile(kt, s, std::integral_constant<int, 0>{});
+        meet(std::integral_constant<int, LT>{});
+        issue_w(kt + 2, s);
+        half_tile(kt, s, std::integral_constant<int, TB / 2>{});
+        read_w(o);
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // ---- out: accumulator e of block (i, j) is weight row 16i + 4q + e, token
     // 16j + lane % 16 of the wavefront's
 #pragma unroll
     for (int j = 0; j < TB; j++) {
-        const int r = th * (BM / 2) + 16 * j + r16;
+        const int r = 32 * j + 16 * th + r16;
         const bool in = r < rows;
         const int64_t p = p0 + r;
         int slot = 0;
@@ -227,8 +292,24 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
                 a.hs[p * (a.N / 32) + n / 32] = (uint8_t)(k + 127);
             continue;
         }
+        // products leave as f16 under a power of two per 64 of a row: half the bytes
+        // of f32 twice over memory, off by 2^-11 of themselves (or 2^-39 of the 64's
+        // largest), an eighth of what the sum's own rounding to bf16 is off by
+        int k16 = 0;
+        float to_f16 = 1.0f;
+        if (MODE == kDown) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WB; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    amax = fmaxf(amax, finite_abs(acc[i][j][e]));
+            k16 = f16_scale_exp(max_x16(amax));
+        }
         if (!fine)
             continue;
+        if (MODE == kDown)
+            to_f16 = exp2_int(-k16);
 #pragma unroll
         for (int i = 0; i < WB; i++) {
             const int n = n0 + 64 * oq + 16 * i + 4 * q;
@@ -239,8 +320,11 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
                 *(u32x2 *)((uint16_t *)a.y + p * a.N + n) =
                     u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
             else
-                *(f32x4 *)((float *)a.y + (int64_t)slot * a.N + n) = v;
+                *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
+                    u32x2{cvt_f16x2(v[0] * to_f16, v[1] * to_f16), cvt_f16x2(v[2] * to_f16, v[3] * to_f16)};
         }
+        if (MODE == kDown && q == 0 && n0 + 64 * oq < a.N)
+            a.hs[(int64_t)slot * ((a.N + 63) / 64) + n0 / 64 + oq] = (uint8_t)k16;
     }
 }
 

@@ -670,8 +670,11 @@ int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const
  *   d_y     [tokens][N] bf16;
  *   d_ws    (256-byte aligned, caller-owned) of engram_experts_down_bytes bytes;
  *           may be NULL where that is 0.  Calls that share it must not overlap.
- * K a multiple of 128 up to 2^20, N of 16 up to 2^24.  d_h and d_w 16-byte, d_y
- * 8-byte, scales 4-byte aligned. */
+ * Where experts have many rows a slot's products pass through d_ws as f16 under a
+ * power of two per 64 outputs (off by 2^-11 of themselves, an eighth of what the
+ * result's own rounding is off by); sums are f32, in the slots' order.
+ * K a multiple of 128 up to 2^20, N of 16 up to 2^24.  d_h, d_w and d_y 16-byte,
+ * scales 4-byte aligned. */
 size_t engram_experts_down_bytes(const engram_routes *routes, int64_t N);
 int32_t engram_experts_down(const engram_routes *routes, const uint8_t *d_h,
                             const void *d_h_scales, int32_t h_f32, const uint8_t *d_w,

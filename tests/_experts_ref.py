@@ -122,6 +122,8 @@ def down(h, w, s, offsets, order, weights):
             slot = torch.as_tensor(order[p:q], device=h.device)
             v, d = product(h[p:q], matrix(w[e], s[e]))
             y.index_add_(0, slot // k, v * flat[slot][:, None])
-            # the weight's product and the sum over k slots, each rounded in f32
-            tol.index_add_(0, slot // k, (d + (k + 1) * 2.0 ** -24 * v.abs()) * flat[slot].abs()[:, None])
+            # a product as f16 under a shared power of two (2^-11 of itself, or 2^-39 of
+            # its row's largest), times its weight and added to k, each rounded in f32
+            f16 = 2.0 ** -11 * v.abs() + 2.0 ** -39 * v.abs().amax(1, keepdim=True)
+            tol.index_add_(0, slot // k, ((1 + 2.0 ** -11) * d + f16 + (k + 1) * 2.0 ** -24 * v.abs()) * flat[slot].abs()[:, None])
     return y, tol

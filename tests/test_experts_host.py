@@ -127,7 +127,7 @@ def test_up_refusals(L, change, code):
     (dict(K=192), E.E_UNSUPPORTED), (dict(K=-128), E.E_UNSUPPORTED), (dict(N=24), E.E_UNSUPPORTED),
     (dict(N=0), E.E_UNSUPPORTED), (dict(h=None), E.E_ARG), (dict(hs=None), E.E_ARG), (dict(w=None), E.E_ARG),
     (dict(ws=None), E.E_ARG), (dict(y=None), E.E_ARG), (dict(h=FAKE + 8), E.E_ARG), (dict(w=FAKE + 8), E.E_ARG),
-    (dict(hs=SC + 2), E.E_ARG), (dict(ws=WS + 2), E.E_ARG), (dict(y=OUT + 4), E.E_ARG)])
+    (dict(hs=SC + 2), E.E_ARG), (dict(ws=WS + 2), E.E_ARG), (dict(y=OUT + 8), E.E_ARG)])
 def test_down_refusals(L, change, code):
     assert down(L, **change) == code and E.last_error()
 
@@ -141,7 +141,7 @@ def test_outputs_over_inputs_are_refused(L):
     for shift in (-256, 0, 8, 512):
         assert f8(L, y=FAKE + shift) == E.E_ARG and "overlap" in E.last_error()
         assert f8(L, y=SC + 8 * (shift > 0)) == E.E_ARG and "overlap" in E.last_error()
-        assert down(L, y=FAKE + shift) == E.E_ARG and "overlap" in E.last_error()
+        assert down(L, y=FAKE + 2 * shift) == E.E_ARG and "overlap" in E.last_error()
     for name in ("h", "hs"):
         assert up(L, **{name: FAKE + 16}) == E.E_ARG and "overlap" in E.last_error()
         assert up(L, **{name: SC + 16}) == E.E_ARG and "overlap" in E.last_error()
