@@ -5,105 +5,242 @@
 namespace engram {
 namespace {
 
-// lane l's operand of a 16 x 128 tile: row l % 16, bytes 16(l / 16) and 64 on
-__device__ __forceinline__ i32x8 operand(const uint8_t *p)
+constexpr int64_t kFewUnits = 1024, kManyUnits = 4096;
+constexpr int64_t kMostRows = 128;
+
+__device__ __forceinline__ i32x8 operand(const u32x4 &a, const u32x4 &b)
 {
-    const u32x4 a = *(const u32x4 *)p, b = *(const u32x4 *)(p + 64);
     return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
-// A wavefront a tile of 16 rows and 32 outputs.
-template <F8Mode MODE, bool XF32>
-__global__ __launch_bounds__(64) void tile_kernel(F8Args a)
+// Row p's 32 outputs from n0 on, of which this lane has 16i + 4q .. + 3, of an
+// expert's products (kUp: v[0..1] of the gate, v[2..3] of the up matrix).
+template <F8Mode MODE>
+__device__ __forceinline__ void give(const F8Args &a, const f32x4 (&v)[4], int64_t p, bool in, int n0,
+                                     int q)
 {
-    const int lane = threadIdx.x, r16 = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * 32, KB = a.K / 128, NB = (a.N + 127) / 128;
-    int expert = 0, tile = blockIdx.y;
-    Span span{0, a.T};
-    if (MODE != kDense) {
-        if (blockIdx.x == 0 && blockIdx.y == 0)
-            raise_bad_plan(a.p);
-        if (!find_expert(blockIdx.y, a.p, [](int n) { return (n + 15) / 16; }, expert, tile, span))
-            return;
-    }
-    const int rows = min(16, span.n - 16 * tile);
-    const int first = span.from + 16 * tile, p = first + min(r16, rows - 1);
-    int slot = p;
-    bool fine = true;
-    if (MODE != kDense) {
+    int slot = 0;
+    if (in) {
         slot = a.p.order[p];
-        fine = slot >= 0 && slot < a.p.slots;
-        if (!fine) {
+        if ((uint32_t)slot >= (uint32_t)a.p.slots) {
             raise(a.p.err, ENGRAM_DEVERR_ROUTE);
-            slot = 0;
+            in = false;
         }
     }
-    const int64_t row = MODE == kUp ? slot / a.p.k : p;
-    const uint8_t *x = a.x + row * a.K + 16 * q;
-    const uint8_t *xs8 = (const uint8_t *)a.xs + row * (a.K / 32) + q;
-    const float *xs32 = (const float *)a.xs + row * KB;
-    constexpr int H = MODE == kUp ? 2 : 1;
-    const uint8_t *w[H][2];
-    const float *ws[H];
-    for (int h = 0; h < H; h++) {
-        const int64_t m = (int64_t)expert * H + h;
-        for (int i = 0; i < 2; i++)
-            w[h][i] = a.w + (m * a.N + min(n0 + 16 * i + r16, a.N - 1)) * a.K + 16 * q;
-        ws[h] = a.ws + (m * NB + n0 / 128) * KB;
-    }
-    f32x4 acc[H][2] = {};
-    for (int kb = 0; kb < KB; kb++) {
-        const i32x8 xf = operand(x + 128 * kb);
-        const int sx = XF32 ? kOne : xs8[4 * kb];
-        const float f = XF32 ? xs32[kb] : 1.0f;
-        for (int h = 0; h < H; h++)
-            for (int i = 0; i < 2; i++) {
-                const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    operand(w[h][i] + 128 * kb), xf, f32x4{}, kFp8, kFp8, 0, kOne, 0, sx);
-                for (int e = 0; e < 4; e++)
-                    acc[h][i][e] += v[e] * (ws[h][kb] * f);
-            }
-    }
     if (MODE == kUp) {
-        float v[2][4], amax = 0.0f;
+        float h[2][4], amax = 0.0f;
+#pragma unroll
         for (int i = 0; i < 2; i++)
+#pragma unroll
             for (int e = 0; e < 4; e++) {
-                v[i][e] = gated(acc[0][i][e], acc[H - 1][i][e]);
-                amax = fmaxf(amax, finite_abs(v[i][e]));
+                h[i][e] = gated(v[i][e], v[2 + i][e]);
+                amax = fmaxf(amax, finite_abs(h[i][e]));
             }
         const int k = e4m3_scale_exp(max_x16(amax));
         const float inv = exp2_int(-k);
-        if (r16 < rows && fine) {
-            for (int i = 0; i < 2; i++)
-                *(uint32_t *)((uint8_t *)a.y + (int64_t)p * a.N + n0 + 16 * i + 4 * q) =
-                    e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-            if (q == 0)
-                a.hs[(int64_t)p * (a.N / 32) + n0 / 32] = (uint8_t)(k + 127);
-        }
+        if (!in)
+            return;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            *(uint32_t *)((uint8_t *)a.y + p * a.N + n0 + 16 * i + 4 * q) =
+                e4m3x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
+        if (q == 0)
+            a.hs[p * (a.N / 32) + n0 / 32] = (uint8_t)(k + 127);
         return;
     }
-    int k16 = 0;
-    if (MODE == kDown) {
-        float amax = 0.0f;
-        for (int i = 0; i < 2; i++)
-            for (int e = 0; e < 4; e++)
-                amax = fmaxf(amax, finite_abs(acc[0][i][e]));
-        k16 = f16_scale_exp(max_x16(amax));
-    }
-    const float to_f16 = exp2_int(-k16);
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            amax = fmaxf(amax, finite_abs(v[i][e]));
+    const int k = f16_scale_exp(max_x16(amax));
+    const float inv = exp2_int(-k);
+#pragma unroll
     for (int i = 0; i < 2; i++) {
         const int n = n0 + 16 * i + 4 * q;
-        if (r16 >= rows || n >= a.N || !fine)
+        if (!in || n >= a.N)
             continue;
-        const f32x4 v = acc[0][i];
-        if (MODE == kDense)
-            *(u32x2 *)((uint16_t *)a.y + (int64_t)p * a.N + n) =
-                u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
-        else
-            *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
-                u32x2{cvt_f16x2(v[0] * to_f16, v[1] * to_f16), cvt_f16x2(v[2] * to_f16, v[3] * to_f16)};
-        if (MODE == kDown && q == 0 && i == 0)
-            a.hs[(int64_t)slot * ((a.N + 31) / 32) + n0 / 32] = (uint8_t)k16;
+        *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
+            u32x2{cvt_f16x2(v[i][0] * inv, v[i][1] * inv), cvt_f16x2(v[i][2] * inv, v[i][3] * inv)};
+        if (q == 0 && i == 0)
+            a.hs[(int64_t)slot * ((a.N + 31) / 32) + n0 / 32] = (uint8_t)k;
+    }
+}
+
+// U: steps of 128 values whose loads go out together, within the registers
+// that two wavefronts a SIMD leave each
+constexpr int steps_ahead(int rt, int mt)
+{
+    const int u = (190 - 4 * rt * mt) / (8 * rt + 9 * mt);
+    return u >= 4 ? 4 : u >= 2 ? 2 : 1;
+}
+
+// A workgroup takes 16 * OT outputs (kUp: of each half) of 16 * MT rows; its W
+// wavefronts split K and their sums meet in LDS.
+template <F8Mode MODE, bool XF32, int OT, int MT, int W>
+__global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
+{
+    constexpr int H = MODE == kUp ? 2 : 1, RT = OT * H, U = steps_ahead(RT, MT);
+    __shared__ f32x4 red[W > 1 ? W / 2 : 1][W > 1 ? MT : 1][W > 1 ? RT : 1][64];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16 * OT, KB = a.K / 128, NB = (a.N + 127) / 128;
+    for (int item = blockIdx.y;; item += gridDim.y) {
+        int expert = 0, tile = item;
+        Span span{0, a.T};
+        if (MODE != kDense) {
+            if (blockIdx.x == 0 && item == 0)
+                raise_bad_plan(a.p);
+            if (!find_expert(item, a.p, [](int n) { return (n + 16 * MT - 1) / (16 * MT); }, expert,
+                             tile, span))
+                return;
+        } else if (16 * MT * item >= a.T) {
+            return;
+        }
+        const int rows = min(16 * MT, span.n - 16 * MT * tile);
+        const int64_t first = span.from + 16 * MT * tile;
+        // the row of x behind row 16j + l % 16 (past the last: the last one)
+        const uint8_t *x[MT];
+        const uint8_t *xs[MT];
+#pragma unroll
+        for (int j = 0; j < MT; j++) {
+            int64_t row = first + min(16 * j + r16, rows - 1);
+            if (MODE == kUp) {
+                const int slot = a.p.order[row];
+                row = (uint32_t)slot < (uint32_t)a.p.slots ? slot / a.p.k : 0;
+            }
+            x[j] = a.x + row * a.K + 16 * q;
+            xs[j] = (const uint8_t *)a.xs + row * (a.K / 32) + (XF32 ? 0 : q);
+        }
+        // the weights through a descriptor of the workgroup's own rows: what lies
+        // past them, or past the wavefront's steps, comes back as zeros
+        const int64_t m0 = (int64_t)expert * H * a.N + n0;
+        const int bytes = min(16 * OT, a.N - n0) * a.K;
+        const __amdgpu_buffer_rsrc_t w0 =
+            __builtin_amdgcn_make_buffer_rsrc((void *)(a.w + m0 * a.K), 0, bytes, 0x00020000);
+        const __amdgpu_buffer_rsrc_t w1 = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(a.w + (m0 + (H - 1) * (int64_t)a.N) * a.K), 0, bytes, 0x00020000);
+        constexpr uint32_t kPast = 0xFFFFFF00u;
+        const uint32_t at = r16 * (uint32_t)a.K + 16 * q;
+        const int begin = KB * wv / W, end = KB * (wv + 1) / W;
+        f32x4 acc[RT][MT];
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int j = 0; j < MT; j++)
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // the scales of row block i (16 * OT rows may meet two blocks of 128)
+        const float *ws[RT];
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+            ws[i] = a.ws + (((int64_t)expert * H + i / OT) * NB +
+                            min(n0 + 16 * (i % OT), a.N - 1) / 128) * KB;
+        for (int k0 = begin; k0 < end; k0 += U) {
+            u32x4 wr[U][RT][2], xr[U][MT][2];
+            uint32_t xsc[U][MT];
+#pragma unroll
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+#pragma unroll
+                    for (int z = 0; z < 2; z++) {
+                        const uint32_t off = k0 + u < end
+                            ? at + 16 * (i % OT) * a.K + 128 * (k0 + u) + 64 * z : kPast;
+                        wr[u][i][z] = i < OT ? __builtin_amdgcn_raw_buffer_load_b128(w0, off, 0, 0)
+                                            : __builtin_amdgcn_raw_buffer_load_b128(w1, off, 0, 0);
+                    }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int k = min(k0 + u, end - 1);
+#pragma unroll
+                for (int j = 0; j < MT; j++) {
+                    xr[u][j][0] = *(const u32x4 *)(x[j] + 128 * k);
+                    xr[u][j][1] = *(const u32x4 *)(x[j] + 128 * k + 64);
+                    xsc[u][j] = XF32 ? *(const uint32_t *)(xs[j] + 4 * k) : xs[j][4 * k];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                // (not multiplied past the end, where a NaN would meet zeros)
+                if (k0 + u >= end)
+                    break;
+                float f[RT];
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+                    f[i] = ws[i][k0 + u];
+#pragma unroll
+                for (int j = 0; j < MT; j++) {
+                    const i32x8 xf = operand(xr[u][j][0], xr[u][j][1]);
+                    const float t = XF32 ? __uint_as_float(xsc[u][j]) : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < RT; i++) {
+                        const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            operand(wr[u][i][0], wr[u][i][1]), xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f},
+                            kFp8, kFp8, 0, kOne, 0, XF32 ? kOne : (int)xsc[u][j]);
+                        const float g = XF32 ? f[i] * t : f[i];
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            acc[i][j][e] = __builtin_fmaf(v[e], g, acc[i][j][e]);
+                    }
+                }
+            }
+        }
+        // the wavefronts' sums: the upper half's to the lower's, which leave theirs
+        if (W > 1) {
+            if (wv >= W / 2)
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+#pragma unroll
+                    for (int j = 0; j < MT; j++)
+                        red[wv - W / 2][j][i][lane] = acc[i][j];
+            __syncthreads();
+            if (wv < W / 2)
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+#pragma unroll
+                    for (int j = 0; j < MT; j++) {
+                        acc[i][j] += red[wv][j][i][lane];
+                        red[wv][j][i][lane] = acc[i][j];
+                    }
+            __syncthreads();
+        }
+        const auto sum = [&](int i, int j) {
+            f32x4 v = acc[i][j];
+            if (W > 1) {
+                v = red[0][j][i][lane];
+#pragma unroll
+                for (int z = 1; z < W / 2; z++)
+                    v += red[z][j][i][lane];
+            }
+            return v;
+        };
+        // accumulator e of block (i, j) is output 16i + 4q + e, row 16j + l % 16; a
+        // wavefront finishes every W-th block (of rows, for the experts)
+#pragma unroll
+        for (int j = 0; j < MT; j++) {
+            const int r = 16 * j + r16;
+            if constexpr (MODE == kDense) {
+#pragma unroll
+                for (int i = 0; i < OT; i++) {
+                    const int n = n0 + 16 * i + 4 * q;
+                    if (W > 1 && (j * OT + i) % W != wv)
+                        continue;
+                    const f32x4 v = sum(i, j);
+                    if (r < rows && n < a.N)
+                        *(u32x2 *)((uint16_t *)a.y + (first + r) * a.N + n) =
+                            u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+                }
+            } else {
+                static_assert(OT == 2, "an expert's outputs leave 32 at a time");
+                if (W > 1 && j % W != wv)
+                    continue;
+                const f32x4 v[4] = {sum(0, j), sum(1, j), sum(RT - 2, j), sum(RT - 1, j)};
+                give<MODE>(a, v, first + r, r < rows, n0, q);
+            }
+        }
+        if (W > 1)
+            __syncthreads();                        // the next item's sums take their place
     }
 }
 
@@ -138,14 +275,53 @@ __global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v
     }
 }
 
-template <F8Mode MODE>
-void launch_tiles(const F8Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
+template <F8Mode MODE, int OT, int MT, int W>
+void launch_split(const F8Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
 {
-    const dim3 grid((unsigned)((a.N + 31) / 32), (unsigned)tiles);
+    const dim3 grid((unsigned)((a.N + 16 * OT - 1) / (16 * OT)), (unsigned)(tiles < 65535 ? tiles : 65535));
     if (f32)
-        dispatch(tile_kernel<MODE, true>, grid, dim3(64), l, true, last, a);
+        dispatch(rows_kernel<MODE, true, OT, MT, W>, grid, dim3(64 * W), l, true, last, a);
     else
-        dispatch(tile_kernel<MODE, false>, grid, dim3(64), l, true, last, a);
+        dispatch(rows_kernel<MODE, false, OT, MT, W>, grid, dim3(64 * W), l, true, last, a);
+}
+
+// K is split over the wavefronts of a workgroup where one a tile would leave the
+// memory waiting.
+template <F8Mode MODE, int MT>
+void launch_experts(const F8Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
+{
+    const int64_t units = tiles * ((a.N + 31) / 32);
+    if (units < kFewUnits && a.K >= 1024)
+        launch_split<MODE, 2, MT, 8>(a, f32, tiles, last, l);
+    else if (units < kManyUnits && a.K >= 512)
+        launch_split<MODE, 2, MT, 4>(a, f32, tiles, last, l);
+    else
+        launch_split<MODE, 2, MT, 1>(a, f32, tiles, last, l);
+}
+
+template <F8Mode MODE>
+void launch_rows(const F8Args &a, bool f32, bool last, const Launch &l)
+{
+    const int64_t rows = 2 * ((int64_t)a.p.slots + a.p.E - 1) / a.p.E;
+    rows <= 16   ? launch_experts<MODE, 1>(a, f32, f8_most_tiles(a.p, 16), last, l)
+    : rows <= 32 ? launch_experts<MODE, 2>(a, f32, f8_most_tiles(a.p, 32), last, l)
+                 : launch_experts<MODE, 4>(a, f32, f8_most_tiles(a.p, 64), last, l);
+}
+
+// Outputs a workgroup: at most 80 (whose sums and loads fill the registers), as
+// many as give every CU the same number of workgroups.  Every workgroup reads all
+// its rows' values, so fewer, wider ones are better.
+template <int MT>
+void launch_dense(const F8Args &a, bool f32, const Launch &l)
+{
+    const int64_t tiles = (a.T + 16 * MT - 1) / (16 * MT), cus = device_cus();
+    const int64_t n = a.N / 16 * tiles, rounds = (n + 5 * cus - 1) / (5 * cus);
+    const int64_t ot = (n + rounds * cus - 1) / (rounds * cus);
+    ot <= 1   ? launch_split<kDense, 1, MT, 8>(a, f32, tiles, true, l)
+    : ot == 2 ? launch_split<kDense, 2, MT, 8>(a, f32, tiles, true, l)
+    : ot == 3 ? launch_split<kDense, 3, MT, 8>(a, f32, tiles, true, l)
+    : ot == 4 ? launch_split<kDense, 4, MT, 8>(a, f32, tiles, true, l)
+              : launch_split<kDense, 5, MT, 8>(a, f32, tiles, true, l);
 }
 
 }  // namespace
@@ -154,10 +330,13 @@ int32_t launch_project_f8(const Rows8 &x, const Blocks8 &w, uint16_t *y, int64_t
                           int64_t N, const Launch &l)
 {
     const F8Args a{Plan{}, x.x, x.s, w.w, w.s, y, nullptr, (int)T, (int)K, (int)N};
-    if (T > 128)
+    if (T > kMostRows)
         launch_f8_tiles<kDense>(a, x.f32, true, l);
     else
-        launch_tiles<kDense>(a, x.f32, (T + 15) / 16, true, l);
+        T <= 16   ? launch_dense<1>(a, x.f32, l)
+        : T <= 32 ? launch_dense<2>(a, x.f32, l)
+        : T <= 48 ? launch_dense<3>(a, x.f32, l)
+                  : launch_dense<4>(a, x.f32, l);
     return launch_status("engram project_f8 kernel");
 }
 
@@ -168,7 +347,7 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
     if (p.slots / p.E >= 48)
         launch_f8_tiles<kUp>(a, x.f32, true, l);
     else
-        launch_tiles<kUp>(a, x.f32, f8_most_tiles(p, 16), true, l);
+        launch_rows<kUp>(a, x.f32, true, l);
     return launch_status("engram experts_up kernel");
 }
 
@@ -190,7 +369,7 @@ int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uin
         dispatch(sum_kernel<64>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     } else {
-        launch_tiles<kDown>(a, h.f32, f8_most_tiles(p, 16), false, l);
+        launch_rows<kDown>(a, h.f32, false, l);
         dispatch(sum_kernel<32>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     }
