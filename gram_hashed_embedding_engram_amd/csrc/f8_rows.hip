@@ -5,8 +5,15 @@
 namespace engram {
 namespace {
 
-constexpr int64_t kFewUnits = 1024, kManyUnits = 4096;
-constexpr int64_t kMostRows = 128;
+// Rows from which the tiles take over (f8_tiles.hip).  Both ways in us: T = 24,
+// 4096 x 4096 10 and 14; 32, 4096 x 20480 19 and 19; 48 23 and 19; 64 of 6144 x
+// 20480 45 and 36.
+constexpr int64_t kMostRows = 32;
+// The same for an expert's rows on average.  Up, 64 experts of 4096 x 2048: 4 rows
+// 186 to 195 and 162 to 165, 16 rows 279 and 181; 16 experts, 2 rows 38 and 49.  Down,
+// 2048 x 4096: 4 rows 89 and 91, 16 rows 172 and 109.
+constexpr int64_t kUpRows = 4, kDownRows = 8;
+constexpr int64_t kFewUnits = 256, kManyUnits = 4096;
 
 __device__ __forceinline__ i32x8 operand(const u32x4 &a, const u32x4 &b)
 {
@@ -287,25 +294,17 @@ void launch_split(const F8Args &a, bool f32, int64_t tiles, bool last, const Lau
 
 // K is split over the wavefronts of a workgroup where one a tile would leave the
 // memory waiting.
-template <F8Mode MODE, int MT>
-void launch_experts(const F8Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
+template <F8Mode MODE>
+void launch_experts(const F8Args &a, bool f32, bool last, const Launch &l)
 {
+    const int64_t tiles = f8_most_tiles(a.p, 16);
     const int64_t units = tiles * ((a.N + 31) / 32);
     if (units < kFewUnits && a.K >= 1024)
-        launch_split<MODE, 2, MT, 8>(a, f32, tiles, last, l);
+        launch_split<MODE, 2, 1, 8>(a, f32, tiles, last, l);
     else if (units < kManyUnits && a.K >= 512)
-        launch_split<MODE, 2, MT, 4>(a, f32, tiles, last, l);
+        launch_split<MODE, 2, 1, 4>(a, f32, tiles, last, l);
     else
-        launch_split<MODE, 2, MT, 1>(a, f32, tiles, last, l);
-}
-
-template <F8Mode MODE>
-void launch_rows(const F8Args &a, bool f32, bool last, const Launch &l)
-{
-    const int64_t rows = 2 * ((int64_t)a.p.slots + a.p.E - 1) / a.p.E;
-    rows <= 16   ? launch_experts<MODE, 1>(a, f32, f8_most_tiles(a.p, 16), last, l)
-    : rows <= 32 ? launch_experts<MODE, 2>(a, f32, f8_most_tiles(a.p, 32), last, l)
-                 : launch_experts<MODE, 4>(a, f32, f8_most_tiles(a.p, 64), last, l);
+        launch_split<MODE, 2, 1, 1>(a, f32, tiles, last, l);
 }
 
 // Outputs a workgroup: at most 80 (whose sums and loads fill the registers), as
@@ -333,10 +332,7 @@ int32_t launch_project_f8(const Rows8 &x, const Blocks8 &w, uint16_t *y, int64_t
     if (T > kMostRows)
         launch_f8_tiles<kDense>(a, x.f32, true, l);
     else
-        T <= 16   ? launch_dense<1>(a, x.f32, l)
-        : T <= 32 ? launch_dense<2>(a, x.f32, l)
-        : T <= 48 ? launch_dense<3>(a, x.f32, l)
-                  : launch_dense<4>(a, x.f32, l);
+        T <= 16 ? launch_dense<1>(a, x.f32, l) : launch_dense<2>(a, x.f32, l);
     return launch_status("engram project_f8 kernel");
 }
 
@@ -344,10 +340,10 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
                           int64_t K, int64_t I, const Launch &l)
 {
     const F8Args a{p, x.x, x.s, w.w, w.s, h, hs, p.T, (int)K, (int)I};
-    if (p.slots / p.E >= 48)
+    if (p.slots / p.E >= kUpRows)
         launch_f8_tiles<kUp>(a, x.f32, true, l);
     else
-        launch_rows<kUp>(a, x.f32, true, l);
+        launch_experts<kUp>(a, x.f32, true, l);
     return launch_status("engram experts_up kernel");
 }
 
@@ -364,12 +360,12 @@ int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uin
     const F8Args a{p, h.x, h.s, w.w, w.s, products, exps, p.T, (int)K, (int)N};
     const int64_t blocks = (p.T * (N / 8) + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-    if (p.slots / p.E >= 48) {
+    if (p.slots / p.E >= kDownRows) {
         launch_f8_tiles<kDown>(a, h.f32, false, l);
         dispatch(sum_kernel<64>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     } else {
-        launch_rows<kDown>(a, h.f32, false, l);
+        launch_experts<kDown>(a, h.f32, false, l);
         dispatch(sum_kernel<32>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     }

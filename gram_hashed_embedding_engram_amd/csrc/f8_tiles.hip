@@ -8,9 +8,9 @@
 namespace engram {
 namespace {
 
-constexpr int BN = 256;            // weight rows a tile (kUp: 128 of the gate, 128 of the up matrix)
 constexpr int XCDS = 8;
-constexpr int WB = 4;              // 16-row weight blocks a wavefront
+constexpr int64_t kRows8 = 192, kRows4 = 64;
+constexpr int64_t kCost[5] = {190, 110, 65, 42, 30};
 
 typedef __attribute__((address_space(3))) void *lptr_t;
 
@@ -31,26 +31,30 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
 // and block, loaded block by block, would ask for as many lines as the codes
 constexpr int SB = 8;
 
-template <int TB>
+template <int TB, int WB>
 struct Stage {
     u32x4 tok[32 * TB * 8];
-    u32x4 w[BN * 8];
+    u32x4 w[64 * WB * 8];
 };
 
 // (one object: of several, the compiler would wait for all loads in flight to
 // one before each read of another)
-template <int TB>
+template <int TB, int WB, int S>
 struct Shared {
-    Stage<TB> stage[2];
+    Stage<TB, WB> stage[S];
     uint32_t xs[2][32 * TB * SB];
 };
 
-template <F8Mode MODE, bool XF32, int TB>
+// A tile of 32 * TB rows and 64 * WB weight rows (kUp: half of them the gate's,
+// half the up matrix's), S stages of K.  Eight wavefronts: two halves of the rows
+// by four quarters of the outputs.
+template <F8Mode MODE, bool XF32, int TB, int WB, int S>
 __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 {
-    constexpr int BM = 32 * TB, LT = BM / 64, LW = BN / 64;
-    __shared__ Shared<TB> sh;
-    Stage<TB> *const stage = sh.stage;
+    constexpr int BM = 32 * TB, BN = 64 * WB, LT = BM / 64, LW = BN / 64;
+    typedef Stage<TB, WB> Stage;
+    __shared__ Shared<TB, WB, S> sh;
+    Stage *const stage = sh.stage;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int th = (wave >> 2), oq = wave & 3;       // token half, output quarter
@@ -96,7 +100,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     const int half = MODE == kUp ? wave & 1 : 0;
     const int64_t mat = (int64_t)expert * H + half;
     // (kUp: LDS rows 64u .. 64u+31 are gate rows 32u .., 64u+32 .. their up rows)
-    const int w_first = MODE == kUp ? n0 + 32 * (wave >> 1) : n0 + 32 * wave;
+    static_assert(MODE != kUp || WB == 4, "32 values of h share a scale");
+    const int w_first = n0 + 8 * WB * (MODE == kUp ? wave >> 1 : wave);
     // (a descriptor bounds a lane's own offset, not the scalar one, which stays
     // within a row: rows past N read as zeros)
     const uint8_t *const w_from = uniform(a.w + (mat * a.N + w_first) * a.K);
@@ -128,7 +133,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     for (int j = 0; j < 2; j++)
         w_at[j] = (uint32_t)(8 * j + lr) * a.K + 16 * (ls ^ swizzle(8 * j + lr));
     // this wavefront's rows of the first half of the tokens, then of the second
-    const auto t_row = [&](int j) { return (j >= LT / 2) * (BM / 2) + wave * (BM / 16) + 8 * (j % (LT / 2)); };
+    constexpr int LH = LT > 1 ? LT / 2 : 1;
+    const auto t_row = [&](int j) { return j / LH * (BM / 2) + wave * (8 * LH) + 8 * (j % LH); };
 #pragma unroll
     for (int j = 0; j < LT; j++) {
         const int r = t_row(j) + lr;
@@ -138,12 +144,12 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 #pragma unroll
     for (int j = 0; j < LT; j++)
         s_at[j] = x_row(wave * (BM / 8) + 8 * j + lr) * (uint32_t)xs_pitch + 4 * ls;
-    const auto issue_w = [&](int kt, Stage<TB> &s) {
+    const auto issue_w = [&](int kt, Stage &s) {
         const int k = min(kt, KB - 1);
 #pragma unroll
         for (int j = 0; j < LW; j++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 ? rw0 : rw1,
-                                                     (lptr_t)&s.w[(32 * wave + 8 * j) * 8], 16,
+                                                     (lptr_t)&s.w[(8 * WB * wave + 8 * j) * 8], 16,
                                                      w_at[j & 1], 128 * k, 0, 0);
     };
     const auto issue_s = [&](int part) {
@@ -153,7 +159,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
                 rs, (lptr_t)&sh.xs[part & 1][(wave * (BM / 8) + 8 * j) * SB], 4,
                 s_at[j] + 4 * SB * part, 0, 0, 0);
     };
-    const auto issue_x = [&](int kt, Stage<TB> &s) {
+    const auto issue_x = [&](int kt, Stage &s) {
         const int k = min(kt, KB - 1);
 #pragma unroll
         for (int j = 0; j < LT; j++)
@@ -165,7 +171,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 #pragma unroll
     for (int h = 0; h < H; h++)
         ws[h] = a.ws + (((int64_t)expert * H + h) * ((a.N + 127) / 128) +
-                        min(MODE == kUp ? n0 : n0 + 64 * oq, a.N - 1) / 128) * KB;
+                        min(MODE == kUp ? n0 : n0 + 16 * WB * oq, a.N - 1) / 128) * KB;
     float wsv[H];
 
     f32x4 acc[WB][TB];
@@ -182,14 +188,14 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     };
     i32x8 wf[WB];
     float f[H];
-    const auto read_w = [&](const Stage<TB> &s) {
-        const char *w0 = (const char *)s.w + oq * 64 * 128 + at0, *w1 = w0 - at0 + at1;
+    const auto read_w = [&](const Stage &s) {
+        const char *w0 = (const char *)s.w + oq * 16 * WB * 128 + at0, *w1 = w0 - at0 + at1;
 #pragma unroll
         for (int i = 0; i < WB; i++)
             wf[i] = fragment(w0, w1, 16 * i);
     };
     // blocks J0 .. J0 + NJ - 1 of the wavefront's tokens
-    const auto some = [&](int kt, const Stage<TB> &s, auto j0, auto nj) {
+    const auto some = [&](int kt, const Stage &s, auto j0, auto nj) {
         const char *t0 = (const char *)s.tok + th * 16 * 128 + at0, *t1 = t0 - at0 + at1;
         const char *xs0 = (const char *)&sh.xs[kt / SB & 1][(th * 16 + r16) * SB + kt % SB] + (XF32 ? 0 : q);
         constexpr int J0 = decltype(j0)::value, NJ = decltype(nj)::value;
@@ -213,47 +219,78 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             }
         }
     };
-    // the half of the tile from block J0 on; of an expert's last rows only what
-    // there is, to 64 (or 32) rows
-    const auto half_tile = [&](int kt, const Stage<TB> &s, auto j0) {
-        constexpr int J0 = decltype(j0)::value;
-        if (MODE == kDense || rows > 32 * (J0 + TB / 4))
-            some(kt, s, j0, std::integral_constant<int, TB / 2>{});
+    // the rows from block J0 to J0 + NJ; of an expert's last rows only what there
+    // is, to half of them
+    const auto part = [&](int kt, const Stage &s, auto j0, auto nj) {
+        constexpr int J0 = decltype(j0)::value, NJ = decltype(nj)::value;
+        if (MODE == kDense || rows > 32 * (J0 + NJ / 2))
+            some(kt, s, j0, nj);
         else if (rows > 32 * J0)
-            some(kt, s, j0, std::integral_constant<int, TB / 4>{});
+            some(kt, s, j0, std::integral_constant<int, NJ / 2>{});
     };
+    // this wavefront's loads but the last n, then everybody's
     const auto meet = [&](auto n) {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    issue_s(0);
-    issue_w(0, stage[0]);
-    issue_x(0, stage[0]);
-    issue_w(1, stage[1]);
-    meet(std::integral_constant<int, LT + LW>{});
-    read_w(stage[0]);
-    for (int kt = 0; kt < KB; kt++) {
+    const auto block_scales = [&](int kt) {
         if ((kt & 63) == 0)
 #pragma unroll
             for (int h = 0; h < H; h++) {
                 wsv[h] = ws[h][min(kt + lane, KB - 1)];
                 asm volatile("" : "+v"(wsv[h]));    // waited for here, not at each use
             }
-        Stage<TB> &s = stage[kt & 1], &o = stage[(kt + 1) & 1];
 #pragma unroll
         for (int h = 0; h < H; h++)
             f[h] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(wsv[h]),
                                                                        kt & 63));
-        meet(std::integral_constant<int, LT / 2 + LW>{});
-        if (kt % SB == 0)
-            issue_s(kt / SB + 1);
-        issue_x(kt + 1, o);
-        half_tile(kt, s, std::integral_constant<int, 0>{});
-        meet(std::integral_constant<int, LT>{});
-        issue_w(kt + 2, s);
-        half_tile(kt, s, std::integral_constant<int, TB / 2>{});
-        read_w(o);
+    };
+    typedef std::integral_constant<int, 0> zero;
+    issue_s(0);
+    if constexpr (S == 2) {
+        // Two stages, and a barrier in the middle of a tile.  The rows of tile kt+1
+        // are loaded from the start of tile kt on, its weights from the middle of
+        // tile kt-1, whose own went to registers before: the first half of the rows
+        // has a whole tile's time to arrive, the second and the weights a half more.
+        issue_w(0, stage[0]);
+        issue_x(0, stage[0]);
+        issue_w(1, stage[1]);
+        meet(std::integral_constant<int, LT + LW>{});
+        read_w(stage[0]);
+        for (int kt = 0; kt < KB; kt++) {
+            Stage &s = stage[kt & 1], &o = stage[(kt + 1) & 1];
+            block_scales(kt);
+            meet(std::integral_constant<int, LT / 2 + LW>{});
+            if (kt % SB == 0)
+                issue_s(kt / SB + 1);
+            issue_x(kt + 1, o);
+            part(kt, s, zero{}, std::integral_constant<int, TB / 2>{});
+            meet(std::integral_constant<int, LT>{});
+            issue_w(kt + 2, s);
+            part(kt, s, std::integral_constant<int, TB / 2>{}, std::integral_constant<int, TB / 2>{});
+            read_w(o);
+        }
+    } else {
+        // S stages, one barrier a tile, loads S - 1 tiles ahead
+#pragma unroll
+        for (int t = 0; t < S - 1; t++) {
+            issue_w(t, stage[t]);
+            issue_x(t, stage[t]);
+        }
+        int at = 0;
+        for (int kt = 0; kt < KB; kt++) {
+            block_scales(kt);
+            meet(std::integral_constant<int, (S - 2) * (LW + LT)>{});
+            if (kt % SB == 0)
+                issue_s(kt / SB + 1);
+            Stage &o = stage[at == 0 ? S - 1 : at - 1];
+            issue_w(kt + S - 1, o);
+            issue_x(kt + S - 1, o);
+            read_w(stage[at]);
+            part(kt, stage[at], zero{}, std::integral_constant<int, TB>{});
+            at = at + 1 == S ? 0 : at + 1;
+        }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
@@ -312,7 +349,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             to_f16 = exp2_int(-k16);
 #pragma unroll
         for (int i = 0; i < WB; i++) {
-            const int n = n0 + 64 * oq + 16 * i + 4 * q;
+            const int n = n0 + 16 * WB * oq + 16 * i + 4 * q;
             if (n >= a.N)
                 continue;
             const f32x4 v = acc[i][j];
@@ -323,18 +360,22 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
                 *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
                     u32x2{cvt_f16x2(v[0] * to_f16, v[1] * to_f16), cvt_f16x2(v[2] * to_f16, v[3] * to_f16)};
         }
-        if (MODE == kDown && q == 0 && n0 + 64 * oq < a.N)
+        if (MODE == kDown && q == 0 && n0 + 16 * WB * oq < a.N)
             a.hs[(int64_t)slot * ((a.N + 63) / 64) + n0 / 64 + oq] = (uint8_t)k16;
     }
 }
 
-template <F8Mode MODE, bool XF32>
-void launch_kind(const F8Args &a, int64_t grid8, int64_t grid4, bool big, bool last, const Launch &l)
+template <F8Mode MODE, int TB, int WB, int S>
+void launch_size(const F8Args &a, bool f32, bool last, const Launch &l)
 {
-    if (big)
-        dispatch(tiles_kernel<MODE, XF32, 8>, dim3((unsigned)grid8), dim3(512), l, true, last, a);
+    constexpr int NT = MODE == kUp ? 32 * WB : 64 * WB;
+    // (of an experts' call, the tiles that any plan of it can ask for)
+    const int64_t tiles_m = MODE == kDense ? (a.T + 32 * TB - 1) / (32 * TB) : f8_most_tiles(a.p, 32 * TB);
+    const dim3 grid((unsigned)(tiles_m * ((a.N + NT - 1) / NT)));
+    if (f32)
+        dispatch(tiles_kernel<MODE, true, TB, WB, S>, grid, dim3(512), l, true, last, a);
     else
-        dispatch(tiles_kernel<MODE, XF32, 4>, dim3((unsigned)grid4), dim3(512), l, true, last, a);
+        dispatch(tiles_kernel<MODE, false, TB, WB, S>, grid, dim3(512), l, true, last, a);
 }
 
 }  // namespace
@@ -342,25 +383,33 @@ void launch_kind(const F8Args &a, int64_t grid8, int64_t grid4, bool big, bool l
 template <F8Mode MODE>
 void launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
 {
-    const int64_t NT = MODE == kUp ? BN / 2 : BN, tiles_n = (a.N + NT - 1) / NT;
-    int64_t g8, g4;
-    bool big;
-    if (MODE == kDense) {
-        const int64_t m8 = (a.T + 255) / 256, m4 = (a.T + 127) / 128;
-        g8 = m8 * tiles_n;
-        g4 = m4 * tiles_n;
-        const int cus = device_cus();
-        big = !(g8 < cus && g4 <= cus);
+    if constexpr (MODE == kDense) {
+        const int64_t cus = device_cus();
+        const int64_t size[5][2] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}, {64, 64}};
+        int pick = 0;
+        int64_t least = INT64_MAX;
+        for (int i = 0; i < 5; i++) {
+            const int64_t tiles = ((a.T + size[i][0] - 1) / size[i][0]) * ((a.N + size[i][1] - 1) / size[i][1]);
+            const int64_t cost = (tiles + cus - 1) / cus * kCost[i];
+            if (cost < least) {
+                least = cost;
+                pick = i;
+            }
+        }
+        pick == 0   ? launch_size<kDense, 8, 4, 2>(a, f32, last, l)
+        : pick == 1 ? launch_size<kDense, 4, 4, 3>(a, f32, last, l)
+        : pick == 2 ? launch_size<kDense, 4, 2, 4>(a, f32, last, l)
+        : pick == 3 ? launch_size<kDense, 2, 2, 5>(a, f32, last, l)
+                    : launch_size<kDense, 2, 1, 8>(a, f32, last, l);
     } else {
-        // tiles that any plan of the call can ask for
-        g8 = f8_most_tiles(a.p, 256) * tiles_n;
-        g4 = f8_most_tiles(a.p, 128) * tiles_n;
-        big = a.p.slots / a.p.E >= 192;
+        const int64_t rows = a.p.slots / a.p.E;
+        if (rows >= kRows8)
+            launch_size<MODE, 8, 4, 2>(a, f32, last, l);
+        else if (rows >= kRows4)
+            launch_size<MODE, 4, 4, 3>(a, f32, last, l);
+        else
+            launch_size<MODE, 2, 4, 3>(a, f32, last, l);
     }
-    if (f32)
-        launch_kind<MODE, true>(a, g8, g4, big, last, l);
-    else
-        launch_kind<MODE, false>(a, g8, g4, big, last, l);
 }
 
 template void launch_f8_tiles<kDense>(const F8Args &, bool, bool, const Launch &);
