@@ -7,8 +7,9 @@
 //   a token's experts: of the top_groups groups with the largest sum of their
 //   group_best best scores + bias, the k with the largest keys
 //
-// A wavefront takes a token: expert e is value e / 64 of lane e % 64, and each
-// of the k choices is one maximum over the wavefront's keys as ordered integers.
+// A wavefront takes a token: of NR experts a lane, expert e is value e % NR of lane
+// e / NR, and each of the k choices is one maximum over the wavefront's keys as
+// ordered integers.
 // Choices are whole numbers, so they must not hang on how a score is rounded:
 // keys are formed in f32, whose error is bounded here, and a token where two
 // keys that are to be told apart lie nearer than that is taken again in 64 bits.
@@ -24,21 +25,25 @@
 namespace engram {
 namespace {
 
-constexpr int kBlockTokens = 64;
+constexpr int kBlockTokens = 64;        // at most: a bit each
 constexpr int kWaves = 16;
 // counts of this many blocks are summed once more before the blocks are placed
 constexpr int kSegment = 64;
 constexpr int kMostBlocks = 256;        // placed from the counts alone
+constexpr int kSpare = 15;              // candidates for a token's choice beyond those needed
 
 typedef unsigned long long u64;
 
 // Where in f32 two keys may stand in the other order than in exact arithmetic.
-// A sigmoid is off by 2^-22 of itself at most (e^-x by an ulp, two roundings),
-// a softmax score by 2^-20 (the rounding of x - max, the sum), a key's own
-// rounding is 2^-24 of it; a group's sum holds two.
+// e^-x is off by (1.5 |x| + 2) 2^-24 of itself (the product with log2 e, the
+// instruction), which a sigmoid, whose slope times |x| is below 0.23, passes on
+// as less than 2^-22, and the sum and reciprocal add another; a softmax score,
+// below 1 and with |d| e^-d below 0.37, is off by 2^-20 (its sum of NR + 6
+// additions included); a key's own rounding is 2^-24 of it.  A group's sum holds
+// two keys.
 __device__ __forceinline__ bool near_keys(float a, float b, bool softmax, float terms)
 {
-    return a - b <= terms * ((softmax ? 0x1p-19f : 0x1p-21f) + 0x1p-22f * fmaxf(fabsf(a), fabsf(b)));
+    return a - b <= terms * ((softmax ? 0x1p-19f : 0x1p-20f) + 0x1p-22f * fmaxf(fabsf(a), fabsf(b)));
 }
 
 // f32 in the order of its value as an unsigned number above 0; 0 = shut.  (-0,
@@ -91,14 +96,52 @@ struct Choice {
     double score;       // its score
 };
 
-// The token in 64 bits.
-template <int NR>
-__device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[NR], const float *bias,
-                                          uint32_t open)
+// e^x to (1.5 |x| + 2) 2^-24 of itself
+__device__ __forceinline__ float fast_exp(float x)
 {
-    const int lane = threadIdx.x & 63;
+    return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+
+// The two largest of what lanes hold, over the 2, 4, .. `lanes` lanes around each.
+template <int CTRL>
+__device__ __forceinline__ void merge_dpp(float &first, float &second)
+{
+    const float f = __int_as_float(dpp_from<CTRL, 0xF>(__float_as_int(first)));
+    const float s = __int_as_float(dpp_from<CTRL, 0xF>(__float_as_int(second)));
+    second = fmaxf(fmaxf(second, s), fminf(first, f));
+    first = fmaxf(first, f);
+}
+__device__ __forceinline__ void merge_best(float &first, float &second, int lanes)
+{
+    if (lanes > 1)
+        merge_dpp<0xB1>(first, second);              // quad_perm [1,0,3,2]
+    if (lanes > 2)
+        merge_dpp<0x4E>(first, second);              // quad_perm [2,3,0,1]
+    if (lanes > 4)
+        merge_dpp<0x141>(first, second);             // row_half_mirror
+    if (lanes > 8)
+        merge_dpp<0x140>(first, second);             // row_mirror
+    for (int m = 16; m < lanes; m *= 2) {
+        const float f = __shfl_xor(first, m), s = __shfl_xor(second, m);
+        second = fmaxf(fmaxf(second, s), fminf(first, f));
+        first = fmaxf(first, f);
+    }
+}
+
+// How a wavefront looks through groups of experts.  lanes: a group is
+// `spread` whole lanes; otherwise `spread` lanes look through a group's experts
+// in LDS.  spread is a power of two.
+struct Groups {
+    int spread;
+    bool lanes;
+};
+
+// The experts' scores and keys (score + bias, -inf where shut) in 64 bits.
+template <int NR>
+__device__ __forceinline__ void scores_f64(const Routing &a, const float (&x)[NR], const float (&b)[NR],
+                                           uint32_t open, double (&score)[NR], double (&key)[NR])
+{
     const double low = -INFINITY;
-    double score[NR], key[NR];
     if (a.softmax) {
         double top = low;
 #pragma unroll
@@ -125,10 +168,33 @@ __device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[
     }
 #pragma unroll
     for (int r = 0; r < NR; r++)
-        key[r] = open >> r & 1 ? score[r] + (bias ? (double)bias[64 * r + lane] : 0.0) : low;
-    if (a.groups > 1) {
+        key[r] = open >> r & 1 ? score[r] + (double)b[r] : low;
+}
+
+// The groups kept by keys in 64 bits, a bit each.
+template <int NR>
+__device__ __forceinline__ u64 groups_f64(const Routing &a, const Groups &gr, const double (&key)[NR])
+{
+    const int lane = threadIdx.x & 63;
+    const double low = -INFINITY;
+    double mine = low;                  // lane g: group g's sum
+    if (gr.lanes) {
+        double first = low, second = low;
+#pragma unroll
+        for (int r = 0; r < NR; r++) {
+            second = fmax(second, fmin(first, key[r]));
+            first = fmax(first, key[r]);
+        }
+        for (int m = 1; m < gr.spread; m *= 2) {
+            const double f = __shfl_xor(first, m), s = __shfl_xor(second, m);
+            second = fmax(fmax(second, s), fmin(first, f));
+            first = fmax(first, f);
+        }
+        if (a.group_best > 1 && second > low)
+            first += second;
+        mine = __shfl(first, lane < a.groups ? lane * gr.spread : 0);
+    } else {
         const int size = a.E / a.groups;
-        double mine = low;              // lane g: group g's sum
         for (int g = 0; g < a.groups; g++) {
             double sum = low;
             int out = -1;
@@ -137,7 +203,7 @@ __device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[
                 int e = 1 << 30;
 #pragma unroll
                 for (int r = 0; r < NR; r++) {
-                    const int i = 64 * r + lane;
+                    const int i = NR * lane + r;
                     if (i / size == g && i != out && key[r] > v) {
                         v = key[r];
                         e = i;
@@ -152,24 +218,22 @@ __device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[
             if (lane == g)
                 mine = sum;
         }
-        int ahead = 0;
-        for (int h = 0; h < a.groups; h++) {
-            const double v = __shfl(mine, h);
-            ahead += v > mine || (v == mine && h < lane);
-        }
-        const u64 kept = __ballot(lane < a.groups && mine > low && ahead < a.top_groups);
-#pragma unroll
-        for (int r = 0; r < NR; r++) {
-            const int i = 64 * r + lane;
-            if (i < a.E && !(kept >> (i / size) & 1))
-                key[r] = low;
-        }
     }
-    if (!bias)
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            if (key[r] > low)
-                key[r] = x[r];
+    int ahead = 0;
+    for (int h = 0; h < a.groups; h++) {
+        const double v = __shfl(mine, h);
+        ahead += v > mine || (v == mine && h < lane);
+    }
+    return __ballot(lane < a.groups && mine > low && ahead < a.top_groups);
+}
+
+// Choices one by one from scores and keys in 64 bits: lane j < k gets its
+// expert and score.
+template <int NR>
+__device__ __forceinline__ Choice choose_f64(const Routing &a, double (&score)[NR], double (&key)[NR])
+{
+    const int lane = threadIdx.x & 63;
+    const double low = -INFINITY;
     Choice c{-1, 0.0};
     for (int j = 0; j < a.k; j++) {
         double v = low;
@@ -178,7 +242,7 @@ __device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[
         for (int r = 0; r < NR; r++)
             if (key[r] > v) {
                 v = key[r];
-                e = 64 * r + lane;
+                e = NR * lane + r;
             }
         wave_best_f64(v, e);
         if (v == low)
@@ -186,7 +250,7 @@ __device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[
         double s = 0.0;
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            if (64 * r + lane == e) {
+            if (NR * lane + r == e) {
                 s = score[r];
                 key[r] = low;
             }
@@ -197,16 +261,50 @@ __device__ __forceinline__ Choice choose_f64(const Routing &a, const float (&x)[
     return c;
 }
 
-// One token; lane j < k returns its j-th expert and weight.  keys: the
-// wavefront's own LDS, E floats (groups only).
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ int lanes_below(u64 mask)
+{
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// How many of lanes 0, step, 2 step, .. (n of them, and one more where n is odd,
+// which holds the least) hold more than this lane's v, or as much
+// and are before it: `own` is its number among them.
+__device__ __forceinline__ int rank_of(uint32_t v, int own, int n, int step)
+{
+    const u64 key = (u64)v << 32 | (uint32_t)(63 - own);
+    int rank = 0;
+    for (int i = 0; i < n; i += 2)
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+            const u64 o = (u64)(uint32_t)__builtin_amdgcn_readlane((int)v, (i + z) * step) << 32 |
+                          (uint32_t)(63 - i - z);
+            rank += o > key;
+        }
+    return rank;
+}
+
+// a / b to an ulp or two, for b and its reciprocal normal numbers
+__device__ __forceinline__ float quotient(float a, float b)
+{
+    const float r = __builtin_amdgcn_rcpf(b), q = a * r;
+    return __builtin_fmaf(__builtin_fmaf(-b, q, a), r, q);
+}
+
+// n candidates, lane i's expert e: in the order of their keys in 64 bits.
 template <int NR>
-__device__ __forceinline__ void choose(const Routing &a, const float (&x)[NR],
-                                       const float (&b)[NR], uint32_t open, const int (&gbit)[NR],
-                                       int spread, float *keys, int &id, float &weight)
+__device__ __forceinline__ int rank_f64(const Routing &a, const float (&x)[NR], uint32_t open, float *values,
+                                        int n, int e)
 {
     const int lane = threadIdx.x & 63;
-    float score[NR];
-    uint32_t key[NR];
+#pragma unroll
+    for (int r = 0; r < NR; r++)
+        values[NR * lane + r] = x[r];
+    const double v = e >= 0 ? values[e] : 0.0, bias = e >= 0 ? a.bias[e] : 0.0;
+    double score;
     if (a.softmax) {
         float top = -FLT_MAX;
 #pragma unroll
@@ -214,115 +312,205 @@ __device__ __forceinline__ void choose(const Routing &a, const float (&x)[NR],
             if (open >> r & 1)
                 top = fmaxf(top, x[r]);
         top = unordered(wave_max_u32(ordered(top)));
-        float sum = 0.0f;
+        double sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            if (open >> r & 1)
+                sum += exp((double)x[r] - (double)top);
+        score = exp(v - (double)top) / wave_sum_f64(sum);
+    } else {
+        score = 1.0 / (1.0 + exp(-v));
+    }
+    const double key = score + bias;
+    int rank = 0;
+    for (int i = 0; i < n; i++) {
+        const double o = __shfl(key, i);
+        const int oe = __builtin_amdgcn_readlane(e, i);
+        rank += o > key || (o == key && oe < e);
+    }
+    if (lane < n)
+        values[rank] = __int_as_float(e);
+    return lane < n ? __float_as_int(values[lane]) : -1;
+}
+
+// One token; lane j < k returns its j-th expert and weight.  values: the
+// wavefront's own LDS, 64 * NR floats (128 at least).  slack: how far below the
+// largest key the last token's bound was.  gbit: the lane that speaks for each
+// expert's group (where groups are not whole lanes).
+template <int NR>
+__device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const float (&x)[NR],
+                                       const float (&b)[NR], uint32_t open, const int (&gbit)[NR],
+                                       float *values, float &slack, int &id, float &weight)
+{
+    const int lane = threadIdx.x & 63;
+    const uint32_t softmax_open = open;              // groups left out still count in the sum
+    float score[NR];
+    uint32_t key[NR];
+    float top = 0.0f, all = 0.0f;
+    if (a.softmax) {
+        top = -FLT_MAX;
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            if (open >> r & 1)
+                top = fmaxf(top, x[r]);
+        top = unordered(wave_max_u32(ordered(top)));
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-            score[r] = open >> r & 1 ? expf(x[r] - top) : 0.0f;
-            sum += score[r];
+            score[r] = open >> r & 1 ? fast_exp(x[r] - top) : 0.0f;
+            all += score[r];
         }
-        sum = wave_sum(sum);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        all = wave_sum(all);
+        const float inv = all > 0.0f ? 1.0f / all : 0.0f;
 #pragma unroll
         for (int r = 0; r < NR; r++)
             score[r] *= inv;
     } else {
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            score[r] = open >> r & 1 ? 1.0f / (1.0f + expf(-x[r])) : 0.0f;
+            score[r] = open >> r & 1 ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[r])) : 0.0f;
     }
-    bool close = false;
 #pragma unroll
     for (int r = 0; r < NR; r++)
         key[r] = !(open >> r & 1) ? 0u : ordered(a.bias ? score[r] + b[r] : x[r]);
     if (a.groups > 1) {
-        const int size = a.E / a.groups, g = lane / spread, sub = lane & (spread - 1);
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            if (64 * r + lane < a.E)
-                keys[64 * r + lane] = open >> r & 1 ? score[r] + b[r] : -INFINITY;
         float first = -INFINITY, second = -INFINITY;
-        if (g < a.groups)
-            for (int i = sub; i < size; i += spread) {
-                const float v = keys[g * size + i];
+        const int g = lane / gr.spread;
+        if (gr.lanes) {
+#pragma unroll
+            for (int r = 0; r < NR; r++) {
+                const float v = open >> r & 1 ? score[r] + b[r] : -INFINITY;
                 second = fmaxf(second, fminf(first, v));
                 first = fmaxf(first, v);
             }
-        for (int m = 1; m < spread; m *= 2) {
-            const float f = __shfl_xor(first, m), s = __shfl_xor(second, m);
-            second = fmaxf(fmaxf(second, s), fminf(first, f));
-            first = fmaxf(first, f);
+        } else {
+#pragma unroll
+            for (int r = 0; r < NR; r++)
+                values[NR * lane + r] = open >> r & 1 ? score[r] + b[r] : -INFINITY;
+            const int size = a.E / a.groups;
+            if (g < a.groups)
+                for (int i = lane & (gr.spread - 1); i < size; i += gr.spread) {
+                    const float v = values[g * size + i];
+                    second = fmaxf(second, fminf(first, v));
+                    first = fmaxf(first, v);
+                }
         }
+        merge_best(first, second, gr.spread);
         float sum = first;
         if (a.group_best > 1 && second > -INFINITY)
             sum += second;
-        int ahead = 0;
-        for (int h = 0; h < a.groups; h++) {
-            const float v = __uint_as_float(
-                (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sum), h * spread));
-            ahead += v > sum || (v == sum && h < g);
-        }
-        const bool in = g < a.groups && sum > -INFINITY, keep = in && ahead < a.top_groups;
-        const u64 kept = __ballot(keep);
-        if (__ballot(in && !keep)) {
-            const float worst = -unordered(wave_max_u32(keep ? ordered(-sum) : 0u));
-            const float next = unordered(wave_max_u32(in && !keep ? ordered(sum) : 0u));
-            close = near_keys(worst, next, a.softmax, 2.0f);
+        // (lanes past the groups hold -inf)
+        const int ahead = rank_of(ordered(sum), g, a.groups, gr.spread);
+        const bool in = g < a.groups && sum > -INFINITY;
+        bool keep = in && ahead < a.top_groups;
+        u64 kept = __ballot(keep);
+        const u64 last = __ballot(in && ahead == a.top_groups - 1), next = __ballot(in && ahead == a.top_groups);
+        if (next && near_keys(lane_value(sum, __builtin_ctzll(last)), lane_value(sum, __builtin_ctzll(next)),
+                              a.softmax, 2.0f)) {
+            double s64[NR], k64[NR];
+            scores_f64<NR>(a, x, b, open, s64, k64);
+            const u64 by_group = groups_f64<NR>(a, gr, k64);
+            keep = g < a.groups && (by_group >> g & 1);
+            kept = __ballot(keep);
         }
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            if (!(kept >> gbit[r] & 1))
+            if (gr.lanes ? !keep : !(kept >> gbit[r] & 1)) {
                 key[r] = 0u;
+                open &= ~(1u << r);
+            }
     }
-    // lane j: the j-th key, its expert and score; one more than k are taken
-    uint32_t mine = 0u;
-    float s = 0.0f;
-    id = -1;
-    for (int j = 0; j <= a.k; j++) {
-        uint32_t v = key[0];
+    // The candidates: keys not below a bound that leaves more than k of them (or
+    // all) and at most 64, found by trial from where the last token's was.
+    uint32_t best = key[0];
 #pragma unroll
-        for (int r = 1; r < NR; r++)
-            v = max(v, key[r]);
-        v = wave_max_u32(v);
-        if (v == 0u)
+    for (int r = 1; r < NR; r++)
+        best = max(best, key[r]);
+    best = wave_max_u32(best);
+    const float high = unordered(best);
+    int total = 0;
+#pragma unroll
+    for (int r = 0; r < NR; r++)
+        total += __popcll(__ballot(key[r] != 0u));
+    const int want = min(a.k + 1, total), most = want + kSpare;
+    int n = total;
+    uint32_t bound = 1u;
+    for (int turn = 0; n > most && turn < 16; turn++) {
+        bound = ordered(high - slack);
+        n = 0;
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            n += __popcll(__ballot(key[r] >= bound));
+        if (n >= want && n <= most)
             break;
-        bool found = false;
+        slack = fminf(fmaxf(slack * (n < want ? 1.75f : 0.75f), 0x1p-20f), 0x1p20f);
+        n = 64 * NR + 1;
+    }
+    uint32_t mine = 0u;
+    int at = -1;
+    bool exact = false;
+    if (n <= 64) {
+        // to the lanes, in the experts' order
+        int before = 0;
 #pragma unroll
-        for (int r = 0; r < NR; r++) {
-            const u64 at = __ballot(key[r] == v);
-            if (!found && at) {
-                found = true;
-                const int l = __builtin_ctzll(at);
-                const float sc = __uint_as_float(
-                    (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(score[r]), l));
-                if (lane == j) {
-                    mine = v;
-                    id = 64 * r + l;
-                    s = sc;
-                }
-                if (lane == l)
-                    key[r] = 0u;
+        for (int r = 0; r < NR; r++)
+            before += lanes_below(__ballot(key[r] >= bound));
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            if (key[r] >= bound) {
+                values[before] = __uint_as_float(key[r]);
+                values[64 + before++] = __int_as_float(NR * lane + r);
+            }
+        const uint32_t v = lane < n ? __float_as_uint(values[lane]) : 0u;
+        const int e = lane < n ? __float_as_int(values[64 + lane]) : -1;
+        const int rank = rank_of(v, lane, n, 1);
+        // in the order of their keys
+        if (lane < n) {
+            values[rank] = __uint_as_float(v);
+            values[64 + rank] = __int_as_float(e);
+        }
+        mine = lane < n ? __float_as_uint(values[lane]) : 0u;
+        at = lane < n ? __float_as_int(values[64 + lane]) : -1;
+        if (a.bias) {
+            const float own = unordered(mine);
+            const uint32_t next = (uint32_t)dpp_from<0x130, 0xF>((int)mine);     // of lane j + 1
+            if (__ballot(lane < a.k && next != 0u && near_keys(own, unordered(next), a.softmax, 1.0f))) {
+                // told apart in 64 bits, if nobody outside can stand among the first k
+                const float least = lane_value(own, n - 1), kth = lane_value(own, min(a.k, n) - 1);
+                exact = n < total && near_keys(kth, least, a.softmax, 1.0f);
+                if (!exact)
+                    at = rank_f64<NR>(a, x, softmax_open, values, n, at);
             }
         }
+    } else {
+        exact = true;
     }
-    if (a.bias) {
-        const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);
-        close = close || __ballot(lane < a.k && next != 0u && mine != 0u &&
-                                  near_keys(unordered(mine), unordered(next), a.softmax, 1.0f));
+    id = -1;
+    float s = 0.0f;
+    if (!exact) {
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            values[NR * lane + r] = x[r];
+        id = lane < a.k ? at : -1;
+        if (id >= 0) {
+            const float v = values[id];
+            s = a.softmax ? quotient(expf(v - top), all) : 1.0f / (1.0f + expf(-v));
+        }
     }
-    if (lane >= a.k) {
-        id = -1;
-        s = 0.0f;
-    }
-    float sum = wave_sum(s);
-    if (__ballot(close) || (sum < 0x1p-90f && __ballot(id >= 0))) {
-        const Choice c = choose_f64<NR>(a, x, a.bias, open);
+    const float sum = wave_sum(s);
+    if (exact || (sum < 0x1p-90f && __ballot(id >= 0))) {
+        double s64[NR], k64[NR];
+        scores_f64<NR>(a, x, b, softmax_open, s64, k64);
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            k64[r] = !(open >> r & 1) ? -INFINITY : a.bias ? k64[r] : (double)x[r];
+        const Choice c = choose_f64<NR>(a, s64, k64);
         id = lane < a.k ? c.id : -1;
         const double sc = id >= 0 ? c.score : 0.0;
-        const double total = wave_sum_f64(sc);
-        weight = (float)((a.renorm ? (total > 0.0 ? sc / total : 0.0) : sc) * (double)a.factor);
+        const double total64 = wave_sum_f64(sc);
+        weight = (float)((a.renorm ? (total64 > 0.0 ? sc / total64 : 0.0) : sc) * (double)a.factor);
         return;
     }
-    weight = (a.renorm ? (sum > 0.0f ? s / sum : 0.0f) : s) * a.factor;
+    weight = (a.renorm ? quotient(s, sum > 0.0f ? sum : 1.0f) : s) * a.factor;
 }
 
 // Exclusive sums over the experts' counts (E <= blockDim.x: thread e has
@@ -345,51 +533,60 @@ __device__ __forceinline__ int before_expert(int count, int *part, int &all)
 }
 
 template <bool BF16, int NR>
-__global__ __launch_bounds__(64 * kWaves) void route_kernel(Routing a, uint8_t *counts, int pitch)
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(Routing a, Groups gr, int block,
+                                                            uint8_t *counts, int pitch)
 {
     __shared__ u64 mask[64 * NR];
     __shared__ int32_t ids_s[kBlockTokens * kMaxChosen];
     __shared__ int start[64 * NR];
     __shared__ int part[kWaves];
-    __shared__ float keys_s[kWaves][64 * NR];
+    __shared__ float values[kWaves][NR > 1 ? 64 * NR : 128];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int t0 = blockIdx.x * kBlockTokens;
+    const int t0 = blockIdx.x * block;
     for (int i = tid; i < 64 * NR; i += 64 * kWaves)
         mask[i] = 0;
-    // lanes a group's experts are looked through by: a power of two
-    int spread = 64;
-    while (spread * a.groups > 64)
-        spread /= 2;
     float b[NR];
     int gbit[NR];
     uint32_t known = 0;
     bool odd = false;
-#pragma unroll
-    for (int r = 0; r < NR; r++) {
-        const int e = 64 * r + lane;
-        b[r] = a.bias && e < a.E ? a.bias[e] : 0.0f;
-        odd |= b[r] > FLT_MAX || b[r] != b[r];
-        known |= (uint32_t)(e < a.E && fabsf(b[r]) <= FLT_MAX) << r;
-        gbit[r] = e < a.E ? e / (a.E / a.groups) * spread : 0;
-    }
-    __syncthreads();
-    for (int t = t0 + wv; t < min(t0 + kBlockTokens, a.T); t += kWaves) {
-        float x[NR];
-        uint32_t open = 0;
+    const auto logits = [&](int t, float (&x)[NR]) {
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-            const int e = 64 * r + lane;
+            const int e = NR * lane + r;
             const int64_t at = (int64_t)t * a.stride + e;
             x[r] = -INFINITY;
             if (e < a.E)
                 x[r] = BF16 ? bf16_lo(((const uint16_t *)a.logits)[at]) : ((const float *)a.logits)[at];
+        }
+    };
+    const int t1 = min(t0 + block, a.T);
+    float slack = 0.5f, ahead[NR];
+    if (t0 + wv < t1)
+        logits(t0 + wv, ahead);
+#pragma unroll
+    for (int r = 0; r < NR; r++) {
+        const int e = NR * lane + r;
+        b[r] = a.bias && e < a.E ? a.bias[e] : 0.0f;
+        odd |= b[r] > FLT_MAX || b[r] != b[r];
+        known |= (uint32_t)(e < a.E && fabsf(b[r]) <= FLT_MAX) << r;
+        gbit[r] = gr.lanes || e >= a.E ? 0 : e / (a.E / a.groups) * gr.spread;
+    }
+    __syncthreads();
+    for (int t = t0 + wv; t < t1; t += kWaves) {
+        float x[NR];
+        uint32_t open = 0;
+#pragma unroll
+        for (int r = 0; r < NR; r++) {
+            x[r] = ahead[r];
             odd |= x[r] > FLT_MAX || x[r] != x[r];
             open |= (uint32_t)((known >> r & 1) && fabsf(x[r]) <= FLT_MAX) << r;
         }
+        if (t + kWaves < t1)
+            logits(t + kWaves, ahead);
         int id;
         float weight;
-        choose<NR>(a, x, b, open, gbit, spread, keys_s[wv], id, weight);
+        choose<NR>(a, gr, x, b, open, gbit, values[wv], slack, id, weight);
         if (lane < a.k) {
             const int64_t slot = (int64_t)t * a.k + lane;
             a.ids[slot] = id;
@@ -416,7 +613,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(Routing a, uint8_t *
     if (tid == 0)
         a.offsets[a.E] = all;
     __syncthreads();
-    for (int i = tid; i < (min(t0 + kBlockTokens, a.T) - t0) * a.k; i += 64 * kWaves) {
+    for (int i = tid; i < (t1 - t0) * a.k; i += 64 * kWaves) {
         const int e = ids_s[i], t = i / a.k;
         if (e >= 0)
             a.order[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = i;
@@ -439,12 +636,15 @@ __global__ __launch_bounds__(256) void segment_kernel(const uint8_t *__restrict_
 // A block's slots to their places, after the counts of the blocks before it.
 // segments: sums of kSegment blocks each, or null (the counts alone).
 __global__ __launch_bounds__(64 * kWaves) void place_kernel(Routing a, const uint8_t *counts,
-                                                            const int32_t *segments, int blocks,
-                                                            int pitch)
+                                                            const int32_t *segments, int tokens,
+                                                            int blocks, int pitch)
 {
     __shared__ u64 mask[kMaxExperts];
     __shared__ int before_s[kMaxExperts], all_s[kMaxExperts], part[kWaves];
-    const int tid = threadIdx.x, block = blockIdx.x, t0 = block * kBlockTokens;
+    const int tid = threadIdx.x, block = blockIdx.x, t0 = block * tokens;
+    const int n = (min(t0 + tokens, a.T) - t0) * a.k;
+    const int32_t *ids = a.ids + (int64_t)t0 * a.k;
+    const int id0 = tid < n ? ids[tid] : -1;        // on its way beside the counts
     mask[tid] = 0;
     before_s[tid] = all_s[tid] = 0;
     __syncthreads();
@@ -465,7 +665,7 @@ __global__ __launch_bounds__(64 * kWaves) void place_kernel(Routing a, const uin
             first = mine * kSegment;
             last = block;
         }
-#pragma unroll 4
+#pragma unroll 16
         for (int i = first + row; i < last; i += rows) {
             const uint32_t v = *(const uint32_t *)(counts + (int64_t)i * pitch + 4 * w);
 #pragma unroll
@@ -481,11 +681,12 @@ __global__ __launch_bounds__(64 * kWaves) void place_kernel(Routing a, const uin
             atomicAdd(&all_s[4 * w + z], all[z]);
         }
     }
-    const int n = (min(t0 + kBlockTokens, a.T) - t0) * a.k;
-    const int32_t *ids = a.ids + (int64_t)t0 * a.k;
-    for (int i = tid; i < n; i += 64 * kWaves)
-        if (ids[i] >= 0)
-            atomicOr(&mask[ids[i]], 1ull << (i / a.k));
+    const auto id_of = [&](int i) { return i == tid ? id0 : ids[i]; };
+    for (int i = tid; i < n; i += 64 * kWaves) {
+        const int e = id_of(i);
+        if (e >= 0)
+            atomicOr(&mask[e], 1ull << (i / a.k));
+    }
     __syncthreads();
     int total;
     const int start = before_expert(tid < pitch ? all_s[tid] : 0, part, total);
@@ -498,21 +699,30 @@ __global__ __launch_bounds__(64 * kWaves) void place_kernel(Routing a, const uin
         a.offsets[a.E] = total;
     __syncthreads();
     for (int i = tid; i < n; i += 64 * kWaves) {
-        const int e = ids[i];
+        const int e = id_of(i);
         if (e >= 0)
             a.order[before_s[e] + __popcll(mask[e] & ((1ull << (i / a.k)) - 1))] = t0 * a.k + i;
     }
 }
 
 int pitch_of(int32_t E) { return (E + 15) / 16 * 16; }
-int64_t blocks_of(int64_t T) { return (T + kBlockTokens - 1) / kBlockTokens; }
+// A block's tokens: one a wavefront where that makes kMostBlocks blocks at most,
+// and all of a call's that one block holds (one launch).
+int64_t block_of(int64_t T) { return T > kBlockTokens && T <= kMostBlocks * kWaves ? kWaves : kBlockTokens; }
+int64_t blocks_of(int64_t T) { return (T + block_of(T) - 1) / block_of(T); }
 size_t counts_bytes(int64_t T, int32_t E) { return ((size_t)(blocks_of(T) * pitch_of(E)) + 255) & ~(size_t)255; }
 
 template <bool BF16, int NR>
 void launch_scores(const Routing &r, uint8_t *counts, const Launch &l)
 {
+    // groups of whole lanes, a power of two of them, or looked through in LDS
+    const int size = r.E / r.groups;
+    Groups gr{size / NR, size % NR == 0 && (size / NR & (size / NR - 1)) == 0};
+    if (!gr.lanes)
+        for (gr.spread = 64; gr.spread * r.groups > 64;)
+            gr.spread /= 2;
     dispatch(route_kernel<BF16, NR>, dim3((unsigned)blocks_of(r.T)), dim3(64 * kWaves), l, true,
-             !counts, r, counts, pitch_of(r.E));
+             !counts, r, gr, (int)block_of(r.T), counts, pitch_of(r.E));
 }
 
 template <bool BF16>
@@ -549,7 +759,8 @@ int32_t launch_route(const Routing &r, void *ws, const Launch &l)
             dispatch(segment_kernel, dim3((unsigned)((blocks + kSegment - 1) / kSegment)), dim3(256),
                      l, false, false, (const uint8_t *)counts, sums, (int)blocks, pitch_of(r.E));
         dispatch(place_kernel, dim3((unsigned)blocks), dim3(64 * kWaves), l, false, true, r,
-                 (const uint8_t *)counts, (const int32_t *)sums, (int)blocks, pitch_of(r.E));
+                 (const uint8_t *)counts, (const int32_t *)sums, (int)block_of(r.T), (int)blocks,
+                 pitch_of(r.E));
     }
     return launch_status("engram route kernels");
 }
