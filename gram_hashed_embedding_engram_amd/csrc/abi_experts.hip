@@ -167,7 +167,8 @@ int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_
     rc = check_operands(d_x, d_x_scales, d_w, d_w_scales, "project_f8");
     if (rc != ENGRAM_OK)
         return rc;
-    CHECK(d_y && aligned(d_y, 8), ENGRAM_E_ARG, "engram project_f8: NULL or unaligned y (8 bytes)");
+    CHECK(d_y && aligned(d_y, 16), ENGRAM_E_ARG,
+          "engram project_f8: NULL or unaligned y (16 bytes)");
     const uint64_t out = (uint64_t)T * (uint64_t)N * 2;
     CHECK(!overlap(d_x, (uint64_t)T * (uint64_t)K, d_y, out) &&
               !overlap(d_x_scales, scale_bytes(T, K, x_f32 != 0), d_y, out),

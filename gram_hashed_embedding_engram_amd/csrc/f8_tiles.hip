@@ -31,6 +31,13 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
 // and block, loaded block by block, would ask for as many lines as the codes
 constexpr int SB = 8;
 
+// the same for weight rows, which are read 4 * RUN * (l / 4) + l % 4
+template <int RUN>
+__device__ __forceinline__ int w_swizzle(int r)
+{
+    return (r >> 1 & 1) | (r >> (RUN == 4 ? 4 : RUN == 2 ? 3 : 2) & 3) << 1;
+}
+
 template <int TB, int WB>
 struct Stage {
     u32x4 tok[32 * TB * 8];
@@ -52,6 +59,10 @@ template <F8Mode MODE, bool XF32, int TB, int WB, int S>
 __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 {
     constexpr int BM = 32 * TB, BN = 64 * WB, LT = BM / 64, LW = BN / 64;
+    // blocks whose outputs a lane has side by side: row m of block i is weight row
+    // 4 * RUN * (m / 4) + 4 * i + m % 4 of the wavefront's, so that a lane's sums,
+    // rows 4q .. 4q + 3 of every block, are 4 * RUN neighbours
+    constexpr int RUN = MODE == kUp ? 2 : WB;
     typedef Stage<TB, WB> Stage;
     __shared__ Shared<TB, WB, S> sh;
     Stage *const stage = sh.stage;
@@ -128,10 +139,11 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         const int slot = a.p.order[p0 + r];
         return (uint32_t)slot < (uint32_t)a.p.slots ? (uint32_t)slot / (uint32_t)a.p.k : 0u;
     };
-    uint32_t w_at[2], x_at[4];           // (of x_at, LT are used)
+    uint32_t w_at[4], x_at[4];           // (LW and LT are used)
 #pragma unroll
-    for (int j = 0; j < 2; j++)
-        w_at[j] = (uint32_t)(8 * j + lr) * a.K + 16 * (ls ^ swizzle(8 * j + lr));
+    for (int j = 0; j < LW; j++)
+        w_at[j] = (uint32_t)(8 * (j & 1) + lr) * a.K +
+                  16 * (ls ^ w_swizzle<RUN>(8 * WB * wave + 8 * j + lr));
     // this wavefront's rows of the first half of the tokens, then of the second
     constexpr int LH = LT > 1 ? LT / 2 : 1;
     const auto t_row = [&](int j) { return j / LH * (BM / 2) + wave * (8 * LH) + 8 * (j % LH); };
@@ -150,7 +162,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         for (int j = 0; j < LW; j++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 ? rw0 : rw1,
                                                      (lptr_t)&s.w[(8 * WB * wave + 8 * j) * 8], 16,
-                                                     w_at[j & 1], 128 * k, 0, 0);
+                                                     w_at[j], 128 * k, 0, 0);
     };
     const auto issue_s = [&](int part) {
 #pragma unroll
@@ -182,6 +194,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // a fragment's two pieces of row r16: at these offsets from its first row
     const int at0 = 128 * r16 + 16 * (q ^ swizzle(r16)), at1 = at0 ^ 64;
+    const int w_row = 4 * RUN * (r16 >> 2) + (r16 & 3);
+    const int w_at0 = 128 * w_row + 16 * (q ^ w_swizzle<RUN>(w_row));
     const auto fragment = [&](const char *p0_, const char *p1_, int r) {
         const u32x4 x = *(const u32x4 *)(p0_ + 128 * r), y = *(const u32x4 *)(p1_ + 128 * r);
         return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
@@ -189,10 +203,10 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     i32x8 wf[WB];
     float f[H];
     const auto read_w = [&](const Stage &s) {
-        const char *w0 = (const char *)s.w + oq * 16 * WB * 128 + at0, *w1 = w0 - at0 + at1;
+        const char *w0 = (const char *)s.w + oq * 16 * WB * 128 + w_at0, *w1 = w0 - w_at0 + (w_at0 ^ 64);
 #pragma unroll
         for (int i = 0; i < WB; i++)
-            wf[i] = fragment(w0, w1, 16 * i);
+            wf[i] = fragment(w0, w1, i / RUN * 32 + i % RUN * 4);
     };
     // blocks J0 .. J0 + NJ - 1 of the wavefront's tokens
     const auto some = [&](int kt, const Stage &s, auto j0, auto nj) {
@@ -294,8 +308,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    // ---- out: accumulator e of block (i, j) is weight row 16i + 4q + e, token
-    // 16j + lane % 16 of the wavefront's
+    // ---- out: accumulator e of block (i, j) is output 4 * RUN * q + 4i + e of the
+    // wavefront's, token 32j + 16th + l % 16
 #pragma unroll
     for (int j = 0; j < TB; j++) {
         const int r = 32 * j + 16 * th + r16;
@@ -321,10 +335,9 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             if (!fine)
                 continue;
             const int n = n0 + 32 * oq;
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-                *(uint32_t *)((uint8_t *)a.y + p * a.N + n + 16 * i + 4 * q) =
-                    e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+            *(u32x2 *)((uint8_t *)a.y + p * a.N + n + 8 * q) =
+                u32x2{e4m3x4(v[0][0] * inv, v[0][1] * inv, v[0][2] * inv, v[0][3] * inv),
+                      e4m3x4(v[1][0] * inv, v[1][1] * inv, v[1][2] * inv, v[1][3] * inv)};
             if (q == 0)
                 a.hs[p * (a.N / 32) + n / 32] = (uint8_t)(k + 127);
             continue;
@@ -333,7 +346,6 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         // of f32 twice over memory, off by 2^-11 of themselves (or 2^-39 of the 64's
         // largest), an eighth of what the sum's own rounding to bf16 is off by
         int k16 = 0;
-        float to_f16 = 1.0f;
         if (MODE == kDown) {
             float amax = 0.0f;
 #pragma unroll
@@ -343,25 +355,26 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
                     amax = fmaxf(amax, finite_abs(acc[i][j][e]));
             k16 = f16_scale_exp(max_x16(amax));
         }
-        if (!fine)
+        const int n = n0 + 16 * WB * oq + 4 * RUN * q;
+        if (!fine || n >= a.N)
             continue;
-        if (MODE == kDown)
-            to_f16 = exp2_int(-k16);
+        const float inv = exp2_int(-k16);
+        uint32_t o[2 * WB];
 #pragma unroll
         for (int i = 0; i < WB; i++) {
-            const int n = n0 + 16 * WB * oq + 16 * i + 4 * q;
-            if (n >= a.N)
-                continue;
             const f32x4 v = acc[i][j];
-            if (MODE == kDense)
-                *(u32x2 *)((uint16_t *)a.y + p * a.N + n) =
-                    u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
-            else
-                *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
-                    u32x2{cvt_f16x2(v[0] * to_f16, v[1] * to_f16), cvt_f16x2(v[2] * to_f16, v[3] * to_f16)};
+            o[2 * i] = MODE == kDense ? cvt_bf16x2(v[0], v[1]) : cvt_f16x2(v[0] * inv, v[1] * inv);
+            o[2 * i + 1] = MODE == kDense ? cvt_bf16x2(v[2], v[3]) : cvt_f16x2(v[2] * inv, v[3] * inv);
         }
-        if (MODE == kDown && q == 0 && n0 + 16 * WB * oq < a.N)
-            a.hs[(int64_t)slot * ((a.N + 63) / 64) + n0 / 64 + oq] = (uint8_t)k16;
+        uint16_t *y = (uint16_t *)a.y + (MODE == kDense ? p : (int64_t)slot) * a.N + n;
+        if constexpr (WB == 1)
+            *(u32x2 *)y = u32x2{o[0], o[1]};
+        else
+#pragma unroll
+            for (int i = 0; i < WB; i += 2)
+                *(u32x4 *)(y + 4 * i) = u32x4{o[2 * i], o[2 * i + 1], o[2 * i + 2], o[2 * i + 3]};
+        if (MODE == kDown && q == 0)
+            a.hs[(int64_t)slot * ((a.N + 63) / 64) + n / 64] = (uint8_t)k16;
     }
 }
 

@@ -595,7 +595,7 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
 /* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ).
  *   d_x, d_x_scales  T rows;  d_w, d_w_scales  weights;  d_y [T][N] bf16.
  * K a positive multiple of 128 up to 2^20, N a positive multiple of 16 up to
- * 2^24, T up to 2^22.  d_x and d_w 16-byte, d_y 8-byte, scales 4-byte aligned.
+ * 2^24, T up to 2^22.  d_x, d_w and d_y 16-byte, scales 4-byte aligned.
  * T = 0 is a no-op. */
 int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_f32,
                           const uint8_t *d_w, const float *d_w_scales, uint16_t *d_y, int64_t T,
