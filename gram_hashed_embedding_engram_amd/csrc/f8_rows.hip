@@ -13,6 +13,7 @@ constexpr int64_t kMostRows = 32;
 // 186 to 195 and 162 to 165, 16 rows 279 and 181; 16 experts, 2 rows 38 and 49.  Down,
 // 2048 x 4096: 4 rows 89 and 91, 16 rows 172 and 109.
 constexpr int64_t kUpRows = 4, kDownRows = 8;
+constexpr int kFewSlots = 16, kFewWaves = 16;
 constexpr int64_t kFewUnits = 256, kManyUnits = 4096;
 
 __device__ __forceinline__ i32x8 operand(const u32x4 &a, const u32x4 &b)
@@ -282,6 +283,104 @@ __global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v
     }
 }
 
+// Down projection and weighted sum of up to kFewSlots slots in one launch: a
+// workgroup has 16 outputs, its wavefronts take pieces of K, `split` of each expert
+// that the plan meets, and the slots' sums stay in LDS until all are there.
+template <bool XF32>
+__global__ __launch_bounds__(64 * kFewWaves) void down_few_kernel(F8Args a, int split)
+{
+    constexpr int U = 4;
+    __shared__ float part[kFewSlots][17];           // [split][slots], split * slots <= kFewSlots
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = blockIdx.x * 16, KB = a.K / 128, NB = (a.N + 127) / 128;
+    if (blockIdx.x == 0)
+        raise_bad_plan(a.p);
+    for (int i = tid; i < kFewSlots * 17; i += 64 * kFewWaves)
+        (&part[0][0])[i] = 0.0f;
+    __syncthreads();
+    int met = 0;
+    for (int base = 0; base < a.p.E; base += 64) {
+        const Span s = base + lane < a.p.E ? span_of(a.p, base + lane) : Span{0, 0};
+        for (uint64_t mask = __ballot(s.n > 0); mask; mask &= mask - 1, met += split) {
+            const int piece = (wv + kFewWaves - met % kFewWaves) % kFewWaves;
+            if (piece >= split)
+                continue;
+            const int begin = KB * piece / split, end = KB * (piece + 1) / split;
+            const int at = __builtin_ctzll(mask);
+            const int from = __builtin_amdgcn_readlane(s.from, at), n = __builtin_amdgcn_readlane(s.n, at);
+            const int64_t m0 = (int64_t)(base + at) * a.N + n0;
+            const uint8_t *w = a.w + (m0 + r16) * a.K + 16 * q;
+            const float *ws = a.ws + ((int64_t)(base + at) * NB + n0 / 128) * KB;
+            for (int r0 = 0; r0 < n; r0 += 16) {
+                const int64_t row = from + r0 + min(r16, n - r0 - 1);
+                const uint8_t *x = a.x + row * a.K + 16 * q;
+                const uint8_t *xs = (const uint8_t *)a.xs + row * (a.K / 32) + (XF32 ? 0 : q);
+                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int k0 = begin; k0 < end; k0 += U) {
+                    u32x4 wr[U][2], xr[U][2];
+                    uint32_t xsc[U];
+                    float f[U];
+#pragma unroll
+                    for (int u = 0; u < U; u++) {
+                        const int k = min(k0 + u, end - 1);
+#pragma unroll
+                        for (int z = 0; z < 2; z++) {
+                            wr[u][z] = *(const u32x4 *)(w + 128 * k + 64 * z);
+                            xr[u][z] = *(const u32x4 *)(x + 128 * k + 64 * z);
+                        }
+                        xsc[u] = XF32 ? *(const uint32_t *)(xs + 4 * k) : xs[4 * k];
+                        f[u] = ws[k];
+                    }
+                    // all loads are under way before the first is waited for
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int u = 0; u < U; u++) {
+                        if (k0 + u >= end)
+                            break;
+                        const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            operand(wr[u][0], wr[u][1]), operand(xr[u][0], xr[u][1]),
+                            f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp8, kFp8, 0, kOne, 0,
+                            XF32 ? kOne : (int)xsc[u]);
+                        const float g = XF32 ? f[u] * __uint_as_float(xsc[u]) : f[u];
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            acc[e] = __builtin_fmaf(v[e], g, acc[e]);
+                    }
+                }
+                if (r16 < n - r0) {
+                    const int slot = a.p.order[row];
+                    if ((uint32_t)slot < (uint32_t)a.p.slots) {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            part[piece * a.p.slots + slot][4 * q + e] = acc[e];
+                    } else {
+                        raise(a.p.err, ENGRAM_DEVERR_ROUTE);
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < a.T * 8; i += 64 * kFewWaves) {
+        const int t = i / 8, n = 2 * (i & 7);
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int j = 0; j < a.p.k; j++) {
+            const int slot = t * a.p.k + j;
+            if ((uint32_t)a.p.ids[slot] >= (uint32_t)a.p.E)
+                continue;
+            float v0 = part[slot][n], v1 = part[slot][n + 1];
+            for (int i = 1; i < split; i++) {
+                v0 += part[i * a.p.slots + slot][n];
+                v1 += part[i * a.p.slots + slot][n + 1];
+            }
+            s0 += v0 * a.p.weights[slot];
+            s1 += v1 * a.p.weights[slot];
+        }
+        *(uint32_t *)((uint16_t *)a.y + (int64_t)t * a.N + n0 + n) = cvt_bf16x2(s0, s1);
+    }
+}
+
 template <F8Mode MODE, int OT, int MT, int W>
 void launch_split(const F8Args &a, bool f32, int64_t tiles, bool last, const Launch &l)
 {
@@ -347,14 +446,34 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
     return launch_status("engram experts_up kernel");
 }
 
+// Whether a call's products stay in LDS.  Both ways in us, 2048 x 4096: 2 slots 8.7
+// and 9.7, 8 slots 15.5 and 20, 16 slots 22 and 26, 32 slots 44 to 51 and 51; 16
+// slots of 1024 x 1024, which make few workgroups, 12 and 10.
+static bool down_few(const Plan &p, int64_t N)
+{
+    return p.slots <= kFewSlots && (p.slots <= 4 || N >= 2048) && p.slots / p.E < kDownRows;
+}
+
 size_t experts_down_bytes(const Plan &p, int64_t N)
 {
-    return (size_t)p.slots * (2 * N + (N + 31) / 32);
+    return down_few(p, N) ? 0 : (size_t)p.slots * (2 * N + (N + 31) / 32);
 }
 
 int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uint16_t *y, int64_t K,
                             int64_t N, void *ws, const Launch &l)
 {
+    if (down_few(p, N)) {
+        const F8Args a{p, h.x, h.s, w.w, w.s, y, nullptr, p.T, (int)K, (int)N};
+        const dim3 grid((unsigned)(N / 16));
+        int split = 1;
+        while (2 * split * p.slots <= kFewSlots && 2 * split <= K / kF8Block)
+            split *= 2;
+        if (h.f32)
+            dispatch(down_few_kernel<true>, grid, dim3(64 * kFewWaves), l, true, true, a, split);
+        else
+            dispatch(down_few_kernel<false>, grid, dim3(64 * kFewWaves), l, true, true, a, split);
+        return launch_status("engram experts_down kernel");
+    }
     uint16_t *products = (uint16_t *)ws;
     uint8_t *exps = (uint8_t *)(products + (int64_t)p.slots * N);
     const F8Args a{p, h.x, h.s, w.w, w.s, products, exps, p.T, (int)K, (int)N};

@@ -248,7 +248,7 @@ def check_h(h, hs, want, tol):
 
 
 @pytest.mark.parametrize("f32", [False, True])
-@pytest.mark.parametrize("K,N", [(128, 16), (640, 272), (1024, 528)])
+@pytest.mark.parametrize("K,N", [(128, 16), (640, 272), (1024, 528), (384, 2064)])
 @pytest.mark.parametrize("T,n,k,empty", PLANS)
 def test_experts_down(E, T, n, k, empty, K, N, f32):
     log(f"experts_down T {T} experts {n} k {k} empty {empty} K {K} N {N} f32 {f32}")
