@@ -27,6 +27,22 @@ struct F8Args {
     int T, K, N;                        // N: outputs, for kUp those of one half
 };
 
+// A block's scale as s = m * 2^(e - 127).  With E8M0 rows the power of two goes
+// into the matrix instruction beside theirs, so that a sum passes f32's range only
+// where the result does (row scales of 2^123 met by block scales of 2^-123).
+struct BlockScale {
+    int e;
+    float m;
+};
+template <bool XF32>
+__device__ __forceinline__ BlockScale block_scale(float s)
+{
+    if (XF32)
+        return BlockScale{kOne, s};
+    const int e = min(max((int)(__float_as_uint(s) >> 23 & 0xFF), 1), 254);
+    return BlockScale{e, __builtin_ldexpf(s, 127 - e)};
+}
+
 // Exponent k >= -126 with amax < 2^15 * 2^k, amax >= 2^14 * 2^k above the floor.
 __device__ __forceinline__ int f16_scale_exp(float amax)
 {
@@ -49,6 +65,6 @@ inline int64_t f8_most_tiles(const Plan &p, int64_t rows)
 }
 
 template <F8Mode MODE>
-void launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l);
+int32_t launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l);
 
 }  // namespace engram

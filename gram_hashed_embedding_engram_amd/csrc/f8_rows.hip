@@ -173,10 +173,10 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
                 // (not multiplied past the end, where a NaN would meet zeros)
                 if (k0 + u >= end)
                     break;
-                float f[RT];
+                BlockScale f[RT];
 #pragma unroll
                 for (int i = 0; i < RT; i++)
-                    f[i] = ws[i][k0 + u];
+                    f[i] = block_scale<XF32>(ws[i][k0 + u]);
 #pragma unroll
                 for (int j = 0; j < MT; j++) {
                     const i32x8 xf = operand(xr[u][j][0], xr[u][j][1]);
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
                     for (int i = 0; i < RT; i++) {
                         const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                             operand(wr[u][i][0], wr[u][i][1]), xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f},
-                            kFp8, kFp8, 0, kOne, 0, XF32 ? kOne : (int)xsc[u][j]);
-                        const float g = XF32 ? f[i] * t : f[i];
+                            kFp8, kFp8, 0, f[i].e, 0, XF32 ? kOne : (int)xsc[u][j]);
+                        const float g = XF32 ? f[i].m * t : f[i].m;
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             acc[i][j][e] = __builtin_fmaf(v[e], g, acc[i][j][e]);
@@ -338,11 +338,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void down_few_kernel(F8Args a, int 
                     for (int u = 0; u < U; u++) {
                         if (k0 + u >= end)
                             break;
+                        const BlockScale b = block_scale<XF32>(f[u]);
                         const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                             operand(wr[u][0], wr[u][1]), operand(xr[u][0], xr[u][1]),
-                            f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp8, kFp8, 0, kOne, 0,
+                            f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp8, kFp8, 0, b.e, 0,
                             XF32 ? kOne : (int)xsc[u]);
-                        const float g = XF32 ? f[u] * __uint_as_float(xsc[u]) : f[u];
+                        const float g = XF32 ? b.m * __uint_as_float(xsc[u]) : b.m;
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             acc[e] = __builtin_fmaf(v[e], g, acc[e]);
@@ -429,9 +430,8 @@ int32_t launch_project_f8(const Rows8 &x, const Blocks8 &w, uint16_t *y, int64_t
 {
     const F8Args a{Plan{}, x.x, x.s, w.w, w.s, y, nullptr, (int)T, (int)K, (int)N};
     if (T > kMostRows)
-        launch_f8_tiles<kDense>(a, x.f32, true, l);
-    else
-        T <= 16 ? launch_dense<1>(a, x.f32, l) : launch_dense<2>(a, x.f32, l);
+        return launch_f8_tiles<kDense>(a, x.f32, true, l);
+    T <= 16 ? launch_dense<1>(a, x.f32, l) : launch_dense<2>(a, x.f32, l);
     return launch_status("engram project_f8 kernel");
 }
 
@@ -440,9 +440,8 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
 {
     const F8Args a{p, x.x, x.s, w.w, w.s, h, hs, p.T, (int)K, (int)I};
     if (p.slots / p.E >= kUpRows)
-        launch_f8_tiles<kUp>(a, x.f32, true, l);
-    else
-        launch_experts<kUp>(a, x.f32, true, l);
+        return launch_f8_tiles<kUp>(a, x.f32, true, l);
+    launch_experts<kUp>(a, x.f32, true, l);
     return launch_status("engram experts_up kernel");
 }
 
@@ -480,7 +479,9 @@ int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uin
     const int64_t blocks = (p.T * (N / 8) + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
     if (p.slots / p.E >= kDownRows) {
-        launch_f8_tiles<kDown>(a, h.f32, false, l);
+        const int32_t rc = launch_f8_tiles<kDown>(a, h.f32, false, l);
+        if (rc != ENGRAM_OK)
+            return rc;
         dispatch(sum_kernel<64>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     } else {

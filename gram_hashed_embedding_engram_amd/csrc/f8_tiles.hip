@@ -201,7 +201,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
     };
     i32x8 wf[WB];
-    float f[H];
+    BlockScale f[H];
     const auto read_w = [&](const Stage &s) {
         const char *w0 = (const char *)s.w + oq * 16 * WB * 128 + w_at0, *w1 = w0 - w_at0 + (w_at0 ^ 64);
 #pragma unroll
@@ -221,12 +221,12 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             float g[H];
 #pragma unroll
             for (int h = 0; h < H; h++)
-                g[h] = XF32 ? f[h] * __uint_as_float(xs) : f[h];
+                g[h] = XF32 ? f[h].m * __uint_as_float(xs) : f[h].m;
 #pragma unroll
             for (int i = 0; i < WB; i++) {
                 const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    wf[i], xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp8, kFp8, 0, kOne, 0,
-                    XF32 ? kOne : (int)xs);
+                    wf[i], xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kFp8, kFp8, 0,
+                    f[MODE == kUp ? i >> 1 : 0].e, 0, XF32 ? kOne : (int)xs);
 #pragma unroll
                 for (int e = 0; e < 4; e++)
                     acc[i][j][e] = __builtin_fmaf(v[e], g[MODE == kUp ? i >> 1 : 0], acc[i][j][e]);
@@ -257,8 +257,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             }
 #pragma unroll
         for (int h = 0; h < H; h++)
-            f[h] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(wsv[h]),
-                                                                       kt & 63));
+            f[h] = block_scale<XF32>(__int_as_float(
+                __builtin_amdgcn_readlane(__float_as_int(wsv[h]), kt & 63)));
     };
     typedef std::integral_constant<int, 0> zero;
     issue_s(0);
@@ -379,22 +379,26 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 }
 
 template <F8Mode MODE, int TB, int WB, int S>
-void launch_size(const F8Args &a, bool f32, bool last, const Launch &l)
+int32_t launch_size(const F8Args &a, bool f32, bool last, const Launch &l)
 {
     constexpr int NT = MODE == kUp ? 32 * WB : 64 * WB;
     // (of an experts' call, the tiles that any plan of it can ask for)
     const int64_t tiles_m = MODE == kDense ? (a.T + 32 * TB - 1) / (32 * TB) : f8_most_tiles(a.p, 32 * TB);
-    const dim3 grid((unsigned)(tiles_m * ((a.N + NT - 1) / NT)));
+    const int64_t tiles = tiles_m * ((a.N + NT - 1) / NT);
+    if (tiles >= (int64_t)1 << 23)                   // a grid counts its threads in 32 bits
+        return fail(ENGRAM_E_RANGE, "engram f8 tiles: %lld workgroups exceed 2^23-1", (long long)tiles);
+    const dim3 grid((unsigned)tiles);
     if (f32)
         dispatch(tiles_kernel<MODE, true, TB, WB, S>, grid, dim3(512), l, true, last, a);
     else
         dispatch(tiles_kernel<MODE, false, TB, WB, S>, grid, dim3(512), l, true, last, a);
+    return launch_status("engram f8 tiles kernel");
 }
 
 }  // namespace
 
 template <F8Mode MODE>
-void launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
+int32_t launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
 {
     if constexpr (MODE == kDense) {
         const int64_t cus = device_cus();
@@ -409,24 +413,21 @@ void launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
                 pick = i;
             }
         }
-        pick == 0   ? launch_size<kDense, 8, 4, 2>(a, f32, last, l)
-        : pick == 1 ? launch_size<kDense, 4, 4, 3>(a, f32, last, l)
-        : pick == 2 ? launch_size<kDense, 4, 2, 4>(a, f32, last, l)
-        : pick == 3 ? launch_size<kDense, 2, 2, 5>(a, f32, last, l)
-                    : launch_size<kDense, 2, 1, 8>(a, f32, last, l);
+        return pick == 0   ? launch_size<kDense, 8, 4, 2>(a, f32, last, l)
+               : pick == 1 ? launch_size<kDense, 4, 4, 3>(a, f32, last, l)
+               : pick == 2 ? launch_size<kDense, 4, 2, 4>(a, f32, last, l)
+               : pick == 3 ? launch_size<kDense, 2, 2, 5>(a, f32, last, l)
+                           : launch_size<kDense, 2, 1, 8>(a, f32, last, l);
     } else {
         const int64_t rows = a.p.slots / a.p.E;
-        if (rows >= kRows8)
-            launch_size<MODE, 8, 4, 2>(a, f32, last, l);
-        else if (rows >= kRows4)
-            launch_size<MODE, 4, 4, 3>(a, f32, last, l);
-        else
-            launch_size<MODE, 2, 4, 3>(a, f32, last, l);
+        return rows >= kRows8   ? launch_size<MODE, 8, 4, 2>(a, f32, last, l)
+               : rows >= kRows4 ? launch_size<MODE, 4, 4, 3>(a, f32, last, l)
+                                : launch_size<MODE, 2, 4, 3>(a, f32, last, l);
     }
 }
 
-template void launch_f8_tiles<kDense>(const F8Args &, bool, bool, const Launch &);
-template void launch_f8_tiles<kUp>(const F8Args &, bool, bool, const Launch &);
-template void launch_f8_tiles<kDown>(const F8Args &, bool, bool, const Launch &);
+template int32_t launch_f8_tiles<kDense>(const F8Args &, bool, bool, const Launch &);
+template int32_t launch_f8_tiles<kUp>(const F8Args &, bool, bool, const Launch &);
+template int32_t launch_f8_tiles<kDown>(const F8Args &, bool, bool, const Launch &);
 
 }  // namespace engram

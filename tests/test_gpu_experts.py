@@ -266,3 +266,396 @@ def test_experts_down(E, T, n, k, empty, K, N, f32):
     want, tol = R.down(h64, w, s, offsets, order, arrays[1])
     within(y, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
     assert int(err) == 0
+
+
+# --------------------------------------------------- tile sizes and their borders
+@pytest.mark.parametrize("T,K,N", [(4090, 256, 4080), (2040, 256, 4080), (2040, 384, 2032), (1000, 256, 2032), (1000, 1152, 1008),
+                                   (97, 2048, 336), (4090, 128, 4096)])
+def test_project_f8_tiles(E, T, K, N):
+    log(f"project_f8 T {T} K {K} N {N}")
+    g = seeded(T + K + N)
+    w, s = R.weights8(g, N, K)
+    for f32 in (False, True):
+        x, xs, x64 = R.rows8(g, T, K, f32)
+        y = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        E.project_f8(x, E.F8(w, s), y[:T], xs)
+        torch.cuda.synchronize()
+        want, tol = R.product(x64, R.matrix(w, s))
+        within(y[:T], want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
+        assert bool((y[T] == 7).all()), "a row past the last is written"
+
+
+def counted_plan(g, counts, shuffled=False):
+    """One expert a token, so many tokens each."""
+    ids = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts))
+    ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(sum(counts)))]
+    offsets, order = R.plan(ids[:, None].numpy(), len(counts))
+    if shuffled:                                       # an expert's slots in any order
+        rng = np.random.default_rng(1)
+        order = np.concatenate([rng.permutation(order[p:q]) for p, q in zip(offsets[:-1], offsets[1:])])
+    i32 = torch.int32
+    weights = torch.rand(len(ids), 1, generator=g, device="cuda") - 0.3
+    return (ids[:, None].to(i32).cuda(), weights, torch.tensor(offsets, dtype=i32, device="cuda"),
+            torch.tensor(order, dtype=i32, device="cuda")), offsets, order
+
+
+def check_experts(E, g, arrays, offsets, order, n, K, I, N, f32=False, err=0):
+    """Both products over a plan, from rows and from h of their own."""
+    T, k = arrays[0].shape
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    routes = E.Routes(*arrays, word)
+    m = len(order)
+    w, s = R.weights8(g, n, 2, I, K)
+    x, xs, x64 = R.rows8(g, T, K, f32)
+    h = torch.full((T * k, I), 0x55, dtype=torch.uint8, device="cuda")
+    hs = torch.full((T * k, I // 32), 0x55, dtype=torch.uint8, device="cuda")
+    E.experts_up(x, xs, E.F8(w, s), routes, h, hs)
+    want, tol = R.up(x64, w, s, offsets, order, k)
+    check_h(h[:m], hs[:m], want, tol)
+    assert bool((h[m:] == 0x55).all()) and bool((hs[m:] == 0x55).all()), "rows past the plan are written"
+    w, s = R.weights8(g, n, N, K)
+    down = E.F8(w, s)
+    h, hs, h64 = R.rows8(g, T * k, K, f32)
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    E.experts_down(h, hs, down, routes, y, space(E, E.experts_down_bytes(down, routes)))
+    want, tol = R.down(h64, w, s, offsets, order, arrays[1])
+    within(y, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
+    assert int(word) == err
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("counts", [[0, 1, 15, 16, 17, 3], [0, 0, 9, 0], [64, 65, 0, 128, 1, 63], [100, 128, 129, 43], [33, 31],
+                                    [129, 256, 257, 0, 512, 300], [255, 193, 192, 320, 321], [1000]])
+def test_experts_borders(E, counts, f32):
+    log(f"experts with {counts} rows f32 {f32}")
+    g = seeded(sum(counts))
+    arrays, offsets, order = counted_plan(g, counts, shuffled=True)
+    check_experts(E, g, arrays, offsets, order, len(counts), 384, 256, 528, f32)
+
+
+def test_experts_many(E):
+    """The most experts, the most of them a token."""
+    g = seeded(12)
+    arrays, offsets, order = some_plan(g, 20, 1024, 32, 0.1)
+    check_experts(E, g, arrays, offsets, order, 1024, 128, 128, 48)
+    arrays, offsets, order = some_plan(g, 700, 32, 32, 0.1)
+    check_experts(E, g, arrays, offsets, order, 32, 128, 128, 48)
+
+
+def test_experts_one_twice(E):
+    """A token's slots may name one expert twice: a row each."""
+    g = seeded(13)
+    for T in (1, 5, 60):
+        ids = torch.full((T, 3), 2, dtype=torch.int32)
+        ids[:, 1] = 0
+        offsets, order = R.plan(ids.numpy(), 4)
+        weights = torch.rand(T, 3, generator=g, device="cuda")
+        arrays = (ids.cuda(), weights, *(torch.tensor(v, dtype=torch.int32, device="cuda") for v in (offsets, order)))
+        check_experts(E, g, arrays, offsets, order, 4, 256, 128, 2048 if T == 5 else 64)
+
+
+# --------------------------------------------------------- values at their ends
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_project_f8_nan(E, T):
+    """NaN codes and scales reach their own row and output alone; an infinite
+    block scale its own outputs."""
+    g = seeded(T)
+    w, s = R.weights8(g, 400, 512)
+    x, xs, x64 = R.rows8(g, T, 512, False)
+    x[1, 77] = 0x7F
+    xs[2, 3] = 255
+    w[5, 200] = 0xFF
+    s[3, 1] = INF
+    x64 = A.grouped(A.e4m3(x), xs)
+    y = torch.zeros(T, 400, dtype=torch.bfloat16, device="cuda")
+    E.project_f8(x, E.F8(w, s), y, xs)
+    bad = torch.zeros(T, 400, dtype=torch.bool, device="cuda")
+    bad[1:3] = True
+    bad[:, 5] = True
+    assert bool(torch.isnan(y[bad]).all())
+    far = torch.zeros_like(bad)
+    far[:, 384:] = True
+    assert not bool(torch.isfinite(y[far]).any())
+    s[3, 1], w[5, 200], x[1, 77], xs[2, 3] = 1.0, 0, 0, 127
+    x64 = A.grouped(A.e4m3(x), xs)
+    want, tol = R.product(x64, R.matrix(w, s))
+    rest = ~(bad | far)
+    within(y[rest], want[rest], (2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol)[rest], "y")
+
+
+@pytest.mark.parametrize("T", [2, 60])
+def test_project_f8_scales(E, T):
+    """Scales from one end of their bytes to the other, undone by the weights'."""
+    g = seeded(T + 1)
+    K, N = 512, 160
+    w, _ = R.weights8(g, N, K)
+    for byte in (1, 40, 127, 200, 250):
+        x, xs, _ = R.rows8(g, T, K, False)
+        xs[:] = byte
+        s = torch.full((2, 4), 2.0 ** (127 - max(byte, 3)) / 4096, device="cuda")
+        y = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        E.project_f8(x, E.F8(w, s), y, xs)
+        want, tol = R.product(A.grouped(A.e4m3(x), xs), R.matrix(w, s))
+        # (byte 1: products reach below f32's normal numbers)
+        within(y, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol + 2.0 ** -126 * K * s[0, 0].double(), f"scale byte {byte}")
+
+
+def test_experts_nan(E):
+    """A NaN or infinity in one token's rows stays with that token."""
+    g = seeded(21)
+    for T in (4, 90):
+        arrays, offsets, order = some_plan(g, T, 3, 2)
+        w, s = R.weights8(g, 3, 2, 128, 256)
+        x, xs, _ = R.rows8(g, T, 256, False)
+        out = []
+        for bad in (False, True):
+            if bad:
+                x[2, 100] = 0x7F
+            h = torch.zeros(2 * T, 128, dtype=torch.uint8, device="cuda")
+            hs = torch.zeros(2 * T, 4, dtype=torch.uint8, device="cuda")
+            E.experts_up(x, xs, E.F8(w, s), E.Routes(*arrays), h, hs)
+            out.append((h, hs))
+        mine = torch.tensor(order // 2 == 2, device="cuda")
+        (h0, hs0), (h1, hs1) = out
+        assert torch.equal(h0[~mine], h1[~mine]) and torch.equal(hs0[~mine], hs1[~mine])
+        assert bool(torch.isnan(A.e4m3(h1[mine])).all())
+        wd, sd = R.weights8(g, 3, 64, 128)
+        down, routes = E.F8(wd, sd), E.Routes(*arrays)
+        ys = []
+        for h, hs in out:
+            y = torch.zeros(T, 64, dtype=torch.bfloat16, device="cuda")
+            E.experts_down(h, hs, down, routes, y, space(E, E.experts_down_bytes(down, routes)))
+            ys.append(y)
+        others = torch.arange(T, device="cuda") != 2
+        assert torch.equal(ys[0][others], ys[1][others]) and bool(torch.isnan(ys[1][2]).all())
+
+
+def test_experts_down_infinite(E):
+    """Products past f16's and f32's range: large ones keep their size, infinite
+    ones are infinite."""
+    g = seeded(22)
+    for T in (3, 70):
+        ids = torch.zeros(T, 1, dtype=torch.int32)
+        offsets, order = R.plan(ids.numpy(), 2)
+        arrays = (ids.cuda(), torch.ones(T, 1, device="cuda"),
+                  *(torch.tensor(v, dtype=torch.int32, device="cuda") for v in (offsets, order)))
+        w, s = R.weights8(g, 2, 64, 128)
+        h, hs, _ = R.rows8(g, T, 128, True)
+        hs[0] *= 2.0 ** 60
+        hs[1] = 2.0 ** 127
+        s[:] = 2.0 ** 20
+        down, routes = E.F8(w, s), E.Routes(*arrays)
+        y = torch.zeros(T, 64, dtype=torch.bfloat16, device="cuda")
+        E.experts_down(h, hs, down, routes, y, space(E, E.experts_down_bytes(down, routes)))
+        h64 = A.e4m3(h) * hs.double()
+        want, tol = R.down(h64, w, s, offsets, order, arrays[1])
+        fine = torch.arange(T, device="cuda") != 1
+        within(y[fine], want[fine], (2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol)[fine], "y")
+        assert not bool(torch.isfinite(y[1]).any())
+
+
+# ------------------------------------------------------------------- bad plans
+@pytest.mark.parametrize("T,k,n", [(6, 2, 4), (40, 2, 3), (400, 2, 3), (1200, 1, 2)])
+def test_bad_plans(E, T, k, n):
+    """Spans and slots out of range set the error bit, and what they do not
+    touch is computed as ever."""
+    log(f"bad plans T {T} k {k} experts {n}")
+    g = seeded(T)
+    (ids, weights, offsets, order), *_ = some_plan(g, T, n, k, skew=0.0)
+    w, s = R.weights8(g, n, 2, 128, 256)
+    up = E.F8(w, s)
+    N = 2048 if T == 6 else 64                         # one launch, and two
+    wd, sd = R.weights8(g, n, N, 128)
+    down = E.F8(wd, sd)
+    x, xs, _ = R.rows8(g, T, 256, False)
+
+    def both(offsets, order):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        routes = E.Routes(ids, weights, offsets, order, err)
+        h = torch.full((T * k, 128), 0x55, dtype=torch.uint8, device="cuda")
+        hs = torch.full((T * k, 4), 0x7F, dtype=torch.uint8, device="cuda")
+        E.experts_up(x, xs, up, routes, h, hs)
+        torch.cuda.synchronize()
+        first = int(err)
+        err.zero_()
+        y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        E.experts_down(h, hs, down, routes, y, space(E, E.experts_down_bytes(down, routes)))
+        torch.cuda.synchronize()
+        return h, hs, y, first, int(err)
+
+    h0, hs0, y0, *errs = both(offsets, order)
+    assert errs == [0, 0]
+    cut = int(offsets[1])
+    for bad in (-5, T * k + 1, 1 << 30):
+        o = offsets.clone()
+        o[0] = bad                                     # the first expert's span does not hold
+        h, hs, _, *errs = both(o, order)
+        assert errs == [E.DEVERR_ROUTE] * 2
+        assert bool((h[:cut] == 0x55).all()) and torch.equal(h[cut:], h0[cut:]) and torch.equal(hs[cut:], hs0[cut:])
+    for bad in (-1, T * k, 1 << 30, -(1 << 31)):
+        p = order.clone()
+        p[cut] = bad                                   # one slot of the second expert
+        h, hs, y, *errs = both(offsets, p)
+        assert errs == [E.DEVERR_ROUTE] * 2
+        keep = torch.arange(T * k, device="cuda") != cut
+        assert bool((h[cut] == 0x55).all()) and torch.equal(h[keep], h0[keep]) and torch.equal(hs[keep], hs0[keep])
+        others = torch.arange(T, device="cuda") != int(order[cut]) // k
+        assert torch.equal(y[others], y0[others])
+
+
+# ------------------------------------------------------------------ far offsets
+def test_weights_past_4_gib(E):
+    g = seeded(31)
+    n, I, K = 520, 1024, 4096
+    w = torch.zeros(n, 2, I, K, dtype=torch.uint8, device="cuda")
+    s = torch.ones(n, 2, I // 128, K // 128, device="cuda") / 4096
+    last, ls = R.weights8(g, 2, 2, I, K)
+    w[-2:], s[-2:] = last, ls
+    for T in (2, 40):
+        ids = torch.arange(T)[:, None] % 2 + n - 2
+        offsets, order = R.plan(ids.numpy(), n)
+        i32 = torch.int32
+        routes = E.Routes(ids.to(i32).cuda(), torch.ones(T, 1, device="cuda"), torch.tensor(offsets, dtype=i32, device="cuda"),
+                          torch.tensor(order, dtype=i32, device="cuda"))
+        x, xs, x64 = R.rows8(g, T, K, False)
+        h = torch.zeros(T, I, dtype=torch.uint8, device="cuda")
+        hs = torch.zeros(T, I // 32, dtype=torch.uint8, device="cuda")
+        E.experts_up(x, xs, E.F8(w, s), routes, h, hs)
+        want, tol = R.up(x64, last, ls, offsets[-3:], order, 1)
+        check_h(h, hs, want, tol)
+
+
+def test_results_past_4_gib(E):
+    g = seeded(32)
+    T, K, N = 70000, 128, 32768
+    w, s = R.weights8(g, N, K)
+    x, xs, x64 = R.rows8(g, T, K, True)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    E.project_f8(x, E.F8(w, s), y, xs)
+    for rows in (slice(0, 40), slice(T // 2, T // 2 + 40), slice(T - 40, T)):
+        want, tol = R.product(x64[rows], R.matrix(w, s))
+        within(y[rows], want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
+
+
+# --------------------------------------------------------- the sub-layer together
+class SubLayer:
+    """Norm, router, experts and the next norm, over buffers of a step."""
+
+    def __init__(self, E, seed, T, dim=256, n=12, k=3, I=128):
+        g = self.g = seeded(seed)
+        self.E, self.T, self.k, self.n = E, T, k, n
+        z = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+        bf, i32 = torch.bfloat16, torch.int32
+        self.h = torch.randn(T, dim, generator=g, device="cuda")
+        self.norm = (1 + 0.1 * torch.randn(dim, generator=g, device="cuda")).to(bf)
+        self.gate, self.up, self.down = (R.weights8(g, *s, spread=0.5) for s in ((n + 4, dim), (n, 2, I, dim), (n, dim, I)))
+        self.bias = 0.1 * torch.randn(n, generator=g, device="cuda")
+        self.w = [E.F8(*p) for p in (self.gate, self.up, self.down)]
+        self.codes, self.scales = z(T, dim), z(T, dim // 32)
+        self.logits = z(T, n + 4, dt=bf)
+        self.routes = E.Routes(z(T, k, dt=i32), z(T, k, dt=torch.float32), z(n + 1, dt=i32), z(T * k, dt=i32), z(1, dt=i32))
+        self.act, self.act_s, self.y = z(T * k, I), z(T * k, I // 32), z(T, dim, dt=bf)
+        self.out, self.out_s, self.sum = z(T, dim), z(T, dim // 32), z(T, dim, dt=torch.float32)
+        self.ws = [space(E, b) for b in (E.route_bytes(self.routes), E.experts_down_bytes(self.w[2], self.routes))]
+
+    def run(self):
+        E = self.E
+        E.add_norm(None, self.h, self.norm, 1e-6, self.codes, self.scales)
+        E.project_f8(self.codes, self.w[0], self.logits, self.scales)
+        E.route(self.logits[:, :self.n], self.routes, self.bias, groups=4, top_groups=2, factor=1.5, d_ws=self.ws[0])
+        E.experts_up(self.codes, self.scales, self.w[1], self.routes, self.act, self.act_s)
+        E.experts_down(self.act, self.act_s, self.w[2], self.routes, self.y, self.ws[1])
+        E.add_norm(self.y, self.h, self.norm, 1e-6, self.out, self.out_s, d_sum=self.sum)
+
+    def results(self):
+        return [t.clone() for t in (self.logits, *self.routes.keep[:4], self.act, self.act_s, self.y, self.out, self.out_s, self.sum)]
+
+
+@pytest.mark.parametrize("T", [1, 3, 37, 300, 1500])
+def test_together(E, T):
+    """Each step against its 64-bit form on what the step before left."""
+    L = SubLayer(E, T, T)
+    L.run()
+    torch.cuda.synchronize()
+    x64 = A.grouped(A.e4m3(L.codes), L.scales)
+    want, tol = R.product(x64, R.matrix(*L.gate))
+    within(L.logits, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "logits")
+    ids, weights, offsets, order = R.route(L.logits[:, :L.n].double().cpu().numpy(), L.bias.double().cpu().numpy(), L.k, False, 4, 2, 2,
+                                           True, 1.5)
+    got = [t.cpu().numpy() for t in L.routes.keep]
+    assert np.array_equal(got[0], ids) and np.array_equal(got[2], offsets) and np.array_equal(got[3], order)
+    assert np.abs(got[1] - weights).max() <= 2.0 ** -17 * 1.5 and got[4][0] == 0
+    want, tol = R.up(x64, *L.up, offsets, order, L.k)
+    check_h(L.act, L.act_s, want, tol)
+    want, tol = R.down(A.grouped(A.e4m3(L.act), L.act_s), *L.down, offsets, order, L.routes.keep[1])
+    within(L.y, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
+    assert torch.equal(L.sum, L.h + L.y.float())
+
+
+@pytest.mark.parametrize("T", [1, 50, 300])
+def test_captured(E, T):
+    """A step captured into a graph and replayed on new tokens, with work of the
+    program's own between the replays, gives the eager step's bits."""
+    L = SubLayer(E, T + 5, T)
+    L.run()                                            # (code is loaded before the capture)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.run()
+    for i in range(4):
+        L.h.copy_(torch.randn(L.h.shape, generator=L.g, device="cuda") * (i + 1))
+        L.run()
+        eager = L.results()
+        for t in (L.logits, L.y, L.out, L.act):
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, L.results()):
+            assert torch.equal(a, b)
+
+
+def test_two_streams(E):
+    """Two steps side by side, each with its own buffers on a stream of its own,
+    and repeated: the bits of the step alone."""
+    steps = [SubLayer(E, 40 + i, T) for i, T in enumerate((64, 700))]
+    alone = []
+    for L in steps:
+        L.run()
+        torch.cuda.synchronize()
+        alone.append(L.results())
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(5):
+        for L, stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                L.run()
+    torch.cuda.synchronize()
+    for L, want in zip(steps, alone):
+        assert all(torch.equal(a, b) for a, b in zip(want, L.results()))
+
+
+def test_stream_argument(E):
+    """A call goes to the stream it is given, not to the current one."""
+    L = SubLayer(E, 50, 30)
+    L.run()
+    torch.cuda.synchronize()
+    want = L.results()
+    stream = torch.cuda.Stream()
+    h = L.h.clone()
+    L.h.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        L.h.copy_(h)
+        E.add_norm(None, L.h, L.norm, 1e-6, L.codes, L.scales)
+    E.project_f8(L.codes, L.w[0], L.logits, L.scales, stream=stream)
+    E.route(L.logits[:, :L.n], L.routes, L.bias, groups=4, top_groups=2, factor=1.5, d_ws=L.ws[0], stream=stream.cuda_stream)
+    E.experts_up(L.codes, L.scales, L.w[1], L.routes, L.act, L.act_s, stream=stream)
+    E.experts_down(L.act, L.act_s, L.w[2], L.routes, L.y, L.ws[1], stream=stream)
+    stream.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want[:8], L.results()[:8]))
+
+
+@pytest.mark.parametrize("T", [4096, 4097])
+def test_route_blocks(E, T):
+    g = seeded(T)
+    check_route(E, torch.randn(T, 12, generator=g, device="cuda"), None, 2, True)
