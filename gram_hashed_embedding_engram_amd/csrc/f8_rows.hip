@@ -1,20 +1,43 @@
-// Products of 8-bit rows with 8-bit weights that carry an f32 scale per
-// 128 x 128 block.
+// Products of few 8-bit rows with 8-bit weights that carry an f32 scale per
+// 128 x 128 block: y[t][n] = sum_b ws[n/128][b] * (sum of block b's 128 products of
+// codes and row scales).
+//
+// One pass over the weights.  A wavefront loads 16 x 128 tiles of them straight
+// into a matrix instruction's registers (four lanes a row of 64 bytes, two such
+// loads a tile), multiplies all its rows of x with each, and joins the block's
+// scale as it adds the block's sum in f32.  K is split over the wavefronts of a
+// workgroup, which keeps enough loads in flight where there are few outputs; the
+// parts meet in LDS.  An expert's rows are found by a scan over the plan's spans.
+//
+// Bound by the weights' bytes.  One token of 4096 x 6144: 6.8 us, of which a launch
+// and two trips to memory are 4; sixteen of 6144 x 20480 (126 MB) 27 us; one token's
+// eight experts of 4096 x (2 x 2048) (134 MB) 28 us; 64 tokens over 256 of them, 164
+// met (2.75 GB), 444 us, 6.2 TB/s; their down projection (1.4 GB) 245 us, 5.6 TB/s.
+//
+// Measured on the way: loads marked non-temporal are slower (444 -> 500 us and
+// more: an expert's second tile and the next call find nothing in the caches); more
+// than two steps of loads ahead, or a fence between loads and products, takes
+// wavefronts away (64 tokens over 256 experts, a wavefront a tile: 575 us with four
+// steps and a fence, 497 without); one wavefront a tile instead of four 486 us.
 #include "f8.h"
 
 namespace engram {
 namespace {
 
-// Rows from which the tiles take over (f8_tiles.hip).  Both ways in us: T = 24,
-// 4096 x 4096 10 and 14; 32, 4096 x 20480 19 and 19; 48 23 and 19; 64 of 6144 x
-// 20480 45 and 36.
+// Rows from which the tiles take over (f8_tiles.hip).  Both ways in us, these
+// kernels first: T = 24, 4096 x 4096 9 and 14; 32, 4096 x 20480 19 and 19; 48 23 and
+// 19; 64 of 6144 x 20480 45 and 36.
 constexpr int64_t kMostRows = 32;
 // The same for an expert's rows on average.  Up, 64 experts of 4096 x 2048: 4 rows
-// 186 to 195 and 162 to 165, 16 rows 279 and 181; 16 experts, 2 rows 38 and 49.  Down,
-// 2048 x 4096: 4 rows 89 and 91, 16 rows 172 and 109.
-constexpr int64_t kUpRows = 4, kDownRows = 8;
+// 162 and 165, 8 rows 185 and 173; 256 of 2048 x 1024, 8 rows 194 and 183; 16
+// experts, 2 rows 38 and 49, 8 rows 57 and 65.  Down, 64 of 2048 x 4096: 4 rows 89
+// and 91, 8 rows 117 and 101; 256 experts, 8 rows 430 and 355.
+constexpr int64_t kTileRows = 8;
 constexpr int kFewSlots = 16, kFewWaves = 16;
-constexpr int64_t kFewUnits = 256, kManyUnits = 4096;
+// Wavefronts that share an expert's K.  Up, 1, 2, 4 and 8 of them: one token 50, 31,
+// 28 and 28 us, 64 tokens 486, 452, 444 and 458.  Down, 1, 2 and 4: 64 tokens 244, 245
+// and 250, three 40, 38 and 36, 8 tokens 84, 81 and 80.
+constexpr int kUpWaves = 4, kDownWaves = 2;
 
 __device__ __forceinline__ i32x8 operand(const u32x4 &a, const u32x4 &b)
 {
@@ -76,12 +99,11 @@ __device__ __forceinline__ void give(const F8Args &a, const f32x4 (&v)[4], int64
     }
 }
 
-// U: steps of 128 values whose loads go out together, within the registers
-// that two wavefronts a SIMD leave each
+// Steps of 128 values whose loads go out together: two, where the registers that
+// two wavefronts a SIMD leave each hold them.
 constexpr int steps_ahead(int rt, int mt)
 {
-    const int u = (190 - 4 * rt * mt) / (8 * rt + 9 * mt);
-    return u >= 4 ? 4 : u >= 2 ? 2 : 1;
+    return (190 - 4 * rt * mt) / (8 * rt + 9 * mt) >= 2 ? 2 : 1;
 }
 
 // A workgroup takes 16 * OT outputs (kUp: of each half) of 16 * MT rows; its W
@@ -90,7 +112,7 @@ template <F8Mode MODE, bool XF32, int OT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
 {
     constexpr int H = MODE == kUp ? 2 : 1, RT = OT * H, U = steps_ahead(RT, MT);
-    __shared__ f32x4 red[W > 1 ? W / 2 : 1][W > 1 ? MT : 1][W > 1 ? RT : 1][64];
+    __shared__ f32x4 red[W / 2][MT][RT][64];
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * OT, KB = a.K / 128, NB = (a.N + 127) / 128;
@@ -195,32 +217,27 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
             }
         }
         // the wavefronts' sums: the upper half's to the lower's, which leave theirs
-        if (W > 1) {
-            if (wv >= W / 2)
+        if (wv >= W / 2)
 #pragma unroll
-                for (int i = 0; i < RT; i++)
+            for (int i = 0; i < RT; i++)
 #pragma unroll
-                    for (int j = 0; j < MT; j++)
-                        red[wv - W / 2][j][i][lane] = acc[i][j];
-            __syncthreads();
-            if (wv < W / 2)
+                for (int j = 0; j < MT; j++)
+                    red[wv - W / 2][j][i][lane] = acc[i][j];
+        __syncthreads();
+        if (wv < W / 2)
 #pragma unroll
-                for (int i = 0; i < RT; i++)
+            for (int i = 0; i < RT; i++)
 #pragma unroll
-                    for (int j = 0; j < MT; j++) {
-                        acc[i][j] += red[wv][j][i][lane];
-                        red[wv][j][i][lane] = acc[i][j];
-                    }
-            __syncthreads();
-        }
+                for (int j = 0; j < MT; j++) {
+                    acc[i][j] += red[wv][j][i][lane];
+                    red[wv][j][i][lane] = acc[i][j];
+                }
+        __syncthreads();
         const auto sum = [&](int i, int j) {
-            f32x4 v = acc[i][j];
-            if (W > 1) {
-                v = red[0][j][i][lane];
+            f32x4 v = red[0][j][i][lane];
 #pragma unroll
-                for (int z = 1; z < W / 2; z++)
-                    v += red[z][j][i][lane];
-            }
+            for (int z = 1; z < W / 2; z++)
+                v += red[z][j][i][lane];
             return v;
         };
         // accumulator e of block (i, j) is output 16i + 4q + e, row 16j + l % 16; a
@@ -232,7 +249,7 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
 #pragma unroll
                 for (int i = 0; i < OT; i++) {
                     const int n = n0 + 16 * i + 4 * q;
-                    if (W > 1 && (j * OT + i) % W != wv)
+                    if ((j * OT + i) % W != wv)
                         continue;
                     const f32x4 v = sum(i, j);
                     if (r < rows && n < a.N)
@@ -241,19 +258,19 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
                 }
             } else {
                 static_assert(OT == 2, "an expert's outputs leave 32 at a time");
-                if (W > 1 && j % W != wv)
+                if (j % W != wv)
                     continue;
                 const f32x4 v[4] = {sum(0, j), sum(1, j), sum(RT - 2, j), sum(RT - 1, j)};
                 give<MODE>(a, v, first + r, r < rows, n0, q);
             }
         }
-        if (W > 1)
-            __syncthreads();                        // the next item's sums take their place
+        __syncthreads();                            // the next item's sums take their place
     }
 }
 
 // y[t] = sum_j weight[t][j] * product[t * k + j], in j's order; GROUP outputs
-// of a product share an exponent
+// of a product share an exponent.  Bound by the products' bytes: 4096 tokens of
+// eight experts, 4096 outputs (268 MB), 58 us, 4.6 TB/s.
 template <int GROUP>
 __global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v,
                                                   const int8_t *__restrict__ exps,
@@ -273,7 +290,7 @@ __global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v
             if ((uint32_t)ids[slot] >= (uint32_t)E)
                 continue;
             const h8 x = __builtin_bit_cast(h8, *(const u32x4 *)(v + slot * N + n));
-            const float f = exp2_int(exps[slot * groups + n / GROUP]) ;
+            const float f = exp2_int(exps[slot * groups + n / GROUP]);
 #pragma unroll
             for (int e = 0; e < 8; e++)
                 s[e] += (float)x[e] * f * weights[slot];
@@ -392,21 +409,6 @@ void launch_split(const F8Args &a, bool f32, int64_t tiles, bool last, const Lau
         dispatch(rows_kernel<MODE, false, OT, MT, W>, grid, dim3(64 * W), l, true, last, a);
 }
 
-// K is split over the wavefronts of a workgroup where one a tile would leave the
-// memory waiting.
-template <F8Mode MODE>
-void launch_experts(const F8Args &a, bool f32, bool last, const Launch &l)
-{
-    const int64_t tiles = f8_most_tiles(a.p, 16);
-    const int64_t units = tiles * ((a.N + 31) / 32);
-    if (units < kFewUnits && a.K >= 1024)
-        launch_split<MODE, 2, 1, 8>(a, f32, tiles, last, l);
-    else if (units < kManyUnits && a.K >= 512)
-        launch_split<MODE, 2, 1, 4>(a, f32, tiles, last, l);
-    else
-        launch_split<MODE, 2, 1, 1>(a, f32, tiles, last, l);
-}
-
 // Outputs a workgroup: at most 80 (whose sums and loads fill the registers), as
 // many as give every CU the same number of workgroups.  Every workgroup reads all
 // its rows' values, so fewer, wider ones are better.
@@ -439,9 +441,9 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
                           int64_t K, int64_t I, const Launch &l)
 {
     const F8Args a{p, x.x, x.s, w.w, w.s, h, hs, p.T, (int)K, (int)I};
-    if (p.slots / p.E >= kUpRows)
+    if (p.slots / p.E >= kTileRows)
         return launch_f8_tiles<kUp>(a, x.f32, true, l);
-    launch_experts<kUp>(a, x.f32, true, l);
+    launch_split<kUp, 2, 1, kUpWaves>(a, x.f32, f8_most_tiles(p, 16), true, l);
     return launch_status("engram experts_up kernel");
 }
 
@@ -450,7 +452,7 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
 // slots of 1024 x 1024, which make few workgroups, 12 and 10.
 static bool down_few(const Plan &p, int64_t N)
 {
-    return p.slots <= kFewSlots && (p.slots <= 4 || N >= 2048) && p.slots / p.E < kDownRows;
+    return p.slots <= kFewSlots && (p.slots <= 4 || N >= 2048) && p.slots / p.E < kTileRows;
 }
 
 size_t experts_down_bytes(const Plan &p, int64_t N)
@@ -478,14 +480,14 @@ int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uin
     const F8Args a{p, h.x, h.s, w.w, w.s, products, exps, p.T, (int)K, (int)N};
     const int64_t blocks = (p.T * (N / 8) + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-    if (p.slots / p.E >= kDownRows) {
+    if (p.slots / p.E >= kTileRows) {
         const int32_t rc = launch_f8_tiles<kDown>(a, h.f32, false, l);
         if (rc != ENGRAM_OK)
             return rc;
         dispatch(sum_kernel<64>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     } else {
-        launch_experts<kDown>(a, h.f32, false, l);
+        launch_split<kDown, 2, 1, kDownWaves>(a, h.f32, f8_most_tiles(p, 16), false, l);
         dispatch(sum_kernel<32>, grid, dim3(256), l, false, true, (const uint16_t *)products,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     }

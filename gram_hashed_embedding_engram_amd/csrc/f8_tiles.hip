@@ -1,6 +1,39 @@
 // Products of many 8-bit rows with 8-bit weights that carry an f32 scale per
 // 128 x 128 block: a plain projection, the experts' gated up projection, and
 // their down projection, as tiles of one matrix kernel.
+//
+// A workgroup's eight wavefronts take a tile of rows by a tile of weight rows, K in
+// blocks of 128.  One matrix instruction makes a 16 x 16 piece's sum over a block
+// from zero, and four multiply-adds join it to the piece's f32 sum under the block's
+// scale: half as many vector cycles as matrix cycles, beside which they run.  The
+// weights are the instruction's rows, so that a lane's sums are neighbouring outputs
+// of one token, and an expert's gate and up rows share a wavefront, so that
+// silu(gate) * up, the 32 values' largest and the codes need no other lane's sums.
+//
+// Data goes from memory to LDS without registers (buffer loads of 1 KiB that fill
+// eight rows of 128 bytes, pieces of 16 bytes swapped so that reads meet all banks),
+// a token's row by its slot in the plan.  Loads are counted, never waited for as a
+// whole: with 256 x 256 tiles a block and a half ahead, with smaller ones as many
+// blocks as LDS holds.  Rows' scales are loaded eight blocks at a time: a dword a row
+// and block asks L2 for as many lines as the codes do (507 -> 476 us below).
+//
+// Consecutive workgroups go to the XCDs in turn, so each XCD gets a contiguous run
+// of tiles: neighbours share weights and rows in its L2.
+//
+// 4096 tokens of 6144 x 20480 (1.03 TFLOP): 472 us, 2.18 PFLOP/s, where the same
+// without its loads takes 395 (without its barriers 375): matrix and vector
+// instructions at the clock that the power limit leaves; the library's product
+// without block scales takes 402.  A round of 256 tiles of 256 x 256 costs 1.8 us a
+// block and 8.6 once (the first loads, the stores of all CUs at once).  500 tokens of
+// 2048 x 5200: 14 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 14 us.
+// 4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 720 us, 1.53 PFLOP/s,
+// unevenly filled tiles and their borders; down 445 us, 58 of them the sum's.
+//
+// Tried and set aside: a workgroup a CU that loads on into its next tile under the
+// stores (a tile's fixed cost 8.6 -> 5.9 us, a block 1.82 -> 1.90, and static shares
+// of uneven tiles: up 724 -> 766); lines touched ahead for L2 (507 -> 655); explicit
+// turns of matrix, vector and LDS instructions (476 -> 500); raised wavefront
+// priority around the matrix instructions (489 -> 513).
 #include <type_traits>
 
 #include "f8.h"
@@ -9,7 +42,17 @@ namespace engram {
 namespace {
 
 constexpr int XCDS = 8;
+// Rows of an expert, on average, from which tiles of 256 and of 128 rows are taken.
+// Up, 64 experts of 4096 x 2048, in us: 128 rows 318 with 256-row tiles and 289 with
+// 128-row ones, 512 rows 722 and 754; 32 rows 208 with 128-row and 199 with 64-row
+// tiles, 48 rows 226 and 216, 64 rows 226 and 225; down, 64 rows 140 and 145, 128
+// rows 173 and 194.
 constexpr int64_t kRows8 = 192, kRows4 = 64;
+// What a block of K costs a round of one tile a CU, in 10 ns, for tiles of 256 x 256,
+// 128 x 256, 128 x 128, 64 x 128 and 64 x 64: the size with the least rounds times
+// cost is taken.  4096 tokens of 4096 x 4096: 67, 82, 102, 131, 208 us; 2048 of 4096
+// x 2048: 60, 38, 27, 35, 54; 1024 of 4096 x 1024: 59, 36, 25, 18, 15; 1000 of 4096 x
+// 10240: 62, 73, 74, 83, 131.
 constexpr int64_t kCost[5] = {190, 110, 65, 42, 30};
 
 typedef __attribute__((address_space(3))) void *lptr_t;
@@ -343,7 +386,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
             continue;
         }
         // products leave as f16 under a power of two per 64 of a row: half the bytes
-        // of f32 twice over memory, off by 2^-11 of themselves (or 2^-39 of the 64's
+        // of f32, twice over memory (577 -> 470 us for the prompt above), off by 2^-11 of themselves (or 2^-39 of the 64's
         // largest), an eighth of what the sum's own rounding to bf16 is off by
         int k16 = 0;
         if (MODE == kDown) {
