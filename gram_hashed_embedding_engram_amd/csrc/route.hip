@@ -8,8 +8,8 @@
 //   group_best best scores + bias, the k with the largest keys
 //
 // A wavefront takes a token: of NR experts a lane, expert e is value e % NR of lane
-// e / NR, and each of the k choices is one maximum over the wavefront's keys as
-// ordered integers.
+// e / NR.  A bound below the largest key, found by trial, leaves a few more
+// candidates than k, one a lane, and each lane counts those ahead of its own.
 // Choices are whole numbers, so they must not hang on how a score is rounded:
 // keys are formed in f32, whose error is bounded here, and a token where two
 // keys that are to be told apart lie nearer than that is taken again in 64 bits.
@@ -18,6 +18,12 @@
 // set one bit each in an expert's 64-bit word, so a token's place among them is
 // the number of bits below its own.  Calls of more tokens count per 64 tokens
 // and place in a second launch, which sums the counts before its own.
+//
+// 16384 tokens of 256 experts in 8 groups (17 MB): 27 us, of which the second
+// launch is 6; bound by the vector instructions of a token, some 450.  One token:
+// 6.2 us, a launch and a chain of some thousand cycles.  Each choice as a maximum of
+// its own took 54 us, 22 of them the few tokens taken again in 64 bits one choice
+// after the other; now the candidates alone are ranked again.
 #include <float.h>
 
 #include "experts.h"
@@ -30,43 +36,57 @@ constexpr int kWaves = 16;
 // counts of this many blocks are summed once more before the blocks are placed
 constexpr int kSegment = 64;
 constexpr int kMostBlocks = 256;        // placed from the counts alone
-constexpr int kSpare = 15;              // candidates for a token's choice beyond those needed
+// candidates for a token's choice beyond those needed: 7, 15 and 30 take 44, 33 and
+// 34 us for 16384 tokens of 256 experts (more trials, more to rank)
+constexpr int kSpare = 15;
 
 typedef unsigned long long u64;
 
-// Where in f32 two keys may stand in the other order than in exact arithmetic.
-// e^-x is off by (1.5 |x| + 2) 2^-24 of itself (the product with log2 e, the
-// instruction), which a sigmoid, whose slope times |x| is below 0.23, passes on
-// as less than 2^-22, and the sum and reciprocal add another; a softmax score,
-// below 1 and with |d| e^-d below 0.37, is off by 2^-20 (its sum of NR + 6
-// additions included); a key's own rounding is 2^-24 of it.  A group's sum holds
-// two keys.
-__device__ __forceinline__ bool near_keys(float a, float b, bool softmax, float terms)
+// Where in f32 two keys may stand in the other order than in exact arithmetic:
+// unit covers what their scores are off by together.  e^-x is off by (1.5 |x| + 2)
+// 2^-24 of itself (the product with log2 e, the instruction), which a sigmoid, whose
+// slope times |x| is below 0.23, passes on as less than 2^-22, and its sum and
+// reciprocal add another: 2^-20 for two.  A softmax score is off by (1.5 |d| + 2) 2^-24
+// of itself at a distance d from the largest logit, so by less than 2.6 * 2^-24 of the
+// largest score, and by NR + 9 roundings of the sum, the reciprocal and the product:
+// 2^-18 of the largest score for two, at NR = 16.  A key's own rounding is 2^-24 of
+// it; a group's sum holds two keys.
+__device__ __forceinline__ bool near_keys(float a, float b, float unit, float terms)
 {
-    return a - b <= terms * ((softmax ? 0x1p-19f : 0x1p-20f) + 0x1p-22f * fmaxf(fabsf(a), fabsf(b)));
+    return a - b <= terms * (unit + 0x1p-22f * fmaxf(fabsf(a), fabsf(b)));
 }
 
-// f32 in the order of its value as an unsigned number above 0; 0 = shut.  (-0,
-// which equals 0, becomes 0.)
+// Where the scores of logits a >= b may be one and the same number of 64 bits, or
+// f32's and theirs differ: next to each other, where a sigmoid is almost 1, or where
+// either vanishes.  (Equal logits have equal scores.)
+__device__ __forceinline__ bool near_logits(float a, float b, float top, bool softmax)
+{
+    return a != b && (a - b < 0x1p-40f || (!softmax && a > 16.0f) || b - top < -600.0f);
+}
+
+// f32 in the order of its value as an unsigned number.  (-0, which equals 0,
+// becomes 0.)
 __device__ __forceinline__ uint32_t ordered(float v)
 {
     const uint32_t u = __float_as_uint(v + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float unordered(uint32_t u)
+// The largest of the wavefront's values.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_max(float v)
 {
-    return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+    const int u = __float_as_int(v);
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(u, u, CTRL, ROWS, 0xF, false)));
 }
-
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
+__device__ __forceinline__ float wave_max(float v)
 {
-    v = max(v, (uint32_t)dpp_from<0x111, 0xF>((int)v));
-    v = max(v, (uint32_t)dpp_from<0x112, 0xF>((int)v));
-    v = max(v, (uint32_t)dpp_from<0x114, 0xF>((int)v));
-    v = max(v, (uint32_t)dpp_from<0x118, 0xF>((int)v));
-    v = max(v, (uint32_t)dpp_from<0x142, 0xA>((int)v));
-    v = max(v, (uint32_t)dpp_from<0x143, 0xC>((int)v));
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    v = dpp_max<0x111, 0xF>(v);
+    v = dpp_max<0x112, 0xF>(v);
+    v = dpp_max<0x114, 0xF>(v);
+    v = dpp_max<0x118, 0xF>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v)
@@ -136,89 +156,65 @@ struct Groups {
     bool lanes;
 };
 
-// The experts' scores and keys (score + bias, -inf where shut) in 64 bits.
-template <int NR>
-__device__ __forceinline__ void scores_f64(const Routing &a, const float (&x)[NR], const float (&b)[NR],
-                                           uint32_t open, double (&score)[NR], double (&key)[NR])
-{
-    const double low = -INFINITY;
-    if (a.softmax) {
-        double top = low;
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            if (open >> r & 1)
-                top = fmax(top, (double)x[r]);
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2)
-            top = fmax(top, __shfl_xor(top, m));
-        double sum = 0.0;
-#pragma unroll
-        for (int r = 0; r < NR; r++) {
-            score[r] = open >> r & 1 ? exp((double)x[r] - top) : 0.0;
-            sum += score[r];
-        }
-        sum = wave_sum_f64(sum);
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            score[r] = sum > 0.0 ? score[r] / sum : 0.0;
-    } else {
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            score[r] = open >> r & 1 ? 1.0 / (1.0 + exp(-(double)x[r])) : 0.0;
+// What a token's scores in 64 bits are made of.
+struct Exact {
+    double top, sum;                    // of a softmax
+    bool softmax;
+    __device__ __forceinline__ double score(double x) const
+    {
+        return softmax ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
     }
+};
+template <int NR>
+__device__ __forceinline__ Exact exact_of(const Routing &a, const float (&x)[NR])
+{
+    Exact e{0.0, 1.0, a.softmax};
+    if (a.softmax) {
+        float top = -FLT_MAX;
 #pragma unroll
-    for (int r = 0; r < NR; r++)
-        key[r] = open >> r & 1 ? score[r] + (double)b[r] : low;
+        for (int r = 0; r < NR; r++)
+            top = fmaxf(top, x[r]);
+        e.top = wave_max(top);
+        e.sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < NR; r++)
+            if (x[r] > -INFINITY)
+                e.sum += exp((double)x[r] - e.top);
+        e.sum = wave_sum_f64(e.sum);
+    }
+    return e;
 }
 
-// The groups kept by keys in 64 bits, a bit each.
+// The groups kept by sums in 64 bits, a bit each: `spread` lanes look through a
+// group's experts.
 template <int NR>
-__device__ __forceinline__ u64 groups_f64(const Routing &a, const Groups &gr, const double (&key)[NR])
+__device__ __forceinline__ u64 groups_f64(const Routing &a, const Groups &gr, const float (&x)[NR],
+                                          float *values)
 {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, g = lane / gr.spread, size = a.E / a.groups;
     const double low = -INFINITY;
-    double mine = low;                  // lane g: group g's sum
-    if (gr.lanes) {
-        double first = low, second = low;
+    const Exact exact = exact_of<NR>(a, x);
 #pragma unroll
-        for (int r = 0; r < NR; r++) {
-            second = fmax(second, fmin(first, key[r]));
-            first = fmax(first, key[r]);
+    for (int r = 0; r < NR; r++)
+        values[NR * lane + r] = x[r];
+    double first = low, second = low;
+    if (g < a.groups)
+        for (int i = g * size + (lane & (gr.spread - 1)); i < (g + 1) * size; i += gr.spread) {
+            const float v = values[i];
+            if (v == -INFINITY)
+                continue;
+            const double key = exact.score(v) + (a.bias ? (double)a.bias[i] : 0.0);
+            second = fmax(second, fmin(first, key));
+            first = fmax(first, key);
         }
-        for (int m = 1; m < gr.spread; m *= 2) {
-            const double f = __shfl_xor(first, m), s = __shfl_xor(second, m);
-            second = fmax(fmax(second, s), fmin(first, f));
-            first = fmax(first, f);
-        }
-        if (a.group_best > 1 && second > low)
-            first += second;
-        mine = __shfl(first, lane < a.groups ? lane * gr.spread : 0);
-    } else {
-        const int size = a.E / a.groups;
-        for (int g = 0; g < a.groups; g++) {
-            double sum = low;
-            int out = -1;
-            for (int z = 0; z < a.group_best; z++) {
-                double v = low;
-                int e = 1 << 30;
-#pragma unroll
-                for (int r = 0; r < NR; r++) {
-                    const int i = NR * lane + r;
-                    if (i / size == g && i != out && key[r] > v) {
-                        v = key[r];
-                        e = i;
-                    }
-                }
-                wave_best_f64(v, e);
-                if (v == low)
-                    break;
-                sum = z ? sum + v : v;
-                out = e;
-            }
-            if (lane == g)
-                mine = sum;
-        }
+    for (int m = 1; m < gr.spread; m *= 2) {
+        const double f = __shfl_xor(first, m), s = __shfl_xor(second, m);
+        second = fmax(fmax(second, s), fmin(first, f));
+        first = fmax(first, f);
     }
+    if (a.group_best > 1 && second > low)
+        first += second;
+    const double mine = __shfl(first, lane < a.groups ? lane * gr.spread : 0);   // lane g: group g's sum
     int ahead = 0;
     for (int h = 0; h < a.groups; h++) {
         const double v = __shfl(mine, h);
@@ -296,32 +292,15 @@ __device__ __forceinline__ float quotient(float a, float b)
 
 // n candidates, lane i's expert e: in the order of their keys in 64 bits.
 template <int NR>
-__device__ __forceinline__ int rank_f64(const Routing &a, const float (&x)[NR], uint32_t open, float *values,
+__device__ __forceinline__ int rank_f64(const Routing &a, const float (&x)[NR], float *values,
                                         int n, int e)
 {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int r = 0; r < NR; r++)
         values[NR * lane + r] = x[r];
-    const double v = e >= 0 ? values[e] : 0.0, bias = e >= 0 ? a.bias[e] : 0.0;
-    double score;
-    if (a.softmax) {
-        float top = -FLT_MAX;
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            if (open >> r & 1)
-                top = fmaxf(top, x[r]);
-        top = unordered(wave_max_u32(ordered(top)));
-        double sum = 0.0;
-#pragma unroll
-        for (int r = 0; r < NR; r++)
-            if (open >> r & 1)
-                sum += exp((double)x[r] - (double)top);
-        score = exp(v - (double)top) / wave_sum_f64(sum);
-    } else {
-        score = 1.0 / (1.0 + exp(-v));
-    }
-    const double key = score + bias;
+    const Exact exact = exact_of<NR>(a, x);
+    const double key = e >= 0 ? exact.score(values[e]) + (double)a.bias[e] : 0.0;
     int rank = 0;
     for (int i = 0; i < n; i++) {
         const double o = __shfl(key, i);
@@ -333,30 +312,27 @@ __device__ __forceinline__ int rank_f64(const Routing &a, const float (&x)[NR], 
     return lane < n ? __float_as_int(values[lane]) : -1;
 }
 
-// One token; lane j < k returns its j-th expert and weight.  values: the
-// wavefront's own LDS, 64 * NR floats (128 at least).  slack: how far below the
-// largest key the last token's bound was.  gbit: the lane that speaks for each
-// expert's group (where groups are not whole lanes).
+// One token; lane j < k returns its j-th expert and weight.  x is -inf where an
+// expert is shut.  values: the wavefront's own LDS, 64 * NR floats (128 at least).
+// slack: how far below the largest key the last token's bound was.  gbit: the lane
+// that speaks for each expert's group (where groups are not whole lanes).
 template <int NR>
 __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const float (&x)[NR],
-                                       const float (&b)[NR], uint32_t open, const int (&gbit)[NR],
-                                       float *values, float &slack, int &id, float &weight)
+                                       const float (&b)[NR], const int (&gbit)[NR], float *values,
+                                       float &slack, int &id, float &weight)
 {
     const int lane = threadIdx.x & 63;
-    const uint32_t softmax_open = open;              // groups left out still count in the sum
-    float score[NR];
-    uint32_t key[NR];
-    float top = 0.0f, all = 0.0f;
+    float score[NR], key[NR];
+    float top = 0.0f, all = 0.0f, unit = 0x1p-20f;
     if (a.softmax) {
         top = -FLT_MAX;
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            if (open >> r & 1)
-                top = fmaxf(top, x[r]);
-        top = unordered(wave_max_u32(ordered(top)));
+            top = fmaxf(top, x[r]);
+        top = wave_max(top);
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-            score[r] = open >> r & 1 ? fast_exp(x[r] - top) : 0.0f;
+            score[r] = fast_exp(x[r] - top);
             all += score[r];
         }
         all = wave_sum(all);
@@ -364,28 +340,31 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
 #pragma unroll
         for (int r = 0; r < NR; r++)
             score[r] *= inv;
+        unit = 0x1p-18f * inv;
     } else {
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            score[r] = open >> r & 1 ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[r])) : 0.0f;
+            score[r] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[r]));
     }
 #pragma unroll
     for (int r = 0; r < NR; r++)
-        key[r] = !(open >> r & 1) ? 0u : ordered(a.bias ? score[r] + b[r] : x[r]);
+        key[r] = !a.bias || x[r] == -INFINITY ? x[r] : score[r] + b[r];
     if (a.groups > 1) {
         float first = -INFINITY, second = -INFINITY;
         const int g = lane / gr.spread;
+        // one best score without a bias: the largest logits say which is more
+        const bool logits = !a.bias && a.group_best == 1;
         if (gr.lanes) {
 #pragma unroll
             for (int r = 0; r < NR; r++) {
-                const float v = open >> r & 1 ? score[r] + b[r] : -INFINITY;
+                const float v = logits || x[r] == -INFINITY ? x[r] : score[r] + b[r];
                 second = fmaxf(second, fminf(first, v));
                 first = fmaxf(first, v);
             }
         } else {
 #pragma unroll
             for (int r = 0; r < NR; r++)
-                values[NR * lane + r] = open >> r & 1 ? score[r] + b[r] : -INFINITY;
+                values[NR * lane + r] = logits || x[r] == -INFINITY ? x[r] : score[r] + b[r];
             const int size = a.E / a.groups;
             if (g < a.groups)
                 for (int i = lane & (gr.spread - 1); i < size; i += gr.spread) {
@@ -404,51 +383,53 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
         bool keep = in && ahead < a.top_groups;
         u64 kept = __ballot(keep);
         const u64 last = __ballot(in && ahead == a.top_groups - 1), next = __ballot(in && ahead == a.top_groups);
-        if (next && near_keys(lane_value(sum, __builtin_ctzll(last)), lane_value(sum, __builtin_ctzll(next)),
-                              a.softmax, 2.0f)) {
-            double s64[NR], k64[NR];
-            scores_f64<NR>(a, x, b, open, s64, k64);
-            const u64 by_group = groups_f64<NR>(a, gr, k64);
+        const float u = next ? lane_value(sum, __builtin_ctzll(last)) : 0.0f;
+        const float v = next ? lane_value(sum, __builtin_ctzll(next)) : 0.0f;
+        if (next && (logits ? near_logits(u, v, top, a.softmax) : near_keys(u, v, unit, 2.0f))) {
+            const u64 by_group = groups_f64<NR>(a, gr, x, values);
             keep = g < a.groups && (by_group >> g & 1);
             kept = __ballot(keep);
         }
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            if (gr.lanes ? !keep : !(kept >> gbit[r] & 1)) {
-                key[r] = 0u;
-                open &= ~(1u << r);
-            }
+            if (gr.lanes ? !keep : !(kept >> gbit[r] & 1))
+                key[r] = -INFINITY;
     }
     // The candidates: keys not below a bound that leaves more than k of them (or
-    // all) and at most 64, found by trial from where the last token's was.
-    uint32_t best = key[0];
+    // all that there are) and at most kSpare besides, found by trial from where the
+    // last token's was.
+    float high = key[0];
 #pragma unroll
     for (int r = 1; r < NR; r++)
-        best = max(best, key[r]);
-    best = wave_max_u32(best);
-    const float high = unordered(best);
+        high = fmaxf(high, key[r]);
+    high = wave_max(high);
     int total = 0;
 #pragma unroll
     for (int r = 0; r < NR; r++)
-        total += __popcll(__ballot(key[r] != 0u));
+        total += __popcll(__ballot(key[r] > -INFINITY));
     const int want = min(a.k + 1, total), most = want + kSpare;
     int n = total;
-    uint32_t bound = 1u;
+    float bound = -FLT_MAX;
     for (int turn = 0; n > most && turn < 16; turn++) {
-        bound = ordered(high - slack);
+        bound = high - slack;
         n = 0;
 #pragma unroll
         for (int r = 0; r < NR; r++)
             n += __popcll(__ballot(key[r] >= bound));
         if (n >= want && n <= most)
             break;
-        slack = fminf(fmaxf(slack * (n < want ? 1.75f : 0.75f), 0x1p-20f), 0x1p20f);
+        slack = fminf(fmaxf(slack * (n < want ? 1.5f : n > 2 * most ? 0.5f : 0.75f), 0x1p-20f), 0x1p20f);
         n = 64 * NR + 1;
     }
-    uint32_t mine = 0u;
+    float mine = -INFINITY;
     int at = -1;
     bool exact = false;
     if (n <= 64) {
+        struct Entry {
+            float key;
+            int id;
+        };
+        Entry *const list = (Entry *)values;
         // to the lanes, in the experts' order
         int before = 0;
 #pragma unroll
@@ -456,29 +437,29 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
             before += lanes_below(__ballot(key[r] >= bound));
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            if (key[r] >= bound) {
-                values[before] = __uint_as_float(key[r]);
-                values[64 + before++] = __int_as_float(NR * lane + r);
-            }
-        const uint32_t v = lane < n ? __float_as_uint(values[lane]) : 0u;
-        const int e = lane < n ? __float_as_int(values[64 + lane]) : -1;
-        const int rank = rank_of(v, lane, n, 1);
+            if (key[r] >= bound)
+                list[before++] = Entry{key[r], NR * lane + r};
+        Entry own{-INFINITY, -1};
+        if (lane < n)
+            own = list[lane];
+        const int rank = rank_of(ordered(own.key), lane, n, 1);
         // in the order of their keys
         if (lane < n) {
-            values[rank] = __uint_as_float(v);
-            values[64 + rank] = __int_as_float(e);
+            list[rank] = own;
+            own = list[lane];
         }
-        mine = lane < n ? __float_as_uint(values[lane]) : 0u;
-        at = lane < n ? __float_as_int(values[64 + lane]) : -1;
+        mine = own.key;
+        at = own.id;
         if (a.bias) {
-            const float own = unordered(mine);
-            const uint32_t next = (uint32_t)dpp_from<0x130, 0xF>((int)mine);     // of lane j + 1
-            if (__ballot(lane < a.k && next != 0u && near_keys(own, unordered(next), a.softmax, 1.0f))) {
+            const int low = __float_as_int(-INFINITY);
+            const float next = __int_as_float(                       // of lane j + 1
+                __builtin_amdgcn_update_dpp(low, __float_as_int(mine), 0x130, 0xF, 0xF, false));
+            if (__ballot(lane < a.k && next > -INFINITY && near_keys(mine, next, unit, 1.0f))) {
                 // told apart in 64 bits, if nobody outside can stand among the first k
-                const float least = lane_value(own, n - 1), kth = lane_value(own, min(a.k, n) - 1);
-                exact = n < total && near_keys(kth, least, a.softmax, 1.0f);
+                const float least = lane_value(mine, n - 1), kth = lane_value(mine, min(a.k, n) - 1);
+                exact = n < total && near_keys(kth, least, unit, 1.0f);
                 if (!exact)
-                    at = rank_f64<NR>(a, x, softmax_open, values, n, at);
+                    at = rank_f64<NR>(a, x, values, n, at);
             }
         }
     } else {
@@ -499,10 +480,12 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
     const float sum = wave_sum(s);
     if (exact || (sum < 0x1p-90f && __ballot(id >= 0))) {
         double s64[NR], k64[NR];
-        scores_f64<NR>(a, x, b, softmax_open, s64, k64);
+        const Exact e64 = exact_of<NR>(a, x);
 #pragma unroll
-        for (int r = 0; r < NR; r++)
-            k64[r] = !(open >> r & 1) ? -INFINITY : a.bias ? k64[r] : (double)x[r];
+        for (int r = 0; r < NR; r++) {
+            s64[r] = x[r] > -INFINITY ? e64.score(x[r]) : 0.0;
+            k64[r] = key[r] == -INFINITY ? -INFINITY : a.bias ? s64[r] + (double)b[r] : (double)x[r];
+        }
         const Choice c = choose_f64<NR>(a, s64, k64);
         id = lane < a.k ? c.id : -1;
         const double sc = id >= 0 ? c.score : 0.0;
@@ -540,7 +523,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(Routing a, Groups gr
     __shared__ int32_t ids_s[kBlockTokens * kMaxChosen];
     __shared__ int start[64 * NR];
     __shared__ int part[kWaves];
-    __shared__ float values[kWaves][NR > 1 ? 64 * NR : 128];
+    __shared__ __attribute__((aligned(8))) float values[kWaves][NR > 1 ? 64 * NR : 128];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t0 = blockIdx.x * block;
@@ -548,49 +531,50 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(Routing a, Groups gr
         mask[i] = 0;
     float b[NR];
     int gbit[NR];
-    uint32_t known = 0;
+    // a class of f32: NaN and +inf, or the finite ones
+    constexpr int kOdd = 0x203, kFinite = 0x1F8;
+    bool known[NR];
     bool odd = false;
     const auto logits = [&](int t, float (&x)[NR]) {
+        const int64_t row = (int64_t)t * a.stride;
 #pragma unroll
         for (int r = 0; r < NR; r++) {
             const int e = NR * lane + r;
-            const int64_t at = (int64_t)t * a.stride + e;
             x[r] = -INFINITY;
             if (e < a.E)
-                x[r] = BF16 ? bf16_lo(((const uint16_t *)a.logits)[at]) : ((const float *)a.logits)[at];
+                x[r] = BF16 ? bf16_lo(((const uint16_t *)a.logits + row)[e])
+                            : ((const float *)a.logits + row)[e];
         }
     };
     const int t1 = min(t0 + block, a.T);
-    float slack = 0.5f, ahead[NR];
+    float slack = a.bias ? 0.3f : 1.4f, ahead[NR];   // (of scores, of normal logits)
     if (t0 + wv < t1)
         logits(t0 + wv, ahead);
 #pragma unroll
     for (int r = 0; r < NR; r++) {
         const int e = NR * lane + r;
         b[r] = a.bias && e < a.E ? a.bias[e] : 0.0f;
-        odd |= b[r] > FLT_MAX || b[r] != b[r];
-        known |= (uint32_t)(e < a.E && fabsf(b[r]) <= FLT_MAX) << r;
+        odd |= __builtin_amdgcn_classf(b[r], kOdd);
+        known[r] = e < a.E && __builtin_amdgcn_classf(b[r], kFinite);
         gbit[r] = gr.lanes || e >= a.E ? 0 : e / (a.E / a.groups) * gr.spread;
     }
     __syncthreads();
     for (int t = t0 + wv; t < t1; t += kWaves) {
         float x[NR];
-        uint32_t open = 0;
 #pragma unroll
         for (int r = 0; r < NR; r++) {
-            x[r] = ahead[r];
-            odd |= x[r] > FLT_MAX || x[r] != x[r];
-            open |= (uint32_t)((known >> r & 1) && fabsf(x[r]) <= FLT_MAX) << r;
+            odd |= __builtin_amdgcn_classf(ahead[r], kOdd);
+            x[r] = known[r] && __builtin_amdgcn_classf(ahead[r], kFinite) ? ahead[r] : -INFINITY;
         }
         if (t + kWaves < t1)
             logits(t + kWaves, ahead);
         int id;
         float weight;
-        choose<NR>(a, gr, x, b, open, gbit, values[wv], slack, id, weight);
+        choose<NR>(a, gr, x, b, gbit, values[wv], slack, id, weight);
         if (lane < a.k) {
-            const int64_t slot = (int64_t)t * a.k + lane;
-            a.ids[slot] = id;
-            a.weights[slot] = weight;
+            const int64_t first = (int64_t)t * a.k;
+            (a.ids + first)[lane] = id;
+            (a.weights + first)[lane] = weight;
             ids_s[(t - t0) * a.k + lane] = id;
             if (id >= 0)
                 atomicOr(&mask[id], 1ull << (t - t0));
@@ -706,9 +690,15 @@ __global__ __launch_bounds__(64 * kWaves) void place_kernel(Routing a, const uin
 }
 
 int pitch_of(int32_t E) { return (E + 15) / 16 * 16; }
-// A block's tokens: one a wavefront where that makes kMostBlocks blocks at most,
-// and all of a call's that one block holds (one launch).
-int64_t block_of(int64_t T) { return T > kBlockTokens && T <= kMostBlocks * kWaves ? kWaves : kBlockTokens; }
+// A block's tokens: a multiple of one a wavefront that makes kMostBlocks blocks at
+// most, and all of a call's that one block holds (one launch).  777 tokens in blocks
+// of 16 and of 64: 9 and 18 us; 16384 in blocks of 32 and of 64: 42 and 30 us, whose
+// blocks each add up the counts of all.
+int64_t block_of(int64_t T)
+{
+    const int64_t n = (T + kMostBlocks * kWaves - 1) / (kMostBlocks * kWaves) * kWaves;
+    return T <= kBlockTokens || n > kBlockTokens ? kBlockTokens : n;
+}
 int64_t blocks_of(int64_t T) { return (T + block_of(T) - 1) / block_of(T); }
 size_t counts_bytes(int64_t T, int32_t E) { return ((size_t)(blocks_of(T) * pitch_of(E)) + 255) & ~(size_t)255; }
 
