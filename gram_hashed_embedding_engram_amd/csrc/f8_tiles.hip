@@ -25,7 +25,7 @@
 // instructions at the clock that the power limit leaves; the library's product
 // without block scales takes 402.  A round of 256 tiles of 256 x 256 costs 1.8 us a
 // block and 8.6 once (the first loads, the stores of all CUs at once).  500 tokens of
-// 2048 x 5200: 14 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 14 us.
+// 2048 x 5200: 13.5 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 14 us.
 // 4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 720 us, 1.53 PFLOP/s,
 // unevenly filled tiles and their borders; down 445 us, 58 of them the sum's.
 //
@@ -73,6 +73,9 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p)
 // scales of the rows for this many blocks of K are loaded at once: a dword a row
 // and block, loaded block by block, would ask for as many lines as the codes
 constexpr int SB = 8;
+// dwords from eight rows' scales to the next eight's: the halves of sixteen rows are
+// read from different banks (500 tokens of 2048 x 5200 14.3 -> 13.5 us)
+constexpr int SG = 8 * SB + 4;
 
 // the same for weight rows, which are read 4 * RUN * (l / 4) + l % 4
 template <int RUN>
@@ -92,7 +95,7 @@ struct Stage {
 template <int TB, int WB, int S>
 struct Shared {
     Stage<TB, WB> stage[S];
-    uint32_t xs[2][32 * TB * SB];
+    uint32_t xs[2][4 * TB * SG];
 };
 
 // A tile of 32 * TB rows and 64 * WB weight rows (kUp: half of them the gate's,
@@ -211,7 +214,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 #pragma unroll
         for (int j = 0; j < LT; j++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rs, (lptr_t)&sh.xs[part & 1][(wave * (BM / 8) + 8 * j) * SB], 4,
+                rs, (lptr_t)&sh.xs[part & 1][(wave * LT + j) * SG], 4,
                 s_at[j] + 4 * SB * part, 0, 0, 0);
     };
     const auto issue_x = [&](int kt, Stage &s) {
@@ -251,16 +254,17 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         for (int i = 0; i < WB; i++)
             wf[i] = fragment(w0, w1, i / RUN * 32 + i % RUN * 4);
     };
+    const int xs_at = (2 * th + (r16 >> 3)) * SG + (r16 & 7) * SB;
     // blocks J0 .. J0 + NJ - 1 of the wavefront's tokens
     const auto some = [&](int kt, const Stage &s, auto j0, auto nj) {
         const char *t0 = (const char *)s.tok + th * 16 * 128 + at0, *t1 = t0 - at0 + at1;
-        const char *xs0 = (const char *)&sh.xs[kt / SB & 1][(th * 16 + r16) * SB + kt % SB] + (XF32 ? 0 : q);
+        const char *xs0 = (const char *)&sh.xs[kt / SB & 1][xs_at + kt % SB] + (XF32 ? 0 : q);
         constexpr int J0 = decltype(j0)::value, NJ = decltype(nj)::value;
 #pragma unroll
         for (int j = J0; j < J0 + NJ; j++) {
             const i32x8 xf = fragment(t0, t1, 32 * j);
-            const uint32_t xs = XF32 ? *(const uint32_t *)(xs0 + 128 * SB * j)
-                                     : *(const uint8_t *)(xs0 + 128 * SB * j);
+            const uint32_t xs = XF32 ? *(const uint32_t *)(xs0 + 16 * SG * j)
+                                     : *(const uint8_t *)(xs0 + 16 * SG * j);
             float g[H];
 #pragma unroll
             for (int h = 0; h < H; h++)
