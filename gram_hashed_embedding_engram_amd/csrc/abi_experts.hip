@@ -145,6 +145,12 @@ int32_t engram_route(const engram_routes *routes, const void *d_logits, int32_t 
               !overlap(d_logits, read, routes->d_order, slots) &&
               !overlap(d_logits, read, routes->d_offsets, 4 * (uint64_t)(E + 1)),
           ENGRAM_E_ARG, "engram route: the routes overlap the logits");
+    CHECK(need == 0 || (!overlap(d_logits, read, d_ws, need) &&
+                        !overlap(routes->d_ids, slots, d_ws, need) &&
+                        !overlap(routes->d_weights, slots, d_ws, need) &&
+                        !overlap(routes->d_order, slots, d_ws, need) &&
+                        !overlap(routes->d_offsets, 4 * (uint64_t)(E + 1), d_ws, need)),
+          ENGRAM_E_ARG, "engram route: the workspace overlaps the logits or the routes");
     const Routing r{d_logits, d_bias, logits_stride, factor, (int32_t)T, (int32_t)E,
                     routes->chosen, groups, top_groups, group_best, logits_bf16 != 0, softmax != 0,
                     renorm != 0, routes->d_ids, routes->d_offsets, routes->d_order, routes->d_err,
@@ -207,6 +213,8 @@ int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const
               !overlap(d_x_scales, scale_bytes(T, K, x_f32 != 0), d_h, hb) &&
               !overlap(d_x_scales, scale_bytes(T, K, x_f32 != 0), d_h_scales, sb),
           ENGRAM_E_ARG, "engram experts_up: h or its scales overlap x or its scales");
+    CHECK(!overlap(d_h, hb, d_h_scales, sb), ENGRAM_E_ARG,
+          "engram experts_up: h overlaps its scales");
     return launch_experts_up(plan_of(routes), Rows8{d_x, d_x_scales, x_f32 != 0},
                              Blocks8{d_w, d_w_scales}, d_h, d_h_scales, K, I, on(stream));
 }
@@ -248,6 +256,11 @@ int32_t engram_experts_down(const engram_routes *routes, const uint8_t *d_h,
     CHECK(!overlap(d_h, (uint64_t)p.slots * (uint64_t)K, d_y, out) &&
               !overlap(d_h_scales, scale_bytes(p.slots, K, h_f32 != 0), d_y, out),
           ENGRAM_E_ARG, "engram experts_down: y overlaps h or its scales");
+    CHECK(need == 0 ||
+              (!overlap(d_h, (uint64_t)p.slots * (uint64_t)K, d_ws, need) &&
+               !overlap(d_h_scales, scale_bytes(p.slots, K, h_f32 != 0), d_ws, need) &&
+               !overlap(d_y, out, d_ws, need)),
+          ENGRAM_E_ARG, "engram experts_down: the workspace overlaps h, its scales or y");
     return launch_experts_down(p, Rows8{d_h, d_h_scales, h_f32 != 0}, Blocks8{d_w, d_w_scales}, d_y,
                                K, N, d_ws, on(stream));
 }

@@ -579,8 +579,8 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
  * projection with the weighted sum over a token's experts
  * (engram_experts_down).  engram_project_f8 is the plain product with weights of
  * the same kind.  As above none of them allocates, keeps state between calls or
- * lets the order of atomics show: equal inputs give equal bits; outputs do not
- * overlap inputs.
+ * lets the order of atomics show: equal inputs give equal bits; outputs and
+ * workspaces overlap nothing else of the call.
  *
  * Weights are e4m3 codes [N][K] with one f32 scale per block of 128 x 128,
  * [ceil(N/128)][K/128]: a weight is its code times its block's scale (whatever
@@ -589,14 +589,17 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
  *               (engram_add_norm's and engram_experts_up's outputs; 255 is NaN);
  *   x_f32 != 0: [rows][K/128] f32.
  * Within a block of 128 the matrix instruction takes the products of eight
- * neighbours together, as engram_project_w4's does; blocks are added in f32. */
+ * neighbours together, as engram_project_w4's does (which moves a block's sum by
+ * about 2^-16 of its size for normal values); blocks are added in f32.  With
+ * x_f32 a row's scale times a block's has to lie within f32's range. */
 #define ENGRAM_F8_BLOCK 128
 
 /* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ).
  *   d_x, d_x_scales  T rows;  d_w, d_w_scales  weights;  d_y [T][N] bf16.
  * K a positive multiple of 128 up to 2^20, N a positive multiple of 16 up to
- * 2^24, T up to 2^22.  d_x, d_w and d_y 16-byte, scales 4-byte aligned.
- * T = 0 is a no-op. */
+ * 2^24, T up to 2^22; ENGRAM_E_RANGE where the output is 2^23 tiles or more (of
+ * 256 x 256 where there are many).  d_x, d_w and d_y 16-byte, scales 4-byte
+ * aligned.  T = 0 is a no-op. */
 int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_f32,
                           const uint8_t *d_w, const float *d_w_scales, uint16_t *d_y, int64_t T,
                           int64_t K, int64_t N, void *stream);
@@ -611,9 +614,11 @@ int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_
  *             expert e, ascending; rows past d_offsets[experts] belong to none;
  *   d_err     nullable.
  * engram_route writes all but d_err; the products read them.  A plan made
- * elsewhere may order an expert's slots as it likes, each slot at most once.
- * Offsets outside 0..tokens*chosen or falling, and slots out of range, set
- * ENGRAM_DEVERR_ROUTE; their rows are not computed. */
+ * elsewhere may order an expert's slots as it likes: each slot with an expert is in
+ * it once, under that expert.  Offsets outside 0..tokens*chosen or falling, and
+ * slots out of range, set ENGRAM_DEVERR_ROUTE; their rows are not computed, and
+ * engram_experts_down's y is unspecified for tokens with an expert whose slot the
+ * plan lacks or holds twice. */
 typedef struct engram_routes {
     int32_t experts;
     int32_t chosen;
@@ -652,12 +657,13 @@ int32_t engram_route(const engram_routes *routes, const void *d_logits, int32_t 
 /* h[p][i] = silu(g) * u for every row p of the plan, with g = x[t] . w[e][0][i]
  * and u = x[t] . w[e][1][i] of its expert e and its slot's token t; h leaves as
  * e4m3 codes under a power of two per 32 values (engram_add_norm's kind), from
- * f32.
+ * f32 (a g or u past f32's range may make its h NaN).
  *   d_x, d_x_scales  tokens rows of K values;
  *   d_w     [experts][2][I][K];  d_w_scales [experts][2][I/128][K/128];
  *   d_h     [tokens*chosen][I];  d_h_scales [tokens*chosen][I/32].
  * Rows of h past the plan's are left as they are.  K and I multiples of 128 up
- * to 2^20, tokens * K below 2^31.  d_x, d_w and d_h 16-byte, scales 4-byte
+ * to 2^20, tokens * K below 2^31, and the tiles that the experts' rows of such a
+ * call can make (128 values of h by 256 rows where there are many) below 2^23.  d_x, d_w and d_h 16-byte, scales 4-byte
  * aligned. */
 int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const void *d_x_scales,
                           int32_t x_f32, const uint8_t *d_w, const float *d_w_scales, uint8_t *d_h,
@@ -670,10 +676,11 @@ int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const
  *   d_y     [tokens][N] bf16;
  *   d_ws    (256-byte aligned, caller-owned) of engram_experts_down_bytes bytes;
  *           may be NULL where that is 0.  Calls that share it must not overlap.
- * Where experts have many rows a slot's products pass through d_ws as f16 under a
- * power of two per 64 outputs (off by 2^-11 of themselves, an eighth of what the
- * result's own rounding is off by); sums are f32, in the slots' order.
- * K a multiple of 128 up to 2^20, N of 16 up to 2^24.  d_h, d_w and d_y 16-byte,
+ * Where d_ws is used a slot's products pass through it as f16 under a power of two
+ * per 32 or 64 outputs (off by 2^-11 of themselves, an eighth of what the result's
+ * own rounding is off by); sums are f32, in the slots' order.
+ * K a multiple of 128 up to 2^20, N of 16 up to 2^24, and tiles (256 x 256 where
+ * experts have many rows) below 2^23, as for engram_experts_up.  d_h, d_w and d_y 16-byte,
  * scales 4-byte aligned. */
 size_t engram_experts_down_bytes(const engram_routes *routes, int64_t N);
 int32_t engram_experts_down(const engram_routes *routes, const uint8_t *d_h,

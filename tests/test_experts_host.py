@@ -149,6 +149,19 @@ def test_outputs_over_inputs_are_refused(L):
         assert route(L, routes_c(**{name: FAKE + 64})) == E.E_ARG and "overlap" in E.last_error()
 
 
+def test_workspaces_over_other_arrays_are_refused(L):
+    """A workspace that reaches into the rows, the results or the routes, and h
+    that reaches into its scales."""
+    many = routes_c(tokens=1000)
+    need = L.engram_route_bytes(ctypes.byref(many))
+    for at in (FAKE, IDS, WTS, OFF, ORD):
+        assert route(L, many, ws=at, nws=need) == E.E_ARG and "workspace overlaps" in E.last_error()
+    need = L.engram_experts_down_bytes(ctypes.byref(many), 64)
+    for at in (FAKE, SC, OUT):
+        assert down(L, many, space=at, n=need) == E.E_ARG and "workspace overlaps" in E.last_error()
+    assert up(L, hs=OUT + 64) == E.E_ARG and "overlaps" in E.last_error()
+
+
 def test_empty_calls_touch_nothing(L):
     none = routes_c(tokens=0, d_ids=None, d_weights=None, d_offsets=None, d_order=None)
     assert f8(L, T=0, x=None, xs=None, w=None, ws=None, y=None) == E.OK
