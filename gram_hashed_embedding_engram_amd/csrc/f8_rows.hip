@@ -25,8 +25,8 @@ namespace engram {
 namespace {
 
 // Rows from which the tiles take over (f8_tiles.hip).  Both ways in us, these
-// kernels first: T = 24, 4096 x 4096 9 and 14; 32, 4096 x 20480 19 and 19; 48 23 and
-// 19; 64 of 6144 x 20480 45 and 36.
+// kernels first: T = 17, 4096 x 4096 8.5 and 12.4; 32 9.7 and 12.5; 24, 6144 x 20480
+// 28.6 and 30.3; 48 50 and 33; 32, 4096 x 20480 18.5 and 17.5; 40, 4096 x 14336 27 and 13.
 constexpr int64_t kMostRows = 32;
 // The same for an expert's rows on average.  Up, 64 experts of 4096 x 2048: 4 rows
 // 162 and 165, 8 rows 185 and 173; 256 of 2048 x 1024, 8 rows 194 and 183; 16

@@ -13,9 +13,12 @@
 // Data goes from memory to LDS without registers (buffer loads of 1 KiB that fill
 // eight rows of 128 bytes, pieces of 16 bytes swapped so that reads meet all banks),
 // a token's row by its slot in the plan.  Loads are counted, never waited for as a
-// whole: with 256 x 256 tiles a block and a half ahead, with smaller ones as many
-// blocks as LDS holds.  Rows' scales are loaded eight blocks at a time: a dword a row
-// and block asks L2 for as many lines as the codes do (507 -> 476 us below).
+// whole: with 256 x 256 tiles a block and a half ahead; with smaller ones one or two
+// blocks ahead, which leaves LDS for a second workgroup on the CU (1000 tokens of
+// 6144 x 20480 in tiles of 128 x 128: 176 us with four stages, 151 with two; 500 of
+// 4096 x 4096 in tiles of 64 x 64: 25 us with five or more, 18 with three).  Rows'
+// scales are loaded eight blocks at a time: a dword a row and block asks L2 for as
+// many lines as the codes do (507 -> 476 us below).
 //
 // Consecutive workgroups go to the XCDs in turn, so each XCD gets a contiguous run
 // of tiles: neighbours share weights and rows in its L2.
@@ -25,15 +28,17 @@
 // instructions at the clock that the power limit leaves; the library's product
 // without block scales takes 402.  A round of 256 tiles of 256 x 256 costs 1.8 us a
 // block and 8.6 once (the first loads, the stores of all CUs at once).  500 tokens of
-// 2048 x 5200: 13.5 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 14 us.
-// 4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 720 us, 1.53 PFLOP/s,
+// 2048 x 5200: 12.7 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 12.9 us.
+// 4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 715 us, 1.54 PFLOP/s,
 // unevenly filled tiles and their borders; down 445 us, 58 of them the sum's.
 //
 // Tried and set aside: a workgroup a CU that loads on into its next tile under the
 // stores (a tile's fixed cost 8.6 -> 5.9 us, a block 1.82 -> 1.90, and static shares
-// of uneven tiles: up 724 -> 766); lines touched ahead for L2 (507 -> 655); explicit
-// turns of matrix, vector and LDS instructions (476 -> 500); raised wavefront
-// priority around the matrix instructions (489 -> 513).
+// of uneven tiles: up 724 -> 766); whole tiles before the experts' last ones, an XCD
+// its share of each (740 -> 766: weights are read twice); two workgroups a CU for the
+// experts' tiles, of 128 x 128 (up 721 -> 769); lines touched ahead for L2 (507 ->
+// 655); explicit turns of matrix, vector and LDS instructions (476 -> 500); raised
+// wavefront priority around the matrix instructions (489 -> 513).
 #include <type_traits>
 
 #include "f8.h"
@@ -48,12 +53,13 @@ constexpr int XCDS = 8;
 // tiles, 48 rows 226 and 216, 64 rows 226 and 225; down, 64 rows 140 and 145, 128
 // rows 173 and 194.
 constexpr int64_t kRows8 = 192, kRows4 = 64;
-// What a block of K costs a round of one tile a CU, in 10 ns, for tiles of 256 x 256,
-// 128 x 256, 128 x 128, 64 x 128 and 64 x 64: the size with the least rounds times
-// cost is taken.  4096 tokens of 4096 x 4096: 67, 82, 102, 131, 208 us; 2048 of 4096
-// x 2048: 60, 38, 27, 35, 54; 1024 of 4096 x 1024: 59, 36, 25, 18, 15; 1000 of 4096 x
-// 10240: 62, 73, 74, 83, 131.
-constexpr int64_t kCost[5] = {190, 110, 65, 42, 30};
+// What a tile on every CU costs, and what each of two does, in 0.1 us at K = 4096, of
+// tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 128 and 64 x 64 (two workgroups a CU
+// from 128 x 128 down): the size with the least is taken.  4096 x 10240, 1000 tokens:
+// 59, 68, 56, 62, 75 us; 4096 x 4096, 2000 tokens: 59, 40, 40, 49, 61, 500 tokens: 57,
+// 34, 23, 17, 18; 4096 x 6144, 100 tokens: 55, 33, 23, 16, 13; 2048 x 5200, 500
+// tokens: 31, 19, 13.6, 12.6, 13.6; 6144 x 20480, 1000 tokens: 173, 170, 151, 194, 243.
+constexpr int64_t kAlone[5] = {610, 380, 240, 165, 127}, kEach[5] = {610, 380, 200, 118, 89};
 
 typedef __attribute__((address_space(3))) void *lptr_t;
 
@@ -177,7 +183,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         (void *)((const uint8_t *)a.xs + x_first * xs_pitch), 0, (int)(x_rows * (uint32_t)xs_pitch),
         0x00020000);
     const int lr = lane >> 3, ls = lane & 7;
-    // the row of x behind tile row r (past the tile's end: its last one)
+    // the row of x behind tile row r (past the tile's end: its last one's scales, and
+    // zeros from past the descriptor, which ask L2 for nothing: 721 -> 715 us below)
     const auto x_row = [&](int r) {
         r = min(r, rows - 1);
         if (MODE != kUp)
@@ -196,7 +203,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 #pragma unroll
     for (int j = 0; j < LT; j++) {
         const int r = t_row(j) + lr;
-        x_at[j] = x_row(r) * (uint32_t)a.K + 16 * (ls ^ swizzle(r));
+        x_at[j] = r < rows ? x_row(r) * (uint32_t)a.K + 16 * (ls ^ swizzle(r)) : 0xFFFFFF00u;
     }
     uint32_t s_at[4];                    // (LT are used) rows 8j .. of this wavefront's eighth
 #pragma unroll
@@ -454,7 +461,8 @@ int32_t launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
         int64_t least = INT64_MAX;
         for (int i = 0; i < 5; i++) {
             const int64_t tiles = ((a.T + size[i][0] - 1) / size[i][0]) * ((a.N + size[i][1] - 1) / size[i][1]);
-            const int64_t cost = (tiles + cus - 1) / cus * kCost[i];
+            const int64_t rounds = (tiles + cus - 1) / cus;
+            const int64_t cost = rounds == 1 ? kAlone[i] : rounds * kEach[i];
             if (cost < least) {
                 least = cost;
                 pick = i;
@@ -462,9 +470,9 @@ int32_t launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
         }
         return pick == 0   ? launch_size<kDense, 8, 4, 2>(a, f32, last, l)
                : pick == 1 ? launch_size<kDense, 4, 4, 3>(a, f32, last, l)
-               : pick == 2 ? launch_size<kDense, 4, 2, 4>(a, f32, last, l)
-               : pick == 3 ? launch_size<kDense, 2, 2, 5>(a, f32, last, l)
-                           : launch_size<kDense, 2, 1, 8>(a, f32, last, l);
+               : pick == 2 ? launch_size<kDense, 4, 2, 2>(a, f32, last, l)
+               : pick == 3 ? launch_size<kDense, 2, 2, 3>(a, f32, last, l)
+                           : launch_size<kDense, 2, 1, 3>(a, f32, last, l);
     } else {
         const int64_t rows = a.p.slots / a.p.E;
         return rows >= kRows8   ? launch_size<MODE, 8, 4, 2>(a, f32, last, l)
