@@ -16,9 +16,10 @@
 // whole: with 256 x 256 tiles a block and a half ahead; with smaller ones one or two
 // blocks ahead, which leaves LDS for a second workgroup on the CU (1000 tokens of
 // 6144 x 20480 in tiles of 128 x 128: 176 us with four stages, 151 with two; 500 of
-// 4096 x 4096 in tiles of 64 x 64: 25 us with five or more, 18 with three).  Rows'
-// scales are loaded eight blocks at a time: a dword a row and block asks L2 for as
-// many lines as the codes do (507 -> 476 us below).
+// 4096 x 4096 in tiles of 64 x 64: 25 us with five or more, 18 with three), and what
+// they read from LDS is less for four wavefronts than for eight (15 us).  Rows'
+// scales are loaded eight blocks at a time: a dword a row and block asks L2 for as many
+// lines as the codes do (507 -> 476 us below).
 //
 // Consecutive workgroups go to the XCDs in turn, so each XCD gets a contiguous run
 // of tiles: neighbours share weights and rows in its L2.
@@ -28,7 +29,7 @@
 // instructions at the clock that the power limit leaves; the library's product
 // without block scales takes 402.  A round of 256 tiles of 256 x 256 costs 1.8 us a
 // block and 8.6 once (the first loads, the stores of all CUs at once).  500 tokens of
-// 2048 x 5200: 12.7 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 12.9 us.
+// 2048 x 5200: 12 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 12.5 us.
 // 4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 715 us, 1.54 PFLOP/s,
 // unevenly filled tiles and their borders; down 445 us, 58 of them the sum's.
 //
@@ -53,13 +54,13 @@ constexpr int XCDS = 8;
 // tiles, 48 rows 226 and 216, 64 rows 226 and 225; down, 64 rows 140 and 145, 128
 // rows 173 and 194.
 constexpr int64_t kRows8 = 192, kRows4 = 64;
-// What a tile on every CU costs, and what each of two does, in 0.1 us at K = 4096, of
-// tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 128 and 64 x 64 (two workgroups a CU
+// What a tile on every CU costs, and what each of several does, in 0.1 us at K = 4096,
+// of tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 128 and 64 x 64 (two workgroups a CU
 // from 128 x 128 down): the size with the least is taken.  4096 x 10240, 1000 tokens:
-// 59, 68, 56, 62, 75 us; 4096 x 4096, 2000 tokens: 59, 40, 40, 49, 61, 500 tokens: 57,
-// 34, 23, 17, 18; 4096 x 6144, 100 tokens: 55, 33, 23, 16, 13; 2048 x 5200, 500
-// tokens: 31, 19, 13.6, 12.6, 13.6; 6144 x 20480, 1000 tokens: 173, 170, 151, 194, 243.
-constexpr int64_t kAlone[5] = {610, 380, 240, 165, 127}, kEach[5] = {610, 380, 200, 118, 89};
+// 59, 68, 57, 59, 66 us; 4096 x 4096, 2000 tokens: 59, 40, 38, 45, 54, 500 tokens: 57,
+// 34, 23, 17, 15; 4096 x 6144, 100 tokens: 55, 33, 23, 17, 13; 4096 x 14336, 200 tokens:
+// 57, 34, 24, 22, 28; 6144 x 20480, 1000 tokens: 173, 170, 149, 193, 239.
+constexpr int64_t kAlone[5] = {610, 380, 245, 165, 127}, kEach[5] = {610, 380, 200, 120, 72};
 
 typedef __attribute__((address_space(3))) void *lptr_t;
 
@@ -90,37 +91,39 @@ __device__ __forceinline__ int w_swizzle(int r)
     return (r >> 1 & 1) | (r >> (RUN == 4 ? 4 : RUN == 2 ? 3 : 2) & 3) << 1;
 }
 
-template <int TB, int WB>
+template <int BM, int BN>
 struct Stage {
-    u32x4 tok[32 * TB * 8];
-    u32x4 w[64 * WB * 8];
+    u32x4 tok[BM * 8];
+    u32x4 w[BN * 8];
 };
 
 // (one object: of several, the compiler would wait for all loads in flight to
 // one before each read of another)
-template <int TB, int WB, int S>
+template <int BM, int BN, int S>
 struct Shared {
-    Stage<TB, WB> stage[S];
-    uint32_t xs[2][4 * TB * SG];
+    Stage<BM, BN> stage[S];
+    uint32_t xs[2][BM / 8 * SG];
 };
 
-// A tile of 32 * TB rows and 64 * WB weight rows (kUp: half of them the gate's,
-// half the up matrix's), S stages of K.  Eight wavefronts: two halves of the rows
-// by four quarters of the outputs.
-template <F8Mode MODE, bool XF32, int TB, int WB, int S>
-__global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
+// A tile of BM rows and BN weight rows (kUp: half of them the gate's, half the up
+// matrix's), S stages of K.  Wavefronts: two halves of the rows by OQ parts of the
+// outputs, TB by WB blocks of 16 each.
+template <F8Mode MODE, bool XF32, int BM, int BN, int S, int OQ>
+__global__ __launch_bounds__(128 * OQ, 2) void tiles_kernel(F8Args a)
 {
-    constexpr int BM = 32 * TB, BN = 64 * WB, LT = BM / 64, LW = BN / 64;
+    constexpr int NW = 2 * OQ, TB = BM / 32, WB = BN / (16 * OQ);
+    // rows that a wavefront loads, eight at a time
+    constexpr int RT = BM / NW, RW = BN / NW, LT = RT / 8, LW = RW / 8;
     // blocks whose outputs a lane has side by side: row m of block i is weight row
     // 4 * RUN * (m / 4) + 4 * i + m % 4 of the wavefront's, so that a lane's sums,
     // rows 4q .. 4q + 3 of every block, are 4 * RUN neighbours
     constexpr int RUN = MODE == kUp ? 2 : WB;
-    typedef Stage<TB, WB> Stage;
-    __shared__ Shared<TB, WB, S> sh;
+    typedef Stage<BM, BN> Stage;
+    __shared__ Shared<BM, BN, S> sh;
     Stage *const stage = sh.stage;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int th = (wave >> 2), oq = wave & 3;       // token half, output quarter
+    const int th = wave / OQ, oq = wave % OQ;        // half of the tokens, part of the outputs
     const int r16 = lane & 15, q = lane >> 4;
     const int KB = a.K / 128;
     constexpr int NT = MODE == kUp ? BN / 2 : BN;    // outputs a tile
@@ -163,8 +166,8 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     const int half = MODE == kUp ? wave & 1 : 0;
     const int64_t mat = (int64_t)expert * H + half;
     // (kUp: LDS rows 64u .. 64u+31 are gate rows 32u .., 64u+32 .. their up rows)
-    static_assert(MODE != kUp || WB == 4, "32 values of h share a scale");
-    const int w_first = n0 + 8 * WB * (MODE == kUp ? wave >> 1 : wave);
+    static_assert(MODE != kUp || (WB == 4 && RW == 32), "32 values of h share a scale");
+    const int w_first = n0 + RW * (MODE == kUp ? wave >> 1 : wave);
     // (a descriptor bounds a lane's own offset, not the scalar one, which stays
     // within a row: rows past N read as zeros)
     const uint8_t *const w_from = uniform(a.w + (mat * a.N + w_first) * a.K);
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
 #pragma unroll
     for (int j = 0; j < LW; j++)
         w_at[j] = (uint32_t)(8 * (j & 1) + lr) * a.K +
-                  16 * (ls ^ w_swizzle<RUN>(8 * WB * wave + 8 * j + lr));
+                  16 * (ls ^ w_swizzle<RUN>(RW * wave + 8 * j + lr));
     // this wavefront's rows of the first half of the tokens, then of the second
     constexpr int LH = LT > 1 ? LT / 2 : 1;
     const auto t_row = [&](int j) { return j / LH * (BM / 2) + wave * (8 * LH) + 8 * (j % LH); };
@@ -205,16 +208,16 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         const int r = t_row(j) + lr;
         x_at[j] = r < rows ? x_row(r) * (uint32_t)a.K + 16 * (ls ^ swizzle(r)) : 0xFFFFFF00u;
     }
-    uint32_t s_at[4];                    // (LT are used) rows 8j .. of this wavefront's eighth
+    uint32_t s_at[4];                    // (LT are used) rows 8j .. of this wavefront's
 #pragma unroll
     for (int j = 0; j < LT; j++)
-        s_at[j] = x_row(wave * (BM / 8) + 8 * j + lr) * (uint32_t)xs_pitch + 4 * ls;
+        s_at[j] = x_row(RT * wave + 8 * j + lr) * (uint32_t)xs_pitch + 4 * ls;
     const auto issue_w = [&](int kt, Stage &s) {
         const int k = min(kt, KB - 1);
 #pragma unroll
         for (int j = 0; j < LW; j++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(j < 2 ? rw0 : rw1,
-                                                     (lptr_t)&s.w[(8 * WB * wave + 8 * j) * 8], 16,
+                                                     (lptr_t)&s.w[(RW * wave + 8 * j) * 8], 16,
                                                      w_at[j], 128 * k, 0, 0);
     };
     const auto issue_s = [&](int part) {
@@ -350,12 +353,17 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
         for (int kt = 0; kt < KB; kt++) {
             block_scales(kt);
             meet(std::integral_constant<int, (S - 2) * (LW + LT)>{});
+            // (before the loads where four wavefronts leave nobody else to go on: 37
+            // tokens of 4096 x 14336 13.0 -> 12.5 us; eight gain nothing, 293 -> 295)
+            if (NW == 4)
+                read_w(stage[at]);
             if (kt % SB == 0)
                 issue_s(kt / SB + 1);
             Stage &o = stage[at == 0 ? S - 1 : at - 1];
             issue_w(kt + S - 1, o);
             issue_x(kt + S - 1, o);
-            read_w(stage[at]);
+            if (NW != 4)
+                read_w(stage[at]);
             part(kt, stage[at], zero{}, std::integral_constant<int, TB>{});
             at = at + 1 == S ? 0 : at + 1;
         }
@@ -432,20 +440,20 @@ __global__ __launch_bounds__(512) void tiles_kernel(F8Args a)
     }
 }
 
-template <F8Mode MODE, int TB, int WB, int S>
+template <F8Mode MODE, int BM, int BN, int S, int OQ>
 int32_t launch_size(const F8Args &a, bool f32, bool last, const Launch &l)
 {
-    constexpr int NT = MODE == kUp ? 32 * WB : 64 * WB;
+    constexpr int NT = MODE == kUp ? BN / 2 : BN;
     // (of an experts' call, the tiles that any plan of it can ask for)
-    const int64_t tiles_m = MODE == kDense ? (a.T + 32 * TB - 1) / (32 * TB) : f8_most_tiles(a.p, 32 * TB);
+    const int64_t tiles_m = MODE == kDense ? (a.T + BM - 1) / BM : f8_most_tiles(a.p, BM);
     const int64_t tiles = tiles_m * ((a.N + NT - 1) / NT);
     if (tiles >= (int64_t)1 << 23)                   // a grid counts its threads in 32 bits
         return fail(ENGRAM_E_RANGE, "engram f8 tiles: %lld workgroups exceed 2^23-1", (long long)tiles);
     const dim3 grid((unsigned)tiles);
     if (f32)
-        dispatch(tiles_kernel<MODE, true, TB, WB, S>, grid, dim3(512), l, true, last, a);
+        dispatch(tiles_kernel<MODE, true, BM, BN, S, OQ>, grid, dim3(128 * OQ), l, true, last, a);
     else
-        dispatch(tiles_kernel<MODE, false, TB, WB, S>, grid, dim3(512), l, true, last, a);
+        dispatch(tiles_kernel<MODE, false, BM, BN, S, OQ>, grid, dim3(128 * OQ), l, true, last, a);
     return launch_status("engram f8 tiles kernel");
 }
 
@@ -468,16 +476,16 @@ int32_t launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
                 pick = i;
             }
         }
-        return pick == 0   ? launch_size<kDense, 8, 4, 2>(a, f32, last, l)
-               : pick == 1 ? launch_size<kDense, 4, 4, 3>(a, f32, last, l)
-               : pick == 2 ? launch_size<kDense, 4, 2, 2>(a, f32, last, l)
-               : pick == 3 ? launch_size<kDense, 2, 2, 3>(a, f32, last, l)
-                           : launch_size<kDense, 2, 1, 3>(a, f32, last, l);
+        return pick == 0   ? launch_size<kDense, 256, 256, 2, 4>(a, f32, last, l)
+               : pick == 1 ? launch_size<kDense, 128, 256, 3, 4>(a, f32, last, l)
+               : pick == 2 ? launch_size<kDense, 128, 128, 2, 4>(a, f32, last, l)
+               : pick == 3 ? launch_size<kDense, 64, 128, 3, 2>(a, f32, last, l)
+                           : launch_size<kDense, 64, 64, 3, 2>(a, f32, last, l);
     } else {
         const int64_t rows = a.p.slots / a.p.E;
-        return rows >= kRows8   ? launch_size<MODE, 8, 4, 2>(a, f32, last, l)
-               : rows >= kRows4 ? launch_size<MODE, 4, 4, 3>(a, f32, last, l)
-                                : launch_size<MODE, 2, 4, 3>(a, f32, last, l);
+        return rows >= kRows8   ? launch_size<MODE, 256, 256, 2, 4>(a, f32, last, l)
+               : rows >= kRows4 ? launch_size<MODE, 128, 256, 3, 4>(a, f32, last, l)
+                                : launch_size<MODE, 64, 256, 3, 4>(a, f32, last, l);
     }
 }
 
