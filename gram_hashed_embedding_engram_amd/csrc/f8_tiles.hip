@@ -61,6 +61,12 @@ constexpr int64_t kRows8 = 192, kRows4 = 64;
 // 34, 23, 17, 15; 4096 x 6144, 100 tokens: 55, 33, 23, 17, 13; 4096 x 14336, 200 tokens:
 // 57, 34, 24, 22, 28; 6144 x 20480, 1000 tokens: 173, 170, 149, 193, 239.
 constexpr int64_t kAlone[5] = {610, 380, 245, 165, 127}, kEach[5] = {610, 380, 200, 120, 72};
+// The same for few rows of weights that no cache keeps, where rows' reads from L2 slow
+// the stream: 6144 x 20480 (126 MB), 64 tokens in tiles of 64 x 128 35 us and of 64 x 64
+// 40, 128 tokens in tiles of 128 x 128 45, of 64 x 64 52; where 4096 x 14336 (59 MB),
+// which the last-level cache holds, takes 18 and 16 us for 128 tokens.
+constexpr int64_t kEachStreamed[5] = {610, 380, 200, 130, 100};
+constexpr int64_t kStreamedRows = 128, kStreamedBytes = (int64_t)96 << 20;
 
 typedef __attribute__((address_space(3))) void *lptr_t;
 
@@ -464,13 +470,15 @@ int32_t launch_f8_tiles(const F8Args &a, bool f32, bool last, const Launch &l)
 {
     if constexpr (MODE == kDense) {
         const int64_t cus = device_cus();
+        const int64_t *const each =
+            a.T <= kStreamedRows && (int64_t)a.N * a.K >= kStreamedBytes ? kEachStreamed : kEach;
         const int64_t size[5][2] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}, {64, 64}};
         int pick = 0;
         int64_t least = INT64_MAX;
         for (int i = 0; i < 5; i++) {
             const int64_t tiles = ((a.T + size[i][0] - 1) / size[i][0]) * ((a.N + size[i][1] - 1) / size[i][1]);
             const int64_t rounds = (tiles + cus - 1) / cus;
-            const int64_t cost = rounds == 1 ? kAlone[i] : rounds * kEach[i];
+            const int64_t cost = rounds == 1 ? kAlone[i] : rounds * each[i];
             if (cost < least) {
                 least = cost;
                 pick = i;
