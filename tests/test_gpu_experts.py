@@ -285,6 +285,14 @@ def test_project_f8_tiles(E, T, K, N):
         assert bool((y[T] == 7).all()), "a row past the last is written"
 
 
+# tiles of 256 x 256, 128 x 256, 128 x 128 and 64 x 128 over more blocks than a load of scales
+# covers, of 128 x 128 and 64 x 128 over one, few rows of weights that no cache keeps
+@pytest.mark.parametrize("T,K,N", [(4090, 1152, 4080), (2000, 1152, 4080), (961, 1152, 10000), (2000, 1408, 2064),
+                                   (1000, 128, 10240), (2040, 128, 2032), (100, 6144, 16400), (35, 6144, 16400)])
+def test_project_f8_long_tiles(E, T, K, N):
+    test_project_f8_tiles(E, T, K, N)
+
+
 def counted_plan(g, counts, shuffled=False):
     """One expert a token, so many tokens each."""
     ids = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts))
@@ -331,6 +339,17 @@ def test_experts_borders(E, counts, f32):
     g = seeded(sum(counts))
     arrays, offsets, order = counted_plan(g, counts, shuffled=True)
     check_experts(E, g, arrays, offsets, order, len(counts), 384, 256, 528, f32)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("counts", [[300, 200, 129], [100, 64, 50], [20, 9, 3], [2, 0, 1]])
+def test_experts_long_rows(E, counts, f32):
+    """More blocks of K than one load of rows' scales covers, at every tile's height."""
+    log(f"experts' rows {counts} of 1408 and 1152 values")
+    g = seeded(sum(counts) + 1)
+    arrays, offsets, order = counted_plan(g, counts)
+    check_experts(E, g, arrays, offsets, order, len(counts), 1408, 256, 272, f32)
+    check_experts(E, g, arrays, offsets, order, len(counts), 1152, 128, 2064, f32)
 
 
 def test_experts_many(E):
