@@ -374,9 +374,11 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
                 }
         }
         merge_best(first, second, gr.spread);
+        // (of two, half their sum: two of f32's lowest or largest values, which masks
+        // are, have a sum past its range)
         float sum = first;
-        if (a.group_best > 1 && second > -INFINITY)
-            sum += second;
+        if (a.group_best > 1)
+            sum = 0.5f * first + (second > -INFINITY ? 0.5f * second : 0.0f);
         // (lanes past the groups hold -inf)
         const int ahead = rank_of(ordered(sum), g, a.groups, gr.spread);
         const bool in = g < a.groups && sum > -INFINITY;

@@ -678,3 +678,28 @@ def test_stream_argument(E):
 def test_route_blocks(E, T):
     g = seeded(T)
     check_route(E, torch.randn(T, 12, generator=g, device="cuda"), None, 2, True)
+
+
+# ------------------------------------------------- group sums at the ends of f32
+LOWEST, MOST = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("n,groups,top,k", [(8, 4, 2, 3), (48, 6, 2, 6), (256, 8, 4, 8), (160, 8, 3, 6), (64, 32, 3, 5)])
+def test_route_lowest_bias(E, n, groups, top, k, softmax):
+    """Biases of the type's lowest or largest value are values: the experts stay
+    open, and two such keys of a group add up to what f32 cannot hold."""
+    g = seeded(n + groups)
+    x = torch.randn(70, n, generator=g, device="cuda")
+    size = n // groups
+    for large in (LOWEST, MOST):
+        for first in (2, size, size + 1, n - 1):       # the experts from here on
+            bias = 0.1 * torch.randn(n, generator=g, device="cuda")
+            bias[first:] = large
+            for best in (1, 2):
+                check_route(E, x, bias, k, softmax, groups, top, best, what=f"{large} from {first} on, best {best}")
+        bias = 0.1 * torch.randn(n, generator=g, device="cuda")
+        bias[::2] = large                              # one key of a group, against the other's own size
+        check_route(E, x, bias, k, softmax, groups, top, 2, what=f"{large} at every second")
+        bias[1::2] = -large                            # sums near zero
+        check_route(E, x, bias, k, softmax, groups, top, 2, what=f"{large} and its negative")
