@@ -49,11 +49,19 @@ typedef unsigned long long u64;
 // reciprocal add another: 2^-20 for two.  A softmax score is off by (1.5 |d| + 2) 2^-24
 // of itself at a distance d from the largest logit, so by less than 2.6 * 2^-24 of the
 // largest score, and by NR + 9 roundings of the sum, the reciprocal and the product:
-// 2^-18 of the largest score for two, at NR = 16.  A key's own rounding is 2^-24 of
-// it; a group's sum holds two keys.
-__device__ __forceinline__ bool near_keys(float a, float b, float unit, float terms)
+// 2^-18 of the largest score for two, at NR = 16.  A key's own rounding is 2^-24 of it.
+__device__ __forceinline__ bool near_keys(float a, float b, float unit)
 {
-    return a - b <= terms * (unit + 0x1p-22f * fmaxf(fabsf(a), fabsf(b)));
+    return a - b <= unit + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
+}
+
+// How far a group's sum (half the sum of two keys, or one key) is off: by half of
+// unit, by its keys' roundings and by its own, which are 2^-24 of the larger key
+// each, and by as much where it is compared.  The sum may be far smaller than its
+// keys, so their size counts.
+__device__ __forceinline__ float sum_error(float first, float second, float unit)
+{
+    return 0.5f * unit + 0x1.8p-23f * fmaxf(fabsf(first), second > -INFINITY ? fabsf(second) : 0.0f);
 }
 
 // Where the scores of logits a >= b may be one and the same number of 64 bits, or
@@ -384,10 +392,19 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
         const bool in = g < a.groups && sum > -INFINITY;
         bool keep = in && ahead < a.top_groups;
         u64 kept = __ballot(keep);
-        const u64 last = __ballot(in && ahead == a.top_groups - 1), next = __ballot(in && ahead == a.top_groups);
-        const float u = next ? lane_value(sum, __builtin_ctzll(last)) : 0.0f;
-        const float v = next ? lane_value(sum, __builtin_ctzll(next)) : 0.0f;
-        if (next && (logits ? near_logits(u, v, top, a.softmax) : near_keys(u, v, unit, 2.0f))) {
+        bool near = false;
+        if (const u64 next = __ballot(in && ahead == a.top_groups)) {
+            if (logits) {
+                const u64 last = __ballot(in && ahead == a.top_groups - 1);
+                near = near_logits(lane_value(sum, __builtin_ctzll(last)),
+                                   lane_value(sum, __builtin_ctzll(next)), top, a.softmax);
+            } else {
+                // the least that a kept sum may be, the most that another may
+                const float e = sum_error(first, a.group_best > 1 ? second : first, unit);
+                near = wave_max(keep ? e - sum : -INFINITY) + wave_max(in && !keep ? sum + e : -INFINITY) >= 0.0f;
+            }
+        }
+        if (near) {
             const u64 by_group = groups_f64<NR>(a, gr, x, values);
             keep = g < a.groups && (by_group >> g & 1);
             kept = __ballot(keep);
@@ -456,10 +473,10 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
             const int low = __float_as_int(-INFINITY);
             const float next = __int_as_float(                       // of lane j + 1
                 __builtin_amdgcn_update_dpp(low, __float_as_int(mine), 0x130, 0xF, 0xF, false));
-            if (__ballot(lane < a.k && next > -INFINITY && near_keys(mine, next, unit, 1.0f))) {
+            if (__ballot(lane < a.k && next > -INFINITY && near_keys(mine, next, unit))) {
                 // told apart in 64 bits, if nobody outside can stand among the first k
                 const float least = lane_value(mine, n - 1), kth = lane_value(mine, min(a.k, n) - 1);
-                exact = n < total && near_keys(kth, least, unit, 1.0f);
+                exact = n < total && near_keys(kth, least, unit);
                 if (!exact)
                     at = rank_f64<NR>(a, x, values, n, at);
             }

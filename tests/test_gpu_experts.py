@@ -703,3 +703,32 @@ def test_route_lowest_bias(E, n, groups, top, k, softmax):
         check_route(E, x, bias, k, softmax, groups, top, 2, what=f"{large} at every second")
         bias[1::2] = -large                            # sums near zero
         check_route(E, x, bias, k, softmax, groups, top, 2, what=f"{large} and its negative")
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("size", [64.0, 1000.0, 1e5])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_group_sums_that_cancel(E, size, softmax, bf16):
+    """Groups whose two keys are large and of opposite signs: what their sum keeps
+    is as far off as the keys' own rounding, however small it is."""
+    log(f"groups of two, biases of +-{size} softmax {softmax} bf16 {bf16}")
+    g = seeded(int(size))
+    T, n, k, top = 150000, 16, 3, 4
+    x = torch.randn(T, n, generator=g, device="cuda")
+    x = x.bfloat16() if bf16 else x
+    bias = 0.1 * torch.randn(n, generator=g, device="cuda")
+    bias[::2] += size
+    bias[1::2] -= size
+    r = new_routes(E, T, n, k)
+    E.route(x, r, bias, softmax, n // 2, top, 2, d_ws=space(E, E.route_bytes(r)))
+    got = r.keep[0].cpu().numpy()
+    x, b = x.double().cpu().numpy(), bias.double().cpu().numpy()
+    score = np.exp(x - x.max(1, keepdims=True))
+    score = score / score.sum(1, keepdims=True) if softmax else 1 / (1 + np.exp(-x))
+    key = score + b
+    sums = key[:, ::2] + key[:, 1::2]
+    kept = np.zeros(sums.shape, dtype=bool)
+    np.put_along_axis(kept, np.argsort(-sums, 1, kind="stable")[:, :top], True, 1)
+    key[~kept.repeat(2, 1)] = -INF
+    want = np.argsort(-key, 1, kind="stable")[:, :k]
+    assert np.array_equal(got, want), f"ids differ in {(got != want).any(1).sum()} tokens"
