@@ -444,11 +444,12 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
     int at = -1;
     bool exact = false;
     if (n <= 64) {
-        struct Entry {
-            float key;
-            int id;
+        // (key, id) pairs, the id's bits as a float: the same LDS holds logits before
+        // and after, so every access to it is of one type
+        const auto put = [&](int i, float key, int id) {
+            values[2 * i] = key;
+            values[2 * i + 1] = __int_as_float(id);
         };
-        Entry *const list = (Entry *)values;
         // to the lanes, in the experts' order
         int before = 0;
 #pragma unroll
@@ -457,18 +458,18 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
 #pragma unroll
         for (int r = 0; r < NR; r++)
             if (key[r] >= bound)
-                list[before++] = Entry{key[r], NR * lane + r};
-        Entry own{-INFINITY, -1};
-        if (lane < n)
-            own = list[lane];
-        const int rank = rank_of(ordered(own.key), lane, n, 1);
+                put(before++, key[r], NR * lane + r);
+        if (lane < n) {
+            mine = values[2 * lane];
+            at = __float_as_int(values[2 * lane + 1]);
+        }
+        const int rank = rank_of(ordered(mine), lane, n, 1);
         // in the order of their keys
         if (lane < n) {
-            list[rank] = own;
-            own = list[lane];
+            put(rank, mine, at);
+            mine = values[2 * lane];
+            at = __float_as_int(values[2 * lane + 1]);
         }
-        mine = own.key;
-        at = own.id;
         if (a.bias) {
             const int low = __float_as_int(-INFINITY);
             const float next = __int_as_float(                       // of lane j + 1
