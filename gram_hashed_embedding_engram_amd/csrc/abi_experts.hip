@@ -19,11 +19,32 @@ constexpr int64_t kMaxSlots = (int64_t)1 << 24;
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
-// Whether an input and an output share memory.
-bool overlap(const void *in, uint64_t in_bytes, const void *out, uint64_t out_bytes)
+// What a call reads or writes; none where p is NULL.
+struct Bytes {
+    const char *name;
+    const void *p;
+    uint64_t n;
+};
+
+bool overlap(const Bytes &a, const Bytes &b)
 {
-    const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
-    return a < b ? b - a < in_bytes : a - b < out_bytes;
+    const uintptr_t i = (uintptr_t)a.p, j = (uintptr_t)b.p;
+    return a.p && b.p && a.n && b.n && (i < j ? j - i < a.n : i - j < b.n);
+}
+
+// What a call writes overlaps nothing else of it.
+template <size_t W, size_t R>
+int32_t check_apart(const char *who, const Bytes (&writes)[W], const Bytes (&reads)[R])
+{
+    for (size_t i = 0; i < W; i++) {
+        for (const Bytes &r : reads)
+            CHECK(!overlap(writes[i], r), ENGRAM_E_ARG, "engram %s: the %s overlaps the %s", who,
+                  writes[i].name, r.name);
+        for (size_t j = i + 1; j < W; j++)
+            CHECK(!overlap(writes[i], writes[j]), ENGRAM_E_ARG, "engram %s: the %s overlaps the %s",
+                  who, writes[i].name, writes[j].name);
+    }
+    return ENGRAM_OK;
 }
 
 Launch on(void *stream)
@@ -37,6 +58,14 @@ uint64_t scale_bytes(int64_t rows, int64_t K, bool f32)
 {
     return (uint64_t)rows * (uint64_t)(f32 ? K / kF8Block * 4 : K / ENGRAM_NORM_GROUP);
 }
+
+uint64_t block_bytes(int64_t matrices, int64_t N, int64_t K)
+{
+    return (uint64_t)matrices * (uint64_t)((N + kF8Block - 1) / kF8Block) * (uint64_t)(K / kF8Block) * 4;
+}
+
+uint64_t slot_bytes(const engram_routes *r) { return (uint64_t)r->tokens * (uint64_t)r->chosen * 4; }
+uint64_t offset_bytes(const engram_routes *r) { return 4 * ((uint64_t)r->experts + 1); }
 
 int32_t check_routes(const engram_routes *r, const char *who)
 {
@@ -138,19 +167,18 @@ int32_t engram_route(const engram_routes *routes, const void *d_logits, int32_t 
           ws_bytes, need);
     CHECK(need == 0 || (d_ws && aligned(d_ws, 256)), ENGRAM_E_ARG,
           "engram route: NULL or unaligned workspace (256 bytes)");
-    const uint64_t read = ((uint64_t)(T - 1) * logits_stride + E) * (logits_bf16 ? 2 : 4);
-    const uint64_t slots = (uint64_t)T * routes->chosen * 4;
-    CHECK(!overlap(d_logits, read, routes->d_ids, slots) &&
-              !overlap(d_logits, read, routes->d_weights, slots) &&
-              !overlap(d_logits, read, routes->d_order, slots) &&
-              !overlap(d_logits, read, routes->d_offsets, 4 * (uint64_t)(E + 1)),
-          ENGRAM_E_ARG, "engram route: the routes overlap the logits");
-    CHECK(need == 0 || (!overlap(d_logits, read, d_ws, need) &&
-                        !overlap(routes->d_ids, slots, d_ws, need) &&
-                        !overlap(routes->d_weights, slots, d_ws, need) &&
-                        !overlap(routes->d_order, slots, d_ws, need) &&
-                        !overlap(routes->d_offsets, 4 * (uint64_t)(E + 1), d_ws, need)),
-          ENGRAM_E_ARG, "engram route: the workspace overlaps the logits or the routes");
+    const Bytes writes[] = {{"workspace", need ? d_ws : nullptr, need},
+                            {"routes' ids", routes->d_ids, slot_bytes(routes)},
+                            {"routes' weights", routes->d_weights, slot_bytes(routes)},
+                            {"routes' offsets", routes->d_offsets, offset_bytes(routes)},
+                            {"routes' order", routes->d_order, slot_bytes(routes)},
+                            {"error word", routes->d_err, 4}};
+    const Bytes reads[] = {
+        {"logits", d_logits, ((uint64_t)(T - 1) * logits_stride + E) * (logits_bf16 ? 2 : 4)},
+        {"bias", d_bias, 4 * (uint64_t)E}};
+    rc = check_apart("route", writes, reads);
+    if (rc != ENGRAM_OK)
+        return rc;
     const Routing r{d_logits, d_bias, logits_stride, factor, (int32_t)T, (int32_t)E,
                     routes->chosen, groups, top_groups, group_best, logits_bf16 != 0, softmax != 0,
                     renorm != 0, routes->d_ids, routes->d_offsets, routes->d_order, routes->d_err,
@@ -175,10 +203,14 @@ int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_
         return rc;
     CHECK(d_y && aligned(d_y, 16), ENGRAM_E_ARG,
           "engram project_f8: NULL or unaligned y (16 bytes)");
-    const uint64_t out = (uint64_t)T * (uint64_t)N * 2;
-    CHECK(!overlap(d_x, (uint64_t)T * (uint64_t)K, d_y, out) &&
-              !overlap(d_x_scales, scale_bytes(T, K, x_f32 != 0), d_y, out),
-          ENGRAM_E_ARG, "engram project_f8: y overlaps x or its scales");
+    const Bytes writes[] = {{"output", d_y, (uint64_t)T * (uint64_t)N * 2}};
+    const Bytes reads[] = {{"rows", d_x, (uint64_t)T * (uint64_t)K},
+                           {"rows' scales", d_x_scales, scale_bytes(T, K, x_f32 != 0)},
+                           {"weights", d_w, (uint64_t)N * (uint64_t)K},
+                           {"weights' scales", d_w_scales, block_bytes(1, N, K)}};
+    rc = check_apart("project_f8", writes, reads);
+    if (rc != ENGRAM_OK)
+        return rc;
     return launch_project_f8(Rows8{d_x, d_x_scales, x_f32 != 0}, Blocks8{d_w, d_w_scales}, d_y, T,
                              K, N, on(stream));
 }
@@ -206,15 +238,21 @@ int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const
         return rc;
     CHECK(d_h && d_h_scales && aligned(d_h, 16) && aligned(d_h_scales, 4), ENGRAM_E_ARG,
           "engram experts_up: NULL or unaligned h (16 bytes) or scales of h (4)");
-    const uint64_t slots = (uint64_t)T * routes->chosen, hb = slots * (uint64_t)I;
-    const uint64_t sb = scale_bytes((int64_t)slots, I, false);
-    CHECK(!overlap(d_x, (uint64_t)T * (uint64_t)K, d_h, hb) &&
-              !overlap(d_x, (uint64_t)T * (uint64_t)K, d_h_scales, sb) &&
-              !overlap(d_x_scales, scale_bytes(T, K, x_f32 != 0), d_h, hb) &&
-              !overlap(d_x_scales, scale_bytes(T, K, x_f32 != 0), d_h_scales, sb),
-          ENGRAM_E_ARG, "engram experts_up: h or its scales overlap x or its scales");
-    CHECK(!overlap(d_h, hb, d_h_scales, sb), ENGRAM_E_ARG,
-          "engram experts_up: h overlaps its scales");
+    const int64_t slots = T * routes->chosen, E = routes->experts;
+    const Bytes writes[] = {{"output", d_h, (uint64_t)slots * (uint64_t)I},
+                            {"output's scales", d_h_scales, scale_bytes(slots, I, false)},
+                            {"error word", routes->d_err, 4}};
+    const Bytes reads[] = {{"rows", d_x, (uint64_t)T * (uint64_t)K},
+                           {"rows' scales", d_x_scales, scale_bytes(T, K, x_f32 != 0)},
+                           {"weights", d_w, 2 * (uint64_t)E * (uint64_t)I * (uint64_t)K},
+                           {"weights' scales", d_w_scales, block_bytes(2 * E, I, K)},
+                           {"routes' ids", routes->d_ids, slot_bytes(routes)},
+                           {"routes' weights", routes->d_weights, slot_bytes(routes)},
+                           {"routes' offsets", routes->d_offsets, offset_bytes(routes)},
+                           {"routes' order", routes->d_order, slot_bytes(routes)}};
+    rc = check_apart("experts_up", writes, reads);
+    if (rc != ENGRAM_OK)
+        return rc;
     return launch_experts_up(plan_of(routes), Rows8{d_x, d_x_scales, x_f32 != 0},
                              Blocks8{d_w, d_w_scales}, d_h, d_h_scales, K, I, on(stream));
 }
@@ -252,15 +290,21 @@ int32_t engram_experts_down(const engram_routes *routes, const uint8_t *d_h,
           "engram experts_down: a workspace of %zu bytes, %zu needed", ws_bytes, need);
     CHECK(need == 0 || (d_ws && aligned(d_ws, 256)), ENGRAM_E_ARG,
           "engram experts_down: NULL or unaligned workspace (256 bytes)");
-    const uint64_t out = (uint64_t)routes->tokens * (uint64_t)N * 2;
-    CHECK(!overlap(d_h, (uint64_t)p.slots * (uint64_t)K, d_y, out) &&
-              !overlap(d_h_scales, scale_bytes(p.slots, K, h_f32 != 0), d_y, out),
-          ENGRAM_E_ARG, "engram experts_down: y overlaps h or its scales");
-    CHECK(need == 0 ||
-              (!overlap(d_h, (uint64_t)p.slots * (uint64_t)K, d_ws, need) &&
-               !overlap(d_h_scales, scale_bytes(p.slots, K, h_f32 != 0), d_ws, need) &&
-               !overlap(d_y, out, d_ws, need)),
-          ENGRAM_E_ARG, "engram experts_down: the workspace overlaps h, its scales or y");
+    const int64_t E = routes->experts;
+    const Bytes writes[] = {{"workspace", need ? d_ws : nullptr, need},
+                            {"output", d_y, (uint64_t)routes->tokens * (uint64_t)N * 2},
+                            {"error word", routes->d_err, 4}};
+    const Bytes reads[] = {{"rows", d_h, (uint64_t)p.slots * (uint64_t)K},
+                           {"rows' scales", d_h_scales, scale_bytes(p.slots, K, h_f32 != 0)},
+                           {"weights", d_w, (uint64_t)E * (uint64_t)N * (uint64_t)K},
+                           {"weights' scales", d_w_scales, block_bytes(E, N, K)},
+                           {"routes' ids", routes->d_ids, slot_bytes(routes)},
+                           {"routes' weights", routes->d_weights, slot_bytes(routes)},
+                           {"routes' offsets", routes->d_offsets, offset_bytes(routes)},
+                           {"routes' order", routes->d_order, slot_bytes(routes)}};
+    rc = check_apart("experts_down", writes, reads);
+    if (rc != ENGRAM_OK)
+        return rc;
     return launch_experts_down(p, Rows8{d_h, d_h_scales, h_f32 != 0}, Blocks8{d_w, d_w_scales}, d_y,
                                K, N, d_ws, on(stream));
 }

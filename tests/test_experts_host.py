@@ -243,3 +243,78 @@ def test_other_device_is_refused(monkeypatch):
     E._here(1)
     with pytest.raises(E.EngramError, match="not on the call's device"):
         E._same_device(1, x=type("T", (), dict(is_cuda=True, device="cuda:0", get_device=lambda self: 0))())
+
+
+# addresses of their own for every array of a call, far apart
+FAR = {name: FAKE + ((16 + i) << 44) for i, name in enumerate(
+    ("x", "xs", "w", "ws", "y", "h", "hs", "space", "logits", "bias", "d_ids", "d_weights", "d_offsets", "d_order", "d_err"))}
+PLAN = ("d_ids", "d_weights", "d_offsets", "d_order")
+
+
+def far_call(L, op, moved, T=1000, k=4, n=64, K=256, I=256, N=208, f32=0):
+    """A call whose arrays are far apart but for those in `moved`."""
+    at = dict(FAR, **moved)
+    r = routes_c(experts=n, chosen=k, tokens=T, **{name: at[name] for name in (*PLAN, "d_err")})
+    ref = ctypes.byref(r)
+    if op == "route":
+        return L.engram_route(ref, at["logits"], 0, n, at["bias"], 0, 1, 1, 2, 1, 1.0, at["space"],
+                              L.engram_route_bytes(ref), None)
+    if op == "f8":
+        return L.engram_project_f8(at["x"], at["xs"], f32, at["w"], at["ws"], at["y"], T, K, N, None)
+    if op == "up":
+        return L.engram_experts_up(ref, at["x"], at["xs"], f32, at["w"], at["ws"], at["h"], at["hs"], K, I, None)
+    return L.engram_experts_down(ref, at["x"], at["xs"], f32, at["w"], at["ws"], at["y"], K, N, at["space"],
+                                 L.engram_experts_down_bytes(ref, N), None)
+
+
+def far_bytes(L, op, T=1000, k=4, n=64, K=256, I=256, N=208, f32=0):
+    """(what a call writes, what it reads), with their sizes."""
+    R, width = T * k, (lambda v: v // 128 * 4 if f32 else v // 32)
+    r = routes_c(experts=n, chosen=k, tokens=T)
+    plan = dict(d_ids=4 * R, d_weights=4 * R, d_offsets=4 * (n + 1), d_order=4 * R)
+    err = dict(d_err=4)
+    if op == "route":
+        return dict(space=L.engram_route_bytes(ctypes.byref(r)), **plan, **err), dict(logits=4 * T * n, bias=4 * n)
+    if op == "f8":
+        return dict(y=2 * T * N), dict(x=T * K, xs=T * width(K), w=N * K, ws=2 * (K // 128) * 4)
+    if op == "up":
+        return (dict(h=R * I, hs=R * I // 32, **err),
+                dict(x=T * K, xs=T * width(K), w=n * 2 * I * K, ws=n * 2 * (I // 128) * (K // 128) * 4, **plan))
+    return (dict(space=L.engram_experts_down_bytes(ctypes.byref(r), N), y=2 * T * N, **err),
+            dict(x=R * K, xs=R * width(K), w=n * N * K, ws=n * 2 * (K // 128) * 4, **plan))
+
+
+@pytest.mark.parametrize("f32", [0, 1])
+@pytest.mark.parametrize("op", ["route", "f8", "up", "down"])
+def test_every_overlap_is_refused(L, op, f32):
+    """What a call writes, over the first and over the last bytes of everything
+    else of the call."""
+    writes, reads = far_bytes(L, op, f32=f32)
+    assert all(writes.values()) and all(reads.values())
+    for out, size in writes.items():
+        for other, theirs in {**reads, **writes}.items():
+            if other == out:
+                continue
+            last = (theirs - 1) // 256 * 256           # the last aligned place in it
+            for place in {0, last, -(size - 1) // 256 * 256}:
+                start = FAR[other] + place
+                if start + size <= FAR[other]:
+                    continue
+                assert far_call(L, op, {out: start}, f32=f32) == E.E_ARG, (op, out, other, place)
+                assert "overlaps" in E.last_error(), (op, out, other, place, E.last_error())
+
+
+@pytest.mark.parametrize("op", ["route", "up", "down"])
+def test_neighbours_are_not_refused(L, op):
+    """An array right behind another: only the error word, which lies in the
+    plan's order, ends such a call."""
+    writes, reads = far_bytes(L, op)
+    for out in writes:
+        for other, theirs in {**reads, **writes}.items():
+            if out in (other, "d_err") or other == "d_err":
+                continue
+            start = FAR[other] + (theirs + 255) // 256 * 256
+            moved = {out: start, "d_err": FAR["d_order"] + 400}
+            if out == "d_order":
+                moved["d_err"] = start + 400
+            assert far_call(L, op, moved) == E.E_ARG and "error word" in E.last_error(), (op, out, other)
