@@ -94,7 +94,7 @@ constexpr int SG = 8 * SB + 4;
 template <int RUN>
 __device__ __forceinline__ int w_swizzle(int r)
 {
-    return (r >> 1 & 1) | (r >> (RUN == 4 ? 4 : RUN == 2 ? 3 : 2) & 3) << 1;
+    return (r >> 1 & 1) | (r >> (RUN == 4 ? 4 : 3) & 3) << 1;
 }
 
 template <int BM, int BN>
@@ -124,6 +124,7 @@ __global__ __launch_bounds__(128 * OQ, 2) void tiles_kernel(F8Args a)
     // 4 * RUN * (m / 4) + 4 * i + m % 4 of the wavefront's, so that a lane's sums,
     // rows 4q .. 4q + 3 of every block, are 4 * RUN neighbours
     constexpr int RUN = MODE == kUp ? 2 : WB;
+    static_assert(RUN == 2 || RUN == 4, "outputs leave 16 bytes at a time");
     typedef Stage<BM, BN> Stage;
     __shared__ Shared<BM, BN, S> sh;
     Stage *const stage = sh.stage;
@@ -435,12 +436,9 @@ __global__ __launch_bounds__(128 * OQ, 2) void tiles_kernel(F8Args a)
             o[2 * i + 1] = MODE == kDense ? cvt_bf16x2(v[2], v[3]) : cvt_f16x2(v[2] * inv, v[3] * inv);
         }
         uint16_t *y = (uint16_t *)a.y + (MODE == kDense ? p : (int64_t)slot) * a.N + n;
-        if constexpr (WB == 1)
-            *(u32x2 *)y = u32x2{o[0], o[1]};
-        else
 #pragma unroll
-            for (int i = 0; i < WB; i += 2)
-                *(u32x4 *)(y + 4 * i) = u32x4{o[2 * i], o[2 * i + 1], o[2 * i + 2], o[2 * i + 3]};
+        for (int i = 0; i < WB; i += 2)
+            *(u32x4 *)(y + 4 * i) = u32x4{o[2 * i], o[2 * i + 1], o[2 * i + 2], o[2 * i + 3]};
         if (MODE == kDown && q == 0)
             a.hs[(int64_t)slot * ((a.N + 63) / 64) + n / 64] = (uint8_t)k16;
     }
