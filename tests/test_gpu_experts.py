@@ -732,3 +732,23 @@ def test_route_group_sums_that_cancel(E, size, softmax, bf16):
     key[~kept.repeat(2, 1)] = -INF
     want = np.argsort(-key, 1, kind="stable")[:, :k]
     assert np.array_equal(got, want), f"ids differ in {(got != want).any(1).sum()} tokens"
+
+
+# ----------------------------------------- few rows: every number of outputs a workgroup
+# 32, 48, 64 and 80 outputs a workgroup (of 256 CUs) over up to 16 and up to 32 rows; last
+# workgroups part filled, workgroups that meet two blocks of scales, last blocks of 16 outputs
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,K,N", [(1, 256, 8208), (3, 384, 12304), (16, 1152, 16400), (16, 640, 20480), (9, 128, 20496),
+                                   (17, 384, 8208), (19, 128, 12272), (24, 896, 12304), (32, 384, 16400), (32, 256, 20496),
+                                   (31, 1152, 20480), (1, 2048, 40976), (20, 256, 41008)])
+def test_project_f8_few_rows(E, T, K, N, f32):
+    log(f"project_f8 T {T} K {K} N {N} f32 {f32}")
+    g = seeded(T + K + N)
+    w, s = R.weights8(g, N, K)
+    x, xs, x64 = R.rows8(g, T, K, f32)
+    y = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    E.project_f8(x, E.F8(w, s), y[:T], xs)
+    torch.cuda.synchronize()
+    want, tol = R.product(x64, R.matrix(w, s))
+    within(y[:T], want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
+    assert bool((y[T] == 7).all()), "a row past the last is written"
