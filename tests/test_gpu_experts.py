@@ -752,3 +752,66 @@ def test_project_f8_few_rows(E, T, K, N, f32):
     want, tol = R.product(x64, R.matrix(w, s))
     within(y[:T], want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
     assert bool((y[T] == 7).all()), "a row past the last is written"
+
+
+# ---------------------------------------------- tiles over more than 64 experts
+def many_counts(n, rows):
+    """Rows of n experts, `rows` on average at least, some experts without any
+    where the experts are looked through 64 at a time."""
+    counts = np.random.default_rng(n + rows).integers(rows // 2, 2 * rows, n)
+    counts[[e for e in (0, 63, 64, 128, 129, 191, 255) if e < n - 1]] = 0
+    counts[-1] += max(0, rows * n - int(counts.sum()))
+    return counts.tolist()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("rows", [9, 64, 192])
+@pytest.mark.parametrize("n", [65, 130, 256])
+def test_experts_many_rows(E, n, rows, f32):
+    """Every tile height, the rows found across several 64s of experts."""
+    log(f"{n} experts of {rows} rows f32 {f32}")
+    g = seeded(n + rows)
+    arrays, offsets, order = counted_plan(g, many_counts(n, rows))
+    check_experts(E, g, arrays, offsets, order, n, 256, 128, 144, f32)
+
+
+@pytest.mark.parametrize("T", [3, 40, 8400])
+def test_down_weights_past_4_gib(E, T):
+    """In one launch, through few rows and through tiles."""
+    log(f"experts_down past 4 GiB T {T}")
+    g = seeded(T)
+    n, N, K = 520, 2048, 4096
+    w = torch.zeros(n, N, K, dtype=torch.uint8, device="cuda")
+    s = torch.ones(n, N // 128, K // 128, device="cuda") / 4096
+    w[-2:], s[-2:] = R.weights8(g, 2, N, K)
+    ids = torch.arange(T)[:, None] % 2 + n - 2
+    offsets, order = R.plan(ids.numpy(), n)
+    i32 = torch.int32
+    arrays = (ids.to(i32).cuda(), torch.rand(T, 1, generator=g, device="cuda"), torch.tensor(offsets, dtype=i32, device="cuda"),
+              torch.tensor(order, dtype=i32, device="cuda"))
+    routes, down = E.Routes(*arrays), E.F8(w, s)
+    h, hs, h64 = R.rows8(g, T, K, False)
+    y = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    E.experts_down(h, hs, down, routes, y, space(E, E.experts_down_bytes(down, routes)))
+    want, tol = R.down(h64, w[-2:], s[-2:], offsets[-3:], order, arrays[1])
+    within(y, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
+
+
+def test_up_weights_past_4_gib_in_tiles(E):
+    log("experts_up past 4 GiB in tiles")
+    g = seeded(33)
+    n, I, K, T = 520, 1024, 4096, 4200
+    w = torch.zeros(n, 2, I, K, dtype=torch.uint8, device="cuda")
+    s = torch.ones(n, 2, I // 128, K // 128, device="cuda") / 4096
+    w[-2:], s[-2:] = R.weights8(g, 2, 2, I, K)
+    ids = torch.arange(T)[:, None] % 2 + n - 2
+    offsets, order = R.plan(ids.numpy(), n)
+    i32 = torch.int32
+    routes = E.Routes(ids.to(i32).cuda(), torch.ones(T, 1, device="cuda"), torch.tensor(offsets, dtype=i32, device="cuda"),
+                      torch.tensor(order, dtype=i32, device="cuda"))
+    x, xs, x64 = R.rows8(g, T, K, False)
+    h = torch.zeros(T, I, dtype=torch.uint8, device="cuda")
+    hs = torch.zeros(T, I // 32, dtype=torch.uint8, device="cuda")
+    E.experts_up(x, xs, E.F8(w, s), routes, h, hs)
+    want, tol = R.up(x64, w[-2:], s[-2:], offsets[-3:], order, 1)
+    check_h(h, hs, want, tol)
