@@ -22,8 +22,9 @@ struct F8Args {
     const void *xs;                     // E8M0 per 32 values, or f32 per 128
     const uint8_t *w;
     const float *ws;
-    void *y;                            // bf16; e4m3 codes; f16 products by slot
-    uint8_t *hs;                        // the codes' exponents + 127; the products' exponents
+    void *y;                            // bf16; e4m3 codes; products by slot, f32 of few
+                                        // rows, f16 of tiles
+    uint8_t *hs;                        // the codes' exponents + 127; f16 products' exponents
     int T, K, N;                        // N: outputs, for kUp those of one half
 };
 

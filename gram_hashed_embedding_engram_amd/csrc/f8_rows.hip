@@ -79,23 +79,13 @@ __device__ __forceinline__ void give(const F8Args &a, const f32x4 (&v)[4], int64
             a.hs[p * (a.N / 32) + n0 / 32] = (uint8_t)(k + 127);
         return;
     }
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            amax = fmaxf(amax, finite_abs(v[i][e]));
-    const int k = f16_scale_exp(max_x16(amax));
-    const float inv = exp2_int(-k);
+    // (as f32: f16 under shared exponents would gain 244 against 248 us for 64 tokens
+    // over 256 experts, and nothing for 8)
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const int n = n0 + 16 * i + 4 * q;
-        if (!in || n >= a.N)
-            continue;
-        *(u32x2 *)((uint16_t *)a.y + (int64_t)slot * a.N + n) =
-            u32x2{cvt_f16x2(v[i][0] * inv, v[i][1] * inv), cvt_f16x2(v[i][2] * inv, v[i][3] * inv)};
-        if (q == 0 && i == 0)
-            a.hs[(int64_t)slot * ((a.N + 31) / 32) + n0 / 32] = (uint8_t)k;
+        if (in && n < a.N)
+            *(f32x4 *)((float *)a.y + (int64_t)slot * a.N + n) = v[i];
     }
 }
 
@@ -268,18 +258,18 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(F8Args a)
     }
 }
 
-// y[t] = sum_j weight[t][j] * product[t * k + j], in j's order; GROUP outputs
-// of a product share an exponent.  Bound by the products' bytes: 4096 tokens of
-// eight experts, 4096 outputs (268 MB), 58 us, 4.6 TB/s.
-template <int GROUP>
-__global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v,
+// y[t] = sum_j weight[t][j] * product[t * k + j], in j's order, in f32.  Products
+// are f32, or f16 where exps has an exponent for each 64 outputs of one.  Bound by
+// their bytes: 4096 tokens of eight experts, 4096 outputs (268 MB of f16), 58 us, 4.6
+// TB/s.
+template <bool F16>
+__global__ __launch_bounds__(256) void sum_kernel(const void *__restrict__ v,
                                                   const int8_t *__restrict__ exps,
                                                   const int32_t *__restrict__ ids,
                                                   const float *__restrict__ weights,
                                                   uint16_t *__restrict__ y, int T, int N, int k, int E)
 {
     typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-    const int groups = (N + GROUP - 1) / GROUP;
     const int64_t pieces = N / 8, all = T * pieces;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
         const int t = (int)(i / pieces), n = 8 * (int)(i - t * pieces);
@@ -289,11 +279,21 @@ __global__ __launch_bounds__(256) void sum_kernel(const uint16_t *__restrict__ v
             const int64_t slot = (int64_t)t * k + j;
             if ((uint32_t)ids[slot] >= (uint32_t)E)
                 continue;
-            const h8 x = __builtin_bit_cast(h8, *(const u32x4 *)(v + slot * N + n));
-            const float f = exp2_int(exps[slot * groups + n / GROUP]);
+            if (F16) {
+                const h8 x = __builtin_bit_cast(h8, *(const u32x4 *)((const uint16_t *)v + slot * N + n));
+                const float f = exp2_int(exps[slot * ((N + 63) / 64) + n / 64]);
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                s[e] += (float)x[e] * f * weights[slot];
+                for (int e = 0; e < 8; e++)
+                    s[e] += (float)x[e] * f * weights[slot];
+            } else {
+                const f32x4 *const x = (const f32x4 *)((const float *)v + slot * N + n);
+                const f32x4 lo = x[0], hi = x[1];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    s[e] += lo[e] * weights[slot];
+                    s[4 + e] += hi[e] * weights[slot];
+                }
+            }
         }
         *(u32x4 *)(y + (int64_t)t * N + n) = u32x4{cvt_bf16x2(s[0], s[1]), cvt_bf16x2(s[2], s[3]),
                                                    cvt_bf16x2(s[4], s[5]), cvt_bf16x2(s[6], s[7])};
@@ -457,7 +457,10 @@ static bool down_few(const Plan &p, int64_t N)
 
 size_t experts_down_bytes(const Plan &p, int64_t N)
 {
-    return down_few(p, N) ? 0 : (size_t)p.slots * (2 * N + (N + 31) / 32);
+    if (down_few(p, N))
+        return 0;
+    return p.slots / p.E >= kTileRows ? (size_t)p.slots * (2 * N + (N + 63) / 64)
+                                      : (size_t)p.slots * N * sizeof(float);
 }
 
 int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uint16_t *y, int64_t K,
@@ -475,21 +478,21 @@ int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uin
             dispatch(down_few_kernel<false>, grid, dim3(64 * kFewWaves), l, true, true, a, split);
         return launch_status("engram experts_down kernel");
     }
-    uint16_t *products = (uint16_t *)ws;
-    uint8_t *exps = (uint8_t *)(products + (int64_t)p.slots * N);
-    const F8Args a{p, h.x, h.s, w.w, w.s, products, exps, p.T, (int)K, (int)N};
     const int64_t blocks = (p.T * (N / 8) + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
     if (p.slots / p.E >= kTileRows) {
+        uint8_t *exps = (uint8_t *)ws + 2 * (int64_t)p.slots * N;
+        const F8Args a{p, h.x, h.s, w.w, w.s, ws, exps, p.T, (int)K, (int)N};
         const int32_t rc = launch_f8_tiles<kDown>(a, h.f32, false, l);
         if (rc != ENGRAM_OK)
             return rc;
-        dispatch(sum_kernel<64>, grid, dim3(256), l, false, true, (const uint16_t *)products,
+        dispatch(sum_kernel<true>, grid, dim3(256), l, false, true, (const void *)ws,
                  (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     } else {
+        const F8Args a{p, h.x, h.s, w.w, w.s, ws, nullptr, p.T, (int)K, (int)N};
         launch_split<kDown, 2, 1, kDownWaves>(a, h.f32, f8_most_tiles(p, 16), false, l);
-        dispatch(sum_kernel<32>, grid, dim3(256), l, false, true, (const uint16_t *)products,
-                 (const int8_t *)exps, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
+        dispatch(sum_kernel<false>, grid, dim3(256), l, false, true, (const void *)ws,
+                 (const int8_t *)nullptr, p.ids, p.weights, y, p.T, (int)N, p.k, p.E);
     }
     return launch_status("engram experts_down kernels");
 }

@@ -411,9 +411,11 @@ __global__ __launch_bounds__(128 * OQ, 2) void tiles_kernel(F8Args a)
                 a.hs[p * (a.N / 32) + n / 32] = (uint8_t)(k + 127);
             continue;
         }
-        // products leave as f16 under a power of two per 64 of a row: half the bytes
-        // of f32, twice over memory (577 -> 470 us for the prompt above), off by 2^-11 of themselves (or 2^-39 of the 64's
-        // largest), an eighth of what the sum's own rounding to bf16 is off by
+        // products leave as f16 under a power of two per 64 of a row: half the bytes of
+        // f32, twice over memory (4096 tokens of eight of 64 experts 455 us, with f32 583;
+        // 1024 tokens 174 and 201, 512 140 and 153).  Each is off by 2^-11 of itself, or
+        // 2^-39 of the 64's largest: an eighth of what the sum's own rounding to bf16 is
+        // off by, but where a token's products cancel.  Few rows (f8_rows.hip) stay f32.
         int k16 = 0;
         if (MODE == kDown) {
             float amax = 0.0f;

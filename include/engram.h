@@ -676,9 +676,12 @@ int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const
  *   d_y     [tokens][N] bf16;
  *   d_ws    (256-byte aligned, caller-owned) of engram_experts_down_bytes bytes;
  *           may be NULL where that is 0.  Calls that share it must not overlap.
- * Where d_ws is used a slot's products pass through it as f16 under a power of two
- * per 32 or 64 outputs (off by 2^-11 of themselves, an eighth of what the result's
- * own rounding is off by); sums are f32, in the slots' order.
+ * Sums are f32, in the slots' order.  In calls of eight slots an expert or more
+ * (tokens * chosen / experts) a slot's products pass through d_ws as f16 under a
+ * power of two per 64 outputs, which moves y by up to the sum over j of
+ * |weight_j| * (2^-11 |product_j| + 2^-39 of the largest of its 64): an eighth of
+ * what y's own rounding is off by where the products do not cancel.  All other
+ * calls keep the products in f32.
  * K a multiple of 128 up to 2^20, N of 16 up to 2^24, and tiles (256 x 256 where
  * experts have many rows) below 2^23, as for engram_experts_up.  d_h, d_w and d_y 16-byte,
  * scales 4-byte aligned. */

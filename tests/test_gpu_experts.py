@@ -815,3 +815,42 @@ def test_up_weights_past_4_gib_in_tiles(E):
     E.experts_up(x, xs, E.F8(w, s), routes, h, hs)
     want, tol = R.up(x64, w[-2:], s[-2:], offsets[-3:], order, 1)
     check_h(h, hs, want, tol)
+
+
+# --------------------------------------------------------- products that cancel
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,n,N", [(1, 4, 64), (8, 4, 2048), (2, 4, 64), (5, 4, 144), (9, 6, 2048), (40, 12, 272), (300, 90, 80)])
+def test_down_products_that_cancel(E, T, n, N, f32):
+    """A token's two experts have the same codes under scales that differ by 2^-9,
+    and its weights are each other's negatives: what is left is as good as f32's
+    products for calls of few rows, of one launch or of two."""
+    log(f"experts_down, cancelling T {T} experts {n} N {N} f32 {f32}")
+    g = seeded(T + n)
+    K = 512
+    assert 2 * T // n < 8
+    ids = 2 * (torch.arange(T) % (n // 2))[:, None] + torch.arange(2)
+    offsets, order = R.plan(ids.numpy(), n)
+    first = torch.rand(T, 1, generator=g, device="cuda") + 0.5
+    weights = torch.cat((first, -first), 1).contiguous()
+    i32 = torch.int32
+    arrays = (ids.to(i32).cuda(), weights, *(torch.tensor(v, dtype=i32, device="cuda") for v in (offsets, order)))
+    w, s = R.weights8(g, n, N, K)
+    w[1::2], s[1::2] = w[::2], s[::2] * (1 + 2.0 ** -9)
+    h, hs, h64 = (v[torch.as_tensor(order, device="cuda") // 2].contiguous() for v in R.rows8(g, T, K, f32))
+    y = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    down, routes = E.F8(w, s), E.Routes(*arrays)
+    E.experts_down(h, hs, down, routes, y, space(E, E.experts_down_bytes(down, routes)))
+    want = torch.zeros(T, N, dtype=F64, device="cuda")
+    tol = torch.zeros_like(want)
+    place = np.argsort(order)
+    for t in range(T):
+        e = 2 * (t % (n // 2))
+        x = h64[place[2 * t]:place[2 * t] + 1]
+        (v, d), (u, _) = (R.product(x, R.matrix(w[i], s[i])) for i in (e, e + 1))
+        size = x.abs() @ R.matrix(w[e], s[e]).abs().t()
+        want[t] = (v - u)[0] * first[t].double()
+        # the sums of a block are the same but for a power of two, so that what they are
+        # off by cancels as they do; the block's factors, the sums over K / 128 blocks, the
+        # weights and the sum of two are rounded in f32, each for two products
+        tol[t] = (2.0 ** -8 * d[0] + 2 * (K / 128 + 4) * 2.0 ** -24 * size[0]) * first[t].double()
+    within(y, want, 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * tol, "y")
