@@ -579,8 +579,7 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
  * projection with the weighted sum over a token's experts
  * (engram_experts_down).  engram_project_f8 is the plain product with weights of
  * the same kind.  As above none of them allocates, keeps state between calls or
- * lets the order of atomics show: equal inputs give equal bits; outputs and
- * workspaces overlap nothing else of the call.
+ * lets the order of atomics show: equal inputs give equal bits.
  *
  * Weights are e4m3 codes [N][K] with one f32 scale per block of 128 x 128,
  * [ceil(N/128)][K/128]: a weight is its code times its block's scale (whatever
@@ -588,10 +587,15 @@ int32_t engram_cache_attend(const engram_cache *cache, const engram_seqs *seqs,
  *   x_f32 = 0:  [rows][K/32] exponents + 127 of a power of two per 32 values
  *               (engram_add_norm's and engram_experts_up's outputs; 255 is NaN);
  *   x_f32 != 0: [rows][K/128] f32.
- * Within a block of 128 the matrix instruction takes the products of eight
- * neighbours together, as engram_project_w4's does (which moves a block's sum by
- * about 2^-16 of its size for normal values); blocks are added in f32.  With
- * x_f32 a row's scale times a block's has to lie within f32's range. */
+ * Within a block of 128 the 8-bit matrix instruction takes the products of eight
+ * neighbours together and cuts each towards zero below 2^-13 of the largest one's
+ * power of two, as engram_project_w4's does: up to 7 * 2^-13 of that power of two
+ * for eight, and for normal values about 2^-16 of the root of the products'
+ * squares' sum (2^-14 where they span 24 powers of two).  Blocks are added in f32.
+ * engram_experts_up's codes follow from such sums: one that lies that near to the
+ * middle of two codes, or a scale to its next power of two, may be the other.
+ * With x_f32 a row's scale times a block's has to lie within f32's range.  What a
+ * call writes and its workspace overlap nothing else of it (ENGRAM_E_ARG). */
 #define ENGRAM_F8_BLOCK 128
 
 /* y[t][n] = bf16( sum_k x[t][k] * w[n][k] ).
