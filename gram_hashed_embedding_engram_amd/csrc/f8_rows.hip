@@ -459,8 +459,13 @@ size_t experts_down_bytes(const Plan &p, int64_t N)
 {
     if (down_few(p, N))
         return 0;
-    return p.slots / p.E >= kTileRows ? (size_t)p.slots * (2 * N + (N + 63) / 64)
-                                      : (size_t)p.slots * N * sizeof(float);
+    // f32 products of few rows; f16 ones and their exponents of tiles, and no less than
+    // f32 ones of the most rows that no tiles take, so that a workspace serves every
+    // call of fewer tokens
+    const int64_t few = kTileRows * p.E - 1;
+    const size_t f32 = (size_t)(p.slots < few ? p.slots : few) * N * sizeof(float);
+    const size_t f16 = (size_t)p.slots * (2 * N + (N + 63) / 64);
+    return p.slots / p.E >= kTileRows && f16 > f32 ? f16 : f32;
 }
 
 int32_t launch_experts_down(const Plan &p, const Rows8 &h, const Blocks8 &w, uint16_t *y, int64_t K,

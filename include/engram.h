@@ -679,7 +679,8 @@ int32_t engram_experts_up(const engram_routes *routes, const uint8_t *d_x, const
  *   d_w     [experts][N][K];  d_w_scales [experts][ceil(N/128)][K/128];
  *   d_y     [tokens][N] bf16;
  *   d_ws    (256-byte aligned, caller-owned) of engram_experts_down_bytes bytes;
- *           may be NULL where that is 0.  Calls that share it must not overlap.
+ *           may be NULL where that is 0; enough for a call of fewer tokens too.
+ *           Calls that share it must not overlap.
  * Sums are f32, in the slots' order.  In calls of eight slots an expert or more
  * (tokens * chosen / experts) a slot's products pass through d_ws as f16 under a
  * power of two per 64 outputs, which moves y by up to the sum over j of

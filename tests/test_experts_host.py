@@ -318,3 +318,19 @@ def test_neighbours_are_not_refused(L, op):
             if out == "d_order":
                 moved["d_err"] = start + 400
             assert far_call(L, op, moved) == E.E_ARG and "error word" in E.last_error(), (op, out, other)
+
+
+def test_a_workspace_serves_fewer_tokens(L):
+    """A workspace made for a call of the most tokens is enough for any call of
+    fewer: what a call needs does not fall as tokens are added."""
+    steps = sorted({*range(1, 1300), *(64 * i + d for i in range(1, 400) for d in (-1, 0, 1)), 40000, 300000, 1 << 20})
+    for n, k in ((1, 1), (4, 2), (60, 4), (256, 8), (1024, 32)):
+        for need in (lambda r: L.engram_experts_down_bytes(ctypes.byref(r), 64),
+                     lambda r: L.engram_experts_down_bytes(ctypes.byref(r), 4112)):
+            last = (0, 0)
+            for T in steps:
+                if T * k > 1 << 24:
+                    break
+                now = need(routes_c(experts=n, chosen=k, tokens=T))
+                assert now >= last[1], f"{n} experts, {k} a token: {T} tokens need {now} bytes, {last[0]} {last[1]}"
+                last = (T, now)
