@@ -720,7 +720,7 @@ int64_t block_of(int64_t T)
     return T <= kBlockTokens || n > kBlockTokens ? kBlockTokens : n;
 }
 int64_t blocks_of(int64_t T) { return (T + block_of(T) - 1) / block_of(T); }
-size_t counts_bytes(int64_t T, int32_t E) { return ((size_t)(blocks_of(T) * pitch_of(E)) + 255) & ~(size_t)255; }
+size_t counts_bytes(int64_t blocks, int32_t E) { return ((size_t)(blocks * pitch_of(E)) + 255) & ~(size_t)255; }
 
 template <bool BF16, int NR>
 void launch_scores(const Routing &r, uint8_t *counts, const Launch &l)
@@ -752,7 +752,10 @@ size_t route_bytes(int64_t T, int32_t E)
     const int64_t blocks = blocks_of(T);
     if (blocks <= 1)
         return 0;
-    size_t n = counts_bytes(T, E);
+    // (calls of fewer tokens may have smaller and so more blocks, up to kMostBlocks: a
+    // workspace serves them too)
+    const int64_t small = (T + kWaves - 1) / kWaves, most = small < kMostBlocks ? small : kMostBlocks;
+    size_t n = counts_bytes(most > blocks ? most : blocks, E);
     if (blocks > kMostBlocks)
         n += (size_t)((blocks + kSegment - 1) / kSegment) * pitch_of(E) * sizeof(int32_t);
     return n;
@@ -764,7 +767,7 @@ int32_t launch_route(const Routing &r, void *ws, const Launch &l)
     uint8_t *counts = blocks > 1 ? (uint8_t *)ws : nullptr;
     r.bf16 ? launch_type<true>(r, counts, l) : launch_type<false>(r, counts, l);
     if (counts) {
-        int32_t *sums = blocks > kMostBlocks ? (int32_t *)(counts + counts_bytes(r.T, r.E)) : nullptr;
+        int32_t *sums = blocks > kMostBlocks ? (int32_t *)(counts + counts_bytes(blocks, r.E)) : nullptr;
         if (sums)
             dispatch(segment_kernel, dim3((unsigned)((blocks + kSegment - 1) / kSegment)), dim3(256),
                      l, false, false, (const uint8_t *)counts, sums, (int)blocks, pitch_of(r.E));

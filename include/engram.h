@@ -650,7 +650,8 @@ typedef struct engram_routes {
  * A token with fewer open experts than `chosen` has id -1 and weight 0 in its
  * last slots, which are not in the plan; a row of -inf goes nowhere.
  *   d_ws  (256-byte aligned, caller-owned) of engram_route_bytes bytes; may be
- *         NULL where that is 0.  Calls that share it must not overlap.
+ *         NULL where that is 0; enough for a call of fewer tokens too.  Calls that
+ *         share it must not overlap.
  * tokens = 0 is a no-op (the plan is not written). */
 size_t engram_route_bytes(const engram_routes *routes);
 int32_t engram_route(const engram_routes *routes, const void *d_logits, int32_t logits_bf16,

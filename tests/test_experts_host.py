@@ -325,7 +325,7 @@ def test_a_workspace_serves_fewer_tokens(L):
     fewer: what a call needs does not fall as tokens are added."""
     steps = sorted({*range(1, 1300), *(64 * i + d for i in range(1, 400) for d in (-1, 0, 1)), 40000, 300000, 1 << 20})
     for n, k in ((1, 1), (4, 2), (60, 4), (256, 8), (1024, 32)):
-        for need in (lambda r: L.engram_experts_down_bytes(ctypes.byref(r), 64),
+        for need in (lambda r: L.engram_route_bytes(ctypes.byref(r)), lambda r: L.engram_experts_down_bytes(ctypes.byref(r), 64),
                      lambda r: L.engram_experts_down_bytes(ctypes.byref(r), 4112)):
             last = (0, 0)
             for T in steps:
