@@ -498,7 +498,9 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
         }
     }
     const float sum = wave_sum(s);
-    if (exact || (sum < 0x1p-90f && __ballot(id >= 0))) {
+    // (a score below 2^-90, whose e^-x or own value f32 holds with few bits or not at
+    // all, is taken in 64 bits as well)
+    if (exact || __ballot(id >= 0 && s < 0x1p-90f)) {
         double s64[NR], k64[NR];
         const Exact e64 = exact_of<NR>(a, x);
 #pragma unroll

@@ -893,3 +893,21 @@ def test_project_f8_sums(E, T, f32, spread):
     y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
     E.project_f8(x.view(torch.uint8), E.F8(w.view(torch.uint8), torch.ones(1, K // 128, device="cuda")), y, xs)
     within(y, want, 2.0 ** -8 * want.abs() + K * 2.0 ** -24 * size, "y")
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_small_scores(E, softmax, renorm):
+    """Scores near and below f32's normal numbers, chosen beside larger ones."""
+    g = seeded(41)
+    T = 400
+    depth = torch.rand(T, 1, generator=g, device="cuda") * 70
+    x = torch.full((T, 8), -INF, device="cuda")
+    x[:, 1] = 0.3
+    x[:, 4:7] = -torch.rand(T, 3, generator=g, device="cuda") * 50 - 45 - depth
+    check_route(E, x, None, 4, softmax, renorm=renorm, what="beside one of a common size")
+    bias = torch.zeros(8, device="cuda")
+    bias[4:] = 5                                       # the second group is kept, the first has the largest score
+    x = torch.rand(T, 8, generator=g, device="cuda")
+    x[:, 4:] = -torch.sort(torch.rand(T, 4, generator=g, device="cuda"), 1).values * 50 - 50 * torch.rand(T, 1, generator=g, device="cuda")
+    check_route(E, x, bias, 4, softmax, 2, 1, 1, renorm=renorm, what="all small")
