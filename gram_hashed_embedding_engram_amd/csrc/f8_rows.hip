@@ -9,10 +9,12 @@
 // workgroup, which keeps enough loads in flight where there are few outputs; the
 // parts meet in LDS.  An expert's rows are found by a scan over the plan's spans.
 //
-// Bound by the weights' bytes.  One token of 4096 x 6144: 6.8 us, of which a launch
-// and two trips to memory are 4; sixteen of 6144 x 20480 (126 MB) 27 us; one token's
-// eight experts of 4096 x (2 x 2048) (134 MB) 28 us; 64 tokens over 256 of them, 164
-// met (2.75 GB), 444 us, 6.2 TB/s; their down projection (1.4 GB) 245 us, 5.6 TB/s.
+// Bound by the weights' bytes.  One token of 4096 x 6144: 6.8 to 7.1 us, of which a
+// launch and two trips to memory are 4; sixteen of 6144 x 20480 (126 MB) 27 us; one
+// token's eight experts of 4096 x (2 x 2048) (134 MB) 28 us; 64 tokens over 256 of
+// them, 164 met (2.75 GB), 440 to 515 us as the clocks go, 6.2 to 5.3 TB/s; their down
+// projection (1.4 GB) 247 to 277 us with its sum, 5.6 to 5 TB/s.  Rows with f32 scales
+// take the same (up 461 to 509, down 250 to 283).
 //
 // Measured on the way: loads marked non-temporal are slower (444 -> 500 us and
 // more: an expert's second tile and the next call find nothing in the caches); more

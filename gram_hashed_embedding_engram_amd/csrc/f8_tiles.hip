@@ -24,14 +24,15 @@
 // Consecutive workgroups go to the XCDs in turn, so each XCD gets a contiguous run
 // of tiles: neighbours share weights and rows in its L2.
 //
-// 4096 tokens of 6144 x 20480 (1.03 TFLOP): 472 us, 2.18 PFLOP/s, where the same
-// without its loads takes 395 (without its barriers 375): matrix and vector
+// 4096 tokens of 6144 x 20480 (1.03 TFLOP): 472 to 515 us, 2.18 to 2.0 PFLOP/s, where
+// the same without its loads takes 395 (without its barriers 375): matrix and vector
 // instructions at the clock that the power limit leaves; the library's product
 // without block scales takes 402.  A round of 256 tiles of 256 x 256 costs 1.8 us a
 // block and 8.6 once (the first loads, the stores of all CUs at once).  500 tokens of
-// 2048 x 5200: 12 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336: 12.5 us.
-// 4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 715 us, 1.54 PFLOP/s,
-// unevenly filled tiles and their borders; down 445 us, 58 of them the sum's.
+// 2048 x 5200: 12 to 12.7 us, bound by the trips of its 16 blocks; 37 of 4096 x 14336:
+// 12.5 to 13 us.  4096 tokens of eight of 64 experts: up (4096 -> 2 x 2048) 714 to 777
+// us, 1.54 to 1.42 PFLOP/s, unevenly filled tiles, their borders and silu; down 445 to
+// 474 us, 58 to 61 of them the sum's.  Rows with f32 scales take the same.
 //
 // Tried and set aside: a workgroup a CU that loads on into its next tile under the
 // stores (a tile's fixed cost 8.6 -> 5.9 us, a block 1.82 -> 1.90, and static shares
@@ -49,22 +50,32 @@ namespace {
 
 constexpr int XCDS = 8;
 // Rows of an expert, on average, from which tiles of 256 and of 128 rows are taken.
-// Up, 64 experts of 4096 x 2048, in us: 128 rows 318 with 256-row tiles and 289 with
-// 128-row ones, 512 rows 722 and 754; 32 rows 208 with 128-row and 199 with 64-row
-// tiles, 48 rows 226 and 216, 64 rows 226 and 225; down, 64 rows 140 and 145, 128
-// rows 173 and 194.
+// In us, tiles of 256, 128 and 64 rows, 64 experts.  Up, 4096 x 2048: 32 rows 223, 206,
+// 200; 64 rows 244, 223, 230; 128 rows 329, 282, 323; 192 rows 390, 367, 411; 256 rows
+// 445, 445, 518; 375 rows 570, 592, 713; 512 rows 719, 760, 925.  Down, 2048 x 4096: 64
+// rows 147, 140, 146; 128 rows 190, 175, 195; 192 rows 236, 227, 254; 256 rows 266, 271,
+// 318.  Eight experts of 250 rows: up 71, 83, 87, down 45, 52, 54, for which the border
+// lies at 192 and not at 256.  Products of few tiles lose by it: eight experts of 250
+// rows take 41, 25 and 32 us for 2048 x 1024, 27, 17 and 12 for 1024 x 512.
 constexpr int64_t kRows8 = 192, kRows4 = 64;
 // What a tile on every CU costs, and what each of several does, in 0.1 us at K = 4096,
 // of tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 128 and 64 x 64 (two workgroups a CU
 // from 128 x 128 down): the size with the least is taken.  4096 x 10240, 1000 tokens:
-// 59, 68, 57, 59, 66 us; 4096 x 4096, 2000 tokens: 59, 40, 38, 45, 54, 500 tokens: 57,
-// 34, 23, 17, 15; 4096 x 6144, 100 tokens: 55, 33, 23, 17, 13; 4096 x 14336, 200 tokens:
-// 57, 34, 24, 22, 28; 6144 x 20480, 1000 tokens: 173, 170, 149, 193, 239.
+// 62, 69, 57, 62, 69 us; 4096 x 4096, 2000 tokens: 59, 41, 40, 49, 56, 500 tokens: 57,
+// 34, 24, 18, 16; 4096 x 6144, 100 tokens: 54, 33, 23, 17, 13; 4096 x 14336, 200 tokens:
+// 56, 35, 25, 24, 30; 6144 x 20480, 1000 tokens: 183, 173, 150, 196, 238.  The costs are
+// compared with each other, so the same serve every K: of 66 products of 40 to 4096
+// tokens, 4096 to 20480 outputs and K = 128 to 6144, 52 take the best size or one
+// within 5% of it, the others within 14%, but one (1000 tokens of 512 x 20480: 26 us
+// and 22).
 constexpr int64_t kAlone[5] = {610, 380, 245, 165, 127}, kEach[5] = {610, 380, 200, 120, 72};
-// The same for few rows of weights that no cache keeps, where rows' reads from L2 slow
-// the stream: 6144 x 20480 (126 MB), 64 tokens in tiles of 64 x 128 35 us and of 64 x 64
-// 40, 128 tokens in tiles of 128 x 128 45, of 64 x 64 52; where 4096 x 14336 (59 MB),
-// which the last-level cache holds, takes 18 and 16 us for 128 tokens.
+// The same for few rows of large weights, where rows' reads from L2 slow the stream of
+// weights.  In us, tiles of 128 x 128, 64 x 128 and 64 x 64, for three matrices in turn
+// (which the last-level cache of 256 MB does not hold) and for one again and again: 64
+// tokens, 59 MB 23, 17, 13 both ways; 101 MB 31, 25, 27 and 24, 18, 18; 126 MB 42, 35, 40
+// and 33, 24, 25; 168 MB 56, 46, 49 and 42, 31, 30; 128 tokens, 88 MB 38, 28, 31 and 33,
+// 24, 23; 101 MB 32, 35, 34 and 26, 24, 24; 126 MB 45, 54, 51 and 34, 35, 35; 168 MB 57,
+// 64, 63 and 44, 42, 42.
 constexpr int64_t kEachStreamed[5] = {610, 380, 200, 130, 100};
 constexpr int64_t kStreamedRows = 128, kStreamedBytes = (int64_t)96 << 20;
 

@@ -19,11 +19,19 @@
 // the number of bits below its own.  Calls of more tokens count per 64 tokens
 // and place in a second launch, which sums the counts before its own.
 //
-// 16384 tokens of 256 experts in 8 groups (17 MB): 27 us, of which the second
-// launch is 6; bound by the vector instructions of a token, some 450.  One token:
-// 6.2 us, a launch and a chain of some thousand cycles.  Each choice as a maximum of
-// its own took 54 us, 22 of them the few tokens taken again in 64 bits one choice
-// after the other; now the candidates alone are ranked again.
+// 16384 tokens of 256 experts in 8 groups (17 MB): 27 to 28 us, of which the second
+// launch is 6.  It waits on itself: the vector units are busy 44% of the time and LDS
+// 10%, with one workgroup of 16 wavefronts a CU (128 registers), each wavefront a chain
+// of some 450 instructions a token, many of them across lanes.  The 64-bit paths stand
+// in the same function, and what does not fit into 128 registers goes to scratch: none
+// of a lane's for up to 256 experts, 34 for 512, 178 for 1024 (16384 tokens of 384
+// experts 42 us, of 1024 141 to 161).  One token: 6.2 us, a launch and a chain of some thousand
+// cycles; 64, in one workgroup, 20.6.  Rows with more than k + 16 equal best keys, such
+// as logits of nothing but zeros, find no bound and choose one expert after the other
+// in 64 bits: three times as long (16384 such rows 87 us, 64 of them 80; of 1024
+// experts 320).  Each choice as a maximum of its own took 54 us, 22 of them the few
+// tokens taken again in 64 bits one choice after the other; now the candidates alone
+// are ranked again.
 #include <float.h>
 
 #include "experts.h"
@@ -36,8 +44,8 @@ constexpr int kWaves = 16;
 // counts of this many blocks are summed once more before the blocks are placed
 constexpr int kSegment = 64;
 constexpr int kMostBlocks = 256;        // placed from the counts alone
-// candidates for a token's choice beyond those needed: 7, 15 and 30 take 44, 33 and
-// 34 us for 16384 tokens of 256 experts (more trials, more to rank)
+// candidates for a token's choice beyond those needed: 7, 15 and 30 take 28.3, 28.3 and
+// 29.4 us for 16384 tokens of 256 experts (more trials, more to rank)
 constexpr int kSpare = 15;
 
 typedef unsigned long long u64;
@@ -713,9 +721,11 @@ __global__ __launch_bounds__(64 * kWaves) void place_kernel(Routing a, const uin
 
 int pitch_of(int32_t E) { return (E + 15) / 16 * 16; }
 // A block's tokens: a multiple of one a wavefront that makes kMostBlocks blocks at
-// most, and all of a call's that one block holds (one launch).  777 tokens in blocks
-// of 16 and of 64: 9 and 18 us; 16384 in blocks of 32 and of 64: 42 and 30 us, whose
-// blocks each add up the counts of all.
+// most, and all of a call's that one block holds, which needs one launch and no
+// workspace.  777 tokens of 60 experts in blocks of 16 and of 64: 9.7 and 14 us, of 256
+// experts 13 and 24; 16384 in blocks of 32 and of 64: 38 and 28 us, whose blocks each
+// add up the counts of all.  17, 33 and 64 tokens of 256 experts in one block 9.7, 13.0
+// and 20.6 us, in blocks of 16 and two launches 11.6, 11.7 and 12.0.
 int64_t block_of(int64_t T)
 {
     const int64_t n = (T + kMostBlocks * kWaves - 1) / (kMostBlocks * kWaves) * kWaves;

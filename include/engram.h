@@ -620,7 +620,8 @@ int32_t engram_project_f8(const uint8_t *d_x, const void *d_x_scales, int32_t x_
  * engram_route writes all but d_err; the products read them.  A plan made
  * elsewhere may order an expert's slots as it likes: each slot with an expert is in
  * it once, under that expert.  Offsets outside 0..tokens*chosen or falling, and
- * slots out of range, set ENGRAM_DEVERR_ROUTE; their rows are not computed, and
+ * slots out of range, set ENGRAM_DEVERR_ROUTE; their rows are not computed (nor may
+ * others be where falling offsets leave spans that overlap), and
  * engram_experts_down's y is unspecified for tokens with an expert whose slot the
  * plan lacks or holds twice. */
 typedef struct engram_routes {
