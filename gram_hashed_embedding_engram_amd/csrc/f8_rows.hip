@@ -32,13 +32,15 @@ namespace {
 constexpr int64_t kMostRows = 32;
 // The same for an expert's rows on average.  Up, 64 experts of 4096 x 2048: 4 rows
 // 162 and 165, 8 rows 185 and 173; 256 of 2048 x 1024, 8 rows 194 and 183; 16
-// experts, 2 rows 38 and 49, 8 rows 57 and 65.  Down, 64 of 2048 x 4096: 4 rows 89
-// and 91, 8 rows 117 and 101; 256 experts, 8 rows 430 and 355.
+// experts, 2 rows 38 and 49, 8 rows 57 and 65.  Down, 64 of 2048 x 4096: 4 rows 95
+// and 96, 6 rows 106 and 98, 8 rows 118 and 100; 256 experts, 8 rows 437 and 355; 16
+// experts, 2 rows 23 and 23, 8 rows 34 and 29.5.
 constexpr int64_t kTileRows = 8;
 constexpr int kFewSlots = 16, kFewWaves = 16;
 // Wavefronts that share an expert's K.  Up, 1, 2, 4 and 8 of them: one token 50, 31,
 // 28 and 28 us, 64 tokens 486, 452, 444 and 458.  Down, 1, 2 and 4: 64 tokens 244, 245
-// and 250, three 40, 38 and 36, 8 tokens 84, 81 and 80.
+// and 250, three 40, 38 and 36, 8 tokens 84, 81 and 80 (with products as f16: as f32
+// 64 tokens take 3 more).
 constexpr int kUpWaves = 4, kDownWaves = 2;
 
 __device__ __forceinline__ i32x8 operand(const u32x4 &a, const u32x4 &b)
@@ -449,9 +451,10 @@ int32_t launch_experts_up(const Plan &p, const Rows8 &x, const Blocks8 &w, uint8
     return launch_status("engram experts_up kernel");
 }
 
-// Whether a call's products stay in LDS.  Both ways in us, 2048 x 4096: 2 slots 8.7
-// and 9.7, 8 slots 15.5 and 20, 16 slots 22 and 26, 32 slots 44 to 51 and 51; 16
-// slots of 1024 x 1024, which make few workgroups, 12 and 10.
+// Whether a call's products stay in LDS.  Both ways in us, 2048 x 4096: 2 slots 8.9
+// and 10.9, 8 slots 14.9 and 18.8, 16 slots 23 and 29, 32 slots 39 and 45, but LDS for
+// as many takes 2 slots from 8.9 to 14; 1024 x 1024, whose workgroups are few: 4 slots
+// 8.4 and 8.9, 16 slots 13 and 10.7.
 static bool down_few(const Plan &p, int64_t N)
 {
     return p.slots <= kFewSlots && (p.slots <= 4 || N >= 2048) && p.slots / p.E < kTileRows;
