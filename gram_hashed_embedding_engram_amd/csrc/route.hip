@@ -403,9 +403,10 @@ __device__ __forceinline__ void choose(const Routing &a, const Groups &gr, const
         bool near = false;
         if (const u64 next = __ballot(in && ahead == a.top_groups)) {
             if (logits) {
+                // (where the last kept and the next are equal, others may be near both)
                 const u64 last = __ballot(in && ahead == a.top_groups - 1);
-                near = near_logits(lane_value(sum, __builtin_ctzll(last)),
-                                   lane_value(sum, __builtin_ctzll(next)), top, a.softmax);
+                const float u = lane_value(sum, __builtin_ctzll(last)), v = lane_value(sum, __builtin_ctzll(next));
+                near = __ballot(in && near_logits(keep ? sum : u, keep ? v : sum, top, a.softmax));
             } else {
                 // the least that a kept sum may be, the most that another may
                 const float e = sum_error(first, a.group_best > 1 ? second : first, unit);

@@ -911,3 +911,19 @@ def test_route_small_scores(E, softmax, renorm):
     x = torch.rand(T, 8, generator=g, device="cuda")
     x[:, 4:] = -torch.sort(torch.rand(T, 4, generator=g, device="cuda"), 1).values * 50 - 50 * torch.rand(T, 1, generator=g, device="cuda")
     check_route(E, x, bias, 4, softmax, 2, 1, 1, renorm=renorm, what="all small")
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("n,groups,top", [(256, 4, 2), (512, 32, 11), (65, 13, 2), (64, 16, 5), (60, 12, 7), (3, 3, 1)])
+def test_route_equal_scores_of_groups(E, n, groups, top, softmax):
+    """A group's one best score, without a bias: logits that differ and whose scores
+    are one number of 64 bits, among equal logits, go by the group's index."""
+    g = seeded(n + top)
+    T, size = 300, n // groups
+    whole = torch.randint(0, 6, (T, n), generator=g, device="cuda").float()
+    for what, x in (("tiny", whole * 1e-30), ("about 0.5", 0.5 + whole * 2.0 ** -24), ("sigmoids of 1", 40 + whole),
+                    ("vanishing", -2000 - 100 * whole), ("lowest", torch.where(whole < 3, whole * 1e30 - 3e38, -whole))):
+        if what == "vanishing":
+            x[:, 0] = 0                                # (a softmax's largest)
+        for v in (x, x.bfloat16()):
+            check_route(E, v, None, min(5, size), softmax, groups, top, 1, what=what)
