@@ -25,8 +25,8 @@
 // of some 450 instructions a token, many of them across lanes.  The 64-bit paths stand
 // in the same function, and what does not fit into 128 registers goes to scratch: none
 // of a lane's for up to 256 experts, 34 for 512, 178 for 1024 (16384 tokens of 384
-// experts 42 us, of 1024 141 to 161).  One token: 6.2 us, a launch and a chain of some thousand
-// cycles; 64, in one workgroup, 20.6.  Rows with more than k + 16 equal best keys, such
+// experts 42 us, of 1024 141 to 161).  One token: 6.2 us, a launch and a chain of some
+// thousand cycles; 64, in one workgroup, 20.6.  Rows with more than k + 16 equal best keys, such
 // as logits of nothing but zeros, find no bound and choose one expert after the other
 // in 64 bits: three times as long (16384 such rows 87 us, 64 of them 80; of 1024
 // experts 320).  Each choice as a maximum of its own took 54 us, 22 of them the few
